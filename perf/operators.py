@@ -219,7 +219,8 @@ def _plain_product(s):
 
 def _own_product(s):
     from hpc_linear_algebra_amd import blocks
-    return blocks.gemm(s["A"], s["B"], dtype=s["out"])
+    # 16-bit results take the 8-bit matrix instructions' sums, float ones (weight gradients) sums in float
+    return blocks.gemm(s["A"], s["B"], dtype=s["out"], fast=s["out"] != "f32")
 
 
 def _plain_moe(s):

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtlrgemm.so")
-SOURCES = ["planner.cpp", "abi.cpp", "executor.cpp", "noalloc.cpp", "gemm.hip", "gemm16.hip", "compress.hip"]
+SOURCES = ["planner.cpp", "abi.cpp", "executor.cpp", "noalloc.cpp", "gemm.hip", "gemm16.hip", "compress.hip",
+           "block.hip", "moe.hip"]
 ARCH = "gfx950"
 
 

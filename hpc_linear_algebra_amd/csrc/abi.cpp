@@ -5,6 +5,7 @@
 #include <new>
 #include <string>
 
+#include "tlr_ops.h"
 #include "tlr_plan.h"
 
 struct tlr_plan {
@@ -257,6 +258,40 @@ tlr_status tlr_dense_gemm(tlr_dtype dt, tlr_op opA, tlr_op opB, int64_t m, int64
                           const void *A, int64_t lda, const void *B, int64_t ldb, double beta, void *C, int64_t ldc,
                           void *stream) {
   TLR_GUARD({ return tlr::dense_gemm(dt, opA, opB, m, n, k, alpha, A, lda, B, ldb, beta, C, ldc, stream); })
+}
+
+tlr_status tlr_block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_t rows, int64_t k, const void *X,
+                              int64_t ldx, void *codes, int64_t ldq, float *scales, int64_t lds, void *codes_t,
+                              int64_t ldq_t, float *scales_t, int64_t lds_t, void *stream) {
+  TLR_GUARD({
+    return tlr::block_quantize(dt, fmt, block, rows, k, X, ldx, codes, ldq, scales, lds, codes_t, ldq_t, scales_t,
+                               lds_t, stream);
+  })
+}
+
+tlr_status tlr_block_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t *bytes_out) {
+  TLR_GUARD({ return tlr::block_gemm_workspace(m, n, k, bytes_out); })
+}
+
+tlr_status tlr_block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alpha, const tlr_block_matrix *A,
+                          const tlr_block_matrix *B, double beta, void *C, int64_t ldc, uint32_t flags,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  TLR_GUARD({
+    return tlr::block_gemm(dt, m, n, k, alpha, A, B, beta, C, ldc, flags, workspace, workspace_bytes, stream);
+  })
+}
+
+tlr_status tlr_moe_workspace_bytes(const tlr_moe_layer *layer, int32_t max_tokens, size_t *bytes_out) {
+  TLR_GUARD({ return tlr::moe_workspace(layer, max_tokens, bytes_out); })
+}
+
+tlr_status tlr_moe_init(const tlr_moe_layer *layer, void *workspace, size_t workspace_bytes, void *stream) {
+  TLR_GUARD({ return tlr::moe_init(layer, workspace, workspace_bytes, stream); })
+}
+
+tlr_status tlr_moe(const tlr_moe_layer *layer, int32_t tokens, const void *X, int64_t ldx, void *Y, int64_t ldy,
+                   int32_t *ids, float *weights, void *workspace, size_t workspace_bytes, void *stream) {
+  TLR_GUARD({ return tlr::moe(layer, tokens, X, ldx, Y, ldy, ids, weights, workspace, workspace_bytes, stream); })
 }
 
 const char *tlr_status_string(tlr_status s) {

@@ -1,0 +1,86 @@
+"""A mixture-of-experts layer for a few tokens (torch plumbing around tlr_moe,
+include/tlrgemm.h): router, softmax, top-k, gated experts (silu), weighted sum.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import tlrgemm as T
+
+MAX_TOKENS = 256
+_DT = {torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
+
+
+class MoELayer:
+    """One layer's weights with the workspace of up to ``max_tokens`` tokens.
+
+    router     (experts, hidden), float16 or bfloat16: the type of x and y
+    gate_up    (experts, 2*inter, hidden): inter gate rows, then inter up rows
+    down       (experts, hidden, inter)
+    The expert weights have the router's type, or are float8_e4m3fn codes with
+    128 x 128 block scales (as blocks.quantize gives them for one expert):
+    gate_up_scales (experts, ceil(hidden/128), ceil(2*inter/128)) and
+    down_scales (experts, ceil(inter/128), ceil(hidden/128)), float32.
+    hidden and inter are multiples of 16, every tensor is contiguous.
+
+    Calls share the layer's workspace: they run in the order of one stream, or
+    with events between them.
+    """
+
+    def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, topk: int,
+                 max_tokens: int = 64, normalize: bool = True, gate_up_scales: Optional[torch.Tensor] = None,
+                 down_scales: Optional[torch.Tensor] = None):
+        if router.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3 or router.dtype not in _DT:
+            raise ValueError("MoELayer: router (experts, hidden) in float16 or bfloat16, gate_up and down of 3 dimensions")
+        experts, hidden = router.shape
+        inter = down.shape[2]
+        if tuple(gate_up.shape) != (experts, 2 * inter, hidden) or tuple(down.shape) != (experts, hidden, inter):
+            raise ValueError("MoELayer: gate_up is (experts, 2*inter, hidden) and down (experts, hidden, inter)")
+        e8 = gate_up.dtype == torch.float8_e4m3fn
+        if gate_up.dtype != down.dtype or not (e8 or gate_up.dtype == router.dtype):
+            raise ValueError("MoELayer: expert weights are of the router's type or float8_e4m3fn")
+        tensors = [router, gate_up, down]
+        if e8:
+            up = lambda n: -(-n // 128)   # noqa: E731
+            for s, shape in ((gate_up_scales, (experts, up(hidden), up(2 * inter))),
+                             (down_scales, (experts, up(inter), up(hidden)))):
+                if s is None or s.dtype != torch.float32 or tuple(s.shape) != shape:
+                    raise ValueError(f"MoELayer: 8-bit weights need float32 scales of shape {shape}")
+            tensors += [gate_up_scales, down_scales]
+        elif gate_up_scales is not None or down_scales is not None:
+            raise ValueError("MoELayer: scales belong to 8-bit weights")
+        self.device = router.device
+        if any(t.device != self.device or not t.is_cuda or not t.is_contiguous() for t in tensors):
+            raise ValueError("MoELayer: contiguous tensors on one GPU are needed")
+        self.dtype, self.hidden, self.inter, self.experts, self.topk = router.dtype, hidden, inter, experts, int(topk)
+        self.max_tokens = int(max_tokens)
+        self._keep = tensors
+        dt = _DT[router.dtype]
+        self.c = T.tlr_moe_layer(hidden, inter, experts, self.topk, dt, T.TLR_E4M3 if e8 else dt, 1 if normalize else 0,
+                                 0, router.data_ptr(), gate_up.data_ptr(), down.data_ptr(),
+                                 gate_up_scales.data_ptr() if e8 else None, down_scales.data_ptr() if e8 else None)
+        self.ws = torch.empty(max(256, T.tlr_moe_workspace_bytes(self.c, self.max_tokens)), dtype=torch.uint8,
+                              device=self.device)
+        with torch.cuda.device(self.device):
+            T.tlr_moe_init(self.c, self.ws.data_ptr(), self.ws.numel(), torch.cuda.current_stream().cuda_stream)
+
+    def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(y, ids, weights) of x (tokens, hidden): the layer's output in x's
+        type, the chosen experts (int32) and their probabilities (float32)."""
+        if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype != self.dtype or x.device != self.device:
+            raise ValueError(f"MoELayer: x is (tokens, {self.hidden}) of type {self.dtype} on {self.device}")
+        t = x.shape[0]
+        if t > self.max_tokens:
+            raise ValueError(f"MoELayer: {t} tokens, made for {self.max_tokens}")
+        if x.stride(1) != 1 or x.data_ptr() % 16 or (t > 1 and x.stride(0) % 8):
+            x = x.contiguous()
+        y = torch.empty((t, self.hidden), dtype=x.dtype, device=x.device)
+        ids = torch.empty((t, self.topk), dtype=torch.int32, device=x.device)
+        weights = torch.empty((t, self.topk), dtype=torch.float32, device=x.device)
+        with torch.cuda.device(self.device):
+            T.tlr_moe(self.c, t, x.data_ptr(), x.stride(0) if t > 1 else self.hidden, y.data_ptr(), self.hidden,
+                      ids.data_ptr(), weights.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                      torch.cuda.current_stream(self.device).cuda_stream)
+        return y, ids, weights

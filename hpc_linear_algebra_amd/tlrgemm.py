@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtlrgemm.
 TLR_OK, TLR_ERR_INVALID_ARG, TLR_ERR_RANK, TLR_ERR_WORKSPACE = 0, -1, -2, -3
 TLR_ERR_UNSUPPORTED, TLR_ERR_HIP, TLR_ERR_NOT_BOUND = -4, -5, -6
 TLR_F32, TLR_F64, TLR_F16, TLR_BF16 = 0, 1, 2, 3
+TLR_E4M3, TLR_E5M2 = 4, 5
+TLR_BLOCK_FAST = 0x1
 TLR_OP_N, TLR_OP_T = 0, 1
 TLR_ORDER_RIGHT, TLR_ORDER_LEFT = 0, 1
 TLR_PLAN_FORCE_RIGHT, TLR_PLAN_FORCE_LEFT, TLR_PLAN_NO_REGIONS, TLR_PLAN_VALIDATE = 0x1, 0x2, 0x4, 0x8
@@ -30,7 +32,8 @@ EXPORTED = [
     "tlr_plan_stage_shapes", "tlr_plan_launch", "tlr_plan_destroy", "tlr_plan_bind",
     "tlr_gemm_execute", "tlr_gemm_execute_noalloc", "tlr_expand", "tlr_compress_workspace_bytes",
     "tlr_compress", "tlr_compress_profile", "tlr_compress_profile_read", "tlr_plan_profile",
-    "tlr_plan_profile_read", "tlr_dense_gemm",
+    "tlr_plan_profile_read", "tlr_dense_gemm", "tlr_block_quantize", "tlr_block_gemm_workspace_bytes",
+    "tlr_block_gemm", "tlr_moe_workspace_bytes", "tlr_moe_init", "tlr_moe",
     "tlr_status_string", "tlr_last_error", "tlr_version",
 ]
 
@@ -52,6 +55,18 @@ class tlr_plan_summary(ctypes.Structure):
                 ("algorithmic_bytes", c_double),
                 ("workspace_bytes", c_size_t), ("descriptor_bytes", c_size_t),
                 ("runs", c_int32), ("groups", c_int32), ("launches", c_int32), ("dtype", c_int32)]
+
+
+class tlr_block_matrix(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("ld", c_int64), ("lds", c_int64),
+                ("block", c_int32), ("fmt", c_int32)]
+
+
+class tlr_moe_layer(ctypes.Structure):
+    _fields_ = [("hidden", c_int32), ("inter", c_int32), ("experts", c_int32), ("topk", c_int32),
+                ("dt", c_int32), ("wdt", c_int32), ("normalize", c_int32), ("reserved", c_int32),
+                ("router", c_void_p), ("gate_up", c_void_p), ("down", c_void_p),
+                ("gate_up_scales", c_void_p), ("down_scales", c_void_p)]
 
 
 class TLRError(RuntimeError):
@@ -99,6 +114,14 @@ def lib():
     L.tlr_plan_profile_read.argtypes = [P, POINTER(c_double), POINTER(c_double), POINTER(c_int32)]
     L.tlr_dense_gemm.argtypes = [c_int32, c_int32, c_int32, c_int64, c_int64, c_int64, c_double, P, c_int64,
                                  P, c_int64, c_double, P, c_int64, P]
+    L.tlr_block_quantize.argtypes = [c_int32, c_int32, c_int32, c_int64, c_int64, P, c_int64, P, c_int64, P, c_int64,
+                                     P, c_int64, P, c_int64, P]
+    L.tlr_block_gemm_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+    L.tlr_block_gemm.argtypes = [c_int32, c_int64, c_int64, c_int64, c_double, POINTER(tlr_block_matrix),
+                                 POINTER(tlr_block_matrix), c_double, P, c_int64, c_uint32, P, c_size_t, P]
+    L.tlr_moe_workspace_bytes.argtypes = [POINTER(tlr_moe_layer), c_int32, POINTER(c_size_t)]
+    L.tlr_moe_init.argtypes = [POINTER(tlr_moe_layer), P, c_size_t, P]
+    L.tlr_moe.argtypes = [POINTER(tlr_moe_layer), c_int32, P, c_int64, P, c_int64, P, P, P, c_size_t, P]
     for name in EXPORTED[:-3]:
         getattr(L, name).restype = c_int32
     L.tlr_status_string.argtypes = [c_int32]
@@ -134,6 +157,10 @@ def _dt(x) -> int:
         return TLR_F16
     if x in ("bf16", TLR_BF16):
         return TLR_BF16
+    if x in ("e4m3", TLR_E4M3):
+        return TLR_E4M3
+    if x in ("e5m2", TLR_E5M2):
+        return TLR_E5M2
     raise ValueError(f"bad dtype {x!r}")
 
 
@@ -306,6 +333,44 @@ def tlr_dense_gemm(dtype, opA, opB, m: int, n: int, k: int, alpha: float, A: int
     st = lib().tlr_dense_gemm(_dt(dtype), _op(opA), _op(opB), m, n, k, alpha, c_void_p(A or None), lda,
                               c_void_p(B or None), ldb, beta, c_void_p(C or None), ldc, c_void_p(stream or None))
     _check(st, "tlr_dense_gemm")
+
+
+def tlr_block_quantize(dtype, fmt, block: int, rows: int, k: int, X: int, ldx: int, codes: int, ldq: int, scales: int,
+                       lds: int, codes_t: int, ldq_t: int, scales_t: int, lds_t: int, stream: int = 0):
+    st = lib().tlr_block_quantize(_dt(dtype), _dt(fmt), block, rows, k, X or None, ldx, codes or None, ldq,
+                                  scales or None, lds, codes_t or None, ldq_t, scales_t or None, lds_t, stream or None)
+    _check(st, "tlr_block_quantize")
+
+
+def tlr_block_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
+    out = c_size_t()
+    _check(lib().tlr_block_gemm_workspace_bytes(m, n, k, ctypes.byref(out)), "tlr_block_gemm_workspace_bytes")
+    return int(out.value)
+
+
+def tlr_block_gemm(dtype, m: int, n: int, k: int, alpha: float, A: tlr_block_matrix, B: tlr_block_matrix, beta: float,
+                   C: int, ldc: int, flags: int = 0, workspace: int = 0, workspace_bytes: int = 0, stream: int = 0):
+    st = lib().tlr_block_gemm(_dt(dtype), m, n, k, alpha, ctypes.byref(A), ctypes.byref(B), beta, C or None, ldc,
+                              flags, workspace or None, workspace_bytes, stream or None)
+    _check(st, "tlr_block_gemm")
+
+
+def tlr_moe_workspace_bytes(layer: tlr_moe_layer, max_tokens: int) -> int:
+    out = c_size_t()
+    _check(lib().tlr_moe_workspace_bytes(ctypes.byref(layer), max_tokens, ctypes.byref(out)),
+           "tlr_moe_workspace_bytes")
+    return int(out.value)
+
+
+def tlr_moe_init(layer: tlr_moe_layer, workspace: int, workspace_bytes: int, stream: int = 0):
+    _check(lib().tlr_moe_init(ctypes.byref(layer), workspace or None, workspace_bytes, stream or None), "tlr_moe_init")
+
+
+def tlr_moe(layer: tlr_moe_layer, tokens: int, X: int, ldx: int, Y: int, ldy: int, ids: int, weights: int,
+            workspace: int, workspace_bytes: int, stream: int = 0):
+    st = lib().tlr_moe(ctypes.byref(layer), tokens, X or None, ldx, Y or None, ldy, ids or None, weights or None,
+                       workspace or None, workspace_bytes, stream or None)
+    _check(st, "tlr_moe")
 
 
 def tlr_status_string(s: int) -> str:

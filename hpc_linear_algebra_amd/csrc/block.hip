@@ -259,6 +259,7 @@ struct GemmArgs {
   void *c;
   int64_t ldc;
   int32_t dt;
+  int32_t vec;              // columns of C 16-byte aligned
 };
 
 // Two codes widened to bfloat16, exactly.
@@ -329,6 +330,45 @@ __device__ __forceinline__ void store_c(const GemmArgs &g, int i, int j, float v
   }
 }
 
+// Eight consecutive rows of a column from row i.
+__device__ __forceinline__ void store_c8(const GemmArgs &g, int i, int j, const float (&v)[8]) {
+  if (!g.vec || i + 8 > g.m) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < g.m) store_c(g, i + e, j, v[e]);
+    return;
+  }
+  const int64_t at = (int64_t)j * g.ldc + i;
+  float x[8];
+  if (g.dt == TLR_F32) {
+    f4 *p = reinterpret_cast<f4 *>(static_cast<float *>(g.c) + at);
+    f4 lo = f4{0, 0, 0, 0}, hi = f4{0, 0, 0, 0};
+    if (g.beta != 0.0f) { lo = p[0]; hi = p[1]; }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = g.beta != 0.0f ? v[e] * g.alpha + g.beta * (e < 4 ? lo[e & 3] : hi[e & 3]) : v[e] * g.alpha;
+    p[0] = f4{x[0], x[1], x[2], x[3]};
+    p[1] = f4{x[4], x[5], x[6], x[7]};
+    return;
+  }
+  u4 *p = reinterpret_cast<u4 *>(static_cast<uint16_t *>(g.c) + at);
+  u4 old = u4{0, 0, 0, 0};
+  if (g.beta != 0.0f) old = *p;
+  if (g.dt == TLR_F16) {
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    const h8 o = __builtin_bit_cast(h8, old);
+    h8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (_Float16)(g.beta != 0.0f ? v[e] * g.alpha + g.beta * (float)o[e] : v[e] * g.alpha);
+    *p = __builtin_bit_cast(u4, y);
+  } else {
+    const b8v o = __builtin_bit_cast(b8v, old);
+    b8v y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (__bf16)(g.beta != 0.0f ? v[e] * g.alpha + g.beta * (float)o[e] : v[e] * g.alpha);
+    *p = __builtin_bit_cast(u4, y);
+  }
+}
+
 // Few columns: a workgroup computes 16 rows of A against NJ x 16 rows of B, its
 // eight waves taking every eighth block of the contraction; fragments come
 // straight from global memory and the partial sums meet in LDS.
@@ -386,11 +426,232 @@ __global__ __launch_bounds__(512) void strip_kernel(GemmArgs g) {
   }
 }
 
+// ---- product, tiles ----------------------------------------------------------------------------------
+
+// Loads through a buffer descriptor: lanes at or past its size write zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00027000);
+}
+typedef __attribute__((address_space(3))) void *lds_ptr;
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t b, uint32_t at, void *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 16, at, 0, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t b, uint32_t at, void *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 4, at, 0, 0, 0);
+}
+
+// LDS rows are a block's 128 codes, unpadded (the loads write 64 lanes x 16
+// bytes in a row); chunk c of a row stands at chunk c ^ key, so that the 16
+// rows which a fragment read takes at one chunk hit all 64 banks once.
+__device__ __forceinline__ int a_key(int row) { return ((row >> 1) & 1) | ((row >> 3) & 3) << 1; }
+__device__ __forceinline__ int b_key(int row) { return (row >> 1) & 7; }
+
+// One operand's tile of ROWS rows: T threads fill a stage of ROWS x 128 codes,
+// one 16-byte chunk each per step.
+template <int ROWS, int T, bool IS_A> struct Panel {
+  static constexpr int N = ROWS * 8 / T;
+  static_assert(T % 256 == 0, "a step keeps the key");
+  const uint8_t *base;      // first row of the tile (uniform)
+  int32_t bytes;            // from there to the end of the last readable chunk
+  int32_t step;             // from one step to the next
+  uint32_t at;              // this thread's first chunk in column block 0
+  __device__ __forceinline__ void init(const Operand &o, int r0, int k, int tid) {
+    base = o.codes + (int64_t)r0 * o.ld;
+    bytes = (min(ROWS, o.rows - r0) - 1) * (int32_t)o.ld + ((k + 15) & ~15);
+    step = (T / 8) * (int32_t)o.ld;
+    at = (uint32_t)(tid >> 3) * (uint32_t)o.ld + chunk(tid);
+  }
+  static __device__ __forceinline__ int chunk(int tid) {
+    return 16 * ((tid & 7) ^ (IS_A ? a_key(tid >> 3) : b_key(tid >> 3)));
+  }
+  // a descriptor of the rows from step i on: the steps share one address register
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int kb, int i) const {
+    const int32_t o = kb * QB + i * step;
+    return buffer(base + o, max(bytes - o, 0));
+  }
+  __device__ __forceinline__ void load(int kb, uint8_t *lds, int wave) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) to_lds16(rows(kb, i), at, lds + (i * T + wave * 64) * 16);
+  }
+  // the last column block, whose columns from `left` on read as zero
+  __device__ __forceinline__ void load_cut(int kb, int left, uint8_t *lds, int tid) const {
+    u4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rows(kb, i), at, 0, 0));
+    u4 keep;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int n = left - chunk(tid) - 4 * w;
+      keep[w] = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : 0xffffffffu >> (32 - 8 * n);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u4 *>(lds + (i * T + tid) * 16) = x[i] & keep;
+  }
+};
+
+// C tiles of TM x TN, WM x WN waves.  AB: A's blocks are 128 rows high (a wave's
+// rows lie in one of them, or in two halves).
+template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(GemmArgs g) {
+  constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
+  __shared__ __attribute__((aligned(16))) uint8_t a0[TM * QB], a1[TM * QB], b0[TN * QB], b1[TN * QB];
+  __shared__ __attribute__((aligned(16))) float s0[TM + TN], s1[TM + TN];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+
+  // tile of this workgroup: workgroups go to the 8 XCDs in turn; each XCD takes
+  // a contiguous part of the tiles, which run down 8 row tiles at a time
+  int mt, nt;
+  {
+    const int tm = (g.m + TM - 1) / TM, tn = (g.n + TN - 1) / TN, all = tm * tn;
+    const int id = blockIdx.x, x = id & 7, part = all >> 3, more = all & 7;
+    const int t = x * part + min(x, more) + (id >> 3);
+    const int width = 8 * tn, band = t / width, h = min(8, tm - 8 * band), in = t - band * width;
+    mt = 8 * band + in % h;
+    nt = in / h;
+  }
+  const int m0 = mt * TM, n0 = nt * TN;
+  Panel<TM, T, true> pa;
+  Panel<TN, T, false> pb;
+  pa.init(g.a, m0, g.k, tid);
+  pb.init(g.b, n0, g.k, tid);
+  // scales: TM + TN floats a stage, 64 a wave and step
+  constexpr int SN = (TM + TN) / T;
+  static_assert((TM + TN) % T == 0 && TM % 64 == 0, "");
+  auto load_scales = [&](int kb, float *ls) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i) {
+      const int w = i * T + wave * 64;
+      const bool isa = w < TM;
+      const Operand &o = isa ? g.a : g.b;
+      const int r0 = isa ? m0 : n0, at = (isa ? w : w - TM) + lane;
+      const int first = r0 >> o.shift, n = ((min(r0 + (isa ? TM : TN), o.rows) - 1) >> o.shift) - first + 1;
+      to_lds4(buffer(o.scales + kb * o.lds + first, 4 * n), 4 * (((r0 + at) >> o.shift) - first), ls + w);
+    }
+  };
+  auto load = [&](int kb, uint8_t *la, uint8_t *lb, float *ls) {
+    load_scales(kb, ls);
+    pa.load(kb, la, wave);
+    pb.load(kb, lb, wave);
+  };
+
+  f4 acc[RI][CJ];
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) acc[i][j] = f4{0, 0, 0, 0};
+
+  // Fragment addresses.  Row tile i = 2h + p: lane r holds block row
+  // 32 h + 8 (r / 4) + 4 p + r % 4, so that the two tiles of a pair leave 8
+  // consecutive rows of C in one lane.
+  const int ar = wm * (TM / WM) + 8 * (r >> 2) + (r & 3), br = wn * (TN / WN) + r;
+  const int aat = ar * QB + 16 * (q ^ a_key(ar)), bat = br * QB + 16 * (q ^ b_key(br));
+
+  auto compute = [&](const uint8_t *la, const uint8_t *lb, const float *ls) {
+    u4 bf[CJ][2];
+    float sb[CJ];
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) {
+      bf[j][0] = *reinterpret_cast<const u4 *>(lb + bat + 16 * QB * j);
+      bf[j][1] = *reinterpret_cast<const u4 *>(lb + (bat ^ 64) + 16 * QB * j);
+      sb[j] = ls[TM + br + 16 * j];
+    }
+    if constexpr (AB) {
+      const float s = ls[wm * (TM / WM)];
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) sb[j] *= s;
+    }
+    // Row tile by row tile: the next one's fragment is read and the last one's
+    // results are added while the matrix instructions of this one run.
+    auto frag = [&](int i, u4 (&x)[2]) {
+      const int o = (i >> 1) * 32 * QB + (i & 1) * 4 * QB;
+      x[0] = *reinterpret_cast<const u4 *>(la + aat + o);
+      x[1] = *reinterpret_cast<const u4 *>(la + (aat ^ 64) + o);
+    };
+    auto add = [&](int i, const f4 (&d)[CJ]) {
+      f4 sa;
+      if constexpr (!AB) sa = *reinterpret_cast<const f4 *>(ls + wm * (TM / WM) + (i >> 1) * 32 + 8 * q + 4 * (i & 1));
+#pragma unroll
+      for (int j = 0; j < CJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(AB ? sb[j] : sa[v] * sb[j], d[j][v], acc[i][j][v]);
+    };
+    u4 x[2][2];
+    f4 d[2][CJ];
+    frag(0, x[0]);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      if (i + 1 < RI) frag(i + 1, x[(i + 1) & 1]);
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) d[i & 1][j] = mma<A5, B5, FAST>(x[i & 1][0], x[i & 1][1], bf[j][0], bf[j][1]);
+      if (i > 0) add(i - 1, d[(i - 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(RI - 1, d[(RI - 1) & 1]);
+  };
+  auto meet = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // Stage 0 is the last column block, which may be cut at column k; stage i > 0
+  // is column block i - 1.  Stages alternate between the buffers, the last one
+  // is in the second.
+  const int nb = (g.k + QB - 1) / QB;
+  bool second = nb & 1;
+  load_scales(nb - 1, second ? s1 : s0);
+  if (g.k & (QB - 1)) {
+    pa.load_cut(nb - 1, g.k & (QB - 1), second ? a1 : a0, tid);
+    pb.load_cut(nb - 1, g.k & (QB - 1), second ? b1 : b0, tid);
+  } else {
+    pa.load(nb - 1, second ? a1 : a0, wave);
+    pb.load(nb - 1, second ? b1 : b0, wave);
+  }
+  meet();
+  int kb = 0;               // column block of the next stage to load
+  do {
+    if (!second) {
+      load(kb++, a1, b1, s1);
+      compute(a0, b0, s0);
+      meet();
+    }
+    second = false;
+    if (kb < nb - 1) load(kb, a0, b0, s0);
+    compute(a1, b1, s1);
+    meet();
+  } while (kb++ < nb - 1);
+
+  // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
+#pragma unroll
+  for (int j = 0; j < CJ; ++j) {
+    const int col = n0 + wn * (TN / WN) + 16 * j + r;
+    if (col < g.n)
+#pragma unroll
+      for (int h = 0; h < RI / 2; ++h) {
+        const int row = m0 + wm * (TM / WM) + 32 * h + 8 * q;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[2 * h + (e >> 2)][j][e & 3];
+        store_c8(g, row, col, v);
+      }
+  }
+}
+
+template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN> void tile_launch(const GemmArgs &g, hipStream_t st) {
+  const unsigned grid = (unsigned)((g.m + TM - 1) / TM) * (unsigned)((g.n + TN - 1) / TN);
+  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
+  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
+}
+
 template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, hipStream_t st) {
   const unsigned gx = (unsigned)((g.m + 15) / 16);
   if (g.n <= 16) strip_kernel<A5, B5, FAST, 1><<<dim3(gx, 1), 512, 0, st>>>(g);
   else if (g.n <= 32) strip_kernel<A5, B5, FAST, 2><<<dim3(gx, 1), 512, 0, st>>>(g);
-  else strip_kernel<A5, B5, FAST, 4><<<dim3(gx, (g.n + 63) / 64), 512, 0, st>>>(g);
+  else if (g.n <= 64) strip_kernel<A5, B5, FAST, 4><<<dim3(gx, (g.n + 63) / 64), 512, 0, st>>>(g);
+  else if ((int64_t)((g.m + 255) / 256) * ((g.n + 255) / 256) >= 192) tile_launch<A5, B5, FAST, 256, 256, 2, 4>(g, st);
+  else tile_launch<A5, B5, FAST, 128, 128, 2, 2>(g, st);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -511,6 +772,7 @@ tlr_status block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alph
   g.c = C;
   g.ldc = ldc;
   g.dt = dt;
+  g.vec = aligned(C, 16) && ldc * (dt == TLR_F32 ? 4 : 2) % 16 == 0;
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const bool a5 = A->fmt == TLR_E5M2, b5 = B->fmt == TLR_E5M2;
   if (flags & TLR_BLOCK_FAST) {

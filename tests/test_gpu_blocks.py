@@ -195,6 +195,31 @@ def test_fast_product(m, n, k, afmt, bfmt, ablk, bblk, dtype):
     assert worst <= 1.0, f"error {worst:.3f} of its bound"
 
 
+@pytest.mark.parametrize("m,n,k", [(3329, 3585, 40), (4097, 3300, 128), (2305, 5900, 300), (3400, 3841, 256),
+                                   (5001, 2550, 640)])
+@pytest.mark.parametrize("bfmt,ablk,dtype,fast", [("e4m3", 128, "bf16", True), ("e5m2", 1, "f32", False),
+                                                  ("e4m3", 1, "f16", True), ("e5m2", 128, "f32", False)])
+def test_product_of_large_tiles(m, n, k, bfmt, ablk, dtype, fast):
+    """Enough 256 x 256 tiles to fill the chip; one to five column blocks, cut and whole.  Every 37th row and 41st
+    column is compared, and the last ones; the bounds are those of check_product and test_fast_product."""
+    from hpc_linear_algebra_amd import blocks
+    A, a = codes(m, k, "e4m3", ablk, m + n)
+    B, b = codes(n, k, bfmt, 1, m + n + 1, pad=16)
+    got = blocks.gemm(A, B, dtype=dtype, fast=fast)
+    i, j = sorted({*range(0, m, 37), m - 1}), sorted({*range(0, n, 41), n - 1})
+    a, b, part = a[i], b[j], got[j][:, i]
+    if fast:
+        ref, mag = b @ a.T, np.abs(b) @ np.abs(a).T
+        t = torch.finfo(TD[dtype])
+        tol = (min(k, 128) + k / 128 + 4) * 2.0 ** -24 * mag + 2.0 ** -13 * largest(a, b, k)
+        tol = tol + t.eps / 2 * (np.abs(ref) + tol) + t.smallest_normal * t.eps
+        assert float(np.max(np.abs(part.double().cpu().numpy() - ref) / tol)) <= 1.0
+    else:
+        check_product(part, a, b, k, dtype)
+    assert torch.isfinite(got).all()
+    assert torch.equal(got, blocks.gemm(A, B, dtype=dtype, fast=fast))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(33, 5, 200), (301, 90, 260), (520, 300, 384)])
 def test_product_adds_into_a_strided_unaligned_c(m, n, k, dtype):

@@ -13,6 +13,8 @@ call runs on torch's current stream of the operands' device.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -23,11 +25,27 @@ BLOCK = 128
 FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _CODE = {torch.float8_e4m3fn: T.TLR_E4M3, torch.float8_e5m2: T.TLR_E5M2}
 _DT = {torch.float32: T.TLR_F32, torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
+_FMT = {"e4m3": T.TLR_E4M3, "e5m2": T.TLR_E5M2}
+_NONE = T.tlr_block_matrix()
 _TORCH = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream      # 0.1 us, the stream object's way 2.7
+
+
+def call(device: torch.device, f, *args) -> int:
+    """f(*args, torch's current stream of the device) with that device current.
+    A decode step is bound by what the host does between launches: the guard is
+    entered only where it changes something."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        return f(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return f(*args, _raw_stream(index))
+
+
+_lib = functools.lru_cache(None)(T.lib)
+_gemm_workspace = functools.lru_cache(4096)(T.tlr_block_gemm_workspace_bytes)      # of the sizes alone
 
 
 class BlockScaled:
@@ -69,9 +87,14 @@ class BlockScaled:
 
 
 def _empty(rows: int, k: int, block: int, fmt: str, device) -> BlockScaled:
-    codes = torch.empty((rows, -(-k // 16) * 16), dtype=FORMATS[fmt], device=device)
-    scales = torch.empty((-(-k // BLOCK), rows if block == 1 else -(-rows // BLOCK)), dtype=torch.float32, device=device)
-    return BlockScaled(codes, scales, rows, k, block)
+    q = BlockScaled.__new__(BlockScaled)        # right by construction: the checks cost more than the launch
+    ld, nr = -(-k // 16) * 16, rows if block == 1 else -(-rows // BLOCK)
+    dt = FORMATS[fmt]
+    q.codes = codes = torch.empty((rows, ld), dtype=dt, device=device)
+    q.scales = scales = torch.empty((-(-k // BLOCK), nr), dtype=torch.float32, device=device)
+    q.rows, q.k, q.block = rows, k, block
+    q.c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, nr, block, _CODE[dt])
+    return q
 
 
 def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool = True,
@@ -91,11 +114,11 @@ def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool 
     a = _empty(rows, k, block, fmt, x.device) if straight else None
     b = _empty(k, rows, block, fmt, x.device) if transposed else None
     ldx = max(x.stride(0), k, 1) if rows <= 1 else x.stride(0)
-    with torch.cuda.device(x.device):
-        T.tlr_block_quantize(_DT[x.dtype], fmt, block, rows, k, x.data_ptr(), ldx,
-                             a.c.codes if a else 0, a.c.ld if a else 0, a.c.scales if a else 0, a.c.lds if a else 0,
-                             b.c.codes if b else 0, b.c.ld if b else 0, b.c.scales if b else 0, b.c.lds if b else 0,
-                             _stream(x.device))
+    p, q = a.c if a else _NONE, b.c if b else _NONE
+    st = call(x.device, _lib().tlr_block_quantize, _DT[x.dtype], _FMT[fmt], block, rows, k, x.data_ptr() or None, ldx,
+              p.codes, p.ld, p.scales, p.lds, q.codes, q.ld, q.scales, q.lds)
+    if st:
+        T._check(st, "tlr_block_quantize")
     return a, b
 
 
@@ -121,11 +144,12 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
     elif tuple(out.shape) != (n, m) or out.dtype not in _DT or out.device != device or (m > 1 and out.stride(1) != 1):
         raise ValueError(f"gemm: out has to be a ({n}, {m}) float32, float16 or bfloat16 tensor with contiguous rows")
     ldc = out.stride(0) if n > 1 else max(out.stride(0), m, 1)
-    nws = T.tlr_block_gemm_workspace_bytes(m, n, A.k)
+    nws = _gemm_workspace(m, n, A.k)
     ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
-    with torch.cuda.device(device):
-        T.tlr_block_gemm(_DT[out.dtype], m, n, A.k, alpha, A.c, B.c, beta, out.data_ptr(), ldc,
-                         T.TLR_BLOCK_FAST if fast else 0, ws.data_ptr() if nws else 0, nws, _stream(device))
+    st = call(device, _lib().tlr_block_gemm, _DT[out.dtype], m, n, A.k, alpha, ctypes.byref(A.c), ctypes.byref(B.c),
+              beta, out.data_ptr() or None, ldc, T.TLR_BLOCK_FAST if fast else 0, ws.data_ptr() if nws else None, nws)
+    if st:
+        T._check(st, "tlr_block_gemm")
     return out
 
 

@@ -26,7 +26,8 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int MAX_TOKENS = 256, MAX_EXPERTS = 512, MAX_TOPK = 16;
-constexpr int MAX_LIST = MAX_TOKENS;      // assignments of one expert: at most one per token
+constexpr int RT_MAX = 8;                 // tokens of a router workgroup, at most
+constexpr int ROUTED = 32, BLOCKS = 64;   // counters: 0.. router groups, ROUTED all groups, BLOCKS.. row blocks of y
 
 // The 16-bit type of x, y and the products.
 template <typename H> struct Num;
@@ -62,11 +63,39 @@ struct MoeArgs {
   const float *gate_up_scales, *down_scales;
   int32_t *ids;
   float *weights;
+  int32_t *arrived;         // counters of workgroups that are done; 0 between calls
+  int32_t *units;           // how many experts were chosen
+  int4 *unit;               // each of them: expert, first place in order, assignments, 0
+  int32_t *order;           // assignments (token * topk + choice) by expert
   double *logits;           // tokens x experts
   uint16_t *hi, *lo;        // tokens*topk x inter: silu(g) u as hi + lo
   float *part;              // tokens*topk x hidden: the experts' outputs
-  int32_t slots;            // grid rows of the expert launches
 };
+
+// Values that workgroups of one launch pass on go past the chiplets' caches, both
+// ways, by relaxed agent-scope accesses.  arrive() counts this workgroup as
+// done once all of its stores have been acknowledged there, and says whether it
+// was the last of n; the counter is 0 again then.  A release fence would write
+// back the whole L2 besides (32 us against 10 for the router of 64 tokens).
+template <typename T> __device__ __forceinline__ void put(T *p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T> __device__ __forceinline__ T get(const T *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool arrive(int32_t *counter, int n, int *shared) {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);      // every wave: its own stores
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *shared = before == n - 1;
+    if (before == n - 1) put(counter, 0);
+  }
+  __syncthreads();
+  asm volatile("" ::: "memory");
+  return *shared != 0;
+}
 
 // Eight 16-bit entries as floats.
 template <typename H> __device__ __forceinline__ void unpack8(u4 w, float (&v)[8]) {
@@ -74,40 +103,6 @@ template <typename H> __device__ __forceinline__ void unpack8(u4 w, float (&v)[8
   const v8 h = __builtin_bit_cast(v8, w);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
-}
-
-constexpr int RT = 8;       // tokens of a router workgroup
-
-// Logits: one wave per expert and RT tokens.  A product of two 16-bit numbers
-// is an exact float; the sums run in double.
-template <typename H> __global__ __launch_bounds__(256) void router_kernel(MoeArgs a) {
-  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t0 = blockIdx.y * RT;
-  if (e >= a.experts) return;
-  const uint16_t *w = a.router + (int64_t)e * a.hidden;
-  double acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = 0.0;
-  for (int c = 8 * lane; c < a.hidden; c += 512) {
-    float wf[8];
-    unpack8<H>(*reinterpret_cast<const u4 *>(w + c), wf);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (t0 + i >= a.tokens) break;
-      float xf[8];
-      unpack8<H>(*reinterpret_cast<const u4 *>(a.x + (t0 + i) * a.ldx + c), xf);
-#pragma unroll
-      for (int v = 0; v < 8; ++v) acc[i] += (double)(wf[v] * xf[v]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if (t0 + i >= a.tokens) break;
-    double s = acc[i];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (lane == 0) a.logits[(int64_t)(t0 + i) * a.experts + e] = s;
-  }
 }
 
 // A double as a number whose order is the logits' order, NaN on top.
@@ -118,153 +113,283 @@ __device__ __forceinline__ uint64_t sort_key(double x) {
   return (z >> 63) ? ~z : z | 0x8000000000000000ull;
 }
 
-// One workgroup per token: an expert's place is the number of experts before
-// it (larger logit, or the same and a lower index); the first topk are chosen.
-__global__ __launch_bounds__(256) void select_kernel(MoeArgs a) {
-  __shared__ uint64_t key[MAX_EXPERTS];
-  __shared__ float zs[4], chosen[MAX_TOPK];
-  __shared__ double best;
-  const int tid = threadIdx.x, t = blockIdx.x;
+// Largest of all lanes' x, in all of them.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x124, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x122, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x121, 0xf, 0xf, true));
+  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)x, 0), (uint32_t)__builtin_amdgcn_readlane((int)x, 16));
+  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)x, 32), (uint32_t)__builtin_amdgcn_readlane((int)x, 48));
+  return max(a, b);
+}
+
+// One wave chooses the experts of token t: topk times the largest key, its high
+// word first, then its low word, then the lowest index.  PER experts a lane.
+template <int PER> __device__ __forceinline__ void select(const MoeArgs &a, int t, int lane) {
   const double *l = a.logits + (int64_t)t * a.experts;
-  for (int e = tid; e < a.experts; e += 256) key[e] = sort_key(l[e]);
-  __syncthreads();
-  int place[MAX_EXPERTS / 256];
+  double x[PER];
+  uint64_t key[PER];
 #pragma unroll
-  for (int i = 0; i < MAX_EXPERTS / 256; ++i) {
-    const int e = tid + 256 * i;
-    place[i] = a.experts;
-    if (e >= a.experts) continue;
-    const uint64_t mine = key[e];
-    int n = 0;
-    for (int f = 0; f < a.experts; ++f) n += (key[f] > mine || (key[f] == mine && f < e)) ? 1 : 0;
-    place[i] = n;
-    if (n == 0) best = l[e];
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    x[i] = e < a.experts ? get(l + e) : 0.0;
+    key[i] = e < a.experts ? sort_key(x[i]) : 0;      // no number's key is 0
   }
-  __syncthreads();
+  double best = 0.0, mine = 0.0;      // lane j: the logit of choice j
+  int id = 0;
+  for (int j = 0; j < a.topk; ++j) {
+    uint64_t top = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) top = max(top, key[i]);
+    const uint32_t hi = wave_max((uint32_t)(top >> 32));
+    const uint32_t lo = wave_max((uint32_t)(top >> 32) == hi ? (uint32_t)top : 0u);
+    const uint64_t k = (uint64_t)hi << 32 | lo;
+    uint32_t at = 0;                  // MAX_EXPERTS - the lowest index
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) at = key[i] == k ? (uint32_t)(MAX_EXPERTS - lane - 64 * i) : at;
+    const int e = MAX_EXPERTS - (int)wave_max(at);
+    double v = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v = i == (e >> 6) ? x[i] : v;
+      if (e == lane + 64 * i) key[i] = 0;
+    }
+    v = __shfl(v, e & 63);
+    if (j == 0) best = v;
+    if (lane == j) {
+      mine = v;
+      id = e;
+    }
+  }
   float z = 0.0f;
 #pragma unroll
-  for (int i = 0; i < MAX_EXPERTS / 256; ++i) {
-    const int e = tid + 256 * i;
-    if (e >= a.experts) continue;
-    const float p = expf((float)(l[e] - best));
-    z += p;
-    if (place[i] < a.topk) {
-      chosen[place[i]] = p;
-      a.ids[t * a.topk + place[i]] = e;
-    }
-  }
+  for (int i = 0; i < PER; ++i) z += lane + 64 * i < a.experts ? expf((float)(x[i] - best)) : 0.0f;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
-  if ((tid & 63) == 0) zs[tid >> 6] = z;
+  const float p = lane < a.topk ? expf((float)(mine - best)) : 0.0f;
+  if (a.normalize) {
+    z = p;                            // 0 past the choices: the sum over 16 lanes
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) z += __shfl_xor(z, o);
+  }
+  if (lane < a.topk) {
+    put(a.ids + t * a.topk + lane, id);
+    a.weights[t * a.topk + lane] = p / z;
+  }
+}
+
+// One workgroup: the assignments by expert and the chosen experts.  Places within
+// an expert go in the order of the atomics, which no result depends on: an
+// assignment is a column of a product, whichever one.
+__device__ __forceinline__ void sort(const MoeArgs &a) {
+  __shared__ int count[MAX_EXPERTS], place[MAX_EXPERTS];
+  const int tid = threadIdx.x, n = a.tokens * a.topk;
+  for (int e = tid; e < MAX_EXPERTS; e += 256) count[e] = 0;
   __syncthreads();
-  if (tid < a.topk) {
-    float sum = zs[0] + zs[1] + zs[2] + zs[3];
-    if (a.normalize) {
-      sum = 0.0f;
-      for (int j = 0; j < a.topk; ++j) sum += chosen[j];
+  for (int i = tid; i < n; i += 256) atomicAdd(&count[get(a.ids + i)], 1);
+  __syncthreads();
+  if (tid < 64) {
+    constexpr int PER = MAX_EXPERTS / 64;
+    int c[PER], sum = 0, some = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = count[tid * PER + i];
+      sum += c[i];
+      some += c[i] > 0 ? 1 : 0;
     }
-    a.weights[t * a.topk + tid] = chosen[tid] / sum;
+    int at = sum, u = some;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(at, o), y = __shfl_up(u, o);
+      at += tid >= o ? x : 0;
+      u += tid >= o ? y : 0;
+    }
+    if (tid == 63) *a.units = u;
+    at -= sum;
+    u -= some;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      place[tid * PER + i] = at;
+      if (c[i] > 0) a.unit[u++] = int4{tid * PER + i, at, c[i], 0};
+      at += c[i];
+    }
   }
+  __syncthreads();
+  for (int i = tid; i < n; i += 256) a.order[atomicAdd(&place[get(a.ids + i)], 1)] = i;
 }
 
-// The expert of this workgroup (grid row) and the list of its assignments
-// (token * topk + choice) in increasing order; false when it has none.  With
-// fewer assignments than experts a grid row is an assignment, which stands for
-// its expert when no earlier one has the same; else a grid row is an expert.
-__device__ __forceinline__ bool my_expert(const MoeArgs &a, int row, int *list, int *scratch, int &e, int &count) {
-  const int n = a.tokens * a.topk, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  e = a.slots == a.experts ? row : a.ids[row];
-  const bool by_row = a.slots != a.experts;
-  count = 0;
-  bool first = true;
-  for (int i0 = 0; i0 < n; i0 += 256) {
-    const int i = i0 + tid;
-    const bool hit = i < n && a.ids[i] == e;
-    const uint64_t b = __ballot(hit);
-    if (lane == 0) scratch[wave] = __popcll(b);
-    __syncthreads();
-    int before = count;
-    for (int w = 0; w < wave; ++w) before += scratch[w];
-    if (hit) list[before + __popcll(b & ((1ull << lane) - 1))] = i;
-    count += scratch[0] + scratch[1] + scratch[2] + scratch[3];
-    __syncthreads();
+// Logits: one wave per expert and RT tokens.  A product of two 16-bit numbers
+// is an exact float; the sums run in double.  The workgroup that is done last
+// with a group of RT tokens chooses their experts, a wave per token, and the
+// last of all sorts the assignments: launches of their own would cost 4 us each.
+template <typename H, int RT> __global__ __launch_bounds__(256) void router_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * RT;
+  if (e < a.experts) {
+    const uint16_t *w = a.router + (int64_t)e * a.hidden;
+    const uint16_t *x[RT];
+    double acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      acc[i] = 0.0;
+      x[i] = a.x + min(t0 + i, a.tokens - 1) * a.ldx;
+    }
+#pragma unroll 2
+    for (int c = 8 * lane; c < a.hidden; c += 512) {
+      const u4 wv = *reinterpret_cast<const u4 *>(w + c);
+      u4 xv[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) xv[i] = *reinterpret_cast<const u4 *>(x[i] + c);
+      float wf[8];
+      unpack8<H>(wv, wf);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float xf[8];
+        unpack8<H>(xv[i], xf);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) acc[i] += (double)(wf[v] * xf[v]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      double s = acc[i];
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+      if (lane == 0 && t0 + i < a.tokens)
+        put(a.logits + (int64_t)(t0 + i) * a.experts + e, s);
+    }
   }
-  if (by_row) first = count > 0 && list[0] == row;
-  return first && count > 0;
+  __shared__ int last;
+  if (!arrive(a.arrived + blockIdx.y, gridDim.x, &last)) return;
+  for (int t = t0 + wave; t < min(t0 + RT, a.tokens); t += 4) {
+    if (a.experts <= 64) select<1>(a, t, lane);
+    else if (a.experts <= 128) select<2>(a, t, lane);
+    else if (a.experts <= 256) select<4>(a, t, lane);
+    else select<8>(a, t, lane);
+  }
+  if (arrive(a.arrived + ROUTED, gridDim.y, &last)) sort(a);
 }
 
-// RTILE row tiles (16 rows each) of an expert's matrix against NJ tiles of 16
-// token columns over this wave's part of the contraction: lane (r, q) =
-// (lane % 16, lane / 16) supplies columns k0 + 16 q .. + 15 of weight row r and
-// of token column r for each group of 64 (two matrix instructions).  TWO: the
-// tokens come as a sum of two matrices.
-template <typename H, bool W8, int NJ, int RTILE, bool TWO>
-__device__ __forceinline__ void multiply(f4 (&acc)[RTILE][NJ], const uint8_t *const (&w)[RTILE],
-                                         const float *const (&ws)[RTILE], int64_t wlds, const uint16_t *const (&x)[NJ],
-                                         const uint16_t *const (&x2)[NJ], int K, int wave, int waves, int q) {
-  for (int g = wave; g * 64 < K; g += waves) {
-    const int k = g * 64 + 16 * q;
-    const bool in = k < K;
+// A column group of an expert's rows and of NJ tiles of 16 token columns, as
+// loaded: lane (r, q) = (lane % 16, lane / 16) holds columns k0 + 64 s + 16 q ..
+// + 15 of weight row r and of token column r.  16-bit weights: 64 columns (a
+// row's piece is a 128-byte line), 8-bit ones: 128, which share a scale.
+template <typename H, bool W8, int RTILE, int NJ, bool TWO> struct Group {
+  static constexpr int SUB = W8 ? 2 : 1, COLS = 64 * SUB;
+  u4 w[RTILE][2], x[NJ][SUB][2], x2[TWO ? NJ : 1][SUB][2];
+  float s[RTILE];
+
+  // CUT: the group may reach past column K (a multiple of 16): zeros there.
+  template <bool CUT>
+  __device__ __forceinline__ void load(int g, int K, int q, const uint8_t *const (&wp)[RTILE], const float *const (&ws)[RTILE],
+                                       int64_t wlds, const uint16_t *const (&xp)[NJ], const uint16_t *const (&xp2)[NJ]) {
     const u4 zero = u4{0, 0, 0, 0};
-    u4 wf[RTILE][2];
 #pragma unroll
-    for (int i = 0; i < RTILE; ++i) {
-      if constexpr (W8) {
-        const u4 c = in ? *reinterpret_cast<const u4 *>(w[i] + k) : zero;
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          wf[i][p] = u4{Num<H>::template widen<false>(c[2 * p]), Num<H>::template widen<true>(c[2 * p]),
-                        Num<H>::template widen<false>(c[2 * p + 1]), Num<H>::template widen<true>(c[2 * p + 1])};
-      } else {
-        const u4 *p = reinterpret_cast<const u4 *>(w[i] + 2 * k);
-        wf[i][0] = in ? p[0] : zero;
-        wf[i][1] = in ? p[1] : zero;
-      }
-    }
-    float s[RTILE];
-    if constexpr (W8)
-#pragma unroll
-      for (int i = 0; i < RTILE; ++i) s[i] = ws[i][(g >> 1) * wlds];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const u4 *p = reinterpret_cast<const u4 *>(x[j] + k);
-      const u4 b0 = in ? p[0] : zero, b1 = in ? p[1] : zero;
-      u4 c0 = zero, c1 = zero;
-      if constexpr (TWO) {
-        const u4 *p2 = reinterpret_cast<const u4 *>(x2[j] + k);
-        c0 = in ? p2[0] : zero;
-        c1 = in ? p2[1] : zero;
-      }
+    for (int b = 0; b < SUB; ++b) {
+      int k = g * COLS + 64 * b + 16 * q;
+      const bool in = !CUT || k < K;
+      if (CUT) k = in ? k : 0;
 #pragma unroll
       for (int i = 0; i < RTILE; ++i) {
-        f4 d = W8 ? f4{0, 0, 0, 0} : acc[i][j];
-        d = Num<H>::mma(wf[i][0], b0, d);
-        d = Num<H>::mma(wf[i][1], b1, d);
-        if constexpr (TWO) {
-          d = Num<H>::mma(wf[i][0], c0, d);
-          d = Num<H>::mma(wf[i][1], c1, d);
-        }
         if constexpr (W8) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(s[i], d[v], acc[i][j][v]);
+          w[i][b] = *reinterpret_cast<const u4 *>(wp[i] + k);
+          if (CUT) w[i][b] = in ? w[i][b] : zero;
         } else {
-          acc[i][j] = d;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            w[i][h] = reinterpret_cast<const u4 *>(wp[i] + 2 * k)[h];
+            if (CUT) w[i][h] = in ? w[i][h] : zero;
+          }
         }
       }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[j][b][h] = reinterpret_cast<const u4 *>(xp[j] + k)[h];
+          if (CUT) x[j][b][h] = in ? x[j][b][h] : zero;
+          if constexpr (TWO) {
+            x2[j][b][h] = reinterpret_cast<const u4 *>(xp2[j] + k)[h];
+            if (CUT) x2[j][b][h] = in ? x2[j][b][h] : zero;
+          }
+        }
     }
+    if constexpr (W8)
+#pragma unroll
+      for (int i = 0; i < RTILE; ++i) s[i] = ws[i][g * wlds];
+  }
+
+  __device__ __forceinline__ void add(f4 (&acc)[RTILE][NJ]) const {
+#pragma unroll
+    for (int i = 0; i < RTILE; ++i) {
+      f4 d[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) d[j] = W8 ? f4{0, 0, 0, 0} : acc[i][j];
+#pragma unroll
+      for (int b = 0; b < SUB; ++b) {
+        u4 f[2];
+        if constexpr (W8) {
+          const u4 c = w[i][b];
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            f[p] = u4{Num<H>::template widen<false>(c[2 * p]), Num<H>::template widen<true>(c[2 * p]),
+                      Num<H>::template widen<false>(c[2 * p + 1]), Num<H>::template widen<true>(c[2 * p + 1])};
+        } else {
+          f[0] = w[i][0];
+          f[1] = w[i][1];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          d[j] = Num<H>::mma(f[0], x[j][b][0], d[j]);
+          d[j] = Num<H>::mma(f[1], x[j][b][1], d[j]);
+          if constexpr (TWO) {
+            d[j] = Num<H>::mma(f[0], x2[j][b][0], d[j]);
+            d[j] = Num<H>::mma(f[1], x2[j][b][1], d[j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if constexpr (W8)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(s[i], d[j][v], acc[i][j][v]);
+        else acc[i][j] = d[j];
+    }
+  }
+};
+
+// RTILE row tiles of an expert's matrix against NJ tiles of token columns, this
+// wave taking every waves-th column group, UNROLL of them in flight.
+template <typename H, bool W8, int RTILE, int NJ, bool TWO, int UNROLL>
+__device__ __forceinline__ void multiply(f4 (&acc)[RTILE][NJ], const uint8_t *const (&w)[RTILE], const float *const (&ws)[RTILE],
+                                         int64_t wlds, const uint16_t *const (&x)[NJ], const uint16_t *const (&x2)[NJ], int K,
+                                         int wave, int waves, int q) {
+  typedef Group<H, W8, RTILE, NJ, TWO> G;
+  const int full = K / G::COLS;
+  int g = wave;
+  for (; g + (UNROLL - 1) * waves < full; g += UNROLL * waves) {
+    G v[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) v[u].template load<false>(g + u * waves, K, q, w, ws, wlds, x, x2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) v[u].add(acc);
+  }
+  for (; g * G::COLS < K; g += waves) {
+    G v;
+    v.template load<true>(g, K, q, w, ws, wlds, x, x2);
+    v.add(acc);
   }
 }
 
 constexpr int WV = 4;       // waves of an expert workgroup
 
-// silu(G x) * (U x) for 16 of an expert's inter rows and all of its tokens.
-template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void gate_up_kernel(MoeArgs a) {
-  __shared__ int list[MAX_LIST], scratch[WV];
-  __shared__ float part[WV][2][4][64];
-  int e, count;
-  if (!my_expert(a, blockIdx.y, list, scratch, e, count)) return;
+// silu(G x) * (U x) for 16 of an expert's inter rows and 16 NJ of its tokens.
+template <typename H, bool W8, int NJ, int UNROLL>
+__device__ __forceinline__ void gate_up(const MoeArgs &a, int4 unit, int n0, float (*part)[2][4][64]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, i0 = blockIdx.x * 16;
+  const int r = lane & 15, q = lane >> 4, i0 = blockIdx.x * 16, e = unit.x, count = unit.z;
   const int64_t es = W8 ? 1 : 2;
   const uint8_t *w[2];
   const float *ws[2] = {nullptr, nullptr};
@@ -275,19 +400,25 @@ template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void gate_u
     w[i] = a.gate_up + ((int64_t)e * 2 * a.inter + row + r) * a.hidden * es;
     if constexpr (W8) ws[i] = a.gate_up_scales + (int64_t)e * ((a.hidden + 127) / 128) * wlds + (row >> 7);
   }
-  for (int n0 = 0; n0 < count; n0 += 16) {
-    f4 acc[2][1] = {{f4{0, 0, 0, 0}}, {f4{0, 0, 0, 0}}};
-    const uint16_t *x[1] = {a.x + (list[min(n0 + r, count - 1)] / a.topk) * a.ldx};
-    multiply<H, W8, 1, 2, false>(acc, w, ws, wlds, x, x, a.hidden, wave, WV, q);
+  const int32_t *order = a.order + unit.y;
+  const uint16_t *x[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) x[j] = a.x + (order[min(n0 + 16 * j + r, count - 1)] / a.topk) * a.ldx;
+  f4 acc[2][NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[0][j] = acc[1][j] = f4{0, 0, 0, 0};
+  multiply<H, W8, 2, NJ, false, UNROLL>(acc, w, ws, wlds, x, x, a.hidden, wave, WV, q);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) part[wave][i][v][lane] = acc[i][0][v];
+      for (int v = 0; v < 4; ++v) part[wave][i][v][lane] = acc[i][j][v];
     __syncthreads();
     // thread (row i, column c) of the 16 x 16 block
     const int i = tid & 15, c = tid >> 4, at = (i >> 2) * 16 + c;
-    if (n0 + c < count) {
+    if (n0 + 16 * j + c < count) {
       float g = 0.0f, u = 0.0f;
 #pragma unroll
       for (int k = 0; k < WV; ++k) {
@@ -298,59 +429,108 @@ template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void gate_u
       const H hi = (H)v;
       const float rest = v - (float)hi;
       const H lo = (H)(__builtin_isfinite(rest) ? rest : 0.0f);     // beyond the type's range hi is infinite
-      const int64_t o = (int64_t)list[n0 + c] * a.inter + i0 + i;
+      const int64_t o = (int64_t)order[n0 + 16 * j + c] * a.inter + i0 + i;
       a.hi[o] = __builtin_bit_cast(uint16_t, hi);
       a.lo[o] = __builtin_bit_cast(uint16_t, lo);
     }
   }
 }
 
-// 16 rows of an expert's down product for all of its tokens.
-template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void down_kernel(MoeArgs a) {
-  __shared__ int list[MAX_LIST], scratch[WV];
-  __shared__ float part[WV][4][64];
-  int e, count;
-  if (!my_expert(a, blockIdx.y, list, scratch, e, count)) return;
+template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void gate_up_kernel(MoeArgs a) {
+  __shared__ float part[WV][2][4][64];
+  if ((int)blockIdx.y >= *a.units) return;
+  const int4 unit = a.unit[blockIdx.y];
+  int n0 = 0;
+  for (; n0 + 16 < unit.z; n0 += 32) gate_up<H, W8, 2, 1>(a, unit, n0, part);
+  if (n0 < unit.z) gate_up<H, W8, 1, 2>(a, unit, n0, part);
+}
+
+// 16 RTILE rows of an expert's down product for 16 NJ of its tokens.
+template <typename H, bool W8, int RTILE, int NJ, int UNROLL>
+__device__ __forceinline__ void down(const MoeArgs &a, int4 unit, int n0, float (*part)[RTILE][4][64]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, h0 = blockIdx.x * 16;
+  const int r = lane & 15, q = lane >> 4, h0 = blockIdx.x * 16 * RTILE, e = unit.x, count = unit.z;
   const int64_t es = W8 ? 1 : 2;
   const int64_t wlds = (a.hidden + 127) / 128;
-  const uint8_t *w[1] = {a.down + ((int64_t)e * a.hidden + h0 + r) * a.inter * es};
-  const float *ws[1] = {nullptr};
-  if constexpr (W8) ws[0] = a.down_scales + (int64_t)e * ((a.inter + 127) / 128) * wlds + (h0 >> 7);
-  for (int n0 = 0; n0 < count; n0 += 16) {
-    f4 acc[1][1] = {{f4{0, 0, 0, 0}}};
-    const int64_t at = (int64_t)list[min(n0 + r, count - 1)] * a.inter;
-    const uint16_t *x[1] = {a.hi + at}, *x2[1] = {a.lo + at};
-    multiply<H, W8, 1, 1, true>(acc, w, ws, wlds, x, x2, a.inter, wave, WV, q);
+  const uint8_t *w[RTILE];
+  const float *ws[RTILE];
+#pragma unroll
+  for (int i = 0; i < RTILE; ++i) {
+    const int h = min(h0 + 16 * i, a.hidden - 16);      // a tile past the end: the last one again, not stored
+    w[i] = a.down + ((int64_t)e * a.hidden + h + r) * a.inter * es;
+    ws[i] = W8 ? a.down_scales + (int64_t)e * ((a.inter + 127) / 128) * wlds + (h >> 7) : nullptr;
+  }
+  const int32_t *order = a.order + unit.y;
+  const uint16_t *x[NJ], *x2[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int64_t at = (int64_t)order[min(n0 + 16 * j + r, count - 1)] * a.inter;
+    x[j] = a.hi + at;
+    x2[j] = a.lo + at;
+  }
+  f4 acc[RTILE][NJ];
+#pragma unroll
+  for (int i = 0; i < RTILE; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f4{0, 0, 0, 0};
+  multiply<H, W8, RTILE, NJ, true, UNROLL>(acc, w, ws, wlds, x, x2, a.inter, wave, WV, q);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[0][0][v];
+    for (int i = 0; i < RTILE; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) part[wave][i][v][lane] = acc[i][j][v];
     __syncthreads();
     const int i = tid & 15, c = tid >> 4, o = (i >> 2) * 16 + c;
-    if (n0 + c < count) {
-      float s = 0.0f;
+    if (n0 + 16 * j + c < count) {
+      float *to = a.part + (int64_t)order[n0 + 16 * j + c] * a.hidden + h0 + i;
 #pragma unroll
-      for (int k = 0; k < WV; ++k) s += part[k][i & 3][o];
-      a.part[(int64_t)list[n0 + c] * a.hidden + h0 + i] = s;
+      for (int t = 0; t < RTILE; ++t) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WV; ++k) s += part[k][t][i & 3][o];
+        if (h0 + 16 * t < a.hidden) put(to + 16 * t, s);
+      }
     }
   }
 }
 
-template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
-  const int h = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
-  if (h >= a.hidden) return;
-  float s = 0.0f;
-  for (int j = 0; j < a.topk; ++j) s += a.weights[t * a.topk + j] * a.part[(int64_t)(t * a.topk + j) * a.hidden + h];
-  a.y[t * a.ldy + h] = __builtin_bit_cast(uint16_t, (H)s);
+// Down products of one expert and 16 RTILE rows of y; the workgroup that is last
+// with these rows adds the experts' parts, in the order of each token's choices.
+template <typename H, bool W8, int RTILE> __global__ __launch_bounds__(64 * WV) void down_kernel(MoeArgs a) {
+  __shared__ float part[WV][RTILE][4][64];
+  __shared__ int last;
+  const int units = *a.units;
+  if ((int)blockIdx.y >= units) return;
+  const int4 unit = a.unit[blockIdx.y];
+  int n0 = 0;
+  for (; n0 + 16 < unit.z; n0 += 32) down<H, W8, RTILE, 2, 1>(a, unit, n0, part);
+  if (n0 < unit.z) down<H, W8, RTILE, 1, 2>(a, unit, n0, part);
+  if (!arrive(a.arrived + BLOCKS + blockIdx.x, units, &last)) return;
+  const int h0 = blockIdx.x * 16 * RTILE;
+  for (int x = threadIdx.x; x < 16 * RTILE * a.tokens; x += 64 * WV) {
+    const int t = x / (16 * RTILE), h = h0 + x % (16 * RTILE);
+    if (h >= a.hidden) continue;
+    const float *from = a.part + (int64_t)t * a.topk * a.hidden + h, *weight = a.weights + t * a.topk;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int j = 0; j < a.topk; ++j) s += weight[j] * get(from + (int64_t)j * a.hidden);
+    a.y[t * a.ldy + h] = __builtin_bit_cast(uint16_t, (H)s);
+  }
 }
 
 template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
-  router_kernel<H><<<dim3((a.experts + 3) / 4, (a.tokens + RT - 1) / RT), 256, 0, st>>>(a);
-  select_kernel<<<dim3(a.tokens), 256, 0, st>>>(a);
-  gate_up_kernel<H, W8><<<dim3(a.inter / 16, a.slots), 64 * WV, 0, st>>>(a);
-  down_kernel<H, W8><<<dim3(a.hidden / 16, a.slots), 64 * WV, 0, st>>>(a);
-  combine_kernel<H><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, st>>>(a);
+  if (a.tokens == 1) router_kernel<H, 1><<<dim3((a.experts + 3) / 4, 1), 256, 0, st>>>(a);
+  else router_kernel<H, RT_MAX><<<dim3((a.experts + 3) / 4, (a.tokens + RT_MAX - 1) / RT_MAX), 256, 0, st>>>(a);
+  const int slots = std::min(a.tokens * a.topk, a.experts);
+  gate_up_kernel<H, W8><<<dim3(a.inter / 16, slots), 64 * WV, 0, st>>>(a);
+  if (slots * (a.hidden / 32) >= 2048) down_kernel<H, W8, 2><<<dim3((a.hidden + 31) / 32, slots), 64 * WV, 0, st>>>(a);
+  else down_kernel<H, W8, 1><<<dim3(a.hidden / 16, slots), 64 * WV, 0, st>>>(a);
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(int32_t *p, int n) {
+  for (int i = threadIdx.x; i < n; i += 256) p[i] = 0;
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -370,13 +550,18 @@ tlr_status check_layer(const tlr_moe_layer *l) {
 
 // Workspace of `tokens` tokens; offsets of its parts.
 struct Parts {
-  size_t logits, hi, lo, part, total;
+  size_t arrived, units, unit, order, logits, hi, lo, part, total;
 };
+size_t counters(const tlr_moe_layer *l) { return BLOCKS + (size_t)l->hidden / 16; }
 Parts parts_of(const tlr_moe_layer *l, int64_t tokens) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Parts p;
   const size_t n = (size_t)tokens * l->topk;
-  p.logits = 0;
+  p.arrived = 0;
+  p.units = p.arrived + counters(l) * 4;
+  p.unit = up(p.units + 4);
+  p.order = p.unit + sizeof(int4) * MAX_EXPERTS;
+  p.logits = p.order + up(n * 4);
   p.hi = p.logits + up((size_t)tokens * l->experts * 8);
   p.lo = p.hi + up(n * l->inter * 2);
   p.part = p.lo + up(n * l->inter * 2);
@@ -398,7 +583,11 @@ tlr_status moe_workspace(const tlr_moe_layer *layer, int32_t max_tokens, size_t 
 tlr_status moe_init(const tlr_moe_layer *layer, void *ws, size_t ws_bytes, void *stream) {
   const tlr_status st = check_layer(layer);
   if (st != TLR_OK) return st;
-  (void)ws, (void)ws_bytes, (void)stream;
+  if (!ws || !aligned(ws, 256)) return fail(TLR_ERR_INVALID_ARG, "moe_init: null or misaligned workspace");
+  if (ws_bytes < parts_of(layer, 0).total) return fail(TLR_ERR_WORKSPACE, "moe_init: workspace too small");
+  clear_kernel<<<1, 256, 0, static_cast<hipStream_t>(stream)>>>(static_cast<int32_t *>(ws), (int)counters(layer));
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TLR_ERR_HIP, std::string("moe_init: ") + hipGetErrorString(e));
   return TLR_OK;
 }
 
@@ -424,9 +613,10 @@ tlr_status moe(const tlr_moe_layer *l, int32_t tokens, const void *X, int64_t ld
             static_cast<const uint16_t *>(X), ldx, static_cast<uint16_t *>(Y), ldy,
             static_cast<const uint16_t *>(l->router), static_cast<const uint8_t *>(l->gate_up),
             static_cast<const uint8_t *>(l->down), l->gate_up_scales, l->down_scales, ids, weights,
+            reinterpret_cast<int32_t *>(b + p.arrived), reinterpret_cast<int32_t *>(b + p.units),
+            reinterpret_cast<int4 *>(b + p.unit), reinterpret_cast<int32_t *>(b + p.order),
             reinterpret_cast<double *>(b + p.logits), reinterpret_cast<uint16_t *>(b + p.hi),
-            reinterpret_cast<uint16_t *>(b + p.lo), reinterpret_cast<float *>(b + p.part),
-            std::min(tokens * l->topk, l->experts)};
+            reinterpret_cast<uint16_t *>(b + p.lo), reinterpret_cast<float *>(b + p.part)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (l->dt == TLR_F16) w8 ? launch<_Float16, true>(a, hs) : launch<_Float16, false>(a, hs);
   else w8 ? launch<__bf16, true>(a, hs) : launch<__bf16, false>(a, hs);

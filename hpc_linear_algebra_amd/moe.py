@@ -3,11 +3,13 @@ include/tlrgemm.h): router, softmax, top-k, gated experts (silu), weighted sum.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional, Tuple
 
 import torch
 
 from . import tlrgemm as T
+from .blocks import call
 
 MAX_TOKENS = 256
 _DT = {torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
@@ -63,6 +65,7 @@ class MoELayer:
                                  gate_up_scales.data_ptr() if e8 else None, down_scales.data_ptr() if e8 else None)
         self.ws = torch.empty(max(256, T.tlr_moe_workspace_bytes(self.c, self.max_tokens)), dtype=torch.uint8,
                               device=self.device)
+        self._ref, self._ws, self._nws = ctypes.byref(self.c), self.ws.data_ptr(), self.ws.numel()
         with torch.cuda.device(self.device):
             T.tlr_moe_init(self.c, self.ws.data_ptr(), self.ws.numel(), torch.cuda.current_stream().cuda_stream)
 
@@ -79,8 +82,9 @@ class MoELayer:
         y = torch.empty((t, self.hidden), dtype=x.dtype, device=x.device)
         ids = torch.empty((t, self.topk), dtype=torch.int32, device=x.device)
         weights = torch.empty((t, self.topk), dtype=torch.float32, device=x.device)
-        with torch.cuda.device(self.device):
-            T.tlr_moe(self.c, t, x.data_ptr(), x.stride(0) if t > 1 else self.hidden, y.data_ptr(), self.hidden,
-                      ids.data_ptr(), weights.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                      torch.cuda.current_stream(self.device).cuda_stream)
+        st = call(self.device, T.lib().tlr_moe, self._ref, t, x.data_ptr() or None, x.stride(0) if t > 1 else self.hidden,
+                  y.data_ptr() or None, self.hidden, ids.data_ptr() or None, weights.data_ptr() or None, self._ws,
+                  self._nws)
+        if st:
+            T._check(st, "tlr_moe")
         return y, ids, weights

@@ -26,7 +26,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int MAX_TOKENS = 256, MAX_EXPERTS = 512, MAX_TOPK = 16;
-constexpr int RT_MAX = 8;                 // tokens of a router workgroup, at most
+constexpr int RT = 16;                    // tokens of a router workgroup
 constexpr int ROUTED = 32, BLOCKS = 64;   // counters: 0.. router groups, ROUTED all groups, BLOCKS.. row blocks of y
 
 // The 16-bit type of x, y and the products.
@@ -67,7 +67,8 @@ struct MoeArgs {
   int32_t *units;           // how many experts were chosen
   int4 *unit;               // each of them: expert, first place in order, assignments, 0
   int32_t *order;           // assignments (token * topk + choice) by expert
-  double *logits;           // tokens x experts
+  double *logits;           // splits x tokens x experts: parts of the router product
+  int32_t splits;
   uint16_t *hi, *lo;        // tokens*topk x inter: silu(g) u as hi + lo
   float *part;              // tokens*topk x hidden: the experts' outputs
 };
@@ -133,7 +134,9 @@ template <int PER> __device__ __forceinline__ void select(const MoeArgs &a, int 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    x[i] = e < a.experts ? get(l + e) : 0.0;
+    x[i] = 0.0;
+    if (e < a.experts)
+      for (int z = 0; z < a.splits; ++z) x[i] += get(l + (int64_t)z * a.tokens * a.experts + e);
     key[i] = e < a.experts ? sort_key(x[i]) : 0;      // no number's key is 0
   }
   double best = 0.0, mine = 0.0;      // lane j: the logit of choice j
@@ -182,12 +185,18 @@ template <int PER> __device__ __forceinline__ void select(const MoeArgs &a, int 
 // One workgroup: the assignments by expert and the chosen experts.  Places within
 // an expert go in the order of the atomics, which no result depends on: an
 // assignment is a column of a product, whichever one.
-__device__ __forceinline__ void sort(const MoeArgs &a) {
+template <int THREADS> __device__ __forceinline__ void sort(const MoeArgs &a) {
   __shared__ int count[MAX_EXPERTS], place[MAX_EXPERTS];
+  constexpr int MAX = MAX_TOKENS * MAX_TOPK / THREADS;
   const int tid = threadIdx.x, n = a.tokens * a.topk;
-  for (int e = tid; e < MAX_EXPERTS; e += 256) count[e] = 0;
+  for (int e = tid; e < MAX_EXPERTS; e += THREADS) count[e] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += 256) atomicAdd(&count[get(a.ids + i)], 1);
+  int id[MAX];
+#pragma unroll
+  for (int i = 0; i < MAX; ++i) {
+    id[i] = tid + i * THREADS < n ? get(a.ids + tid + i * THREADS) : -1;
+    if (id[i] >= 0) atomicAdd(&count[id[i]], 1);
+  }
   __syncthreads();
   if (tid < 64) {
     constexpr int PER = MAX_EXPERTS / 64;
@@ -216,59 +225,92 @@ __device__ __forceinline__ void sort(const MoeArgs &a) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < n; i += 256) a.order[atomicAdd(&place[get(a.ids + i)], 1)] = i;
+#pragma unroll
+  for (int i = 0; i < MAX; ++i)
+    if (id[i] >= 0) a.order[atomicAdd(&place[id[i]], 1)] = tid + i * THREADS;
 }
 
-// Logits: one wave per expert and RT tokens.  A product of two 16-bit numbers
-// is an exact float; the sums run in double.  The workgroup that is done last
-// with a group of RT tokens chooses their experts, a wave per token, and the
-// last of all sorts the assignments: launches of their own would cost 4 us each.
-template <typename H, int RT> __global__ __launch_bounds__(256) void router_kernel(MoeArgs a) {
+// The experts of token t chosen by one wave.
+__device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
+  if (a.experts <= 64) select<1>(a, t, lane);
+  else if (a.experts <= 128) select<2>(a, t, lane);
+  else if (a.experts <= 256) select<4>(a, t, lane);
+  else select<8>(a, t, lane);
+}
+
+// One token: a wave per expert.  A product of two 16-bit numbers is an exact
+// float; the sums run in double.  The workgroup that is done last chooses: a
+// launch of its own would cost 4 us.
+template <typename H> __global__ __launch_bounds__(256) void router_one_kernel(MoeArgs a) {
+  __shared__ int last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * RT;
+  const int e = blockIdx.x * 4 + wave;
   if (e < a.experts) {
     const uint16_t *w = a.router + (int64_t)e * a.hidden;
-    const uint16_t *x[RT];
-    double acc[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      acc[i] = 0.0;
-      x[i] = a.x + min(t0 + i, a.tokens - 1) * a.ldx;
-    }
-#pragma unroll 2
+    double s = 0.0;
+#pragma unroll 4
     for (int c = 8 * lane; c < a.hidden; c += 512) {
-      const u4 wv = *reinterpret_cast<const u4 *>(w + c);
-      u4 xv[RT];
+      float wf[8], xf[8];
+      unpack8<H>(*reinterpret_cast<const u4 *>(w + c), wf);
+      unpack8<H>(*reinterpret_cast<const u4 *>(a.x + c), xf);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) xv[i] = *reinterpret_cast<const u4 *>(x[i] + c);
-      float wf[8];
-      unpack8<H>(wv, wf);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float xf[8];
-        unpack8<H>(xv[i], xf);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) acc[i] += (double)(wf[v] * xf[v]);
-      }
+      for (int v = 0; v < 8; ++v) s += (double)(wf[v] * xf[v]);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      double s = acc[i];
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-      if (lane == 0 && t0 + i < a.tokens)
-        put(a.logits + (int64_t)(t0 + i) * a.experts + e, s);
-    }
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) put(a.logits + e, s);
   }
+  if (!arrive(a.arrived, gridDim.x, &last) || wave > 0) return;
+  choose(a, 0, lane);
+  if (lane < a.topk) {                // no expert twice: nothing to sort
+    a.unit[lane] = int4{a.ids[lane], lane, 1, 0};
+    a.order[lane] = lane;
+  }
+  if (lane == 0) *a.units = a.topk;
+}
+
+constexpr int RW = 16;      // waves of a router workgroup
+static_assert(RW == RT, "a wave chooses for each token");
+
+// More tokens: 16 experts x 16 tokens on the 64-bit matrix cores, the waves
+// and the workgroups of grid z taking groups of 32 columns in turn.  Lane (r, q) supplies columns 8 q ..
+// + 7 of expert row r and of token r and holds the sums of experts q + 4 v and
+// token r.  The vector units took 20 us for 64 tokens, most of it converting
+// every product; here every entry is converted once a tile.  The workgroup that
+// is done last with its tokens chooses their experts, a wave per token, and the
+// last of all sorts the assignments.
+template <typename H> __global__ __launch_bounds__(64 * RW) void router_kernel(MoeArgs a) {
+  typedef double d4 __attribute__((ext_vector_type(4)));
+  __shared__ double part[RW][4][64];
   __shared__ int last;
-  if (!arrive(a.arrived + blockIdx.y, gridDim.x, &last)) return;
-  for (int t = t0 + wave; t < min(t0 + RT, a.tokens); t += 4) {
-    if (a.experts <= 64) select<1>(a, t, lane);
-    else if (a.experts <= 128) select<2>(a, t, lane);
-    else if (a.experts <= 256) select<4>(a, t, lane);
-    else select<8>(a, t, lane);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4, e0 = blockIdx.x * 16, t0 = blockIdx.y * RT;
+  const uint16_t *w = a.router + (int64_t)min(e0 + r, a.experts - 1) * a.hidden;
+  const uint16_t *x = a.x + min(t0 + r, a.tokens - 1) * a.ldx;
+  d4 acc = d4{0, 0, 0, 0};
+  for (int k0 = 32 * (wave + RW * (int)blockIdx.z); k0 < a.hidden; k0 += 32 * RW * (int)gridDim.z) {
+    const int k = k0 + 8 * q;
+    const bool in = k < a.hidden;
+    float wf[8], xf[8];
+    unpack8<H>(*reinterpret_cast<const u4 *>(w + (in ? k : 0)), wf);
+    unpack8<H>(*reinterpret_cast<const u4 *>(x + (in ? k : 0)), xf);
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(in ? (double)wf[v] : 0.0, in ? (double)xf[v] : 0.0, acc, 0, 0, 0);
   }
-  if (arrive(a.arrived + ROUTED, gridDim.y, &last)) sort(a);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[v];
+  __syncthreads();
+  if (tid < 256) {
+    const int i = tid & 15, t = tid >> 4;       // expert e0 + i = q + 4 v, token t0 + t
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < RW; ++k) s += part[k][i >> 2][(i & 3) * 16 + t];
+    if (e0 + i < a.experts && t0 + t < a.tokens) put(a.logits + ((int64_t)blockIdx.z * a.tokens + t0 + t) * a.experts + e0 + i, s);
+  }
+  if (!arrive(a.arrived + blockIdx.y, gridDim.x * gridDim.z, &last)) return;
+  if (t0 + wave < a.tokens) choose(a, t0 + wave, lane);
+  if (arrive(a.arrived + ROUTED, gridDim.y, &last)) sort<64 * RW>(a);
 }
 
 // A column group of an expert's rows and of NJ tiles of 16 token columns, as
@@ -521,8 +563,8 @@ template <typename H, bool W8, int RTILE> __global__ __launch_bounds__(64 * WV) 
 }
 
 template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
-  if (a.tokens == 1) router_kernel<H, 1><<<dim3((a.experts + 3) / 4, 1), 256, 0, st>>>(a);
-  else router_kernel<H, RT_MAX><<<dim3((a.experts + 3) / 4, (a.tokens + RT_MAX - 1) / RT_MAX), 256, 0, st>>>(a);
+  if (a.tokens == 1) router_one_kernel<H><<<dim3((a.experts + 3) / 4), 256, 0, st>>>(a);
+  else router_kernel<H><<<dim3((a.experts + 15) / 16, (a.tokens + RT - 1) / RT, a.splits), 64 * RW, 0, st>>>(a);
   const int slots = std::min(a.tokens * a.topk, a.experts);
   gate_up_kernel<H, W8><<<dim3(a.inter / 16, slots), 64 * WV, 0, st>>>(a);
   if (slots * (a.hidden / 32) >= 2048) down_kernel<H, W8, 2><<<dim3((a.hidden + 31) / 32, slots), 64 * WV, 0, st>>>(a);
@@ -553,6 +595,10 @@ struct Parts {
   size_t arrived, units, unit, order, logits, hi, lo, part, total;
 };
 size_t counters(const tlr_moe_layer *l) { return BLOCKS + (size_t)l->hidden / 16; }
+// Workgroups that share a router tile's columns: one group of 32 a wave, up to 8.
+int splits_of(const tlr_moe_layer *l, int64_t tokens) {
+  return tokens == 1 ? 1 : std::min(8, (l->hidden + 32 * RW - 1) / (32 * RW));
+}
 Parts parts_of(const tlr_moe_layer *l, int64_t tokens) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Parts p;
@@ -562,7 +608,7 @@ Parts parts_of(const tlr_moe_layer *l, int64_t tokens) {
   p.unit = up(p.units + 4);
   p.order = p.unit + sizeof(int4) * MAX_EXPERTS;
   p.logits = p.order + up(n * 4);
-  p.hi = p.logits + up((size_t)tokens * l->experts * 8);
+  p.hi = p.logits + up((size_t)splits_of(l, tokens) * tokens * l->experts * 8);
   p.lo = p.hi + up(n * l->inter * 2);
   p.part = p.lo + up(n * l->inter * 2);
   p.total = p.part + up(n * l->hidden * 4);
@@ -615,7 +661,7 @@ tlr_status moe(const tlr_moe_layer *l, int32_t tokens, const void *X, int64_t ld
             static_cast<const uint8_t *>(l->down), l->gate_up_scales, l->down_scales, ids, weights,
             reinterpret_cast<int32_t *>(b + p.arrived), reinterpret_cast<int32_t *>(b + p.units),
             reinterpret_cast<int4 *>(b + p.unit), reinterpret_cast<int32_t *>(b + p.order),
-            reinterpret_cast<double *>(b + p.logits), reinterpret_cast<uint16_t *>(b + p.hi),
+            reinterpret_cast<double *>(b + p.logits), splits_of(l, tokens), reinterpret_cast<uint16_t *>(b + p.hi),
             reinterpret_cast<uint16_t *>(b + p.lo), reinterpret_cast<float *>(b + p.part)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (l->dt == TLR_F16) w8 ? launch<_Float16, true>(a, hs) : launch<_Float16, false>(a, hs);

@@ -27,6 +27,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int MAX_TOKENS = 256, MAX_EXPERTS = 512, MAX_TOPK = 16;
 constexpr int RT = 16;                    // tokens of a router workgroup
+constexpr int MAX_SPLITS = 4;             // workgroups that share a router tile's columns
 constexpr int ROUTED = 32, BLOCKS = 64;   // counters: 0.. router groups, ROUTED all groups, BLOCKS.. row blocks of y
 
 // The 16-bit type of x, y and the products.
@@ -134,9 +135,13 @@ template <int PER> __device__ __forceinline__ void select(const MoeArgs &a, int 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    x[i] = 0.0;
-    if (e < a.experts)
-      for (int z = 0; z < a.splits; ++z) x[i] += get(l + (int64_t)z * a.tokens * a.experts + e);
+    double part[MAX_SPLITS];          // clamped, not branched on: all loads in flight at once
+#pragma unroll
+    for (int z = 0; z < MAX_SPLITS; ++z)
+      part[z] = get(l + (int64_t)min(z, a.splits - 1) * a.tokens * a.experts + min(e, a.experts - 1));
+    x[i] = part[0];
+#pragma unroll
+    for (int z = 1; z < MAX_SPLITS; ++z) x[i] += z < a.splits ? part[z] : 0.0;
     key[i] = e < a.experts ? sort_key(x[i]) : 0;      // no number's key is 0
   }
   double best = 0.0, mine = 0.0;      // lane j: the logit of choice j
@@ -146,19 +151,25 @@ template <int PER> __device__ __forceinline__ void select(const MoeArgs &a, int 
 #pragma unroll
     for (int i = 1; i < PER; ++i) top = max(top, key[i]);
     const uint32_t hi = wave_max((uint32_t)(top >> 32));
-    const uint32_t lo = wave_max((uint32_t)(top >> 32) == hi ? (uint32_t)top : 0u);
+    const uint64_t tied = __ballot((uint32_t)(top >> 32) == hi);
+    // one lane has that high word, most often: its low word then
+    const uint32_t lo = (tied & (tied - 1)) == 0 ? (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)top, __builtin_ctzll(tied))
+                                                 : wave_max((uint32_t)(top >> 32) == hi ? (uint32_t)top : 0u);
     const uint64_t k = (uint64_t)hi << 32 | lo;
-    uint32_t at = 0;                  // MAX_EXPERTS - the lowest index
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i) at = key[i] == k ? (uint32_t)(MAX_EXPERTS - lane - 64 * i) : at;
-    const int e = MAX_EXPERTS - (int)wave_max(at);
+    int e = -1;
     double v = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      v = i == (e >> 6) ? x[i] : v;
-      if (e == lane + 64 * i) key[i] = 0;
+      const uint64_t b = __ballot(key[i] == k);
+      if (e < 0 && b != 0) {
+        const int at = __builtin_ctzll(b);
+        e = at + 64 * i;
+        const uint64_t w = __builtin_bit_cast(uint64_t, x[i]);
+        v = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(w >> 32), at) << 32 |
+                                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)w, at));
+        if (lane == at) key[i] = 0;
+      }
     }
-    v = __shfl(v, e & 63);
     if (j == 0) best = v;
     if (lane == j) {
       mine = v;
@@ -302,10 +313,10 @@ template <typename H> __global__ __launch_bounds__(64 * RW) void router_kernel(M
   for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[v];
   __syncthreads();
   if (tid < 256) {
-    const int i = tid & 15, t = tid >> 4;       // expert e0 + i = q + 4 v, token t0 + t
+    const int i = q + 4 * wave, t = r;
     double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < RW; ++k) s += part[k][i >> 2][(i & 3) * 16 + t];
+    for (int k = 0; k < RW; ++k) s += part[k][wave][lane];
     if (e0 + i < a.experts && t0 + t < a.tokens) put(a.logits + ((int64_t)blockIdx.z * a.tokens + t0 + t) * a.experts + e0 + i, s);
   }
   if (!arrive(a.arrived + blockIdx.y, gridDim.x * gridDim.z, &last)) return;
@@ -532,34 +543,51 @@ __device__ __forceinline__ void down(const MoeArgs &a, int4 unit, int n0, float 
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < WV; ++k) s += part[k][t][i & 3][o];
-        if (h0 + 16 * t < a.hidden) put(to + 16 * t, s);
+        if (h0 + 16 * t >= a.hidden) continue;
+        if constexpr (RTILE == 1) put(to + 16 * t, s);
+        else to[16 * t] = s;
       }
     }
   }
 }
 
-// Down products of one expert and 16 RTILE rows of y; the workgroup that is last
-// with these rows adds the experts' parts, in the order of each token's choices.
-template <typename H, bool W8, int RTILE> __global__ __launch_bounds__(64 * WV) void down_kernel(MoeArgs a) {
+// y of a token at row h from the parts of its experts, in the order of its choices.
+template <typename H, bool SAME_LAUNCH> __device__ __forceinline__ void add_parts(const MoeArgs &a, int t, int h) {
+  const float *from = a.part + (int64_t)t * a.topk * a.hidden + h, *weight = a.weights + t * a.topk;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int j = 0; j < a.topk; ++j) {
+    const float *p = from + (int64_t)j * a.hidden;
+    s += weight[j] * (SAME_LAUNCH ? get(p) : *p);
+  }
+  a.y[t * a.ldy + h] = __builtin_bit_cast(uint16_t, (H)s);
+}
+
+// Down products of one expert and 16 RTILE rows of y.  RTILE 1: the workgroup
+// that is last with its rows adds the parts.  RTILE 2 (many workgroups): left to
+// a launch of its own, since a workgroup would hold its place for another 2 us
+// until it knows whether it is the last (8-bit weights, 13 tokens: 110 us with,
+// 104 without); 4 waves a SIMD for 8-bit weights, whose two groups in flight
+// would take 148 registers.
+template <typename H, bool W8, int RTILE>
+__global__ __launch_bounds__(64 * WV, W8 && RTILE == 2 ? 4 : 1) void down_kernel(MoeArgs a) {
   __shared__ float part[WV][RTILE][4][64];
-  __shared__ int last;
   const int units = *a.units;
   if ((int)blockIdx.y >= units) return;
   const int4 unit = a.unit[blockIdx.y];
   int n0 = 0;
   for (; n0 + 16 < unit.z; n0 += 32) down<H, W8, RTILE, 2, 1>(a, unit, n0, part);
-  if (n0 < unit.z) down<H, W8, RTILE, 1, 2>(a, unit, n0, part);
-  if (!arrive(a.arrived + BLOCKS + blockIdx.x, units, &last)) return;
-  const int h0 = blockIdx.x * 16 * RTILE;
-  for (int x = threadIdx.x; x < 16 * RTILE * a.tokens; x += 64 * WV) {
-    const int t = x / (16 * RTILE), h = h0 + x % (16 * RTILE);
-    if (h >= a.hidden) continue;
-    const float *from = a.part + (int64_t)t * a.topk * a.hidden + h, *weight = a.weights + t * a.topk;
-    float s = 0.0f;
-#pragma unroll 8
-    for (int j = 0; j < a.topk; ++j) s += weight[j] * get(from + (int64_t)j * a.hidden);
-    a.y[t * a.ldy + h] = __builtin_bit_cast(uint16_t, (H)s);
+  if (n0 < unit.z) down<H, W8, RTILE, 1, W8 && RTILE == 2 ? 1 : 2>(a, unit, n0, part);
+  if constexpr (RTILE == 1) {
+    __shared__ int last;
+    if (!arrive(a.arrived + BLOCKS + blockIdx.x, units, &last)) return;
+    for (int x = threadIdx.x; x < 16 * a.tokens; x += 64 * WV) add_parts<H, true>(a, x >> 4, blockIdx.x * 16 + (x & 15));
   }
+}
+
+template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
+  const int h = blockIdx.x * 256 + threadIdx.x;
+  if (h < a.hidden) add_parts<H, false>(a, blockIdx.y, h);
 }
 
 template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
@@ -567,8 +595,12 @@ template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
   else router_kernel<H><<<dim3((a.experts + 15) / 16, (a.tokens + RT - 1) / RT, a.splits), 64 * RW, 0, st>>>(a);
   const int slots = std::min(a.tokens * a.topk, a.experts);
   gate_up_kernel<H, W8><<<dim3(a.inter / 16, slots), 64 * WV, 0, st>>>(a);
-  if (slots * (a.hidden / 32) >= 2048) down_kernel<H, W8, 2><<<dim3((a.hidden + 31) / 32, slots), 64 * WV, 0, st>>>(a);
-  else down_kernel<H, W8, 1><<<dim3(a.hidden / 16, slots), 64 * WV, 0, st>>>(a);
+  if (slots * (a.hidden / 32) < 2048) {
+    down_kernel<H, W8, 1><<<dim3(a.hidden / 16, slots), 64 * WV, 0, st>>>(a);
+    return;
+  }
+  down_kernel<H, W8, 2><<<dim3((a.hidden + 31) / 32, slots), 64 * WV, 0, st>>>(a);
+  combine_kernel<H><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, st>>>(a);
 }
 
 __global__ __launch_bounds__(256) void clear_kernel(int32_t *p, int n) {
@@ -595,9 +627,9 @@ struct Parts {
   size_t arrived, units, unit, order, logits, hi, lo, part, total;
 };
 size_t counters(const tlr_moe_layer *l) { return BLOCKS + (size_t)l->hidden / 16; }
-// Workgroups that share a router tile's columns: one group of 32 a wave, up to 8.
+// Workgroups that share a router tile's columns: one group of 32 a wave.
 int splits_of(const tlr_moe_layer *l, int64_t tokens) {
-  return tokens == 1 ? 1 : std::min(8, (l->hidden + 32 * RW - 1) / (32 * RW));
+  return tokens == 1 ? 1 : std::min(MAX_SPLITS, (l->hidden + 32 * RW - 1) / (32 * RW));
 }
 Parts parts_of(const tlr_moe_layer *l, int64_t tokens) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

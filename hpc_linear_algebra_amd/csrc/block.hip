@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "tlr_ops.h"
@@ -259,7 +260,6 @@ struct GemmArgs {
   void *c;
   int64_t ldc;
   int32_t dt;
-  int32_t vec;              // columns of C 16-byte aligned
 };
 
 // Two codes widened to bfloat16, exactly.
@@ -282,18 +282,30 @@ template <bool E5> __device__ __forceinline__ b8v widen8(uint32_t w0, uint32_t w
 // Frobenius error on normal data).  Otherwise the codes are widened and the
 // bfloat16 instructions add in float (9e-9 on the same data).  In registers
 // only, the x128 instruction reaches 4.19 PFLOP/s on the whole chip.
-template <bool A5, bool B5, bool FAST> __device__ __forceinline__ f4 mma(u4 a0, u4 a1, u4 b0, u4 b1) {
+__device__ __forceinline__ i8v join(u4 a, u4 b) {
+  return __builtin_bit_cast(i8v, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// A fragment: the lane's 32 codes of a row, as the instructions take them.
+template <bool E5, bool FAST> struct Fragment;
+template <bool E5> struct Fragment<E5, true> {
+  i8v x;
+  Fragment() = default;
+  __device__ __forceinline__ Fragment(i8v c) : x(c) {}
+};
+template <bool E5> struct Fragment<E5, false> {
+  b8v x[4];
+  Fragment() = default;
+  __device__ __forceinline__ Fragment(i8v c)
+      : x{widen8<E5>(c[0], c[1]), widen8<E5>(c[2], c[3]), widen8<E5>(c[4], c[5]), widen8<E5>(c[6], c[7])} {}
+};
+template <bool A5, bool B5> __device__ __forceinline__ f4 mma(const Fragment<A5, true> &a, const Fragment<B5, true> &b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.x, b.x, f4{0, 0, 0, 0}, A5 ? 1 : 0, B5 ? 1 : 0, 0, 0, 0, 0);
+}
+template <bool A5, bool B5> __device__ __forceinline__ f4 mma(const Fragment<A5, false> &a, const Fragment<B5, false> &b) {
   f4 d = f4{0, 0, 0, 0};
-  if constexpr (FAST) {
-    const i8v a = __builtin_bit_cast(i8v, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
-    const i8v b = __builtin_bit_cast(i8v, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, A5 ? 1 : 0, B5 ? 1 : 0, 0, 0, 0, 0);
-  } else {
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<A5>(a0[0], a0[1]), widen8<B5>(b0[0], b0[1]), d, 0, 0, 0);
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<A5>(a0[2], a0[3]), widen8<B5>(b0[2], b0[3]), d, 0, 0, 0);
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<A5>(a1[0], a1[1]), widen8<B5>(b1[0], b1[1]), d, 0, 0, 0);
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<A5>(a1[2], a1[3]), widen8<B5>(b1[2], b1[3]), d, 0, 0, 0);
-  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[i], b.x[i], d, 0, 0, 0);
   return d;
 }
 
@@ -330,115 +342,134 @@ __device__ __forceinline__ void store_c(const GemmArgs &g, int i, int j, float v
   }
 }
 
-// Eight consecutive rows of a column from row i.
+// Eight consecutive rows of a column from row i, all of them C's, as vectors of
+// any alignment (2501 x 1111 x 1792 of odd columns: 14.7 us, element by element
+// through LDS 15.7, 2560 x 1152 x 1792 of aligned ones 13.3).
 __device__ __forceinline__ void store_c8(const GemmArgs &g, int i, int j, const float (&v)[8]) {
-  if (!g.vec || i + 8 > g.m) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (i + e < g.m) store_c(g, i + e, j, v[e]);
-    return;
-  }
   const int64_t at = (int64_t)j * g.ldc + i;
-  float x[8];
+  const bool add = g.beta != 0.0f;
   if (g.dt == TLR_F32) {
-    f4 *p = reinterpret_cast<f4 *>(static_cast<float *>(g.c) + at);
-    f4 lo = f4{0, 0, 0, 0}, hi = f4{0, 0, 0, 0};
-    if (g.beta != 0.0f) { lo = p[0]; hi = p[1]; }
+    float *p = static_cast<float *>(g.c) + at, x[8];
+    if (add) __builtin_memcpy(x, p, 32);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = g.beta != 0.0f ? v[e] * g.alpha + g.beta * (e < 4 ? lo[e & 3] : hi[e & 3]) : v[e] * g.alpha;
-    p[0] = f4{x[0], x[1], x[2], x[3]};
-    p[1] = f4{x[4], x[5], x[6], x[7]};
-    return;
-  }
-  u4 *p = reinterpret_cast<u4 *>(static_cast<uint16_t *>(g.c) + at);
-  u4 old = u4{0, 0, 0, 0};
-  if (g.beta != 0.0f) old = *p;
-  if (g.dt == TLR_F16) {
-    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-    const h8 o = __builtin_bit_cast(h8, old);
-    h8 y;
+    for (int e = 0; e < 8; ++e) x[e] = add ? v[e] * g.alpha + g.beta * x[e] : v[e] * g.alpha;
+    __builtin_memcpy(p, x, 32);
+  } else if (g.dt == TLR_F16) {
+    _Float16 *p = static_cast<_Float16 *>(g.c) + at, x[8];
+    if (add) __builtin_memcpy(x, p, 16);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (_Float16)(g.beta != 0.0f ? v[e] * g.alpha + g.beta * (float)o[e] : v[e] * g.alpha);
-    *p = __builtin_bit_cast(u4, y);
+    for (int e = 0; e < 8; ++e) x[e] = (_Float16)(add ? v[e] * g.alpha + g.beta * (float)x[e] : v[e] * g.alpha);
+    __builtin_memcpy(p, x, 16);
   } else {
-    const b8v o = __builtin_bit_cast(b8v, old);
-    b8v y;
+    __bf16 *p = static_cast<__bf16 *>(g.c) + at, x[8];
+    if (add) __builtin_memcpy(x, p, 16);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (__bf16)(g.beta != 0.0f ? v[e] * g.alpha + g.beta * (float)o[e] : v[e] * g.alpha);
-    *p = __builtin_bit_cast(u4, y);
+    for (int e = 0; e < 8; ++e) x[e] = (__bf16)(add ? v[e] * g.alpha + g.beta * (float)x[e] : v[e] * g.alpha);
+    __builtin_memcpy(p, x, 16);
   }
 }
 
-// Few columns: a workgroup computes 16 rows of A against NJ x 16 rows of B, its
-// eight waves taking every eighth block of the contraction; fragments come
-// straight from global memory and the partial sums meet in LDS.
-template <bool A5, bool B5, bool FAST, int NJ>
-__global__ __launch_bounds__(512) void strip_kernel(GemmArgs g) {
-  constexpr int W = 8;
-  __shared__ float part[W][NJ][4][64];
+// Few columns or little work: a workgroup computes 16 rows of A against 16 rows
+// of B, its eight waves taking every eighth block of the contraction; fragments
+// come straight from global memory, UNROLL blocks in flight a wave, and the
+// partial sums meet in LDS.  AB: A's blocks are 128 rows high.
+template <bool A5, bool B5, bool FAST, bool AB>
+__global__ __launch_bounds__(512, 4) void strip_kernel(GemmArgs g) {
+  constexpr int W = 8, SA = AB ? 1 : 4, UNROLL = AB ? 4 : 2;      // 128 registers each way
+  __shared__ float part[W][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int m0 = blockIdx.x * 16, n0 = blockIdx.y * 16 * NJ;
-  const int ar = min(m0 + r, g.m - 1);
-  const uint8_t *arow = g.a.codes + (int64_t)ar * g.a.ld;
-  const uint8_t *brow[NJ];
-  const float *bs[NJ];
+  const int m0 = blockIdx.x * 16, n0 = blockIdx.y * 16;
+  const uint8_t *arow = g.a.codes + (int64_t)min(m0 + r, g.m - 1) * g.a.ld + 16 * q;
+  const int br = min(n0 + r, g.n - 1);
+  const uint8_t *brow = g.b.codes + (int64_t)br * g.b.ld + 16 * q;
+  const float *as[SA], *bs = g.b.scales + (br >> g.b.shift);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int br = min(n0 + 16 * j + r, g.n - 1);
-    brow[j] = g.b.codes + (int64_t)br * g.b.ld;
-    bs[j] = g.b.scales + (br >> g.b.shift);
-  }
-  const float *as[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) as[v] = g.a.scales + (min(m0 + 4 * q + v, g.m - 1) >> g.a.shift);
+  for (int v = 0; v < SA; ++v) as[v] = g.a.scales + (AB ? m0 >> 7 : min(m0 + 4 * q + v, g.m - 1));
 
-  f4 acc[NJ];
+  f4 acc = f4{0, 0, 0, 0};
+  struct Block {
+    u4 a[2], b[2];
+    float sa[SA], sb;
+  };
+  auto scales = [&](int kb, Block &x) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) acc[j] = f4{0, 0, 0, 0};
-  const int nb = (g.k + QB - 1) / QB;
-  for (int kb = wave; kb < nb; kb += W) {
-    const int c = kb * QB + 16 * q;
-    const u4 a0 = load16(arow, c, g.k), a1 = load16(arow, c + 64, g.k);
-    float sa[4];
+    for (int v = 0; v < SA; ++v) x.sa[v] = as[v][kb * g.a.lds];
+    x.sb = bs[kb * g.b.lds];
+  };
+  auto load = [&](int kb, Block &x) {
+    const int64_t c = (int64_t)kb * QB;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) sa[v] = as[v][kb * g.a.lds];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const u4 b0 = load16(brow[j], c, g.k), b1 = load16(brow[j], c + 64, g.k);
-      const float sb = bs[j][kb * g.b.lds];
-      const f4 d = mma<A5, B5, FAST>(a0, a1, b0, b1);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[j][v] = __builtin_fmaf(sa[v] * sb, d[v], acc[j][v]);
+    for (int h = 0; h < 2; ++h) {
+      x.a[h] = *reinterpret_cast<const u4 *>(arow + c + 64 * h);
+      x.b[h] = *reinterpret_cast<const u4 *>(brow + c + 64 * h);
     }
+    scales(kb, x);
+  };
+  auto add = [&](const Block &x) {
+    const f4 d = mma<A5, B5>(Fragment<A5, FAST>(join(x.a[0], x.a[1])), Fragment<B5, FAST>(join(x.b[0], x.b[1])));
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(x.sa[AB ? 0 : v] * x.sb, d[v], acc[v]);
+  };
+  const int full = g.k / QB;
+  int kb = wave;
+  for (; kb + (UNROLL - 1) * W < full; kb += UNROLL * W) {
+    Block x[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) load(kb + u * W, x[u]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) add(x[u]);
+  }
+  for (; kb < full; kb += W) {
+    Block x;
+    load(kb, x);
+    add(x);
+  }
+  if (kb == full && g.k > full * QB) {          // the cut block
+    Block x;
+    const int64_t o = (int64_t)full * QB - 16 * q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x.a[h] = load16(arow + o, 16 * q + 64 * h, g.k - full * QB);
+      x.b[h] = load16(brow + o, 16 * q + 64 * h, g.k - full * QB);
+    }
+    scales(full, x);
+    add(x);
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) part[wave][j][v][lane] = acc[j][v];
+  for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[v];
   __syncthreads();
-  for (int x = threadIdx.x; x < NJ * 256; x += 512) {
-    const int i = x & 15, j = x >> 4;      // row, column of the workgroup's block
+  if (threadIdx.x < 256) {
+    const int i = threadIdx.x & 15, j = threadIdx.x >> 4;      // row, column of the workgroup's block
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += part[w][j >> 4][i & 3][(i >> 2) * 16 + (j & 15)];
+    for (int w = 0; w < W; ++w) v += part[w][i & 3][(i >> 2) * 16 + j];
     if (m0 + i < g.m && n0 + j < g.n) store_c(g, m0 + i, n0 + j, v);
   }
 }
 
 // ---- product, tiles ----------------------------------------------------------------------------------
 
-// Loads through a buffer descriptor: lanes at or past its size write zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00027000);
+// Buffer descriptor of `bytes` bytes: reads at or past them give zeros.
+__device__ __forceinline__ u4 buffer(const void *p, int32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return u4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, (uint32_t)bytes, 0x00027000u};
 }
-typedef __attribute__((address_space(3))) void *lds_ptr;
-__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t b, uint32_t at, void *lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 16, at, 0, 0, 0);
+
+// Loads from a lane's offset in a descriptor, moved by the uniform `by`, straight
+// into LDS: lane l writes its 16 (4) bytes at lds + 16 (4) l.  Written out, with
+// no register for a result, since the compiler, where it issues them, has LDS
+// reads wait for them; the stage loop does the waiting.  Nothing else here uses
+// m0.
+__device__ __forceinline__ void to_lds16(u4 b, uint32_t at, uint32_t by, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" : : "s"(lds), "v"(at), "s"(b), "s"(by) : "memory");
 }
-__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t b, uint32_t at, void *lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 4, at, 0, 0, 0);
+__device__ __forceinline__ void to_lds4(u4 b, uint32_t at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(lds), "v"(at), "s"(b) : "memory");
 }
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_byte *)p; }
 
 // LDS rows are a block's 128 codes, unpadded (the loads write 64 lanes x 16
 // bytes in a row); chunk c of a row stands at chunk c ^ key, so that the 16
@@ -455,47 +486,62 @@ template <int ROWS, int T, bool IS_A> struct Panel {
   int32_t bytes;            // from there to the end of the last readable chunk
   int32_t step;             // from one step to the next
   uint32_t at;              // this thread's first chunk in column block 0
+  u4 rows[N];               // descriptors of the rows from step i on: the steps share `at`
   __device__ __forceinline__ void init(const Operand &o, int r0, int k, int tid) {
     base = o.codes + (int64_t)r0 * o.ld;
     bytes = (min(ROWS, o.rows - r0) - 1) * (int32_t)o.ld + ((k + 15) & ~15);
     step = (T / 8) * (int32_t)o.ld;
     at = (uint32_t)(tid >> 3) * (uint32_t)o.ld + chunk(tid);
+#pragma unroll
+    for (int i = 0; i < N; ++i) rows[i] = buffer(base + i * step, max(bytes - i * step, 0));
   }
   static __device__ __forceinline__ int chunk(int tid) {
     return 16 * ((tid & 7) ^ (IS_A ? a_key(tid >> 3) : b_key(tid >> 3)));
   }
-  // a descriptor of the rows from step i on: the steps share one address register
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int kb, int i) const {
-    const int32_t o = kb * QB + i * step;
-    return buffer(base + o, max(bytes - o, 0));
-  }
-  __device__ __forceinline__ void load(int kb, uint8_t *lds, int wave) const {
+  // a whole column block (rows past the operand's give zeros)
+  __device__ __forceinline__ void load(int kb, uint32_t lds, int wave) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) to_lds16(rows(kb, i), at, lds + (i * T + wave * 64) * 16);
+    for (int i = 0; i < N; ++i) to_lds16(rows[i], at, kb * QB, lds + (i * T + wave * 64) * 16);
   }
-  // the last column block, whose columns from `left` on read as zero
-  __device__ __forceinline__ void load_cut(int kb, int left, uint8_t *lds, int tid) const {
-    u4 x[N];
+  // the last column block (its descriptors end with the operand)
+  __device__ __forceinline__ void load_last(int kb, uint32_t lds, int wave) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rows(kb, i), at, 0, 0));
+    for (int i = 0; i < N; ++i) {
+      const int32_t o = kb * QB + i * step;
+      to_lds16(buffer(base + o, max(bytes - o, 0)), at, 0, lds + (i * T + wave * 64) * 16);
+    }
+  }
+  // zeros in a stage's columns from `left` on
+  static __device__ __forceinline__ void cut(int left, uint8_t *lds, int tid) {
+    left -= chunk(tid);
+    if (left >= 16) return;
     u4 keep;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int n = left - chunk(tid) - 4 * w;
+      const int n = left - 4 * w;
       keep[w] = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : 0xffffffffu >> (32 - 8 * n);
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<u4 *>(lds + (i * T + tid) * 16) = x[i] & keep;
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u4 *>(lds + (i * T + tid) * 16) &= keep;
   }
 };
 
-// C tiles of TM x TN, WM x WN waves.  AB: A's blocks are 128 rows high (a wave's
-// rows lie in one of them, or in two halves).
+// C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16.  AB: A's
+// blocks are 128 rows high (a wave's rows lie in one of them).
+//
+// Two stages of one column block each in LDS.  A wave goes through a stage row
+// tile by row tile; with the last one's matrix instructions under way it waits
+// for the next stage, has the one after it loaded into the buffer that is now
+// used up, and reads its first fragments of the next: one barrier a stage, and
+// the matrix cores have work on both sides of it.
 template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(GemmArgs g) {
   constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
-  __shared__ __attribute__((aligned(16))) uint8_t a0[TM * QB], a1[TM * QB], b0[TN * QB], b1[TN * QB];
-  __shared__ __attribute__((aligned(16))) float s0[TM + TN], s1[TM + TN];
+  static_assert(RI % 2 == 0 && (!AB || 128 % (TM / WM) == 0), "");
+  // a stage: A's codes, B's codes, A's and B's scales
+  constexpr int SN = (TM + TN + T - 1) / T;                // scales a thread loads
+  constexpr int AT_B = TM * QB, AT_S = (TM + TN) * QB, STAGE = AT_S + SN * T * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
 
@@ -515,24 +561,30 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   Panel<TN, T, false> pb;
   pa.init(g.a, m0, g.k, tid);
   pb.init(g.b, n0, g.k, tid);
-  // scales: TM + TN floats a stage, 64 a wave and step
-  constexpr int SN = (TM + TN) / T;
-  static_assert((TM + TN) % T == 0 && TM % 64 == 0, "");
-  auto load_scales = [&](int kb, float *ls) {
+  // scales: TM + TN floats a stage, 64 a wave and step (the waves past them write zeros)
+  const float *sbase[SN];
+  int64_t sld[SN];
+  int32_t sbytes[SN];
+  uint32_t sat[SN];
 #pragma unroll
-    for (int i = 0; i < SN; ++i) {
-      const int w = i * T + wave * 64;
-      const bool isa = w < TM;
-      const Operand &o = isa ? g.a : g.b;
-      const int r0 = isa ? m0 : n0, at = (isa ? w : w - TM) + lane;
-      const int first = r0 >> o.shift, n = ((min(r0 + (isa ? TM : TN), o.rows) - 1) >> o.shift) - first + 1;
-      to_lds4(buffer(o.scales + kb * o.lds + first, 4 * n), 4 * (((r0 + at) >> o.shift) - first), ls + w);
-    }
+  for (int i = 0; i < SN; ++i) {
+    const int w = i * T + wave * 64;
+    const bool isa = w < TM;
+    const Operand &o = isa ? g.a : g.b;
+    const int r0 = isa ? m0 : n0, first = r0 >> o.shift;
+    sbase[i] = o.scales + first;
+    sld[i] = o.lds;
+    sbytes[i] = w < TM + TN ? 4 * (((min(r0 + (isa ? TM : TN), o.rows) - 1) >> o.shift) - first + 1) : 0;
+    sat[i] = 4 * (((r0 + (isa ? w : w - TM) + lane) >> o.shift) - first);
+  }
+  auto load_scales = [&](int kb, uint32_t ls) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i) to_lds4(buffer(sbase[i] + kb * sld[i], sbytes[i]), sat[i], ls + 4 * (i * T + wave * 64));
   };
-  auto load = [&](int kb, uint8_t *la, uint8_t *lb, float *ls) {
-    load_scales(kb, ls);
-    pa.load(kb, la, wave);
-    pb.load(kb, lb, wave);
+  auto load = [&](int kb, uint32_t to) {
+    load_scales(kb, to + AT_S);
+    pa.load(kb, to, wave);
+    pb.load(kb, to + AT_B, wave);
   };
 
   f4 acc[RI][CJ];
@@ -545,49 +597,35 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   // 32 h + 8 (r / 4) + 4 p + r % 4, so that the two tiles of a pair leave 8
   // consecutive rows of C in one lane.
   const int ar = wm * (TM / WM) + 8 * (r >> 2) + (r & 3), br = wn * (TN / WN) + r;
-  const int aat = ar * QB + 16 * (q ^ a_key(ar)), bat = br * QB + 16 * (q ^ b_key(br));
-
-  auto compute = [&](const uint8_t *la, const uint8_t *lb, const float *ls) {
-    u4 bf[CJ][2];
-    float sb[CJ];
+  const int aat = ar * QB + 16 * (q ^ a_key(ar)), bat = AT_B + br * QB + 16 * (q ^ b_key(br));
+  i8v x[2], b[CJ];            // of row tile i (mod 2) and of the stage's columns
+  f4 sa[2];                   // scales of the lane's rows of row tile i (AB: in sb)
+  float sb[CJ], sn[CJ];       // of its columns, and those of the next stage
+  auto read_a = [&](const uint8_t *l, int i) {
+    const int o = (i >> 1) * 32 * QB + (i & 1) * 4 * QB;
+    x[i & 1] = join(*reinterpret_cast<const u4 *>(l + aat + o), *reinterpret_cast<const u4 *>(l + (aat ^ 64) + o));
+  };
+  auto read_sa = [&](const uint8_t *l, int i) {
+    if constexpr (!AB)
+      sa[i & 1] = *reinterpret_cast<const f4 *>(l + AT_S + 4 * (wm * (TM / WM) + (i >> 1) * 32 + 8 * q + 4 * (i & 1)));
+  };
+  auto read_b = [&](const uint8_t *l) {
 #pragma unroll
     for (int j = 0; j < CJ; ++j) {
-      bf[j][0] = *reinterpret_cast<const u4 *>(lb + bat + 16 * QB * j);
-      bf[j][1] = *reinterpret_cast<const u4 *>(lb + (bat ^ 64) + 16 * QB * j);
-      sb[j] = ls[TM + br + 16 * j];
+      b[j] = join(*reinterpret_cast<const u4 *>(l + bat + 16 * QB * j), *reinterpret_cast<const u4 *>(l + (bat ^ 64) + 16 * QB * j));
+      sn[j] = *reinterpret_cast<const float *>(l + AT_S + 4 * (TM + br + 16 * j));
     }
     if constexpr (AB) {
-      const float s = ls[wm * (TM / WM)];
+      const float s = *reinterpret_cast<const float *>(l + AT_S + 4 * wm * (TM / WM));
 #pragma unroll
-      for (int j = 0; j < CJ; ++j) sb[j] *= s;
+      for (int j = 0; j < CJ; ++j) sn[j] *= s;
     }
-    // Row tile by row tile: the next one's fragment is read and the last one's
-    // results are added while the matrix instructions of this one run.
-    auto frag = [&](int i, u4 (&x)[2]) {
-      const int o = (i >> 1) * 32 * QB + (i & 1) * 4 * QB;
-      x[0] = *reinterpret_cast<const u4 *>(la + aat + o);
-      x[1] = *reinterpret_cast<const u4 *>(la + (aat ^ 64) + o);
-    };
-    auto add = [&](int i, const f4 (&d)[CJ]) {
-      f4 sa;
-      if constexpr (!AB) sa = *reinterpret_cast<const f4 *>(ls + wm * (TM / WM) + (i >> 1) * 32 + 8 * q + 4 * (i & 1));
+  };
+  auto add = [&](int i, const f4 (&d)[CJ]) {
 #pragma unroll
-      for (int j = 0; j < CJ; ++j)
+    for (int j = 0; j < CJ; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(AB ? sb[j] : sa[v] * sb[j], d[j][v], acc[i][j][v]);
-    };
-    u4 x[2][2];
-    f4 d[2][CJ];
-    frag(0, x[0]);
-#pragma unroll
-    for (int i = 0; i < RI; ++i) {
-      if (i + 1 < RI) frag(i + 1, x[(i + 1) & 1]);
-#pragma unroll
-      for (int j = 0; j < CJ; ++j) d[i & 1][j] = mma<A5, B5, FAST>(x[i & 1][0], x[i & 1][1], bf[j][0], bf[j][1]);
-      if (i > 0) add(i - 1, d[(i - 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    add(RI - 1, d[(RI - 1) & 1]);
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(AB ? sb[j] : sa[i & 1][v] * sb[j], d[j][v], acc[i][j][v]);
   };
   auto meet = [&]() {
     asm volatile("" ::: "memory");
@@ -596,62 +634,221 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     asm volatile("" ::: "memory");
   };
 
-  // Stage 0 is the last column block, which may be cut at column k; stage i > 0
-  // is column block i - 1.  Stages alternate between the buffers, the last one
-  // is in the second.
-  const int nb = (g.k + QB - 1) / QB;
-  bool second = nb & 1;
-  load_scales(nb - 1, second ? s1 : s0);
-  if (g.k & (QB - 1)) {
-    pa.load_cut(nb - 1, g.k & (QB - 1), second ? a1 : a0, tid);
-    pb.load_cut(nb - 1, g.k & (QB - 1), second ? b1 : b0, tid);
+  // This workgroup's column blocks: all, or the part of grid y.  Stage 0 is its
+  // last one, which may be cut at column k; stage i > 0 is block kb0 + i - 1.
+  const int blocks = (g.k + QB - 1) / QB;
+  const int kb0 = (int)((int64_t)blocks * blockIdx.y / gridDim.y);
+  const int nb = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
+  const bool cut = (g.k & (QB - 1)) != 0 && kb0 + nb == blocks;
+  const uint32_t base = lds_address(lds);
+  load_scales(kb0 + nb - 1, base + AT_S);
+  pa.load_last(kb0 + nb - 1, base, wave);
+  pb.load_last(kb0 + nb - 1, base + AT_B, wave);
+  if (nb > 1) {
+    load(kb0, base + STAGE);
+    constexpr int LOADS = Panel<TM, T, true>::N + Panel<TN, T, false>::N + SN;      // of stage 1, still under way
+    static_assert(LOADS < 16, "");
+    __builtin_amdgcn_s_waitcnt(LOADS | 0xf << 8 | 7 << 4);
   } else {
-    pa.load(nb - 1, second ? a1 : a0, wave);
-    pb.load(nb - 1, second ? b1 : b0, wave);
+    __builtin_amdgcn_s_waitcnt(0);
   }
-  meet();
-  int kb = 0;               // column block of the next stage to load
-  do {
-    if (!second) {
-      load(kb++, a1, b1, s1);
-      compute(a0, b0, s0);
-      meet();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (cut) {
+    pa.cut(g.k & (QB - 1), lds, tid);
+    pb.cut(g.k & (QB - 1), lds + AT_B, tid);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);      // LDS only
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  read_b(lds);
+  read_a(lds, 0);
+  f4 d[2][CJ];
+  auto row_tiles = [&](const uint8_t *l) {     // all sums of a stage but the last row tile's
+    Fragment<B5, FAST> bf[CJ];
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) {
+      sb[j] = sn[j];
+      bf[j] = Fragment<B5, FAST>(b[j]);
     }
-    second = false;
-    if (kb < nb - 1) load(kb, a0, b0, s0);
-    compute(a1, b1, s1);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      if (i + 1 < RI) read_a(l, i + 1);
+      read_sa(l, i);
+      const Fragment<A5, FAST> af(x[i & 1]);
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) d[i & 1][j] = mma<A5, B5>(af, bf[j]);
+      if (i > 0) add(i - 1, d[(i - 1) & 1]);
+      // here, not where the sums are next used: sunk there past the branches
+      // below, they would keep every d in registers
+      if (i > 0)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) asm volatile("" : "+v"(acc[i - 1][j]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int now = 0, next = STAGE;
+  for (int stage = 0; stage < nb - 1; ++stage) {
+    row_tiles(lds + now);
     meet();
-  } while (kb++ < nb - 1);
+    if (stage + 2 < nb) load(kb0 + stage + 1, base + now);
+    read_b(lds + next);
+    read_a(lds + next, 0);
+    add(RI - 1, d[1]);
+    const int t = now;
+    now = next;
+    next = t;
+  }
+  row_tiles(lds + now);
+  add(RI - 1, d[1]);
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
+  if (gridDim.y > 1) g.c = static_cast<float *>(g.c) + (int64_t)blockIdx.y * g.m * g.n;      // a part's sums
+  constexpr int ROWS = TM / WM;
+  const int row0 = m0 + wm * ROWS, col0 = n0 + wn * (TN / WN);
 #pragma unroll
   for (int j = 0; j < CJ; ++j) {
-    const int col = n0 + wn * (TN / WN) + 16 * j + r;
+    const int col = col0 + 16 * j + r;
     if (col < g.n)
 #pragma unroll
       for (int h = 0; h < RI / 2; ++h) {
-        const int row = m0 + wm * (TM / WM) + 32 * h + 8 * q;
+        const int row = row0 + 32 * h + 8 * q;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[2 * h + (e >> 2)][j][e & 3];
-        store_c8(g, row, col, v);
+        if (row + 8 <= g.m) store_c8(g, row, col, v);
+        else if (row < g.m)
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (row + e < g.m) store_c(g, row + e, col, v[e]);
       }
   }
 }
 
-template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN> void tile_launch(const GemmArgs &g, hipStream_t st) {
-  const unsigned grid = (unsigned)((g.m + TM - 1) / TM) * (unsigned)((g.n + TN - 1) / TN);
-  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
-  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
+// C = alpha (sum of PARTS m x n matrices of floats, in their order) + beta C: a
+// thread takes 8 consecutive rows of a column.
+template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(GemmArgs g, const float *part) {
+  const int up = (g.m + 7) / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int j = (int)(at / up), i = 8 * (int)(at - (int64_t)j * up);
+  if (j >= g.n) return;
+  const float *p = part + (int64_t)j * g.m + i;
+  const int64_t step = (int64_t)g.m * g.n;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (i + 8 <= g.m) {
+    float x[PARTS][8];
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) __builtin_memcpy(x[z], p + z * step, 32);
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += x[z][e];
+    store_c8(g, i, j, v);
+    return;
+  }
+  for (int e = 0; i + e < g.m; ++e) {
+    float s = 0.0f;
+    for (int z = 0; z < PARTS; ++z) s += p[z * step + e];
+    store_c(g, i + e, j, s);
+  }
 }
 
-template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, hipStream_t st) {
-  const unsigned gx = (unsigned)((g.m + 15) / 16);
-  if (g.n <= 16) strip_kernel<A5, B5, FAST, 1><<<dim3(gx, 1), 512, 0, st>>>(g);
-  else if (g.n <= 32) strip_kernel<A5, B5, FAST, 2><<<dim3(gx, 1), 512, 0, st>>>(g);
-  else if (g.n <= 64) strip_kernel<A5, B5, FAST, 4><<<dim3(gx, (g.n + 63) / 64), 512, 0, st>>>(g);
-  else if ((int64_t)((g.m + 255) / 256) * ((g.n + 255) / 256) >= 192) tile_launch<A5, B5, FAST, 256, 256, 2, 4>(g, st);
-  else tile_launch<A5, B5, FAST, 128, 128, 2, 2>(g, st);
+// ---- which kernel -----------------------------------------------------------------------------------
+
+enum Kind { STRIP, TILE_64, TILE_128, TILE_128W, TILE_256 };
+struct Choice {
+  Kind kind;
+  int parts;                // of the contraction, with a launch that adds them if more than one
+};
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The kernel with the least estimated time (us).  Each estimate is a fit to
+// measured times (graph replays, 16-bit C with `fast`, float C of e4m3 and e5m2
+// operands without).  Some of them, the kernel chosen first:
+//   fast   512 x 20 x 512       strip 2.9, 128 x 64 tiles 4.6
+//          8192 x 1 x 4096      strip 7.9, 128 x 64 tiles 20.0, four parts 11.2
+//          1024 x 1024 x 1024   128 x 64 tiles 6.4, 128 x 128 8.4, strip 20.5
+//          8192 x 64 x 8192     128 x 64 tiles in four parts 19.7, one 37.7, strip 60.2
+//          2048 x 2048 x 512    128 x 128 on eight waves 7.3, on four 8.1, 256 x 256 13.3
+//          2048 x 4096 x 2048   128 x 128 on four waves 23.3, on eight 27.2, 256 x 256 31.5
+//          4096 x 4096 x 4096   256 x 256 tiles 63.0, 128 x 128 76.5
+//   exact  1024 x 1024 x 1024   128 x 64 tiles 9.4, 128 x 128 13.2, strip 23.0
+//          4096 x 4096 x 8192   128 x 128 on four waves 247, on eight 295, 256 x 256 (not kept) 307
+Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
+  const double nb = (double)cdiv(k, QB);
+  Choice best{TILE_128, 1};
+  double least = 1e300;
+  auto offer = [&](Kind kind, int parts, double t) {
+    if (t < least) {
+      least = t;
+      best = Choice{kind, parts};
+    }
+  };
+  // 4 KB a workgroup and block out of the caches
+  if (cdiv(n, 16) <= 65535) offer(STRIP, 1, 2.8 + cdiv(m, 16) * cdiv(n, 16) * nb * (fast ? 0.00040 : 0.00048));
+  // One workgroup a CU takes `one` a column block, two together `two`.
+  auto tiles = [&](Kind kind, int tn, double one, double two, double first, double next) {
+    for (const int parts : {1, 2, 4, 8}) {
+      if (parts > 1 && nb < 4 * parts) break;
+      const double t = (double)cdiv(m, 128) * (double)cdiv(n, tn) * parts;
+      const double rounds = std::ceil(t / 512), rest = t - 512 * (rounds - 1);
+      double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
+      if (parts > 1) us += 3.0 + parts * (double)m * (double)n * 2.5e-6;
+      offer(kind, parts, us);
+    }
+  };
+  if (fast) {
+    tiles(TILE_64, 64, 0.57, 1.15, 3.2, 3.0);
+    tiles(TILE_128W, 128, 0.66, 1.43, 4.0, 4.0);
+    tiles(TILE_128, 128, 0.70, 1.10, 5.0, 5.0);
+    const double rounds = std::ceil((double)cdiv(m, 256) * (double)cdiv(n, 256) / 256);
+    offer(TILE_256, 1, 6.0 + (rounds - 1) * 4.0 + nb * rounds * 1.8);
+  } else {
+    tiles(TILE_64, 64, 0.75, 1.6, 3.5, 3.0);
+    tiles(TILE_128W, 128, 1.2, 2.2, 4.0, 4.0);
+    tiles(TILE_128, 128, 1.25, 1.85, 5.0, 5.0);
+  }
+  return best;
+}
+
+template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN>
+void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
+  const dim3 grid((unsigned)(cdiv(g.m, TM) * cdiv(g.n, TN)), (unsigned)parts);
+  GemmArgs h = g;
+  if (parts > 1) {
+    h.alpha = 1.0f;
+    h.beta = 0.0f;
+    h.c = ws;
+    h.ldc = g.m;
+    h.dt = TLR_F32;
+  }
+  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(h);
+  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(h);
+  if (parts == 1) return;
+  const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
+  if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
+  else if (parts == 4) parts_kernel<4><<<sum, 256, 0, st>>>(g, ws);
+  else parts_kernel<8><<<sum, 256, 0, st>>>(g, ws);
+}
+
+template <bool A5, bool B5, bool FAST> void strip_launch(const GemmArgs &g, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(g.m, 16), (unsigned)cdiv(g.n, 16));
+  if (g.a.shift) strip_kernel<A5, B5, FAST, true><<<grid, 512, 0, st>>>(g);
+  else strip_kernel<A5, B5, FAST, false><<<grid, 512, 0, st>>>(g);
+}
+
+template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, float *ws, hipStream_t st) {
+  const Choice c = choose(g.m, g.n, g.k, FAST);
+  switch (c.kind) {
+    case STRIP: return strip_launch<A5, B5, FAST>(g, st);
+    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4>(g, c.parts, ws, st);
+    case TILE_256:
+      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4>(g, c.parts, ws, st);
+  }
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -735,6 +932,11 @@ tlr_status block_gemm_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes) 
   if (m < 0 || n < 0 || k < 0 || m > SIZE_LIM || n > SIZE_LIM || k > SIZE_LIM)
     return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: size out of range");
   *bytes = 0;
+  if (m > 0 && n > 0 && k > 0)
+    for (const bool fast : {false, true}) {
+      const Choice c = choose(m, n, k, fast);
+      if (c.parts > 1) *bytes = std::max(*bytes, sizeof(float) * (size_t)c.parts * m * n);
+    }
   return TLR_OK;
 }
 
@@ -772,15 +974,15 @@ tlr_status block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alph
   g.c = C;
   g.ldc = ldc;
   g.dt = dt;
-  g.vec = aligned(C, 16) && ldc * (dt == TLR_F32 ? 4 : 2) % 16 == 0;
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  float *part = static_cast<float *>(ws);
   const bool a5 = A->fmt == TLR_E5M2, b5 = B->fmt == TLR_E5M2;
   if (flags & TLR_BLOCK_FAST) {
-    if (a5) b5 ? gemm_launch<true, true, true>(g, hs) : gemm_launch<true, false, true>(g, hs);
-    else b5 ? gemm_launch<false, true, true>(g, hs) : gemm_launch<false, false, true>(g, hs);
+    if (a5) b5 ? gemm_launch<true, true, true>(g, part, hs) : gemm_launch<true, false, true>(g, part, hs);
+    else b5 ? gemm_launch<false, true, true>(g, part, hs) : gemm_launch<false, false, true>(g, part, hs);
   } else {
-    if (a5) b5 ? gemm_launch<true, true, false>(g, hs) : gemm_launch<true, false, false>(g, hs);
-    else b5 ? gemm_launch<false, true, false>(g, hs) : gemm_launch<false, false, false>(g, hs);
+    if (a5) b5 ? gemm_launch<true, true, false>(g, part, hs) : gemm_launch<true, false, false>(g, part, hs);
+    else b5 ? gemm_launch<false, true, false>(g, part, hs) : gemm_launch<false, false, false>(g, part, hs);
   }
   return launched("block_gemm");
 }

@@ -220,6 +220,38 @@ def test_product_of_large_tiles(m, n, k, bfmt, ablk, dtype, fast):
     assert torch.equal(got, blocks.gemm(A, B, dtype=dtype, fast=fast))
 
 
+@pytest.mark.parametrize("m,n,k", [(300, 64, 8000), (517, 90, 4100), (300, 300, 8072), (1300, 70, 5000), (2100, 1030, 520),
+                                   (2600, 3001, 300), (5003, 301, 130), (260, 2050, 4000), (777, 6000, 259)])
+@pytest.mark.parametrize("bfmt,ablk,dtype,fast", [("e4m3", 128, "bf16", True), ("e5m2", 1, "f32", False),
+                                                  ("e5m2", 1, "f16", True), ("e4m3", 128, "bf16", False)])
+def test_product_of_few_tiles_and_in_parts(m, n, k, bfmt, ablk, dtype, fast):
+    """Shapes between the strips and the large tiles, long contractions whose parts are added among them.  The bounds of
+    check_product and test_fast_product; up to eight parts add as many float additions."""
+    from hpc_linear_algebra_amd import blocks
+    A, a = codes(m, k, "e4m3", ablk, m + n)
+    B, b = codes(n, k, bfmt, 1, m + n + 1, pad=32)
+    big = torch.zeros(n, m + 3, dtype=TD[dtype], device="cuda")
+    out = big[:, 1:m + 1]
+    blocks.gemm(A, B, out=out, fast=fast)
+    i, j = sorted({*range(0, m, 23), m - 1}), sorted({*range(0, n, 19), n - 1})
+    a, b, got = a[i], b[j], out[j][:, i].double().cpu().numpy()
+    ref, mag = b @ a.T, np.abs(b) @ np.abs(a).T
+    t = torch.finfo(TD[dtype])
+    tol = (min(k, 128) + k / 128 + 4 + 8) * 2.0 ** -24 * mag
+    if fast:
+        tol = tol + 2.0 ** -13 * largest(a, b, k)
+    tol = tol + t.eps / 2 * (np.abs(ref) + tol) + t.smallest_normal * t.eps
+    assert float(np.max(np.abs(got - ref) / tol)) <= 1.0
+    assert torch.isfinite(out).all() and not torch.any(big[:, 0]) and not torch.any(big[:, m + 1:])
+    again = torch.zeros_like(out)
+    blocks.gemm(A, B, out=again, fast=fast)
+    assert torch.equal(out, again)
+    blocks.gemm(A, B, out=again, alpha=0.5, beta=-1.0, fast=fast)
+    got = again[j][:, i].double().cpu().numpy()
+    prev = out[j][:, i].double().cpu().numpy()
+    assert float(np.max(np.abs(got - (0.5 * ref - prev)) / (0.5 * tol + t.eps / 2 * (0.5 * np.abs(ref) + np.abs(prev)) + tol))) <= 1.0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(33, 5, 200), (301, 90, 260), (520, 300, 384)])
 def test_product_adds_into_a_strided_unaligned_c(m, n, k, dtype):

@@ -26,11 +26,11 @@ FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _CODE = {torch.float8_e4m3fn: T.TLR_E4M3, torch.float8_e5m2: T.TLR_E5M2}
 _DT = {torch.float32: T.TLR_F32, torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
 _FMT = {"e4m3": T.TLR_E4M3, "e5m2": T.TLR_E5M2}
-_NONE = T.tlr_block_matrix()
 _TORCH = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream      # 0.1 us, the stream object's way 2.7
+_device = torch._C._cuda_getDevice                    # what torch.cuda.current_device asks once torch is set up
 
 
 def call(device: torch.device, f, *args) -> int:
@@ -38,7 +38,7 @@ def call(device: torch.device, f, *args) -> int:
     A decode step is bound by what the host does between launches: the guard is
     entered only where it changes something."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         return f(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return f(*args, _raw_stream(index))
@@ -57,7 +57,7 @@ class BlockScaled:
     block    rows of a block: 1 or 128
     """
 
-    __slots__ = ("codes", "scales", "rows", "k", "block", "c")
+    __slots__ = ("codes", "scales", "rows", "k", "block", "_c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, block: int):
         if codes.dtype not in _CODE or codes.dim() != 2:
@@ -76,7 +76,16 @@ class BlockScaled:
         if tuple(scales.shape) != (nq, nr) or (nr > 1 and scales.stride(1) != 1):
             raise ValueError(f"scales: shape {(nq, nr)}, rows contiguous, is needed")
         self.codes, self.scales, self.rows, self.k, self.block = codes, scales, rows, k, block
-        self.c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, lds, block, _CODE[codes.dtype])
+        self._c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, lds, block, _CODE[codes.dtype])
+
+    @property
+    def c(self) -> T.tlr_block_matrix:
+        """What the C ABI takes; made when a product first asks for it."""
+        if self._c is None:
+            codes, scales = self.codes, self.scales
+            self._c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), codes.shape[1], scales.shape[1], self.block,
+                                         _CODE[codes.dtype])
+        return self._c
 
     def dequantize(self) -> torch.Tensor:
         """The (rows, k) float32 matrix that the codes and scales stand for."""
@@ -86,15 +95,21 @@ class BlockScaled:
         return self.codes[:, :self.k].float() * s
 
 
-def _empty(rows: int, k: int, block: int, fmt: str, device) -> BlockScaled:
+def _empty(rows: int, k: int, block: int, dt: torch.dtype, device) -> BlockScaled:
     q = BlockScaled.__new__(BlockScaled)        # right by construction: the checks cost more than the launch
-    ld, nr = -(-k // 16) * 16, rows if block == 1 else -(-rows // BLOCK)
-    dt = FORMATS[fmt]
-    q.codes = codes = torch.empty((rows, ld), dtype=dt, device=device)
-    q.scales = scales = torch.empty((-(-k // BLOCK), nr), dtype=torch.float32, device=device)
-    q.rows, q.k, q.block = rows, k, block
-    q.c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, nr, block, _CODE[dt])
+    nr = rows if block == 1 else -(-rows // BLOCK)
+    q.codes = torch.empty((rows, -(-k // 16) * 16), dtype=dt, device=device)
+    q.scales = torch.empty((-(-k // BLOCK), nr), dtype=torch.float32, device=device)
+    q.rows, q.k, q.block, q._c = rows, k, block, None
     return q
+
+
+def _result(q: Optional[BlockScaled]):
+    """(codes, ld, scales, lds) of a result of _empty for the C ABI."""
+    if q is None:
+        return None, 0, None, 0
+    codes, scales = q.codes, q.scales
+    return codes.data_ptr() or None, codes.shape[1], scales.data_ptr() or None, scales.shape[1]
 
 
 def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool = True,
@@ -104,19 +119,23 @@ def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool 
     x is a 2-d float32, float16 or bfloat16 tensor whose rows are contiguous
     (any row stride).  block 1: a scale for every 128 entries of a row of the
     result; block 128: one for every 128 x 128 tile."""
-    if x.dim() != 2 or x.dtype not in _DT or not x.is_cuda:
+    dt = _DT.get(x.dtype)
+    if dt is None or x.dim() != 2 or not x.is_cuda:
         raise ValueError("quantize: a 2-d float32, float16 or bfloat16 tensor on a GPU is needed")
-    if fmt not in FORMATS or block not in (1, BLOCK) or not (straight or transposed):
+    f8 = FORMATS.get(fmt)
+    if f8 is None or block not in (1, BLOCK) or not (straight or transposed):
         raise ValueError("quantize: fmt is e4m3 or e5m2, block 1 or 128, and a result has to be wanted")
     rows, k = x.shape
-    if k > 1 and x.stride(1) != 1:
+    ldx, step = x.stride()
+    if k > 1 and step != 1:
         raise ValueError("quantize: the rows of x have to be contiguous")
-    a = _empty(rows, k, block, fmt, x.device) if straight else None
-    b = _empty(k, rows, block, fmt, x.device) if transposed else None
-    ldx = max(x.stride(0), k, 1) if rows <= 1 else x.stride(0)
-    p, q = a.c if a else _NONE, b.c if b else _NONE
-    st = call(x.device, _lib().tlr_block_quantize, _DT[x.dtype], _FMT[fmt], block, rows, k, x.data_ptr() or None, ldx,
-              p.codes, p.ld, p.scales, p.lds, q.codes, q.ld, q.scales, q.lds)
+    if rows <= 1:
+        ldx = max(ldx, k, 1)
+    device = x.device
+    a = _empty(rows, k, block, f8, device) if straight else None
+    b = _empty(k, rows, block, f8, device) if transposed else None
+    st = call(device, _lib().tlr_block_quantize, dt, _FMT[fmt], block, rows, k, x.data_ptr() or None, ldx, *_result(a),
+              *_result(b))
     if st:
         T._check(st, "tlr_block_quantize")
     return a, b

@@ -273,11 +273,6 @@ template <typename H> __global__ __launch_bounds__(256) void router_one_kernel(M
   }
   if (!arrive(a.arrived, gridDim.x, &last) || wave > 0) return;
   choose(a, 0, lane);
-  if (lane < a.topk) {                // no expert twice: nothing to sort
-    a.unit[lane] = int4{a.ids[lane], lane, 1, 0};
-    a.order[lane] = lane;
-  }
-  if (lane == 0) *a.units = a.topk;
 }
 
 constexpr int RW = 16;      // waves of a router workgroup
@@ -436,6 +431,17 @@ __device__ __forceinline__ void multiply(f4 (&acc)[RTILE][NJ], const uint8_t *co
   }
 }
 
+// silu(g) u as a sum of two numbers of the type: one would round the sum that
+// the down product takes to 8 or 11 bits.
+template <typename H> __device__ __forceinline__ void put_act(const MoeArgs &a, int64_t at, float g, float u) {
+  const float v = g / (1.0f + expf(-g)) * u;
+  const H hi = (H)v;
+  const float rest = v - (float)hi;
+  const H lo = (H)(__builtin_isfinite(rest) ? rest : 0.0f);     // beyond the type's range hi is infinite
+  a.hi[at] = __builtin_bit_cast(uint16_t, hi);
+  a.lo[at] = __builtin_bit_cast(uint16_t, lo);
+}
+
 constexpr int WV = 4;       // waves of an expert workgroup
 
 // silu(G x) * (U x) for 16 of an expert's inter rows and 16 NJ of its tokens.
@@ -478,13 +484,7 @@ __device__ __forceinline__ void gate_up(const MoeArgs &a, int4 unit, int n0, flo
         g += part[k][0][i & 3][at];
         u += part[k][1][i & 3][at];
       }
-      const float v = g / (1.0f + expf(-g)) * u;
-      const H hi = (H)v;
-      const float rest = v - (float)hi;
-      const H lo = (H)(__builtin_isfinite(rest) ? rest : 0.0f);     // beyond the type's range hi is infinite
-      const int64_t o = (int64_t)order[n0 + 16 * j + c] * a.inter + i0 + i;
-      a.hi[o] = __builtin_bit_cast(uint16_t, hi);
-      a.lo[o] = __builtin_bit_cast(uint16_t, lo);
+      put_act<H>(a, (int64_t)order[n0 + 16 * j + c] * a.inter + i0 + i, g, u);
     }
   }
 }
@@ -585,6 +585,138 @@ __global__ __launch_bounds__(64 * WV, W8 && RTILE == 2 ? 4 : 1) void down_kernel
   }
 }
 
+// 16 weights of a row as floats.
+template <typename H, bool W8> __device__ __forceinline__ void floats16(const u4 (&w)[W8 ? 1 : 2], float (&y)[16]) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    float z[8];
+    if constexpr (W8) {
+      typedef float f2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = (int)w[0][2 * b + i];
+        const f2 l = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), h = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+        z[4 * i] = l[0];
+        z[4 * i + 1] = l[1];
+        z[4 * i + 2] = h[0];
+        z[4 * i + 3] = h[1];
+      }
+    } else {
+      unpack8<H>(w[b], z);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[8 * b + i] = z[i];
+  }
+}
+
+// One token.  Its products are the weights' bytes and nothing else, and one
+// column of sixteen is all that the matrix cores would have, so they run in
+// float on the vector units, threads side by side along a row.
+
+// silu(G x) * (U x) of one choice: a wave takes ONE_PAIRS gate rows and their up
+// rows (2048 x 1024, 8 of 64 experts in bf16, the whole layer: 26.1 us with one
+// pair, 26.4 with two, 28.6 with four, 27.8 with the matrix kernel).
+constexpr int ONE_PAIRS = 1;
+template <typename H, bool W8> __global__ __launch_bounds__(256) void gate_up_one_kernel(MoeArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = (blockIdx.x * 4 + wave) * ONE_PAIRS, j = blockIdx.y, e = a.ids[j];
+  const int64_t slds = (2 * a.inter + 127) / 128, sblocks = (a.hidden + 127) / 128;
+  constexpr int N = W8 ? 1 : 2, ES = W8 ? 1 : 2;
+  float acc[ONE_PAIRS][2];
+#pragma unroll
+  for (int p = 0; p < ONE_PAIRS; ++p) acc[p][0] = acc[p][1] = 0.0f;
+#pragma unroll 1
+  for (int c = 16 * lane; c < a.hidden; c += 1024) {
+    u4 w[ONE_PAIRS][2][N];
+    float s[ONE_PAIRS][2];
+#pragma unroll
+    for (int p = 0; p < ONE_PAIRS; ++p)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int64_t row = (int64_t)g * a.inter + i0 + p;
+        const u4 *from = reinterpret_cast<const u4 *>(a.gate_up + (((int64_t)e * 2 * a.inter + row) * a.hidden + c) * ES);
+#pragma unroll
+        for (int b = 0; b < N; ++b) w[p][g][b] = from[b];
+        if constexpr (W8) s[p][g] = a.gate_up_scales[(e * sblocks + (c >> 7)) * slds + (row >> 7)];
+      }
+    const u4 x2[2] = {reinterpret_cast<const u4 *>(a.x + c)[0], reinterpret_cast<const u4 *>(a.x + c)[1]};
+    float x[16];
+    floats16<H, false>(x2, x);
+#pragma unroll
+    for (int p = 0; p < ONE_PAIRS; ++p)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float y[16], d = W8 ? 0.0f : acc[p][g];
+        floats16<H, W8>(w[p][g], y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d = __builtin_fmaf(y[i], x[i], d);
+        acc[p][g] = W8 ? __builtin_fmaf(s[p][g], d, acc[p][g]) : d;
+      }
+  }
+#pragma unroll
+  for (int p = 0; p < ONE_PAIRS; ++p) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      acc[p][0] += __shfl_xor(acc[p][0], o);
+      acc[p][1] += __shfl_xor(acc[p][1], o);
+    }
+    if (lane == 0) put_act<H>(a, (int64_t)j * a.inter + i0 + p, acc[p][0], acc[p][1]);
+  }
+}
+
+// ONE_ROWS rows of y whole: the threads share the (choice, 16 columns) pairs of
+// the topk down products and weight every sum where it arises, so that nothing is
+// left to add and no workgroup waits for another (2048 rows of 8 x 1024 in bf16:
+// 9.8 us on the matrix cores with the last workgroups adding, this way 7).
+constexpr int ONE_ROWS = 2;
+template <typename H, bool W8> __global__ __launch_bounds__(256) void down_one_kernel(MoeArgs a) {
+  __shared__ float part[4][ONE_ROWS];
+  const int tid = threadIdx.x, h0 = blockIdx.x * ONE_ROWS;
+  const int chunks = a.inter / 16, all = a.topk * chunks;
+  const int64_t slds = (a.hidden + 127) / 128, sblocks = (a.inter + 127) / 128;
+  constexpr int N = W8 ? 1 : 2, ES = W8 ? 1 : 2;
+  float acc[ONE_ROWS];
+#pragma unroll
+  for (int r = 0; r < ONE_ROWS; ++r) acc[r] = 0.0f;
+#pragma unroll 1
+  for (int f = tid; f < all; f += 256) {
+    const int j = f / chunks, c = 16 * (f - j * chunks), e = a.ids[j];
+    float p = a.weights[j];
+    const int64_t at = (int64_t)j * a.inter + c;
+    const u4 hi[2] = {reinterpret_cast<const u4 *>(a.hi + at)[0], reinterpret_cast<const u4 *>(a.hi + at)[1]};
+    const u4 lo[2] = {reinterpret_cast<const u4 *>(a.lo + at)[0], reinterpret_cast<const u4 *>(a.lo + at)[1]};
+    const uint8_t *from = a.down + (((int64_t)e * a.hidden + h0) * a.inter + c) * ES;
+    u4 w[ONE_ROWS][N];
+#pragma unroll
+    for (int r = 0; r < ONE_ROWS; ++r)
+#pragma unroll
+      for (int b = 0; b < N; ++b) w[r][b] = reinterpret_cast<const u4 *>(from + (int64_t)r * a.inter * ES)[b];
+    if constexpr (W8) p *= a.down_scales[(e * sblocks + (c >> 7)) * slds + (h0 >> 7)];
+    float x[16], l[16];
+    floats16<H, false>(hi, x);
+    floats16<H, false>(lo, l);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] += l[i];      // exact: lo ends where the float that both were cut from did
+#pragma unroll
+    for (int r = 0; r < ONE_ROWS; ++r) {
+      float y[16], d = 0.0f;
+      floats16<H, W8>(w[r], y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d = __builtin_fmaf(y[i], x[i], d);
+      acc[r] = __builtin_fmaf(p, d, acc[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ONE_ROWS; ++r) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) acc[r] += __shfl_xor(acc[r], o);
+    if ((tid & 63) == 0) part[tid >> 6][r] = acc[r];
+  }
+  __syncthreads();
+  if (tid < ONE_ROWS)
+    a.y[h0 + tid] = __builtin_bit_cast(uint16_t, (H)(part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]));
+}
+
 template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
   const int h = blockIdx.x * 256 + threadIdx.x;
   if (h < a.hidden) add_parts<H, false>(a, blockIdx.y, h);
@@ -594,6 +726,11 @@ template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
   if (a.tokens == 1) router_one_kernel<H><<<dim3((a.experts + 3) / 4), 256, 0, st>>>(a);
   else router_kernel<H><<<dim3((a.experts + 15) / 16, (a.tokens + RT - 1) / RT, a.splits), 64 * RW, 0, st>>>(a);
   const int slots = std::min(a.tokens * a.topk, a.experts);
+  if (a.tokens == 1) {
+    gate_up_one_kernel<H, W8><<<dim3(a.inter / (4 * ONE_PAIRS), a.topk), 256, 0, st>>>(a);
+    down_one_kernel<H, W8><<<dim3(a.hidden / ONE_ROWS), 256, 0, st>>>(a);
+    return;
+  }
   gate_up_kernel<H, W8><<<dim3(a.inter / 16, slots), 64 * WV, 0, st>>>(a);
   if (slots * (a.hidden / 32) < 2048) {
     down_kernel<H, W8, 1><<<dim3(a.hidden / 16, slots), 64 * WV, 0, st>>>(a);

@@ -110,6 +110,22 @@ def test_quantize_extremes(block, fmt):
     check_result(b, np.ascontiguousarray(x.double().numpy().T), block, fmt, "transposed")
 
 
+@pytest.mark.parametrize("rows,k,dtype,block", [(4096, 4096, "bf16", 1), (4096, 4224, "f32", 128), (4200, 4104, "f16", 1)])
+def test_quantize_of_large_matrices_is_that_of_their_parts(rows, k, dtype, block):
+    from hpc_linear_algebra_amd import blocks
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(rows, k, generator=g, device="cuda").to(TD[dtype])
+    a, b = blocks.quantize(x, block=block, transposed=True)
+    rb = 1 if block == 1 else 128
+    for r0 in range(0, rows, 1024):
+        r1 = min(rows, r0 + 1024)
+        pa, pb = blocks.quantize(x[r0:r1], block=block, transposed=True)
+        assert torch.equal(a.codes[r0:r1].view(torch.uint8), pa.codes.view(torch.uint8))
+        assert torch.equal(a.scales[:, r0 // rb:-(-r1 // rb)], pa.scales)
+        assert torch.equal(b.codes[:, r0:r1].view(torch.uint8), pb.codes[:, :r1 - r0].view(torch.uint8))
+        assert torch.equal(b.scales[r0 // 128:-(-r1 // 128)], pb.scales)
+
+
 # ---- product ------------------------------------------------------------------------------------------
 
 def codes(rows, k, fmt, block, seed, pad=0):

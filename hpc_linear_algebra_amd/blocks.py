@@ -26,25 +26,22 @@ FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _CODE = {torch.float8_e4m3fn: T.TLR_E4M3, torch.float8_e5m2: T.TLR_E5M2}
 _DT = {torch.float32: T.TLR_F32, torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
 _FMT = {"e4m3": T.TLR_E4M3, "e5m2": T.TLR_E5M2}
-_TORCH = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+_NEW = {"f32": T.TLR_F32, "f16": T.TLR_F16, "bf16": T.TLR_BF16}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream      # 0.1 us, the stream object's way 2.7
-_device = torch._C._cuda_getDevice                    # what torch.cuda.current_device asks once torch is set up
+@functools.lru_cache(None)
+def binding():
+    """The extension module, calling the entries of the loaded library."""
+    lib = T.lib()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the extension module is not built: python -m hpc_linear_algebra_amd.build") from e
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value   # noqa: E731
+    _binding.connect(address(lib.tlr_block_quantize), address(lib.tlr_block_gemm), address(lib.tlr_moe))
+    return _binding
 
 
-def call(device: torch.device, f, *args) -> int:
-    """f(*args, torch's current stream of the device) with that device current.
-    A decode step is bound by what the host does between launches: the guard is
-    entered only where it changes something."""
-    index = device.index
-    if _device() == index:
-        return f(*args, _raw_stream(index))
-    with torch.cuda.device(index):
-        return f(*args, _raw_stream(index))
-
-
-_lib = functools.lru_cache(None)(T.lib)
 _gemm_workspace = functools.lru_cache(4096)(T.tlr_block_gemm_workspace_bytes)      # of the sizes alone
 
 
@@ -57,7 +54,7 @@ class BlockScaled:
     block    rows of a block: 1 or 128
     """
 
-    __slots__ = ("codes", "scales", "rows", "k", "block", "_c")
+    __slots__ = ("codes", "scales", "rows", "k", "block", "_c", "_at")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, block: int):
         if codes.dtype not in _CODE or codes.dim() != 2:
@@ -77,6 +74,7 @@ class BlockScaled:
             raise ValueError(f"scales: shape {(nq, nr)}, rows contiguous, is needed")
         self.codes, self.scales, self.rows, self.k, self.block = codes, scales, rows, k, block
         self._c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, lds, block, _CODE[codes.dtype])
+        self._at = 0
 
     @property
     def c(self) -> T.tlr_block_matrix:
@@ -87,6 +85,13 @@ class BlockScaled:
                                          _CODE[codes.dtype])
         return self._c
 
+    @property
+    def address(self) -> int:
+        """Where c is, as long as this object lives."""
+        if not self._at:
+            self._at = ctypes.addressof(self.c)
+        return self._at
+
     def dequantize(self) -> torch.Tensor:
         """The (rows, k) float32 matrix that the codes and scales stand for."""
         s = self.scales.t().repeat_interleave(BLOCK, dim=1)[:, :self.k]
@@ -95,21 +100,10 @@ class BlockScaled:
         return self.codes[:, :self.k].float() * s
 
 
-def _empty(rows: int, k: int, block: int, dt: torch.dtype, device) -> BlockScaled:
+def _made(codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, block: int) -> BlockScaled:
     q = BlockScaled.__new__(BlockScaled)        # right by construction: the checks cost more than the launch
-    nr = rows if block == 1 else -(-rows // BLOCK)
-    q.codes = torch.empty((rows, -(-k // 16) * 16), dtype=dt, device=device)
-    q.scales = torch.empty((-(-k // BLOCK), nr), dtype=torch.float32, device=device)
-    q.rows, q.k, q.block, q._c = rows, k, block, None
+    q.codes, q.scales, q.rows, q.k, q.block, q._c, q._at = codes, scales, rows, k, block, None, 0
     return q
-
-
-def _result(q: Optional[BlockScaled]):
-    """(codes, ld, scales, lds) of a result of _empty for the C ABI."""
-    if q is None:
-        return None, 0, None, 0
-    codes, scales = q.codes, q.scales
-    return codes.data_ptr() or None, codes.shape[1], scales.data_ptr() or None, scales.shape[1]
 
 
 def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool = True,
@@ -119,26 +113,15 @@ def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool 
     x is a 2-d float32, float16 or bfloat16 tensor whose rows are contiguous
     (any row stride).  block 1: a scale for every 128 entries of a row of the
     result; block 128: one for every 128 x 128 tile."""
-    dt = _DT.get(x.dtype)
-    if dt is None or x.dim() != 2 or not x.is_cuda:
-        raise ValueError("quantize: a 2-d float32, float16 or bfloat16 tensor on a GPU is needed")
-    f8 = FORMATS.get(fmt)
+    f8 = _FMT.get(fmt)
     if f8 is None or block not in (1, BLOCK) or not (straight or transposed):
         raise ValueError("quantize: fmt is e4m3 or e5m2, block 1 or 128, and a result has to be wanted")
+    got = binding().quantize(x, f8, block, straight, transposed)
+    if type(got) is int:
+        T._check(got, "tlr_block_quantize")
     rows, k = x.shape
-    ldx, step = x.stride()
-    if k > 1 and step != 1:
-        raise ValueError("quantize: the rows of x have to be contiguous")
-    if rows <= 1:
-        ldx = max(ldx, k, 1)
-    device = x.device
-    a = _empty(rows, k, block, f8, device) if straight else None
-    b = _empty(k, rows, block, f8, device) if transposed else None
-    st = call(device, _lib().tlr_block_quantize, dt, _FMT[fmt], block, rows, k, x.data_ptr() or None, ldx, *_result(a),
-              *_result(b))
-    if st:
-        T._check(st, "tlr_block_quantize")
-    return a, b
+    return (_made(got[0], got[1], rows, k, block) if straight else None,
+            _made(got[2], got[3], k, rows, block) if transposed else None)
 
 
 def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alpha: float = 1.0, beta: float = 0.0,
@@ -159,17 +142,13 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
     if out is None:
         if beta != 0.0:
             raise ValueError("gemm: beta needs an out to add to")
-        out = torch.empty((n, m), dtype=_TORCH[dtype], device=device)
     elif tuple(out.shape) != (n, m) or out.dtype not in _DT or out.device != device or (m > 1 and out.stride(1) != 1):
         raise ValueError(f"gemm: out has to be a ({n}, {m}) float32, float16 or bfloat16 tensor with contiguous rows")
-    ldc = out.stride(0) if n > 1 else max(out.stride(0), m, 1)
-    nws = _gemm_workspace(m, n, A.k)
-    ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
-    st = call(device, _lib().tlr_block_gemm, _DT[out.dtype], m, n, A.k, alpha, ctypes.byref(A.c), ctypes.byref(B.c),
-              beta, out.data_ptr() or None, ldc, T.TLR_BLOCK_FAST if fast else 0, ws.data_ptr() if nws else None, nws)
-    if st:
-        T._check(st, "tlr_block_gemm")
-    return out
+    got = binding().gemm(A.address, B.address, m, n, A.k, alpha, beta, out, _NEW[dtype], B.codes,
+                      T.TLR_BLOCK_FAST if fast else 0, _gemm_workspace(m, n, A.k))
+    if type(got) is int:
+        T._check(got, "tlr_block_gemm")
+    return got
 
 
 class _Linear(torch.autograd.Function):

@@ -3,7 +3,8 @@
 Usage: python -m hpc_linear_algebra_amd.build   (or call build()).
 Every source is compiled with hipcc; device code is built for gfx950 only and
 with packed-fp32 instructions disabled (the compiler would otherwise form
-v_pk_* fp32 arithmetic from ordinary float code).
+v_pk_* fp32 arithmetic from ordinary float code).  binding.cpp, host code against
+torch's headers, becomes the extension module _binding beside it.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ LIB = os.path.join(PKG, "libtlrgemm.so")
 SOURCES = ["planner.cpp", "abi.cpp", "executor.cpp", "noalloc.cpp", "gemm.hip", "gemm16.hip", "compress.hip",
            "block.hip", "moe.hip"]
 ARCH = "gfx950"
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def hipcc() -> str:
@@ -50,11 +53,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> str:
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp"
+    cmd = [hipcc(), "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths("cuda"):
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += [f"-L{path}" for path in cpp_extension.library_paths("cuda")]
+    cmd += ["-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("hipcc failed for binding.cpp:\n" + r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libtlrgemm.so next to this file."""
+    """Compile every source and link libtlrgemm.so and _binding next to this file."""
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=4) as ex:
+    with ThreadPoolExecutor(max_workers=5) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

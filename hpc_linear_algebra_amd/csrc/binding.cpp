@@ -1,0 +1,168 @@
+// Python's way to the calls that a decode step makes often: checks, allocation
+// and stream look-up in C++ (host time of a quantizer call with one result 5.2
+// us, of a product 4.5, through ctypes and torch's Python 8.9 and 7.1).  The C
+// entries are handed over by address at start-up; a status other than TLR_OK is
+// returned as an int for the caller to raise.
+#include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "tlrgemm.h"
+
+namespace {
+
+decltype(&tlr_block_quantize) quantize_entry = nullptr;
+decltype(&tlr_block_gemm) gemm_entry = nullptr;
+decltype(&tlr_moe) moe_entry = nullptr;
+
+// TLR_* of a tensor's type, -1 for types that are not X's or C's.
+int code_of(const at::Tensor &t) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return TLR_F32;
+    case at::kHalf: return TLR_F16;
+    case at::kBFloat16: return TLR_BF16;
+    default: return -1;
+  }
+}
+
+void *stream_of(const at::Device &d) { return c10::hip::getCurrentHIPStream(d.index()).stream(); }
+
+PyObject *value_error(const char *text) {
+  PyErr_SetString(PyExc_ValueError, text);
+  return nullptr;
+}
+
+// connect(addresses of tlr_block_quantize, tlr_block_gemm, tlr_moe)
+PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 3) return value_error("connect: 3 addresses");
+  quantize_entry = reinterpret_cast<decltype(quantize_entry)>(PyLong_AsVoidPtr(args[0]));
+  gemm_entry = reinterpret_cast<decltype(gemm_entry)>(PyLong_AsVoidPtr(args[1]));
+  moe_entry = reinterpret_cast<decltype(moe_entry)>(PyLong_AsVoidPtr(args[2]));
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
+
+struct Result {
+  at::Tensor codes, scales;
+  Result(bool wanted, int64_t rows, int64_t k, int64_t block, at::ScalarType f8, const at::Device &d) {
+    if (!wanted) return;
+    codes = at::empty({rows, (k + 15) / 16 * 16}, at::TensorOptions().dtype(f8).device(d));
+    scales = at::empty({(k + 127) / 128, block == 1 ? rows : (rows + 127) / 128}, at::TensorOptions().dtype(at::kFloat).device(d));
+  }
+  int64_t ld() const { return codes.defined() ? codes.size(1) : 0; }
+  int64_t lds() const { return scales.defined() ? scales.size(1) : 0; }
+  void *code_ptr() const { return codes.defined() ? codes.data_ptr() : nullptr; }
+  float *scale_ptr() const { return scales.defined() ? static_cast<float *>(scales.data_ptr()) : nullptr; }
+};
+
+PyObject *wrap(const at::Tensor &t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+
+// quantize(x, fmt, block, straight, transposed) -> (codes, scales, codes_t, scales_t) or a status
+PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5 || !THPVariable_Check(args[0])) return value_error("quantize: a tensor and four numbers");
+  const at::Tensor &x = THPVariable_Unpack(args[0]);
+  const int dt = code_of(x);
+  if (dt < 0 || x.dim() != 2 || !x.is_cuda())
+    return value_error("quantize: a 2-d float32, float16 or bfloat16 tensor on a GPU is needed");
+  const long fmt = PyLong_AsLong(args[1]), block = PyLong_AsLong(args[2]);
+  const int straight = PyObject_IsTrue(args[3]), transposed = PyObject_IsTrue(args[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const int64_t rows = x.size(0), k = x.size(1);
+  if (k > 1 && x.stride(1) != 1) return value_error("quantize: the rows of x have to be contiguous");
+  const int64_t ldx = rows > 1 ? x.stride(0) : std::max<int64_t>({x.stride(0), k, 1});
+  const c10::DeviceGuard guard(x.device());
+  const at::ScalarType f8 = fmt == TLR_E5M2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn;
+  const Result a(straight, rows, k, block, f8, x.device()), b(transposed, k, rows, block, f8, x.device());
+  const tlr_status st = quantize_entry((tlr_dtype)dt, (tlr_dtype)fmt, (int32_t)block, rows, k, x.data_ptr(), ldx, a.code_ptr(),
+                                       a.ld(), a.scale_ptr(), a.lds(), b.code_ptr(), b.ld(), b.scale_ptr(), b.lds(),
+                                       stream_of(x.device()));
+  if (st != TLR_OK) return PyLong_FromLong(st);
+  PyObject *out = PyTuple_New(4);
+  if (!out) return nullptr;
+  const at::Tensor *t[4] = {&a.codes, &a.scales, &b.codes, &b.scales};
+  for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(out, i, wrap(*t[i]));
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm(address of A's tlr_block_matrix, of B's, m, n, k, alpha, beta, out or None, type of a new one, a tensor on
+// their device, flags, workspace bytes) -> out or a status
+PyObject *gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 12 || !(args[7] == Py_None || THPVariable_Check(args[7])) || !THPVariable_Check(args[9]))
+    return value_error("gemm: 12 arguments");
+  const auto *A = static_cast<const tlr_block_matrix *>(PyLong_AsVoidPtr(args[0]));
+  const auto *B = static_cast<const tlr_block_matrix *>(PyLong_AsVoidPtr(args[1]));
+  const int64_t m = PyLong_AsLongLong(args[2]), n = PyLong_AsLongLong(args[3]), k = PyLong_AsLongLong(args[4]);
+  const double alpha = PyFloat_AsDouble(args[5]), beta = PyFloat_AsDouble(args[6]);
+  const long type = PyLong_AsLong(args[8]);
+  const unsigned long flags = PyLong_AsUnsignedLong(args[10]);
+  const size_t bytes = PyLong_AsSize_t(args[11]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Device device = THPVariable_Unpack(args[9]).device();
+  if (!device.is_cuda()) return value_error("gemm: operands on a GPU are needed");
+  const c10::DeviceGuard guard(device);
+  at::Tensor c, ws;
+  if (args[7] == Py_None)
+    c = at::empty({n, m}, at::TensorOptions().device(device).dtype(type == TLR_F32 ? at::kFloat : type == TLR_F16 ? at::kHalf : at::kBFloat16));
+  else
+    c = THPVariable_Unpack(args[7]);
+  const int64_t ldc = n > 1 ? c.stride(0) : std::max<int64_t>({c.stride(0), m, 1});
+  if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(device));
+  const tlr_status st = gemm_entry((tlr_dtype)code_of(c), m, n, k, alpha, A, B, beta, c.data_ptr(), ldc, (uint32_t)flags,
+                                   bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream_of(device));
+  return st == TLR_OK ? wrap(c) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// moe(address of a tlr_moe_layer, x of its type and width, max tokens, address and bytes of its workspace) ->
+// (y, ids, weights) or a status
+PyObject *moe(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5 || !THPVariable_Check(args[1])) return value_error("moe: a tensor and four numbers");
+  const auto *layer = static_cast<const tlr_moe_layer *>(PyLong_AsVoidPtr(args[0]));
+  at::Tensor x = THPVariable_Unpack(args[1]);
+  const long most = PyLong_AsLong(args[2]);
+  void *ws = PyLong_AsVoidPtr(args[3]);
+  const size_t bytes = PyLong_AsSize_t(args[4]);
+  if (PyErr_Occurred()) return nullptr;
+  if (x.dim() != 2 || x.size(1) != layer->hidden || code_of(x) != layer->dt || !x.is_cuda())
+    return value_error("MoELayer: x is (tokens, hidden), of the layer's type and on its GPU");
+  const int64_t tokens = x.size(0);
+  if (tokens > most) return value_error("MoELayer: more tokens than the layer was made for");
+  const c10::DeviceGuard guard(x.device());
+  if (x.stride(1) != 1 || reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 != 0 || (tokens > 1 && x.stride(0) % 8 != 0))
+    x = x.clone(at::MemoryFormat::Contiguous);      // 16-byte aligned rows; a fresh allocation starts aligned
+  const at::TensorOptions on = at::TensorOptions().device(x.device());
+  const at::Tensor y = at::empty({tokens, layer->hidden}, on.dtype(x.scalar_type()));
+  const at::Tensor ids = at::empty({tokens, layer->topk}, on.dtype(at::kInt));
+  const at::Tensor weights = at::empty({tokens, layer->topk}, on.dtype(at::kFloat));
+  const tlr_status st = moe_entry(layer, (int32_t)tokens, x.data_ptr(), tokens > 1 ? x.stride(0) : layer->hidden, y.data_ptr(),
+                                  layer->hidden, static_cast<int32_t *>(ids.data_ptr()), static_cast<float *>(weights.data_ptr()),
+                                  ws, bytes, stream_of(x.device()));
+  if (st != TLR_OK) return PyLong_FromLong(st);
+  PyObject *out = PyTuple_New(3);
+  if (!out) return nullptr;
+  const at::Tensor *t[3] = {&y, &ids, &weights};
+  for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(out, i, wrap(*t[i]));
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {
+    {"connect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(connect)), METH_FASTCALL, nullptr},
+    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
+    {"gemm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm)), METH_FASTCALL, nullptr},
+    {"moe", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(moe)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }

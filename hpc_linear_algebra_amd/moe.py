@@ -9,7 +9,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import tlrgemm as T
-from .blocks import call
+from .blocks import binding
 
 MAX_TOKENS = 256
 _DT = {torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
@@ -65,26 +65,16 @@ class MoELayer:
                                  gate_up_scales.data_ptr() if e8 else None, down_scales.data_ptr() if e8 else None)
         self.ws = torch.empty(max(256, T.tlr_moe_workspace_bytes(self.c, self.max_tokens)), dtype=torch.uint8,
                               device=self.device)
-        self._ref, self._ws, self._nws = ctypes.byref(self.c), self.ws.data_ptr(), self.ws.numel()
+        self._at, self._ws, self._nws = ctypes.addressof(self.c), self.ws.data_ptr(), self.ws.numel()
         with torch.cuda.device(self.device):
             T.tlr_moe_init(self.c, self.ws.data_ptr(), self.ws.numel(), torch.cuda.current_stream().cuda_stream)
 
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(y, ids, weights) of x (tokens, hidden): the layer's output in x's
         type, the chosen experts (int32) and their probabilities (float32)."""
-        if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype != self.dtype or x.device != self.device:
-            raise ValueError(f"MoELayer: x is (tokens, {self.hidden}) of type {self.dtype} on {self.device}")
-        t = x.shape[0]
-        if t > self.max_tokens:
-            raise ValueError(f"MoELayer: {t} tokens, made for {self.max_tokens}")
-        if x.stride(1) != 1 or x.data_ptr() % 16 or (t > 1 and x.stride(0) % 8):
-            x = x.contiguous()
-        y = torch.empty((t, self.hidden), dtype=x.dtype, device=x.device)
-        ids = torch.empty((t, self.topk), dtype=torch.int32, device=x.device)
-        weights = torch.empty((t, self.topk), dtype=torch.float32, device=x.device)
-        st = call(self.device, T.lib().tlr_moe, self._ref, t, x.data_ptr() or None, x.stride(0) if t > 1 else self.hidden,
-                  y.data_ptr() or None, self.hidden, ids.data_ptr() or None, weights.data_ptr() or None, self._ws,
-                  self._nws)
-        if st:
-            T._check(st, "tlr_moe")
-        return y, ids, weights
+        if x.device != self.device:
+            raise ValueError(f"MoELayer: x is on {self.device}")
+        got = binding().moe(self._at, x, self.max_tokens, self._ws, self._nws)
+        if type(got) is int:
+            T._check(got, "tlr_moe")
+        return got

@@ -131,3 +131,18 @@ def test_python_refusals():
         bf = torch.bfloat16
         moe.MoELayer(torch.zeros(4, 32, dtype=bf), torch.zeros(4, 30, 32, dtype=bf), torch.zeros(4, 32, 16, dtype=bf), 2)
     assert ctypes.sizeof(T.tlr_block_matrix) == 40 and ctypes.sizeof(T.tlr_moe_layer) == 72
+
+
+def test_block_operators_refuse_host_tensors():
+    """No pointer to host memory reaches a kernel."""
+    import torch
+
+    from hpc_linear_algebra_amd import blocks
+    with pytest.raises(ValueError):
+        blocks.quantize(torch.zeros(4, 32))
+    with pytest.raises(ValueError):
+        blocks.quantize("x")
+    q = blocks.BlockScaled(torch.zeros(4, 32, dtype=torch.float8_e4m3fn), torch.ones(1, 4), 4, 32, 1)
+    for out in (None, torch.zeros(4, 4)):
+        with pytest.raises(ValueError):
+            blocks.gemm(q, q, out=out, dtype="f32")

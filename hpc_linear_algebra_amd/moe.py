@@ -9,10 +9,20 @@ from typing import Optional, Tuple
 import torch
 
 from . import tlrgemm as T
-from .blocks import binding
+from .blocks import binding, quantize
 
 MAX_TOKENS = 256
 _DT = {torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
+
+
+def quantize_experts(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales) of expert weights (experts, rows, k), k a multiple of 16,
+    as MoELayer takes them: e4m3 with 128 x 128 block scales, done once when
+    the weights are loaded."""
+    if w.dim() != 3 or w.shape[2] % 16:
+        raise ValueError("quantize_experts: weights are (experts, rows, k), k a multiple of 16")
+    parts = [quantize(e, block=128)[0] for e in w]
+    return torch.stack([p.codes.view(torch.uint8) for p in parts]).view(torch.float8_e4m3fn), torch.stack([p.scales for p in parts])
 
 
 class MoELayer:

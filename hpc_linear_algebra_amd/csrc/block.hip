@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "tlr_ops.h"
 
@@ -519,10 +520,9 @@ template <int ROWS, int T, bool IS_A> struct Panel {
   static __device__ __forceinline__ int chunk(int tid) {
     return 16 * ((tid & 7) ^ (IS_A ? a_key(tid >> 3) : b_key(tid >> 3)));
   }
-  // a whole column block (rows past the operand's give zeros)
-  __device__ __forceinline__ void load(int kb, uint32_t lds, int wave) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) to_lds16(rows[i], at, kb * QB, lds + (i * T + wave * 64) * 16);
+  // step i of a whole column block (rows past the operand's give zeros)
+  __device__ __forceinline__ void load(int i, int kb, uint32_t lds, int wave) const {
+    to_lds16(rows[i], at, kb * QB, lds + (i * T + wave * 64) * 16);
   }
   // the last column block (its descriptors end with the operand)
   __device__ __forceinline__ void load_last(int kb, uint32_t lds, int wave) const {
@@ -552,10 +552,20 @@ template <int ROWS, int T, bool IS_A> struct Panel {
 //
 // Two stages of one column block each in LDS.  A wave goes through a stage row
 // tile by row tile; with the last one's matrix instructions under way it waits
-// for the next stage, has the one after it loaded into the buffer that is now
-// used up, and reads its first fragments of the next: one barrier a stage, and
-// the matrix cores have work on both sides of it.
-template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN>
+// for the next stage and reads its first fragments: one barrier a stage, and the
+// matrix cores have work on both sides of it.  The stage after that is loaded
+// into the buffer that is then used up, SPREAD pieces under each row tile's matrix
+// instructions, or all at once (SPREAD 0), which a short stage needs: 8192^3 in
+// 256 x 256 tiles 460 us with two pieces, 475 at once; 4096 x 4096 x 8192 exact in
+// 128 x 128 tiles on four waves 243 with three, 259 at once; 2501 x 1111 x 1747 on
+// eight waves 19.0 spread, 17.7 at once.
+//
+// What bounds 8192^3 (2.4 PFLOP/s, 86% of the library's product without blocks):
+// the matrix cores are busy 53% of the clocks.  Timing copies: matrix instructions
+// and barriers alone 319 us, the scaled additions add 48, the loads 94 (alone they
+// take 377; two, three or four stages of them in flight make no difference, nor do
+// odd strides), the fragment reads from LDS 10.
+template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN, int SPREAD>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(GemmArgs g) {
   constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
   static_assert(RI % 2 == 0 && (!AB || 128 % (TM / WM) == 0), "");
@@ -602,10 +612,12 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
     for (int i = 0; i < SN; ++i) to_lds4(buffer(sbase[i] + kb * sld[i], sbytes[i]), sat[i], ls + 4 * (i * T + wave * 64));
   };
-  auto load = [&](int kb, uint32_t to) {
-    load_scales(kb, to + AT_S);
-    pa.load(kb, to, wave);
-    pb.load(kb, to + AT_B, wave);
+  // Column block kb into a stage, in LOADS pieces.
+  constexpr int NA = Panel<TM, T, true>::N, LOADS = NA + Panel<TN, T, false>::N + 1;
+  auto load = [&](int piece, int kb, uint32_t to) {
+    if (piece == 0) load_scales(kb, to + AT_S);
+    else if (piece <= NA) pa.load(piece - 1, kb, to, wave);
+    else pb.load(piece - 1 - NA, kb, to + AT_B, wave);
   };
 
   f4 acc[RI][CJ];
@@ -665,16 +677,20 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   load_scales(kb0 + nb - 1, base + AT_S);
   pa.load_last(kb0 + nb - 1, base, wave);
   pb.load_last(kb0 + nb - 1, base + AT_B, wave);
-  if (nb > 1) {
-    load(kb0, base + STAGE);
-    constexpr int LOADS = Panel<TM, T, true>::N + Panel<TN, T, false>::N + SN;      // of stage 1, still under way
-    static_assert(LOADS < 16, "");
-    __builtin_amdgcn_s_waitcnt(LOADS | 0xf << 8 | 7 << 4);
+  auto load_all = [&](int kb, uint32_t to) {
+#pragma unroll
+    for (int c = 0; c < LOADS; ++c) load(c, kb, to);
+  };
+  if (SPREAD == 0 && nb > 1) {
+    load_all(kb0, base + STAGE);
+    constexpr int LEFT = LOADS - 1 + SN;        // stage 1, still under way
+    static_assert(LEFT < 16, "");
+    __builtin_amdgcn_s_waitcnt(LEFT | 0xf << 8 | 7 << 4);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   } else {
-    __builtin_amdgcn_s_waitcnt(0);
+    meet();
   }
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
   if (cut) {
     pa.cut(g.k & (QB - 1), lds, tid);
     pb.cut(g.k & (QB - 1), lds + AT_B, tid);
@@ -686,7 +702,9 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   read_b(lds);
   read_a(lds, 0);
   f4 d[2][CJ];
-  auto row_tiles = [&](const uint8_t *l) {     // all sums of a stage but the last row tile's
+  // All sums of a stage but the last row tile's, column block kb loaded meanwhile.
+  auto row_tiles = [&](const uint8_t *l, auto live, int kb, uint32_t to) {
+    static_assert(SPREAD == 0 || SPREAD * RI >= LOADS, "");
     Fragment<B5, FAST> bf[CJ];
 #pragma unroll
     for (int j = 0; j < CJ; ++j) {
@@ -700,6 +718,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
       const Fragment<A5, FAST> af(x[i & 1]);
 #pragma unroll
       for (int j = 0; j < CJ; ++j) d[i & 1][j] = mma<A5, B5>(af, bf[j]);
+      if constexpr (decltype(live)::value)
+#pragma unroll
+        for (int c = 0; c < SPREAD; ++c)
+          if (i * SPREAD + c < LOADS) load(i * SPREAD + c, kb, to);
       if (i > 0) add(i - 1, d[(i - 1) & 1]);
       // here, not where the sums are next used: sunk there past the branches
       // below, they would keep every d in registers
@@ -711,9 +733,9 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   };
   int now = 0, next = STAGE;
   for (int stage = 0; stage < nb - 1; ++stage) {
-    row_tiles(lds + now);
+    row_tiles(lds + now, std::true_type{}, kb0 + stage, base + next);
     meet();
-    if (stage + 2 < nb) load(kb0 + stage + 1, base + now);
+    if (SPREAD == 0 && stage + 2 < nb) load_all(kb0 + stage + 1, base + now);
     read_b(lds + next);
     read_a(lds + next, 0);
     add(RI - 1, d[1]);
@@ -721,7 +743,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     now = next;
     next = t;
   }
-  row_tiles(lds + now);
+  row_tiles(lds + now, std::false_type{}, 0, 0);
   add(RI - 1, d[1]);
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
@@ -834,7 +856,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
   return best;
 }
 
-template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN>
+template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN, int SPREAD>
 void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
   const dim3 grid((unsigned)(cdiv(g.m, TM) * cdiv(g.n, TN)), (unsigned)parts);
   GemmArgs h = g;
@@ -845,8 +867,8 @@ void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
     h.ldc = g.m;
     h.dt = TLR_F32;
   }
-  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(h);
-  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(h);
+  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN, SPREAD><<<grid, 64 * WM * WN, 0, st>>>(h);
+  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN, SPREAD><<<grid, 64 * WM * WN, 0, st>>>(h);
   if (parts == 1) return;
   const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
   if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
@@ -864,11 +886,11 @@ template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, float
   const Choice c = choose(g.m, g.n, g.k, FAST);
   switch (c.kind) {
     case STRIP: return strip_launch<A5, B5, FAST>(g, st);
-    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2>(g, c.parts, ws, st);
-    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2>(g, c.parts, ws, st);
-    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4>(g, c.parts, ws, st);
+    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2, 0>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 3>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4, 0>(g, c.parts, ws, st);
     case TILE_256:
-      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4>(g, c.parts, ws, st);
+      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4, 2>(g, c.parts, ws, st);
   }
 }
 

@@ -164,6 +164,7 @@ class _Linear(torch.autograd.Function):
         return gemm(w8, x8, out=out, fast=x.dtype != torch.float32).reshape(*x.shape[:-1], w.shape[0])
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
         dx = dw = None
@@ -185,7 +186,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3") -> torch.Te
     blocks along each contraction, w in 128 x 128 blocks.  The forward pass
     keeps the transposed codes, a byte an entry, in place of x and w.  Results
     in 16 bits are summed with ``fast`` (see gemm), float32 ones in float.  No
-    double backward."""
+    double backward.  In a captured graph take torch.autograd.grad, or leaves
+    that no live eager graph holds: their accumulation belongs to its stream."""
     if x.shape[-1:] != w.shape[1:] or w.dim() != 2:
         raise ValueError("linear: x is (..., k) and w (features, k)")
     if grad_fmt not in FORMATS:

@@ -560,7 +560,7 @@ template <int ROWS, int T, bool IS_A> struct Panel {
 // 128 x 128 tiles on four waves 243 with three, 259 at once; 2501 x 1111 x 1747 on
 // eight waves 19.0 spread, 17.7 at once.
 //
-// What bounds 8192^3 (2.4 PFLOP/s, 86% of the library's product without blocks):
+// What bounds 8192^3 (455 us, 2.4 PFLOP/s, 88% of the library's product without blocks):
 // the matrix cores are busy 53% of the clocks.  Timing copies: matrix instructions
 // and barriers alone 319 us, the scaled additions add 48, the loads 94 (alone they
 // take 377; two, three or four stages of them in flight make no difference, nor do
@@ -830,7 +830,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
     }
   };
   // 4 KB a workgroup and block out of the caches
-  if (cdiv(n, 16) <= 65535) offer(STRIP, 1, 2.8 + cdiv(m, 16) * cdiv(n, 16) * nb * (fast ? 0.00040 : 0.00048));
+  if (cdiv(n, 16) <= 65535 && cdiv(m, 16) < 1 << 22) offer(STRIP, 1, 2.8 + cdiv(m, 16) * cdiv(n, 16) * nb * (fast ? 0.00040 : 0.00048));
   // One workgroup a CU takes `one` a column block, two together `two`.
   auto tiles = [&](Kind kind, int tn, double one, double two, double first, double next) {
     for (const int parts : {1, 2, 4, 8}) {
@@ -902,7 +902,7 @@ tlr_status launched(const char *what) {
   return TLR_OK;
 }
 
-constexpr int64_t SIZE_LIM = 0x7fffffff, LD_LIM = (int64_t)1 << 22;
+constexpr int64_t SIZE_LIM = 0x7fffffff, PRODUCT_LIM = SIZE_LIM - 511, LD_LIM = (int64_t)1 << 22;
 
 // Checks one result of the quantizer: rows x k codes with blocks of `block` rows.
 tlr_status check_result(const char *name, int block, int64_t rows, int64_t k, const void *codes, int64_t ld,
@@ -979,7 +979,8 @@ tlr_status block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_t ro
 
 tlr_status block_gemm_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes) {
   if (!bytes) return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: null output");
-  if (m < 0 || n < 0 || k < 0 || m > SIZE_LIM || n > SIZE_LIM || k > SIZE_LIM)
+  // a tile's rows past the end are still an int
+  if (m < 0 || n < 0 || k < 0 || m > PRODUCT_LIM || n > PRODUCT_LIM || k > SIZE_LIM)
     return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: size out of range");
   *bytes = 0;
   if (m > 0 && n > 0 && k > 0)

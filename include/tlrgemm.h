@@ -520,7 +520,7 @@ tlr_status tlr_block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_
  * codes propagate.  The product of two scales has to be a finite float.
  *   workspace  device, tlr_block_gemm_workspace_bytes (may be 0: then NULL is
  *              fine), 256-byte aligned; its contents need not be cleared.
- * Sizes up to 2^31 - 1, ld < 2^22.
+ * m and n up to 2^31 - 512, ld < 2^22.
  * Errors: TLR_ERR_INVALID_ARG (unknown flags among it), TLR_ERR_UNSUPPORTED (dt TLR_F64),
  * TLR_ERR_WORKSPACE, TLR_ERR_HIP.
  */

@@ -376,3 +376,59 @@ def test_linear_gradients_are_differences():
         assert float(step) == float((x.grad.double() * (x1 - x).double()).sum()) and float(step) != 0.0
         step = value(x, w1) - value(x, w)
         assert float(step) == float((w.grad.double() * (w1 - w).double()).sum()) and float(step) != 0.0
+
+
+def test_linear_captured_into_a_graph():
+    """Forward and backward in one graph, replayed on new inputs between eager steps."""
+    from hpc_linear_algebra_amd import blocks
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
+    x, w, dy = rn(96, 260).bfloat16(), rn(400, 260) / 16, rn(96, 400).bfloat16()
+
+    def step(a, b, c):
+        a, b = a.detach().requires_grad_(), b.detach().requires_grad_()      # leaves of this step alone
+        y = blocks.linear(a, b)
+        return (y, *torch.autograd.grad(y, (a, b), c))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x, w, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    static = [x.clone(), w.clone(), dy.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*static)
+    for k in range(4):
+        new = [rn(96, 260).bfloat16(), rn(400, 260) / 16, rn(96, 400).bfloat16()]
+        want = step(*new)
+        for a, b in zip(static, new):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_linear_of_strided_and_broadcast_inputs(dtype):
+    """A transposed view, an expanded one (whose gradient is the sum over its copies), and a single token."""
+    from hpc_linear_algebra_amd import blocks
+    g = torch.Generator().manual_seed(6)
+    w = (torch.randn(136, 144, generator=g) / 12).to(TD[dtype]).cuda().requires_grad_()
+    base = torch.randn(144, 40, generator=g).to(TD[dtype]).cuda().requires_grad_()
+    y = blocks.linear(base.t(), w)
+    same = blocks.linear(base.detach().t().contiguous(), w)
+    assert torch.equal(y, same)
+    one = torch.randn(1, 144, generator=g).to(TD[dtype]).cuda().requires_grad_()
+    dy = torch.randn(3, 136, generator=g).to(TD[dtype]).cuda()
+    blocks.linear(one.expand(3, 144), w).backward(dy)
+    alone = one.detach().expand(3, 144).contiguous().requires_grad_()
+    w.grad = None
+    blocks.linear(alone, w).backward(dy)
+    # the same three rows, summed by torch in any order: two additions in the type
+    assert torch.all((one.grad.float() - alone.grad.float().sum(0)).abs() <= 2 * torch.finfo(TD[dtype]).eps * alone.grad.float().abs().sum(0))
+    assert blocks.linear(one.reshape(144), w).shape == (136,)
+    y = blocks.linear(one, w)
+    gx, = torch.autograd.grad(y.sum(), one, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gx.sum().backward()

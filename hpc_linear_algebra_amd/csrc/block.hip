@@ -524,12 +524,12 @@ template <int ROWS, int T, bool IS_A> struct Panel {
   __device__ __forceinline__ void load(int i, int kb, uint32_t lds, int wave) const {
     to_lds16(rows[i], at, kb * QB, lds + (i * T + wave * 64) * 16);
   }
-  // the last column block (its descriptors end with the operand)
-  __device__ __forceinline__ void load_last(int kb, uint32_t lds, int wave) const {
+  // the last column blocks (their descriptors end with the operand); zeros if there is none
+  __device__ __forceinline__ void load_last(int kb, uint32_t lds, int wave, bool real) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int32_t o = kb * QB + i * step;
-      to_lds16(buffer(base + o, max(bytes - o, 0)), at, 0, lds + (i * T + wave * 64) * 16);
+      to_lds16(buffer(base + o, real ? max(bytes - o, 0) : 0), at, 0, lds + (i * T + wave * 64) * 16);
     }
   }
   // zeros in a stage's columns from `left` on
@@ -548,9 +548,12 @@ template <int ROWS, int T, bool IS_A> struct Panel {
 };
 
 // C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16.  AB: A's
-// blocks are 128 rows high (a wave's rows lie in one of them).
+// blocks are 128 rows high (a wave's rows lie in one of them).  KG 2: two such
+// halves of waves take every other column block and add their sums at the end,
+// which halves the barriers and lets waves be larger (fewer bytes from LDS); it
+// pays from about 16 column blocks on.
 //
-// Two stages of one column block each in LDS.  A wave goes through a stage row
+// Two stages of KG column blocks each in LDS.  A wave goes through a stage row
 // tile by row tile; with the last one's matrix instructions under way it waits
 // for the next stage and reads its first fragments: one barrier a stage, and the
 // matrix cores have work on both sides of it.  The stage after that is loaded
@@ -565,16 +568,16 @@ template <int ROWS, int T, bool IS_A> struct Panel {
 // and barriers alone 319 us, the scaled additions add 48, the loads 94 (alone they
 // take 377; two, three or four stages of them in flight make no difference, nor do
 // odd strides), the fragment reads from LDS 10.
-template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN, int SPREAD>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(GemmArgs g) {
-  constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
+template <bool A5, bool B5, bool FAST, bool AB, int TM, int TN, int WM, int WN, int KG, int SPREAD>
+__global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(GemmArgs g) {
+  constexpr int T = 64 * WM * WN * KG, RI = TM / WM / 16, CJ = TN / WN / 16;
   static_assert(RI % 2 == 0 && (!AB || 128 % (TM / WM) == 0), "");
-  // a stage: A's codes, B's codes, A's and B's scales
+  // a column block: A's codes, B's codes, A's and B's scales; a stage: KG of them
   constexpr int SN = (TM + TN + T - 1) / T;                // scales a thread loads
-  constexpr int AT_B = TM * QB, AT_S = (TM + TN) * QB, STAGE = AT_S + SN * T * 4;
+  constexpr int AT_B = TM * QB, AT_S = (TM + TN) * QB, BLOCK = AT_S + SN * T * 4, STAGE = KG * BLOCK;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, q = lane >> 4, kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
 
   // tile of this workgroup: workgroups go to the 8 XCDs in turn; each XCD takes
   // a contiguous part of the tiles, which run down 8 row tiles at a time
@@ -608,14 +611,17 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     sbytes[i] = w < TM + TN ? 4 * (((min(r0 + (isa ? TM : TN), o.rows) - 1) >> o.shift) - first + 1) : 0;
     sat[i] = 4 * (((r0 + (isa ? w : w - TM) + lane) >> o.shift) - first);
   }
-  auto load_scales = [&](int kb, uint32_t ls) {
+  auto load_scales = [&](int kb, uint32_t ls, bool real) {
 #pragma unroll
-    for (int i = 0; i < SN; ++i) to_lds4(buffer(sbase[i] + kb * sld[i], sbytes[i]), sat[i], ls + 4 * (i * T + wave * 64));
+    for (int i = 0; i < SN; ++i) to_lds4(buffer(sbase[i] + kb * sld[i], real ? sbytes[i] : 0), sat[i], ls + 4 * (i * T + wave * 64));
   };
-  // Column block kb into a stage, in LOADS pieces.
-  constexpr int NA = Panel<TM, T, true>::N, LOADS = NA + Panel<TN, T, false>::N + 1;
+  // The stage of column blocks kb, kb + 1, .., in LOADS pieces.
+  constexpr int NA = Panel<TM, T, true>::N, PIECES = NA + Panel<TN, T, false>::N + 1, LOADS = KG * PIECES;
   auto load = [&](int piece, int kb, uint32_t to) {
-    if (piece == 0) load_scales(kb, to + AT_S);
+    kb += piece / PIECES;
+    to += piece / PIECES * BLOCK;
+    piece %= PIECES;
+    if (piece == 0) load_scales(kb, to + AT_S, true);
     else if (piece <= NA) pa.load(piece - 1, kb, to, wave);
     else pb.load(piece - 1 - NA, kb, to + AT_B, wave);
   };
@@ -668,22 +674,28 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   };
 
   // This workgroup's column blocks: all, or the part of grid y.  Stage 0 is its
-  // last one, which may be cut at column k; stage i > 0 is block kb0 + i - 1.
+  // last one to KG, the very last of which may be cut at column k; stage i > 0
+  // is the KG from kb0 + (i - 1) KG on.
   const int blocks = (g.k + QB - 1) / QB;
   const int kb0 = (int)((int64_t)blocks * blockIdx.y / gridDim.y);
-  const int nb = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
-  const bool cut = (g.k & (QB - 1)) != 0 && kb0 + nb == blocks;
+  const int mine = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
+  const int nb = (mine + KG - 1) / KG, last = mine - (nb - 1) * KG;      // stages; column blocks of stage 0
+  const bool cut = (g.k & (QB - 1)) != 0 && kb0 + mine == blocks;
   const uint32_t base = lds_address(lds);
-  load_scales(kb0 + nb - 1, base + AT_S);
-  pa.load_last(kb0 + nb - 1, base, wave);
-  pb.load_last(kb0 + nb - 1, base + AT_B, wave);
+#pragma unroll
+  for (int c = 0; c < KG; ++c) {
+    const int kb = c < last ? kb0 + mine - last + c : 0;
+    load_scales(kb, base + c * BLOCK + AT_S, c < last);
+    pa.load_last(kb, base + c * BLOCK, wave, c < last);
+    pb.load_last(kb, base + c * BLOCK + AT_B, wave, c < last);
+  }
   auto load_all = [&](int kb, uint32_t to) {
 #pragma unroll
     for (int c = 0; c < LOADS; ++c) load(c, kb, to);
   };
   if (SPREAD == 0 && nb > 1) {
     load_all(kb0, base + STAGE);
-    constexpr int LEFT = LOADS - 1 + SN;        // stage 1, still under way
+    constexpr int LEFT = LOADS + KG * (SN - 1);      // stage 1, still under way
     static_assert(LEFT < 16, "");
     __builtin_amdgcn_s_waitcnt(LEFT | 0xf << 8 | 7 << 4);
     __builtin_amdgcn_s_barrier();
@@ -692,15 +704,15 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     meet();
   }
   if (cut) {
-    pa.cut(g.k & (QB - 1), lds, tid);
-    pb.cut(g.k & (QB - 1), lds + AT_B, tid);
+    pa.cut(g.k & (QB - 1), lds + (last - 1) * BLOCK, tid);
+    pb.cut(g.k & (QB - 1), lds + (last - 1) * BLOCK + AT_B, tid);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);      // LDS only
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
-  read_b(lds);
-  read_a(lds, 0);
+  read_b(lds + kg * BLOCK);
+  read_a(lds + kg * BLOCK, 0);
   f4 d[2][CJ];
   // All sums of a stage but the last row tile's, column block kb loaded meanwhile.
   auto row_tiles = [&](const uint8_t *l, auto live, int kb, uint32_t to) {
@@ -733,18 +745,34 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   };
   int now = 0, next = STAGE;
   for (int stage = 0; stage < nb - 1; ++stage) {
-    row_tiles(lds + now, std::true_type{}, kb0 + stage, base + next);
+    row_tiles(lds + now + kg * BLOCK, std::true_type{}, kb0 + stage * KG, base + next);
     meet();
-    if (SPREAD == 0 && stage + 2 < nb) load_all(kb0 + stage + 1, base + now);
-    read_b(lds + next);
-    read_a(lds + next, 0);
+    if (SPREAD == 0 && stage + 2 < nb) load_all(kb0 + (stage + 1) * KG, base + now);
+    read_b(lds + next + kg * BLOCK);
+    read_a(lds + next + kg * BLOCK, 0);
     add(RI - 1, d[1]);
     const int t = now;
     now = next;
     next = t;
   }
-  row_tiles(lds + now, std::false_type{}, 0, 0);
+  row_tiles(lds + now + kg * BLOCK, std::false_type{}, 0, 0);
   add(RI - 1, d[1]);
+  if constexpr (KG == 2) {                // the second half's sums to the first half
+    static_assert(WM * WN * RI * CJ * 1024 <= 2 * STAGE, "");
+    f4 *sums = reinterpret_cast<f4 *>(lds) + (wave % (WM * WN)) * RI * CJ * 64 + lane;
+    __syncthreads();
+    if (kg == 1)
+#pragma unroll
+      for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) sums[(i * CJ + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) acc[i][j] += sums[(i * CJ + j) * 64];
+  }
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
   if (gridDim.y > 1) g.c = static_cast<float *>(g.c) + (int64_t)blockIdx.y * g.m * g.n;      // a part's sums
@@ -799,7 +827,7 @@ template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(GemmArg
 
 // ---- which kernel -----------------------------------------------------------------------------------
 
-enum Kind { STRIP, TILE_64, TILE_128, TILE_128W, TILE_256 };
+enum Kind { STRIP, TILE_64, TILE_64K, TILE_128, TILE_128W, TILE_128K, TILE_256 };
 struct Choice {
   Kind kind;
   int parts;                // of the contraction, with a launch that adds them if more than one
@@ -817,7 +845,10 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //          2048 x 2048 x 512    128 x 128 on eight waves 7.3, on four 8.1, 256 x 256 13.3
 //          2048 x 4096 x 2048   128 x 128 on four waves 23.3, on eight 27.2, 256 x 256 31.5
 //          4096 x 4096 x 4096   256 x 256 tiles 63.0, 128 x 128 76.5
+//          4096 x 512 x 4096    128 x 64 in two halves 18.0, whole 21.3, 128 x 128 23.5
+//          2000 x 1000 x 8000   128 x 128 in two halves and two parts 32.7, whole in two parts 35.4
 //   exact  1024 x 1024 x 1024   128 x 64 tiles 9.4, 128 x 128 13.2, strip 23.0
+//          2048 x 2048 x 4096   128 x 128 in two halves 38.2, whole 43.0
 //          4096 x 4096 x 8192   128 x 128 on four waves 247, on eight 295, 256 x 256 (not kept) 307
 Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
   const double nb = (double)cdiv(k, QB);
@@ -846,17 +877,21 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
     tiles(TILE_64, 64, 0.57, 1.15, 3.2, 3.0);
     tiles(TILE_128W, 128, 0.66, 1.43, 4.0, 4.0);
     tiles(TILE_128, 128, 0.70, 1.10, 5.0, 5.0);
+    tiles(TILE_64K, 64, 0.47, 0.96, 4.0, 3.0);
+    tiles(TILE_128K, 128, 0.60, 1.22, 6.0, 6.0);
     const double rounds = std::ceil((double)cdiv(m, 256) * (double)cdiv(n, 256) / 256);
     offer(TILE_256, 1, 6.0 + (rounds - 1) * 4.0 + nb * rounds * 1.8);
   } else {
     tiles(TILE_64, 64, 0.75, 1.6, 3.5, 3.0);
     tiles(TILE_128W, 128, 1.2, 2.2, 4.0, 4.0);
     tiles(TILE_128, 128, 1.25, 1.85, 5.0, 5.0);
+    tiles(TILE_64K, 64, 0.67, 1.32, 4.0, 3.0);
+    tiles(TILE_128K, 128, 1.02, 2.04, 6.0, 6.0);
   }
   return best;
 }
 
-template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN, int SPREAD>
+template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN, int KG, int SPREAD>
 void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
   const dim3 grid((unsigned)(cdiv(g.m, TM) * cdiv(g.n, TN)), (unsigned)parts);
   GemmArgs h = g;
@@ -867,8 +902,8 @@ void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
     h.ldc = g.m;
     h.dt = TLR_F32;
   }
-  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN, SPREAD><<<grid, 64 * WM * WN, 0, st>>>(h);
-  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN, SPREAD><<<grid, 64 * WM * WN, 0, st>>>(h);
+  if (g.a.shift) tile_kernel<A5, B5, FAST, true, TM, TN, WM, WN, KG, SPREAD><<<grid, 64 * WM * WN * KG, 0, st>>>(h);
+  else tile_kernel<A5, B5, FAST, false, TM, TN, WM, WN, KG, SPREAD><<<grid, 64 * WM * WN * KG, 0, st>>>(h);
   if (parts == 1) return;
   const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
   if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
@@ -886,11 +921,13 @@ template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, float
   const Choice c = choose(g.m, g.n, g.k, FAST);
   switch (c.kind) {
     case STRIP: return strip_launch<A5, B5, FAST>(g, st);
-    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2, 0>(g, c.parts, ws, st);
-    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 3>(g, c.parts, ws, st);
-    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4, 0>(g, c.parts, ws, st);
+    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2, 1, 0>(g, c.parts, ws, st);
+    case TILE_64K: return tile_launch<A5, B5, FAST, 128, 64, 2, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 1, 3>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4, 1, 0>(g, c.parts, ws, st);
+    case TILE_128K: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 2, FAST ? 0 : 3>(g, c.parts, ws, st);
     case TILE_256:
-      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4, 2>(g, c.parts, ws, st);
+      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4, 1, 2>(g, c.parts, ws, st);
   }
 }
 

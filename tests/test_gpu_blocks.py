@@ -268,6 +268,35 @@ def test_product_of_few_tiles_and_in_parts(m, n, k, bfmt, ablk, dtype, fast):
     assert float(np.max(np.abs(got - (0.5 * ref - prev)) / (0.5 * tol + t.eps / 2 * (0.5 * np.abs(ref) + np.abs(prev)) + tol))) <= 1.0
 
 
+EVERY_KERNEL = [  # one shape at least for each kernel and number of parts that the library chooses, fast and exact
+    (1163, 3472, 257), (652, 2801, 1450), (138, 4130, 6719), (1397, 421, 132), (1084, 294, 1966), (713, 225, 4009),
+    (625, 769, 788), (401, 1061, 2078), (714, 278, 3517), (487, 209, 6820), (388, 4590, 133), (4157, 70, 5411),
+    (1204, 3376, 386), (403, 4186, 4363), (262, 2790, 8542), (511, 571, 2513), (531, 266, 5075), (131, 4225, 5310),
+    (260, 649, 8238), (469, 197, 8431), (146, 4167, 7021), (3900, 500, 2050), (1500, 1500, 4225)]
+
+
+@pytest.mark.parametrize("m,n,k", EVERY_KERNEL)
+@pytest.mark.parametrize("bfmt,ablk,dtype,fast", [("e4m3", 128, "bf16", True), ("e5m2", 1, "f32", False)])
+def test_every_kernel_of_the_product(m, n, k, bfmt, ablk, dtype, fast):
+    """The bounds of check_product and test_fast_product; the contraction's parts, up to eight, and halves add as many
+    float additions."""
+    from hpc_linear_algebra_amd import blocks
+    A, a = codes(m, k, "e4m3", ablk, m + n)
+    B, b = codes(n, k, bfmt, 1, m + n + 1, pad=16)
+    got = blocks.gemm(A, B, dtype=dtype, fast=fast)
+    assert torch.isfinite(got).all()
+    i, j = sorted({*range(0, m, 41), m - 1}), sorted({*range(0, n, 37), n - 1})
+    a, b, part = a[i], b[j], got[j][:, i].double().cpu().numpy()
+    ref, mag = b @ a.T, np.abs(b) @ np.abs(a).T
+    t = torch.finfo(TD[dtype])
+    tol = (min(k, 128) + k / 128 + 4 + 9) * 2.0 ** -24 * mag
+    if fast:
+        tol = tol + 2.0 ** -13 * largest(a, b, k)
+    tol = tol + t.eps / 2 * (np.abs(ref) + tol) + t.smallest_normal * t.eps
+    assert float(np.max(np.abs(part - ref) / tol)) <= 1.0
+    assert torch.equal(got, blocks.gemm(A, B, dtype=dtype, fast=fast))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(33, 5, 200), (301, 90, 260), (520, 300, 384)])
 def test_product_adds_into_a_strided_unaligned_c(m, n, k, dtype):

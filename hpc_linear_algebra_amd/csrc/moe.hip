@@ -30,6 +30,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int MAX_TOKENS = 256, MAX_EXPERTS = 512, MAX_TOPK = 16;
 constexpr int RT = 16;                    // tokens of a router workgroup
+constexpr int FEW = 256;                  // assignments that an expert's workgroup looks through itself
 constexpr int MAX_SPLITS = 4;             // workgroups that share a router tile's columns
 constexpr int ROUTED = 32, BLOCKS = 64;   // counters: 0.. router groups, ROUTED all groups, BLOCKS.. row blocks of y
 
@@ -73,6 +74,7 @@ struct MoeArgs {
   int32_t *order;           // assignments (token * topk + choice) by expert
   double *logits;           // splits x tokens x experts: parts of the router product
   int32_t splits;
+  int32_t sorted;           // the experts' workgroups take their assignments from the router's tables
   uint16_t *hi, *lo;        // tokens*topk x inter: silu(g) u as hi + lo
   float *part;              // tokens*topk x hidden: the experts' outputs
 };
@@ -321,6 +323,7 @@ template <typename H> __global__ __launch_bounds__(64 * RW) void router_kernel(M
   }
   if (!arrive(a.arrived + blockIdx.y, gridDim.x * gridDim.z, &last)) return;
   if (t0 + wave < a.tokens) choose(a, t0 + wave, lane);
+  if (!a.sorted) return;
   if (arrive(a.arrived + ROUTED, gridDim.y, &last)) sort<64 * RW>(a);
 }
 
@@ -449,11 +452,46 @@ template <typename H> __device__ __forceinline__ void put_act(const MoeArgs &a, 
 
 constexpr int WV = 4;       // waves of an expert workgroup
 
+// The expert of this workgroup's grid row and its assignments, order[0 .. count).
+// SORTED: from the router's tables.  Otherwise every workgroup looks through the
+// choices (at most FEW, one a thread): with fewer of them than experts a grid row
+// is an assignment, which stands for its expert when no earlier one has the same,
+// else a grid row is an expert.  False if there is nothing to do.
+template <bool SORTED>
+__device__ __forceinline__ bool work(const MoeArgs &a, int *list, int *places, int &e, int &count, const int *&order) {
+  if constexpr (SORTED) {
+    if ((int)blockIdx.y >= *a.units) return false;
+    const int4 unit = a.unit[blockIdx.y];
+    e = unit.x;
+    count = unit.z;
+    order = a.order + unit.y;
+    return true;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.tokens * a.topk;
+  const bool by_row = n < a.experts;
+  e = by_row ? a.ids[blockIdx.y] : (int)blockIdx.y;
+  const bool hit = tid < n && a.ids[min(tid, n - 1)] == e;
+  const uint64_t b = __ballot(hit);
+  if (lane == 0) places[wave] = __popcll(b);
+  __syncthreads();
+  int before = 0;
+  count = 0;
+#pragma unroll
+  for (int w = 0; w < WV; ++w) {
+    before += w < wave ? places[w] : 0;
+    count += places[w];
+  }
+  if (hit) list[before + __popcll(b & ((1ull << lane) - 1))] = tid;
+  __syncthreads();
+  order = list;
+  return count > 0 && (!by_row || list[0] == (int)blockIdx.y);
+}
+
 // silu(G x) * (U x) for 16 of an expert's inter rows and 16 NJ of its tokens.
 template <typename H, bool W8, int NJ, int UNROLL>
-__device__ __forceinline__ void gate_up(const MoeArgs &a, int4 unit, int n0, float (*part)[2][4][64]) {
+__device__ __forceinline__ void gate_up(const MoeArgs &a, int e, int count, const int *order, int n0, float (*part)[2][4][64]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, i0 = blockIdx.x * 16, e = unit.x, count = unit.z;
+  const int r = lane & 15, q = lane >> 4, i0 = blockIdx.x * 16;
   const int64_t es = W8 ? 1 : 2;
   const uint8_t *w[2];
   const float *ws[2] = {nullptr, nullptr};
@@ -464,7 +502,6 @@ __device__ __forceinline__ void gate_up(const MoeArgs &a, int4 unit, int n0, flo
     w[i] = a.gate_up + ((int64_t)e * 2 * a.inter + row + r) * a.hidden * es;
     if constexpr (W8) ws[i] = a.gate_up_scales + (int64_t)e * ((a.hidden + 127) / 128) * wlds + (row >> 7);
   }
-  const int32_t *order = a.order + unit.y;
   const uint16_t *x[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) x[j] = a.x + (order[min(n0 + 16 * j + r, count - 1)] / a.topk) * a.ldx;
@@ -494,20 +531,22 @@ __device__ __forceinline__ void gate_up(const MoeArgs &a, int4 unit, int n0, flo
   }
 }
 
-template <typename H, bool W8> __global__ __launch_bounds__(64 * WV) void gate_up_kernel(MoeArgs a) {
+template <typename H, bool W8, bool SORTED> __global__ __launch_bounds__(64 * WV) void gate_up_kernel(MoeArgs a) {
   __shared__ float part[WV][2][4][64];
-  if ((int)blockIdx.y >= *a.units) return;
-  const int4 unit = a.unit[blockIdx.y];
+  __shared__ int list[SORTED ? 1 : FEW], places[WV];
+  int e, count;
+  const int *order;
+  if (!work<SORTED>(a, list, places, e, count, order)) return;
   int n0 = 0;
-  for (; n0 + 16 < unit.z; n0 += 32) gate_up<H, W8, 2, 1>(a, unit, n0, part);
-  if (n0 < unit.z) gate_up<H, W8, 1, 2>(a, unit, n0, part);
+  for (; n0 + 16 < count; n0 += 32) gate_up<H, W8, 2, 1>(a, e, count, order, n0, part);
+  if (n0 < count) gate_up<H, W8, 1, 2>(a, e, count, order, n0, part);
 }
 
 // 16 RTILE rows of an expert's down product for 16 NJ of its tokens.
 template <typename H, bool W8, int RTILE, int NJ, int UNROLL>
-__device__ __forceinline__ void down(const MoeArgs &a, int4 unit, int n0, float (*part)[RTILE][4][64]) {
+__device__ __forceinline__ void down(const MoeArgs &a, int e, int count, const int *order, int n0, float (*part)[RTILE][4][64]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, h0 = blockIdx.x * 16 * RTILE, e = unit.x, count = unit.z;
+  const int r = lane & 15, q = lane >> 4, h0 = blockIdx.x * 16 * RTILE;
   const int64_t es = W8 ? 1 : 2;
   const int64_t wlds = (a.hidden + 127) / 128;
   const uint8_t *w[RTILE];
@@ -518,7 +557,6 @@ __device__ __forceinline__ void down(const MoeArgs &a, int4 unit, int n0, float 
     w[i] = a.down + ((int64_t)e * a.hidden + h + r) * a.inter * es;
     ws[i] = W8 ? a.down_scales + (int64_t)e * ((a.inter + 127) / 128) * wlds + (h >> 7) : nullptr;
   }
-  const int32_t *order = a.order + unit.y;
   const uint16_t *x[NJ], *x2[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -574,18 +612,23 @@ template <typename H, bool SAME_LAUNCH> __device__ __forceinline__ void add_part
 // until it knows whether it is the last (8-bit weights, 13 tokens: 110 us with,
 // 104 without); 4 waves a SIMD for 8-bit weights, whose two groups in flight
 // would take 148 registers.
-template <typename H, bool W8, int RTILE>
+template <typename H, bool W8, int RTILE, bool SORTED>
 __global__ __launch_bounds__(64 * WV, W8 && RTILE == 2 ? 4 : 1) void down_kernel(MoeArgs a) {
   __shared__ float part[WV][RTILE][4][64];
-  const int units = *a.units;
-  if ((int)blockIdx.y >= units) return;
-  const int4 unit = a.unit[blockIdx.y];
-  int n0 = 0;
-  for (; n0 + 16 < unit.z; n0 += 32) down<H, W8, RTILE, 2, 1>(a, unit, n0, part);
-  if (n0 < unit.z) down<H, W8, RTILE, 1, W8 && RTILE == 2 ? 1 : 2>(a, unit, n0, part);
+  __shared__ int list[SORTED ? 1 : FEW], places[WV];
+  int e, count;
+  const int *order;
+  const bool some = work<SORTED>(a, list, places, e, count, order);
+  if (SORTED && !some) return;
+  if (some) {
+    int n0 = 0;
+    for (; n0 + 16 < count; n0 += 32) down<H, W8, RTILE, 2, 1>(a, e, count, order, n0, part);
+    if (n0 < count) down<H, W8, RTILE, 1, W8 && RTILE == 2 ? 1 : 2>(a, e, count, order, n0, part);
+  }
   if constexpr (RTILE == 1) {
     __shared__ int last;
-    if (!arrive(a.arrived + BLOCKS + blockIdx.x, units, &last)) return;
+    // rows without an expert count too where their number is not known
+    if (!arrive(a.arrived + BLOCKS + blockIdx.x, SORTED ? *a.units : gridDim.y, &last)) return;
     for (int x = threadIdx.x; x < 16 * a.tokens; x += 64 * WV) add_parts<H, true>(a, x >> 4, blockIdx.x * 16 + (x & 15));
   }
 }
@@ -727,21 +770,32 @@ template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeA
   if (h < a.hidden) add_parts<H, false>(a, blockIdx.y, h);
 }
 
-template <typename H, bool W8> void launch(const MoeArgs &a, hipStream_t st) {
+template <typename H, bool W8> void launch(MoeArgs &a, hipStream_t st) {
+  // Sorting takes the router 3 us; without it every workgroup of an expert spends
+  // a little (4 tokens, 4 of 32 experts of 1024 x 512: 26.2 us sorted, 23.9 not;
+  // 8 tokens 32.2 and 32.8; 13 tokens, 6 of 96 of 2064 x 1168: 100 and 103).
+  const int slots = std::min(a.tokens * a.topk, a.experts);
+  a.sorted = a.tokens * a.topk > FEW || slots * (a.inter / 16) >= 1024;
   if (a.tokens == 1) router_one_kernel<H><<<dim3((a.experts + 3) / 4), 256, 0, st>>>(a);
   else router_kernel<H><<<dim3((a.experts + 15) / 16, (a.tokens + RT - 1) / RT, a.splits), 64 * RW, 0, st>>>(a);
-  const int slots = std::min(a.tokens * a.topk, a.experts);
   if (a.tokens == 1) {
     gate_up_one_kernel<H, W8><<<dim3(a.inter / (4 * ONE_PAIRS), a.topk), 256, 0, st>>>(a);
     down_one_kernel<H, W8><<<dim3(a.hidden / ONE_ROWS), 256, 0, st>>>(a);
     return;
   }
-  gate_up_kernel<H, W8><<<dim3(a.inter / 16, slots), 64 * WV, 0, st>>>(a);
+  const bool sorted = a.sorted != 0;
+  const dim3 gate(a.inter / 16, slots);
+  if (sorted) gate_up_kernel<H, W8, true><<<gate, 64 * WV, 0, st>>>(a);
+  else gate_up_kernel<H, W8, false><<<gate, 64 * WV, 0, st>>>(a);
   if (slots * (a.hidden / 32) < 2048) {
-    down_kernel<H, W8, 1><<<dim3(a.hidden / 16, slots), 64 * WV, 0, st>>>(a);
+    const dim3 rows(a.hidden / 16, slots);
+    if (sorted) down_kernel<H, W8, 1, true><<<rows, 64 * WV, 0, st>>>(a);
+    else down_kernel<H, W8, 1, false><<<rows, 64 * WV, 0, st>>>(a);
     return;
   }
-  down_kernel<H, W8, 2><<<dim3((a.hidden + 31) / 32, slots), 64 * WV, 0, st>>>(a);
+  const dim3 rows((a.hidden + 31) / 32, slots);
+  if (sorted) down_kernel<H, W8, 2, true><<<rows, 64 * WV, 0, st>>>(a);
+  else down_kernel<H, W8, 2, false><<<rows, 64 * WV, 0, st>>>(a);
   combine_kernel<H><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, st>>>(a);
 }
 
@@ -835,7 +889,7 @@ tlr_status moe(const tlr_moe_layer *l, int32_t tokens, const void *X, int64_t ld
             static_cast<const uint8_t *>(l->down), l->gate_up_scales, l->down_scales, ids, weights,
             reinterpret_cast<int32_t *>(b + p.arrived), reinterpret_cast<int32_t *>(b + p.units),
             reinterpret_cast<int4 *>(b + p.unit), reinterpret_cast<int32_t *>(b + p.order),
-            reinterpret_cast<double *>(b + p.logits), splits_of(l, tokens), reinterpret_cast<uint16_t *>(b + p.hi),
+            reinterpret_cast<double *>(b + p.logits), splits_of(l, tokens), 0, reinterpret_cast<uint16_t *>(b + p.hi),
             reinterpret_cast<uint16_t *>(b + p.lo), reinterpret_cast<float *>(b + p.part)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (l->dt == TLR_F16) w8 ? launch<_Float16, true>(a, hs) : launch<_Float16, false>(a, hs);

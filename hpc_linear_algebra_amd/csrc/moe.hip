@@ -606,12 +606,13 @@ template <typename H, bool SAME_LAUNCH> __device__ __forceinline__ void add_part
   a.y[t * a.ldy + h] = __builtin_bit_cast(uint16_t, (H)s);
 }
 
-// Down products of one expert and 16 RTILE rows of y.  RTILE 1: the workgroup
-// that is last with its rows adds the parts.  RTILE 2 (many workgroups): left to
-// a launch of its own, since a workgroup would hold its place for another 2 us
-// until it knows whether it is the last (8-bit weights, 13 tokens: 110 us with,
-// 104 without); 4 waves a SIMD for 8-bit weights, whose two groups in flight
-// would take 148 registers.
+// Down products of one expert and 16 RTILE rows of y.  RTILE 1 (few workgroups):
+// the workgroup that is last with its rows adds the parts.  RTILE 2: left to a
+// launch of its own, since a workgroup would hold its place for another 2 us until
+// it knows whether it is the last (2 tokens, 1 of 8 experts of 512 x 256: 13.7 us
+// with, 14.5 without; 4 tokens, 8 of 64: 21.6 and 18.6; 8 tokens, 4 of 32 of 1024 x
+// 512 in e4m3: 28.1 and 23.4); 4 waves a SIMD for 8-bit weights, whose two groups
+// in flight would take 148 registers.
 template <typename H, bool W8, int RTILE, bool SORTED>
 __global__ __launch_bounds__(64 * WV, W8 && RTILE == 2 ? 4 : 1) void down_kernel(MoeArgs a) {
   __shared__ float part[WV][RTILE][4][64];
@@ -772,8 +773,8 @@ template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeA
 
 template <typename H, bool W8> void launch(MoeArgs &a, hipStream_t st) {
   // Sorting takes the router 3 us; without it every workgroup of an expert spends
-  // a little (4 tokens, 4 of 32 experts of 1024 x 512: 26.2 us sorted, 23.9 not;
-  // 8 tokens 32.2 and 32.8; 13 tokens, 6 of 96 of 2064 x 1168: 100 and 103).
+  // a little (4 tokens, 4 of 32 experts of 1024 x 512: 2 us less without; 8 tokens
+  // 0.5 more, 13 tokens, 6 of 96 of 2064 x 1168, 3 more).
   const int slots = std::min(a.tokens * a.topk, a.experts);
   a.sorted = a.tokens * a.topk > FEW || slots * (a.inter / 16) >= 1024;
   if (a.tokens == 1) router_one_kernel<H><<<dim3((a.experts + 3) / 4), 256, 0, st>>>(a);
@@ -787,7 +788,7 @@ template <typename H, bool W8> void launch(MoeArgs &a, hipStream_t st) {
   const dim3 gate(a.inter / 16, slots);
   if (sorted) gate_up_kernel<H, W8, true><<<gate, 64 * WV, 0, st>>>(a);
   else gate_up_kernel<H, W8, false><<<gate, 64 * WV, 0, st>>>(a);
-  if (slots * (a.hidden / 32) < 2048) {
+  if (slots * (a.hidden / 32) < 200) {
     const dim3 rows(a.hidden / 16, slots);
     if (sorted) down_kernel<H, W8, 1, true><<<rows, 64 * WV, 0, st>>>(a);
     else down_kernel<H, W8, 1, false><<<rows, 64 * WV, 0, st>>>(a);

@@ -66,7 +66,7 @@ PyObject *wrap(const at::Tensor &t) {
 PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 5 || !THPVariable_Check(args[0])) return value_error("quantize: a tensor and four numbers");
-  const at::Tensor &x = THPVariable_Unpack(args[0]);
+  at::Tensor x = THPVariable_Unpack(args[0]);
   const int dt = code_of(x);
   if (dt < 0 || x.dim() != 2 || !x.is_cuda())
     return value_error("quantize: a 2-d float32, float16 or bfloat16 tensor on a GPU is needed");
@@ -75,8 +75,9 @@ PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   const int64_t rows = x.size(0), k = x.size(1);
   if (k > 1 && x.stride(1) != 1) return value_error("quantize: the rows of x have to be contiguous");
-  const int64_t ldx = rows > 1 ? x.stride(0) : std::max<int64_t>({x.stride(0), k, 1});
   const c10::DeviceGuard guard(x.device());
+  if (rows > 1 && x.stride(0) < k) x = x.clone(at::MemoryFormat::Contiguous);     // an expanded row
+  const int64_t ldx = rows > 1 ? x.stride(0) : std::max<int64_t>({x.stride(0), k, 1});
   const at::ScalarType f8 = fmt == TLR_E5M2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn;
   const Result a(straight, rows, k, block, f8, x.device()), b(transposed, k, rows, block, f8, x.device());
   const tlr_status st = quantize_entry((tlr_dtype)dt, (tlr_dtype)fmt, (int32_t)block, rows, k, x.data_ptr(), ldx, a.code_ptr(),
@@ -137,7 +138,8 @@ PyObject *moe(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const int64_t tokens = x.size(0);
   if (tokens > most) return value_error("MoELayer: more tokens than the layer was made for");
   const c10::DeviceGuard guard(x.device());
-  if (x.stride(1) != 1 || reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 != 0 || (tokens > 1 && x.stride(0) % 8 != 0))
+  if (x.stride(1) != 1 || reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 != 0 ||
+      (tokens > 1 && (x.stride(0) % 8 != 0 || x.stride(0) < layer->hidden)))
     x = x.clone(at::MemoryFormat::Contiguous);      // 16-byte aligned rows; a fresh allocation starts aligned
   const at::TensorOptions on = at::TensorOptions().device(x.device());
   const at::Tensor y = at::empty({tokens, layer->hidden}, on.dtype(x.scalar_type()));

@@ -461,3 +461,13 @@ def test_linear_of_strided_and_broadcast_inputs(dtype):
     gx, = torch.autograd.grad(y.sum(), one, create_graph=True)
     with pytest.raises(RuntimeError):
         gx.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_of_an_expanded_row(dtype):
+    from hpc_linear_algebra_amd import blocks
+    row = inputs(1, 144, dtype, 7).cuda()
+    got, want = (blocks.quantize(x, transposed=True) for x in (row.expand(5, 144), row.expand(5, 144).contiguous()))
+    for a, b in zip(got, want):
+        assert torch.equal(a.scales, b.scales)
+        assert torch.equal(a.codes[:, :a.k].view(torch.uint8), b.codes[:, :b.k].view(torch.uint8))

@@ -180,3 +180,29 @@ def test_captured_into_a_graph():
         assert all(torch.equal(a, b.roll(k, 0)) for a, b in zip(got, want))
         eager = layer(x)                                 # the same workspace, in order
         assert all(torch.equal(a, b) for a, b in zip(eager, want))
+
+
+@pytest.mark.parametrize("tokens,hidden,inter,experts,topk", [
+    (8, 64, 256, 64, 8),      # routed one by one, sorted, parts added by a launch
+    (16, 64, 1024, 16, 2),    # routed one by one, sorted, parts added by the down product
+    (16, 96, 64, 32, 3),      # routed one by one, lists by the experts
+    (12, 64, 48, 64, 4),      # routed together, lists by the experts
+    (17, 64, 1024, 16, 2),    # routed together, sorted, parts added by the down product
+    (33, 400, 64, 24, 8)])    # routed together, sorted, parts added by a launch
+@pytest.mark.parametrize("weights", ["bf16", "e4m3"])
+def test_every_way_through_the_kernels(tokens, hidden, inter, experts, topk, weights):
+    t = make(tokens, hidden, inter, experts, "bf16", weights, tokens + experts)
+    layer, x = layer_of(t, topk)
+    want = reference(t, topk, True)
+    for _ in range(3):                                   # the counters are back at 0
+        check(layer(x), want)
+
+
+def test_expanded_and_transposed_tokens():
+    t = make(6, 80, 48, 8, "f16", "f16", 9)
+    layer, x = layer_of(t, 2)
+    want = layer(x)
+    back = x.t().contiguous().t()
+    assert not back.is_contiguous() and all(torch.equal(a, b) for a, b in zip(layer(back), want))
+    one = layer(x[:1].expand(5, 80).contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(layer(x[:1].expand(5, 80)), one))

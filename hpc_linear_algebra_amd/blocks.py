@@ -151,13 +151,19 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
     return got
 
 
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x as a matrix of contiguous rows, copied only where they are not."""
+    x = x.reshape(x.shape[:-1].numel(), x.shape[-1])
+    return x if x.stride(1) == 1 else x.contiguous()
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, grad_fmt):
-        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        x2 = _rows(x)
         need_x, need_w = ctx.needs_input_grad[:2]
         x8, x8t = quantize(x2, transposed=need_w)
-        w8, w8t = quantize(w.contiguous(), block=BLOCK, transposed=need_x)
+        w8, w8t = quantize(_rows(w), block=BLOCK, transposed=need_x)
         ctx.x8t, ctx.w8t, ctx.grad_fmt = x8t, w8t, grad_fmt
         ctx.shape, ctx.types = x.shape, (x.dtype, w.dtype)
         out = torch.empty((x2.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
@@ -169,7 +175,7 @@ class _Linear(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad[:2]
         dx = dw = None
         if need_x or need_w:
-            dy = dy.reshape(-1, dy.shape[-1]).contiguous()
+            dy = _rows(dy)
             d8, d8t = quantize(dy, fmt=ctx.grad_fmt, straight=need_x, transposed=need_w)
             if need_x:
                 dx = torch.empty((dy.shape[0], ctx.shape[-1]), dtype=ctx.types[0], device=dy.device)

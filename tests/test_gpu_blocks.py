@@ -471,3 +471,27 @@ def test_quantize_of_an_expanded_row(dtype):
     for a, b in zip(got, want):
         assert torch.equal(a.scales, b.scales)
         assert torch.equal(a.codes[:, :a.k].view(torch.uint8), b.codes[:, :b.k].view(torch.uint8))
+
+
+def test_linear_of_slices_and_of_nothing():
+    """Rows at a stride are read where they are; no tokens and no columns give empty sums."""
+    from hpc_linear_algebra_amd import blocks
+    g = torch.Generator().manual_seed(8)
+    wide = torch.randn(2, 9, 300, generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn(40, 200, generator=g) / 14).to(torch.bfloat16).cuda()
+    dy = torch.randn(2, 9, 90, generator=g).to(torch.bfloat16).cuda()
+    results = []
+    for copy in (False, True):
+        x, v = wide[:, :, 7:151].detach(), w[:, 3:147].detach()
+        x, v = (t.contiguous() if copy else t for t in (x, v))
+        x, v, d = x.requires_grad_(), v.requires_grad_(), dy[:, :, 5:45]
+        y = blocks.linear(x, v)
+        results.append((y, *torch.autograd.grad(y, (x, v), d.contiguous() if copy else d)))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    for tokens, k in ((0, 144), (5, 0)):
+        x, v = (torch.ones(r, k, device="cuda", dtype=torch.bfloat16, requires_grad=True) for r in (tokens, 40))
+        y = blocks.linear(x, v)
+        assert y.shape == (tokens, 40) and not y.any()
+        dx, dw = torch.autograd.grad(y, (x, v), torch.ones_like(y))
+        assert dx.shape == x.shape and dw.shape == v.shape and not dw.any()

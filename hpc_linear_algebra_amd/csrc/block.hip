@@ -847,6 +847,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //          4096 x 4096 x 4096   256 x 256 tiles 63.0, 128 x 128 76.5
 //          4096 x 512 x 4096    128 x 64 in two halves 18.0, whole 21.3, 128 x 128 23.5
 //          2000 x 1000 x 8000   128 x 128 in two halves and two parts 32.7, whole in two parts 35.4
+//          4096 x 1024 x 4096   128 x 128 in two halves 24.6, on eight waves 25.9
 //   exact  1024 x 1024 x 1024   128 x 64 tiles 9.4, 128 x 128 13.2, strip 23.0
 //          2048 x 2048 x 4096   128 x 128 in two halves 38.2, whole 43.0
 //          4096 x 4096 x 8192   128 x 128 on four waves 247, on eight 295, 256 x 256 (not kept) 307
@@ -869,16 +870,16 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
       const double t = (double)cdiv(m, 128) * (double)cdiv(n, tn) * parts;
       const double rounds = std::ceil(t / 512), rest = t - 512 * (rounds - 1);
       double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
-      if (parts > 1) us += 3.0 + parts * (double)m * (double)n * 2.5e-6;
+      if (parts > 1) us += 2.8 + parts * (0.1 + (double)m * (double)n * 2.1e-6);
       offer(kind, parts, us);
     }
   };
   if (fast) {
     tiles(TILE_64, 64, 0.57, 1.15, 3.2, 3.0);
-    tiles(TILE_128W, 128, 0.66, 1.43, 4.0, 4.0);
+    tiles(TILE_128W, 128, 0.69, 1.48, 3.9, 4.0);
     tiles(TILE_128, 128, 0.70, 1.10, 5.0, 5.0);
-    tiles(TILE_64K, 64, 0.47, 0.96, 4.0, 3.0);
-    tiles(TILE_128K, 128, 0.60, 1.22, 6.0, 6.0);
+    tiles(TILE_64K, 64, 0.47, 0.96, 3.8, 3.0);
+    tiles(TILE_128K, 128, 0.56, 1.25, 6.4, 5.5);
     const double rounds = std::ceil((double)cdiv(m, 256) * (double)cdiv(n, 256) / 256);
     offer(TILE_256, 1, 6.0 + (rounds - 1) * 4.0 + nb * rounds * 1.8);
   } else {

@@ -272,7 +272,10 @@ EVERY_KERNEL = [  # one shape at least for each kernel and number of parts that 
     (1163, 3472, 257), (652, 2801, 1450), (138, 4130, 6719), (1397, 421, 132), (1084, 294, 1966), (713, 225, 4009),
     (625, 769, 788), (401, 1061, 2078), (714, 278, 3517), (487, 209, 6820), (388, 4590, 133), (4157, 70, 5411),
     (1204, 3376, 386), (403, 4186, 4363), (262, 2790, 8542), (511, 571, 2513), (531, 266, 5075), (131, 4225, 5310),
-    (260, 649, 8238), (469, 197, 8431), (146, 4167, 7021), (3900, 500, 2050), (1500, 1500, 4225)]
+    (260, 649, 8238), (469, 197, 8431), (146, 4167, 7021), (3900, 500, 2050), (1500, 1500, 4225),
+    (658, 681, 2745), (517, 387, 4418), (643, 679, 9975), (544, 793, 7155), (37, 8384, 4920), (17, 5229, 7133),
+    (394, 532, 14218), (1090, 903, 8397), (2000, 1000, 8000), (132, 1049, 10835), (2049, 1030, 4100),
+    (133, 2107, 7711), (434, 536, 19823), (324, 468, 5188)]
 
 
 @pytest.mark.parametrize("m,n,k", EVERY_KERNEL)

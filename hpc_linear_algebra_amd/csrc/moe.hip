@@ -293,7 +293,7 @@ static_assert(RW == RT, "a wave chooses for each token");
 // supplies columns 8 q .. + 7 of expert row r and of token r and holds the sums
 // of experts q + 4 v and token r.  The vector units took 20 us for 64 tokens of
 // 128 experts (2048 columns), much of it converting every product; here every
-// entry is converted once a tile: 14 us, 3.5 of them the product, the rest loads
+// entry is converted once a tile: 13 us, 3.5 of them the product, the rest loads
 // and counts from one workgroup to the next.  The workgroup that is done last
 // with its tokens chooses their experts, a wave per token, and the last of all
 // sorts the assignments.

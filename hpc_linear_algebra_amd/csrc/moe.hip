@@ -614,9 +614,9 @@ template <typename H, bool SAME_LAUNCH> __device__ __forceinline__ void add_part
 // Down products of one expert and 16 RTILE rows of y.  RTILE 1 (few workgroups):
 // the workgroup that is last with its rows adds the parts.  RTILE 2: left to a
 // launch of its own, since a workgroup would hold its place for another 2 us until
-// it knows whether it is the last (2 tokens, 1 of 8 experts of 512 x 256: 13.7 us
-// with, 14.5 without; 4 tokens, 8 of 64: 21.6 and 18.6; 8 tokens, 4 of 32 of 1024 x
-// 512 in e4m3: 28.1 and 23.4); 4 waves a SIMD for 8-bit weights, whose two groups
+// it knows whether it is the last (2 tokens, 1 of 8 experts of 512 x 256: 12.7 us
+// with, 14.2 without; 16 tokens, 2 of 8 of 512 x 1024: 17.5 and 18.3; 4 tokens, 8
+// of 64 of 512 x 256: 20.6 and 17.5); 4 waves a SIMD for 8-bit weights, whose two groups
 // in flight would take 148 registers.
 template <typename H, bool W8, int RTILE, bool SORTED>
 __global__ __launch_bounds__(64 * WV, W8 && RTILE == 2 ? 4 : 1) void down_kernel(MoeArgs a) {
@@ -777,11 +777,12 @@ template <typename H> __global__ __launch_bounds__(256) void combine_kernel(MoeA
 }
 
 template <typename H, bool W8> void launch(MoeArgs &a, hipStream_t st) {
-  // Sorting takes the router 3 us; without it every workgroup of an expert spends
-  // a little (4 tokens, 4 of 32 experts of 1024 x 512: 2 us less without; 8 tokens
-  // 0.5 more, 13 tokens, 6 of 96 of 2064 x 1168, 3 more).
+  // Sorting takes the router 2 - 3 us; without it every workgroup of an expert
+  // spends a little.  4 tokens, 4 of 32 experts of 1024 x 512: 21.2 us without,
+  // 23.8 sorted; 16 tokens 29.6 and 32.0; 8 tokens in e4m3 21.4 and 23.1; 10 tokens,
+  // 8 of 96, 53.1 and 50.0; 13 tokens, 6 of 96 of 2064 x 1168, 102.3 and 99.3.
   const int slots = std::min(a.tokens * a.topk, a.experts);
-  a.sorted = a.tokens > 1 && (a.tokens * a.topk > FEW || slots * (a.inter / 16) >= 1024);
+  a.sorted = a.tokens > 1 && (a.tokens * a.topk > FEW || slots * (a.inter / 16) >= 2048);
   if (singly(a.tokens, a.experts)) router_one_kernel<H><<<dim3((a.experts + 3) / 4, a.tokens), 256, 0, st>>>(a);
   else router_kernel<H><<<dim3((a.experts + 15) / 16, (a.tokens + RT - 1) / RT, a.splits), 64 * RW, 0, st>>>(a);
   if (a.tokens == 1) {

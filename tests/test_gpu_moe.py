@@ -183,11 +183,13 @@ def test_captured_into_a_graph():
 
 
 @pytest.mark.parametrize("tokens,hidden,inter,experts,topk", [
-    (8, 64, 256, 64, 8),      # routed one by one, sorted, parts added by a launch
-    (16, 64, 1024, 16, 2),    # routed one by one, sorted, parts added by the down product
+    (8, 64, 256, 64, 8), (16, 64, 1024, 16, 2), (17, 64, 1024, 16, 2),
+    (8, 128, 512, 64, 8),     # routed one by one, sorted, parts added by a launch
+    (16, 64, 2048, 16, 2),    # routed one by one, sorted, parts added by the down product
     (16, 96, 64, 32, 3),      # routed one by one, lists by the experts
-    (12, 64, 48, 64, 4),      # routed together, lists by the experts
-    (17, 64, 1024, 16, 2),    # routed together, sorted, parts added by the down product
+    (12, 64, 48, 64, 4),      # routed together, lists by the experts, parts added by the down product
+    (13, 256, 48, 64, 4),     # routed together, lists by the experts, parts added by a launch
+    (17, 64, 2048, 32, 2),    # routed together, sorted, parts added by the down product
     (33, 400, 64, 24, 8)])    # routed together, sorted, parts added by a launch
 @pytest.mark.parametrize("weights", ["bf16", "e4m3"])
 def test_every_way_through_the_kernels(tokens, hidden, inter, experts, topk, weights):

@@ -498,3 +498,23 @@ def test_linear_of_slices_and_of_nothing():
         assert y.shape == (tokens, 40) and not y.any()
         dx, dw = torch.autograd.grad(y, (x, v), torch.ones_like(y))
         assert dx.shape == x.shape and dw.shape == v.shape and not dw.any()
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_results_without_gradients(mode):
+    """Codes and scales are ordinary tensors in every mode: copied, changed and multiplied on their own."""
+    from hpc_linear_algebra_amd import blocks
+    x = inputs(40, 300, "bf16", 11).cuda()
+    want = blocks.quantize(x)[0].dequantize()
+    with mode():
+        q, qt = blocks.quantize(x, transposed=True)
+        codes, scales = q.codes.clone(), q.scales.clone()
+        assert torch.equal(q.dequantize(), want)
+        y = blocks.gemm(q, q)
+        q.scales.mul_(2)
+        assert torch.equal(q.codes.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(q.scales, 2 * scales)
+        assert torch.equal(q.dequantize(), 2 * want)
+        assert torch.equal(blocks.gemm(q, q).float(), 4 * y.float())
+        kept = qt.scales.clone()
+        qt.codes.view(torch.uint8).zero_()
+        assert torch.equal(qt.scales, kept) and not qt.dequantize().any()

@@ -54,9 +54,16 @@ class BlockScaled:
     block    rows of a block: 1 or 128
     """
 
-    __slots__ = ("codes", "scales", "rows", "k", "block", "_c", "_at")
+    __slots__ = ("codes", "scales", "rows", "k", "block")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, block: int):
+        self.codes, self.scales, self.rows, self.k, self.block = codes, scales, rows, k, block
+        self.c      # its checks
+
+    @property
+    def c(self) -> T.tlr_block_matrix:
+        """What the C ABI takes, made anew from the tensors as they are: it points into them and does not keep them."""
+        codes, scales, rows, k, block = self.codes, self.scales, self.rows, self.k, self.block
         if codes.dtype not in _CODE or codes.dim() != 2:
             raise ValueError("codes: a 2-d float8_e4m3fn or float8_e5m2 tensor is needed")
         if block not in (1, BLOCK):
@@ -72,25 +79,7 @@ class BlockScaled:
             raise ValueError("codes: every row has to be readable up to a multiple of 16 entries")
         if tuple(scales.shape) != (nq, nr) or (nr > 1 and scales.stride(1) != 1):
             raise ValueError(f"scales: shape {(nq, nr)}, rows contiguous, is needed")
-        self.codes, self.scales, self.rows, self.k, self.block = codes, scales, rows, k, block
-        self._c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, lds, block, _CODE[codes.dtype])
-        self._at = 0
-
-    @property
-    def c(self) -> T.tlr_block_matrix:
-        """What the C ABI takes; made when a product first asks for it."""
-        if self._c is None:
-            codes, scales = self.codes, self.scales
-            self._c = T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), codes.shape[1], scales.shape[1], self.block,
-                                         _CODE[codes.dtype])
-        return self._c
-
-    @property
-    def address(self) -> int:
-        """Where c is, as long as this object lives."""
-        if not self._at:
-            self._at = ctypes.addressof(self.c)
-        return self._at
+        return T.tlr_block_matrix(codes.data_ptr(), scales.data_ptr(), ld, lds, block, _CODE[codes.dtype])
 
     def dequantize(self) -> torch.Tensor:
         """The (rows, k) float32 matrix that the codes and scales stand for."""
@@ -102,7 +91,7 @@ class BlockScaled:
 
 def _made(codes: torch.Tensor, scales: torch.Tensor, rows: int, k: int, block: int) -> BlockScaled:
     q = BlockScaled.__new__(BlockScaled)        # right by construction: the checks cost more than the launch
-    q.codes, q.scales, q.rows, q.k, q.block, q._c, q._at = codes, scales, rows, k, block, None, 0
+    q.codes, q.scales, q.rows, q.k, q.block = codes, scales, rows, k, block
     return q
 
 
@@ -144,8 +133,8 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
             raise ValueError("gemm: beta needs an out to add to")
     elif tuple(out.shape) != (n, m) or out.dtype not in _DT or out.device != device or (m > 1 and out.stride(1) != 1):
         raise ValueError(f"gemm: out has to be a ({n}, {m}) float32, float16 or bfloat16 tensor with contiguous rows")
-    got = binding().gemm(A.address, B.address, m, n, A.k, alpha, beta, out, _NEW[dtype], B.codes,
-                      T.TLR_BLOCK_FAST if fast else 0, _gemm_workspace(m, n, A.k))
+    got = binding().gemm(A.codes, A.scales, A.block, B.codes, B.scales, B.block, m, n, A.k, alpha, beta, out, _NEW[dtype],
+                         T.TLR_BLOCK_FAST if fast else 0, _gemm_workspace(m, n, A.k))
     if type(got) is int:
         T._check(got, "tlr_block_gemm")
     return got

@@ -105,31 +105,59 @@ PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// gemm(address of A's tlr_block_matrix, of B's, m, n, k, alpha, beta, out or None, type of a new one, a tensor on
-// their device, flags, workspace bytes) -> out or a status
+// An operand of a product from its tensors as they are now (they may have been replaced or changed since their matrix
+// was made); null, or what is wrong with them.
+const char *operand(const at::Tensor &codes, const at::Tensor &scales, int64_t rows, int64_t k, long block, tlr_block_matrix *x) {
+  const bool e5 = codes.scalar_type() == at::kFloat8_e5m2;
+  if (codes.dim() != 2 || !(e5 || codes.scalar_type() == at::kFloat8_e4m3fn)) return "codes: a 2-d float8_e4m3fn or float8_e5m2 tensor is needed";
+  if (block != 1 && block != 128) return "blocks are 1 or 128 rows high";
+  if (scales.dim() != 2 || scales.scalar_type() != at::kFloat || scales.device() != codes.device())
+    return "scales: a 2-d float32 tensor on the codes' device is needed";
+  if (codes.size(0) != rows || codes.size(1) < k || (codes.size(1) > 1 && codes.stride(1) != 1))
+    return "codes: a contiguous row of the matrix's entries for each of its rows is needed";
+  const int64_t nq = (k + 127) / 128, nr = block == 1 ? rows : (rows + 127) / 128;
+  if (scales.size(0) != nq || scales.size(1) != nr || (nr > 1 && scales.stride(1) != 1))
+    return "scales: (column blocks, row blocks), rows contiguous, are needed";
+  x->ld = rows > 1 ? codes.stride(0) : std::max(codes.stride(0), codes.size(1));
+  x->lds = nq > 1 ? scales.stride(0) : std::max(scales.stride(0), nr);
+  if (rows > 0 && k > 0 && codes.storage_offset() + (rows - 1) * x->ld + (k + 15) / 16 * 16 > (int64_t)codes.storage().nbytes())
+    return "codes: every row has to be readable up to a multiple of 16 entries";
+  x->codes = codes.data_ptr();
+  x->scales = static_cast<const float *>(scales.data_ptr());
+  x->block = (int32_t)block;
+  x->fmt = e5 ? TLR_E5M2 : TLR_E4M3;
+  return nullptr;
+}
+
+// gemm(A's codes, scales, block, B's codes, scales, block, m, n, k, alpha, beta, out or None, type of a new one, flags,
+// workspace bytes) -> out or a status
 PyObject *gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   HANDLE_TH_ERRORS
-  if (n_args != 12 || !(args[7] == Py_None || THPVariable_Check(args[7])) || !THPVariable_Check(args[9]))
-    return value_error("gemm: 12 arguments");
-  const auto *A = static_cast<const tlr_block_matrix *>(PyLong_AsVoidPtr(args[0]));
-  const auto *B = static_cast<const tlr_block_matrix *>(PyLong_AsVoidPtr(args[1]));
-  const int64_t m = PyLong_AsLongLong(args[2]), n = PyLong_AsLongLong(args[3]), k = PyLong_AsLongLong(args[4]);
-  const double alpha = PyFloat_AsDouble(args[5]), beta = PyFloat_AsDouble(args[6]);
-  const long type = PyLong_AsLong(args[8]);
-  const unsigned long flags = PyLong_AsUnsignedLong(args[10]);
-  const size_t bytes = PyLong_AsSize_t(args[11]);
+  if (n_args != 15 || !(args[11] == Py_None || THPVariable_Check(args[11]))) return value_error("gemm: 15 arguments");
+  for (const int i : {0, 1, 3, 4})
+    if (!THPVariable_Check(args[i])) return value_error("gemm: codes and scales are tensors");
+  const int64_t m = PyLong_AsLongLong(args[6]), n = PyLong_AsLongLong(args[7]), k = PyLong_AsLongLong(args[8]);
+  const double alpha = PyFloat_AsDouble(args[9]), beta = PyFloat_AsDouble(args[10]);
+  const long a_block = PyLong_AsLong(args[2]), b_block = PyLong_AsLong(args[5]), type = PyLong_AsLong(args[12]);
+  const unsigned long flags = PyLong_AsUnsignedLong(args[13]);
+  const size_t bytes = PyLong_AsSize_t(args[14]);
   if (PyErr_Occurred()) return nullptr;
-  const at::Device device = THPVariable_Unpack(args[9]).device();
+  const at::Tensor &a_codes = THPVariable_Unpack(args[0]), &b_codes = THPVariable_Unpack(args[3]);
+  tlr_block_matrix A{}, B{};
+  if (const char *wrong = operand(a_codes, THPVariable_Unpack(args[1]), m, k, a_block, &A)) return value_error(wrong);
+  if (const char *wrong = operand(b_codes, THPVariable_Unpack(args[4]), n, k, b_block, &B)) return value_error(wrong);
+  const at::Device device = b_codes.device();
+  if (a_codes.device() != device) return value_error("gemm: operands on different devices");
   if (!device.is_cuda()) return value_error("gemm: operands on a GPU are needed");
   const c10::DeviceGuard guard(device);
   at::Tensor c, ws;
-  if (args[7] == Py_None)
+  if (args[11] == Py_None)
     c = at::empty({n, m}, at::TensorOptions().device(device).dtype(type == TLR_F32 ? at::kFloat : type == TLR_F16 ? at::kHalf : at::kBFloat16));
   else
-    c = THPVariable_Unpack(args[7]);
+    c = THPVariable_Unpack(args[11]);
   const int64_t ldc = n > 1 ? c.stride(0) : std::max<int64_t>({c.stride(0), m, 1});
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(device));
-  const tlr_status st = gemm_entry((tlr_dtype)code_of(c), m, n, k, alpha, A, B, beta, c.data_ptr(), ldc, (uint32_t)flags,
+  const tlr_status st = gemm_entry((tlr_dtype)code_of(c), m, n, k, alpha, &A, &B, beta, c.data_ptr(), ldc, (uint32_t)flags,
                                    bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream_of(device));
   return st == TLR_OK ? wrap(c) : PyLong_FromLong(st);
   END_HANDLE_TH_ERRORS

@@ -35,10 +35,13 @@ class MoELayer:
     128 x 128 block scales (as blocks.quantize gives them for one expert):
     gate_up_scales (experts, ceil(hidden/128), ceil(2*inter/128)) and
     down_scales (experts, ceil(inter/128), ceil(hidden/128)), float32.
-    hidden and inter are multiples of 16, every tensor is contiguous.
+    hidden and inter are multiples of 16, every tensor is contiguous.  The layer
+    keeps the memory that the tensors have when it is made: changes in place are
+    seen, a tensor that is given other memory (``.data = ``) afterwards is not.
 
-    Calls share the layer's workspace: they run in the order of one stream, or
-    with events between them.
+    Calls share the layer's workspace, which is cleared on the stream that is
+    current when the layer is made: making it and calling it run in the order of
+    one stream, or with events between them.
     """
 
     def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, topk: int,
@@ -68,23 +71,34 @@ class MoELayer:
             raise ValueError("MoELayer: contiguous tensors on one GPU are needed")
         self.dtype, self.hidden, self.inter, self.experts, self.topk = router.dtype, hidden, inter, experts, int(topk)
         self.max_tokens = int(max_tokens)
-        self._keep = tensors
+        self._keep = [t.detach() for t in tensors]       # the memory that the addresses below belong to
         dt = _DT[router.dtype]
-        self.c = T.tlr_moe_layer(hidden, inter, experts, self.topk, dt, T.TLR_E4M3 if e8 else dt, 1 if normalize else 0,
-                                 0, router.data_ptr(), gate_up.data_ptr(), down.data_ptr(),
-                                 gate_up_scales.data_ptr() if e8 else None, down_scales.data_ptr() if e8 else None)
-        self.ws = torch.empty(max(256, T.tlr_moe_workspace_bytes(self.c, self.max_tokens)), dtype=torch.uint8,
-                              device=self.device)
-        self._at, self._ws, self._nws = ctypes.addressof(self.c), self.ws.data_ptr(), self.ws.numel()
+        self._c = T.tlr_moe_layer(hidden, inter, experts, self.topk, dt, T.TLR_E4M3 if e8 else dt, 1 if normalize else 0,
+                                  0, router.data_ptr(), gate_up.data_ptr(), down.data_ptr(),
+                                  gate_up_scales.data_ptr() if e8 else None, down_scales.data_ptr() if e8 else None)
+        self._ws = torch.empty(max(256, T.tlr_moe_workspace_bytes(self._c, self.max_tokens)), dtype=torch.uint8,
+                               device=self.device)
+        self._at, self._ws_at, self._ws_bytes = ctypes.addressof(self._c), self._ws.data_ptr(), self._ws.numel()
         with torch.cuda.device(self.device):
-            T.tlr_moe_init(self.c, self.ws.data_ptr(), self.ws.numel(), torch.cuda.current_stream().cuda_stream)
+            T.tlr_moe_init(self._c, self._ws_at, self._ws_bytes, torch.cuda.current_stream().cuda_stream)
+
+    # Calls use the addresses of these two: neither can be replaced, and the first is handed out as a copy.
+    @property
+    def c(self) -> T.tlr_moe_layer:
+        """What the C ABI takes."""
+        return T.tlr_moe_layer.from_buffer_copy(self._c)
+
+    @property
+    def ws(self) -> torch.Tensor:
+        """The workspace."""
+        return self._ws
 
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(y, ids, weights) of x (tokens, hidden): the layer's output in x's
         type, the chosen experts (int32) and their probabilities (float32)."""
         if x.device != self.device:
             raise ValueError(f"MoELayer: x is on {self.device}")
-        got = binding().moe(self._at, x, self.max_tokens, self._ws, self._nws)
+        got = binding().moe(self._at, x, self.max_tokens, self._ws_at, self._ws_bytes)
         if type(got) is int:
             T._check(got, "tlr_moe")
         return got

@@ -82,3 +82,14 @@ def test_a_replaced_tensor_that_does_not_fit_is_refused(codes, scales):
         q.c
     with pytest.raises(ValueError):
         blocks.gemm(q, made())
+
+
+def test_a_layer_hands_out_nothing_that_its_calls_point_into():
+    from hpc_linear_algebra_amd import moe
+    layer = moe.MoELayer.__new__(moe.MoELayer)
+    for name in ("c", "ws"):
+        with pytest.raises(AttributeError):
+            setattr(layer, name, torch.zeros(1))
+    layer._c = blocks.T.tlr_moe_layer(64, 32, 8, 2)
+    layer.c.hidden = 1 << 20
+    assert layer.c.hidden == 64 and ctypes.addressof(layer.c) != ctypes.addressof(layer._c)

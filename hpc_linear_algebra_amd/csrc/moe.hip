@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "tlr_ops.h"
 
@@ -254,8 +255,9 @@ __device__ __forceinline__ void choose(const MoeArgs &a, int t, int lane) {
   else select<8>(a, t, lane);
 }
 
-// Few tokens, one by one: a wave per expert.  A product of two 16-bit numbers is
-// an exact float; the sums run in double.  The workgroup that is done last with a
+// Few tokens, one by one: a wave per expert, sums in double.  A product of two half
+// precision numbers is an exact float; one of two bfloat16 numbers may lie outside
+// float's range and is taken in double.  The workgroup that is done last with a
 // token chooses: a launch of its own would cost 4 us.  Against the matrix kernel
 // below the layer takes 1.8 us less at 16 tokens and 8 experts, 1.0 less at 8 and
 // 32, 0.8 less at 16 and 32; 0.8 more at 12 and 64, 0.6 more at 8 and 96.
@@ -273,7 +275,9 @@ template <typename H> __global__ __launch_bounds__(256) void router_one_kernel(M
       unpack8<H>(*reinterpret_cast<const u4 *>(w + c), wf);
       unpack8<H>(*reinterpret_cast<const u4 *>(x + c), xf);
 #pragma unroll
-      for (int v = 0; v < 8; ++v) s += (double)(wf[v] * xf[v]);
+      for (int v = 0; v < 8; ++v)
+        if constexpr (std::is_same_v<H, _Float16>) s += (double)(wf[v] * xf[v]);
+        else s = __builtin_fma((double)wf[v], (double)xf[v], s);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);

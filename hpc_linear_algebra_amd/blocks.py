@@ -121,7 +121,9 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
 
     Sums are held in float.  ``fast`` sums within a block on the 8-bit matrix
     instructions, which cut every product below 2^-13 of the block's largest
-    one: about 2e-5 of the result, for results in 16 bits."""
+    one: about 2e-5 of the result on normally distributed data, ten times that
+    with one strong channel in each block, all of it where large products cancel.
+    For results in 16 bits whose operands allow it."""
     if A.k != B.k:
         raise ValueError(f"gemm: contraction lengths differ ({A.k} and {B.k})")
     device = A.codes.device
@@ -148,15 +150,15 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, grad_fmt):
+    def forward(ctx, x, w, grad_fmt, fast):
         x2 = _rows(x)
         need_x, need_w = ctx.needs_input_grad[:2]
         x8, x8t = quantize(x2, transposed=need_w)
         w8, w8t = quantize(_rows(w), block=BLOCK, transposed=need_x)
-        ctx.x8t, ctx.w8t, ctx.grad_fmt = x8t, w8t, grad_fmt
+        ctx.x8t, ctx.w8t, ctx.grad_fmt, ctx.fast = x8t, w8t, grad_fmt, fast
         ctx.shape, ctx.types = x.shape, (x.dtype, w.dtype)
         out = torch.empty((x2.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-        return gemm(w8, x8, out=out, fast=x.dtype != torch.float32).reshape(*x.shape[:-1], w.shape[0])
+        return gemm(w8, x8, out=out, fast=fast and x.dtype != torch.float32).reshape(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -168,23 +170,24 @@ class _Linear(torch.autograd.Function):
             d8, d8t = quantize(dy, fmt=ctx.grad_fmt, straight=need_x, transposed=need_w)
             if need_x:
                 dx = torch.empty((dy.shape[0], ctx.shape[-1]), dtype=ctx.types[0], device=dy.device)
-                dx = gemm(ctx.w8t, d8, out=dx, fast=dx.dtype != torch.float32).reshape(ctx.shape)
+                dx = gemm(ctx.w8t, d8, out=dx, fast=ctx.fast and dx.dtype != torch.float32).reshape(ctx.shape)
             if need_w:
                 dw = torch.empty((dy.shape[1], ctx.shape[-1]), dtype=ctx.types[1], device=dy.device)
-                gemm(ctx.x8t, d8t, out=dw, fast=dw.dtype != torch.float32)
-        return dx, dw, None
+                gemm(ctx.x8t, d8t, out=dw, fast=ctx.fast and dw.dtype != torch.float32)
+        return dx, dw, None, None
 
 
-def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3") -> torch.Tensor:
+def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3", fast: bool = False) -> torch.Tensor:
     """x W^T (x: (..., k), w: (features, k)) with both operands, and in the
     backward pass dy, quantized to block-scaled 8 bits: x and dy in 1 x 128
     blocks along each contraction, w in 128 x 128 blocks.  The forward pass
-    keeps the transposed codes, a byte an entry, in place of x and w.  Results
-    in 16 bits are summed with ``fast`` (see gemm), float32 ones in float.  No
-    double backward.  In a captured graph take torch.autograd.grad, or leaves
-    that no live eager graph holds: their accumulation belongs to its stream."""
+    keeps the transposed codes, a byte an entry, in place of x and w.  Sums are
+    held in float; ``fast`` sums those of the three results that have 16 bits on
+    the 8-bit instructions (see gemm).  No double backward.  In a captured graph
+    take torch.autograd.grad, or leaves that no live eager graph holds: their
+    accumulation belongs to its stream."""
     if x.shape[-1:] != w.shape[1:] or w.dim() != 2:
         raise ValueError("linear: x is (..., k) and w (features, k)")
     if grad_fmt not in FORMATS:
         raise ValueError("linear: grad_fmt is e4m3 or e5m2")
-    return _Linear.apply(x, w, grad_fmt)
+    return _Linear.apply(x, w, grad_fmt, fast)

@@ -148,6 +148,10 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     return x if x.stride(1) == 1 else x.contiguous()
 
 
+def _parts(q: Optional[BlockScaled]) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    return (q.codes, q.scales) if q is not None else (None, None)
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, grad_fmt, fast):
@@ -155,7 +159,8 @@ class _Linear(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad[:2]
         x8, x8t = quantize(x2, transposed=need_w)
         w8, w8t = quantize(_rows(w), block=BLOCK, transposed=need_x)
-        ctx.x8t, ctx.w8t, ctx.grad_fmt, ctx.fast = x8t, w8t, grad_fmt, fast
+        ctx.save_for_backward(*_parts(x8t), *_parts(w8t))
+        ctx.grad_fmt, ctx.fast = grad_fmt, fast
         ctx.shape, ctx.types = x.shape, (x.dtype, w.dtype)
         out = torch.empty((x2.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
         return gemm(w8, x8, out=out, fast=fast and x.dtype != torch.float32).reshape(*x.shape[:-1], w.shape[0])
@@ -165,15 +170,20 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
         dx = dw = None
+        x_codes, x_scales, w_codes, w_scales = ctx.saved_tensors
         if need_x or need_w:
             dy = _rows(dy)
+            tokens, features = dy.shape
+            width = ctx.shape[-1]
             d8, d8t = quantize(dy, fmt=ctx.grad_fmt, straight=need_x, transposed=need_w)
             if need_x:
-                dx = torch.empty((dy.shape[0], ctx.shape[-1]), dtype=ctx.types[0], device=dy.device)
-                dx = gemm(ctx.w8t, d8, out=dx, fast=ctx.fast and dx.dtype != torch.float32).reshape(ctx.shape)
+                dx = torch.empty((tokens, width), dtype=ctx.types[0], device=dy.device)
+                w8t = _made(w_codes, w_scales, width, features, BLOCK)
+                dx = gemm(w8t, d8, out=dx, fast=ctx.fast and dx.dtype != torch.float32).reshape(ctx.shape)
             if need_w:
-                dw = torch.empty((dy.shape[1], ctx.shape[-1]), dtype=ctx.types[1], device=dy.device)
-                gemm(ctx.x8t, d8t, out=dw, fast=ctx.fast and dw.dtype != torch.float32)
+                dw = torch.empty((features, width), dtype=ctx.types[1], device=dy.device)
+                x8t = _made(x_codes, x_scales, width, tokens, 1)
+                gemm(x8t, d8t, out=dw, fast=ctx.fast and dw.dtype != torch.float32)
         return dx, dw, None, None
 
 
@@ -181,7 +191,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3", fast: bool 
     """x W^T (x: (..., k), w: (features, k)) with both operands, and in the
     backward pass dy, quantized to block-scaled 8 bits: x and dy in 1 x 128
     blocks along each contraction, w in 128 x 128 blocks.  The forward pass
-    keeps the transposed codes, a byte an entry, in place of x and w.  Sums are
+    saves the transposed codes, a byte an entry, in place of x and w.  Sums are
     held in float; ``fast`` sums those of the three results that have 16 bits on
     the 8-bit instructions (see gemm).  No double backward.  In a captured graph
     take torch.autograd.grad, or leaves that no live eager graph holds: their

@@ -69,3 +69,18 @@ def test_linear_cuts_no_product_unless_asked():
     y = blocks.linear(x.half().cuda(), w.half().cuda())
     check(y, w8, x8, 128, "f16", False)
     assert torch.all((y - 64 * 448.0 * 2.0 ** -14).abs() <= 2.0 ** -11 * 2)
+
+
+def test_saved_codes_through_host_memory():
+    """Codes that a saved-tensor hook moves away and back give the same gradients; a second backward needs them kept."""
+    from hpc_linear_algebra_amd import blocks
+    x, w, dy = operands(150, 260, 200, "bf16", "f32", 9)
+    y = blocks.linear(x, w)
+    want = torch.autograd.grad(y, (x, w), dy)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, (x, w), dy)
+    with torch.autograd.graph.save_on_cpu():
+        y = blocks.linear(x, w)
+    for keep in (True, False):
+        got = torch.autograd.grad(y, (x, w), dy, retain_graph=keep)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

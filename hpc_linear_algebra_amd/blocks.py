@@ -101,7 +101,8 @@ def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool 
 
     x is a 2-d float32, float16 or bfloat16 tensor whose rows are contiguous
     (any row stride).  block 1: a scale for every 128 entries of a row of the
-    result; block 128: one for every 128 x 128 tile."""
+    result; block 128: one for every 128 x 128 tile.  Codes and scales carry no
+    gradient, whatever x does: linear is the differentiable function."""
     f8 = _FMT.get(fmt)
     if f8 is None or block not in (1, BLOCK) or not (straight or transposed):
         raise ValueError("quantize: fmt is e4m3 or e5m2, block 1 or 128, and a result has to be wanted")
@@ -117,7 +118,9 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
          dtype: str = "bf16", fast: bool = False) -> torch.Tensor:
     """alpha B A^T + beta out, a (B.rows, A.rows) tensor: column-major A.rows x
     B.rows to the C ABI, x W^T to a linear layer with A = W and B = x.  Without
-    ``out`` the result is a new tensor of type ``dtype`` (beta must be 0).
+    ``out`` the result is a new tensor of type ``dtype`` (beta must be 0).  It has
+    no gradient: where gradients are on, scales or an out that require one are
+    refused.
 
     Sums are held in float.  ``fast`` sums within a block on the 8-bit matrix
     instructions, which cut every product below 2^-13 of the block's largest

@@ -5,6 +5,7 @@
 // TLR_OK is returned as an int for the caller to raise.
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -150,11 +151,16 @@ PyObject *gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   if (a_codes.device() != device) return value_error("gemm: operands on different devices");
   if (!device.is_cuda()) return value_error("gemm: operands on a GPU are needed");
   const c10::DeviceGuard guard(device);
+  const bool grad = c10::GradMode::is_enabled();
+  if (grad && (THPVariable_Unpack(args[1]).requires_grad() || THPVariable_Unpack(args[4]).requires_grad()))
+    return value_error("gemm: scales that require a gradient would get none");
   at::Tensor c, ws;
   if (args[11] == Py_None)
     c = at::empty({n, m}, at::TensorOptions().device(device).dtype(type == TLR_F32 ? at::kFloat : type == TLR_F16 ? at::kHalf : at::kBFloat16));
   else
     c = THPVariable_Unpack(args[11]);
+  if (grad && c.requires_grad()) return value_error("gemm: an out that requires a gradient would get none");
+  if (!c.is_inference()) c.unsafeGetTensorImpl()->bump_version();      // written in place, as autograd sees it
   const int64_t ldc = n > 1 ? c.stride(0) : std::max<int64_t>({c.stride(0), m, 1});
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(device));
   const tlr_status st = gemm_entry((tlr_dtype)code_of(c), m, n, k, alpha, &A, &B, beta, c.data_ptr(), ldc, (uint32_t)flags,

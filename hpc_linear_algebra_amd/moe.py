@@ -42,6 +42,9 @@ class MoELayer:
     Calls share the layer's workspace, which is cleared on the stream that is
     current when the layer is made: making it and calling it run in the order of
     one stream, or with events between them.
+
+    There is no backward pass: where gradients are on, an x or weights that
+    require one are refused.
     """
 
     def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, topk: int,
@@ -71,6 +74,7 @@ class MoELayer:
             raise ValueError("MoELayer: contiguous tensors on one GPU are needed")
         self.dtype, self.hidden, self.inter, self.experts, self.topk = router.dtype, hidden, inter, experts, int(topk)
         self.max_tokens = int(max_tokens)
+        self._trained = any(t.requires_grad for t in tensors)
         self._keep = [t.detach() for t in tensors]       # the memory that the addresses below belong to
         dt = _DT[router.dtype]
         self._c = T.tlr_moe_layer(hidden, inter, experts, self.topk, dt, T.TLR_E4M3 if e8 else dt, 1 if normalize else 0,
@@ -96,6 +100,8 @@ class MoELayer:
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(y, ids, weights) of x (tokens, hidden): the layer's output in x's
         type, the chosen experts (int32) and their probabilities (float32)."""
+        if torch.is_grad_enabled() and (x.requires_grad or self._trained):
+            raise RuntimeError("MoELayer has no backward pass: call it under torch.no_grad() or on detached tensors")
         if x.device != self.device:
             raise ValueError(f"MoELayer: x is on {self.device}")
         got = binding().moe(self._at, x, self.max_tokens, self._ws_at, self._ws_bytes)

@@ -41,3 +41,23 @@ def test_the_choice_holds_over_bfloat16s_range(tokens, experts, x2, w2):
     assert torch.equal(ids.cpu().long(), want)
     top = torch.softmax(logits, 1).gather(1, want)
     assert torch.all((p.cpu().double() - top / top.sum(1, keepdim=True)).abs() <= 80 * 2.0 ** -24)
+
+
+def test_a_layer_cuts_no_graph_without_a_word():
+    from hpc_linear_algebra_amd.moe import MoELayer
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()   # noqa: E731
+    x, router, gate_up, down = rn(3, 64), rn(8, 64), rn(8, 64, 64) / 8, rn(8, 64, 32) / 8
+    layer = MoELayer(router, gate_up, down, 2)
+    want = layer(x)
+    x.requires_grad_()
+    with pytest.raises(RuntimeError, match="no backward"):
+        layer(x)
+    assert all(torch.equal(a, b) for a, b in zip(layer(x.detach()), want))
+    with torch.no_grad():
+        assert all(torch.equal(a, b) for a, b in zip(layer(x), want))
+    trained = MoELayer(router, gate_up.requires_grad_(), down, 2)
+    with pytest.raises(RuntimeError, match="no backward"):
+        trained(x.detach())
+    with torch.inference_mode():
+        assert all(torch.equal(a, b) for a, b in zip(trained(x), want))

@@ -93,3 +93,17 @@ def test_a_layer_hands_out_nothing_that_its_calls_point_into():
     layer._c = blocks.T.tlr_moe_layer(64, 32, 8, 2)
     layer.c.hidden = 1 << 20
     assert layer.c.hidden == 64 and ctypes.addressof(layer.c) != ctypes.addressof(layer._c)
+
+
+def test_a_layer_refuses_what_requires_a_gradient():
+    from hpc_linear_algebra_amd import moe
+    layer = moe.MoELayer.__new__(moe.MoELayer)
+    layer.device, layer._trained = torch.device("cuda", 0), False
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="no backward"):
+        layer(x.requires_grad_())
+    with torch.no_grad(), pytest.raises(ValueError):             # x is not on the layer's device
+        layer(x)
+    layer._trained = True
+    with pytest.raises(RuntimeError, match="no backward"):
+        layer(x.detach())

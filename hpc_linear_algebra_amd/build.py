@@ -63,7 +63,7 @@ def _build_binding() -> str:
            "-isystem", sysconfig.get_paths()["include"]]
     for path in cpp_extension.include_paths("cuda"):
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += ["-x", "c++", os.path.join(CSRC, "binding.cpp"), "-o", tmp]
     cmd += [f"-L{path}" for path in cpp_extension.library_paths("cuda")]
     cmd += ["-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)

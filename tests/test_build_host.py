@@ -53,3 +53,10 @@ def test_without_torch_the_library_is_built_alone(commands, monkeypatch, tmp_pat
 def test_both_are_built(commands, tmp_path):
     build.build()
     assert (tmp_path / "libtlrgemm.so").exists() and (tmp_path / "_binding.so").exists()
+
+
+def test_the_extension_is_host_code(commands):
+    """hipcc takes a .cpp for HIP and, unless told, builds device code for an architecture of its own choice."""
+    build.build()
+    cmd, = [c for c in commands if any(str(a).endswith("binding.cpp") for a in c)]
+    assert cmd[cmd.index("-x") + 1] == "c++" and cmd.index("-x") < [str(a).endswith("binding.cpp") for a in cmd].index(True)

@@ -273,6 +273,10 @@ tlr_status tlr_block_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, size_
   TLR_GUARD({ return tlr::block_gemm_workspace(m, n, k, bytes_out); })
 }
 
+tlr_status tlr_block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out) {
+  TLR_GUARD({ return tlr::block_gemm_plan(m, n, k, flags, out); })
+}
+
 tlr_status tlr_block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alpha, const tlr_block_matrix *A,
                           const tlr_block_matrix *B, double beta, void *C, int64_t ldc, uint32_t flags,
                           void *workspace, size_t workspace_bytes, void *stream) {

@@ -828,12 +828,29 @@ template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(GemmArg
 // ---- which kernel -----------------------------------------------------------------------------------
 
 enum Kind { STRIP, TILE_64, TILE_64K, TILE_128, TILE_128W, TILE_128K, TILE_256 };
+struct Shape {
+  int rows, cols, threads;  // of C and of the workgroup that computes them
+  int halves;               // of its waves, which share the column blocks
+};
+constexpr Shape SHAPE[] = {{16, 16, 512, 1},   {128, 64, 512, 1},  {128, 64, 512, 2}, {128, 128, 256, 1},
+                           {128, 128, 512, 1}, {128, 128, 512, 2}, {256, 256, 512, 1}};
 struct Choice {
   Kind kind;
   int parts;                // of the contraction, with a launch that adds them if more than one
 };
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A launch has less than 2^32 threads along x.  128 x 128 tiles of four waves fit
+// whatever the others do, where a result has less than TILE_LIM of them.
+constexpr int64_t THREAD_LIM = (int64_t)1 << 32, TILE_LIM = (int64_t)1 << 24;
+int64_t workgroups(Kind kind, int64_t m, int64_t n) {
+  return kind == STRIP ? cdiv(m, 16) : cdiv(m, SHAPE[kind].rows) * cdiv(n, SHAPE[kind].cols);      // along x
+}
+bool fits(Kind kind, int parts, int64_t m, int64_t n) {
+  return workgroups(kind, m, n) * SHAPE[kind].threads < THREAD_LIM && (kind != STRIP || cdiv(n, 16) <= 65535) &&
+         (parts == 1 || cdiv(m, 8) * n < THREAD_LIM - 256);
+}
 
 // The kernel with the least estimated time (us).  Each estimate is a fit to
 // measured times (graph replays, 16-bit C with `fast`, float C of e4m3 and e5m2
@@ -856,13 +873,13 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
   Choice best{TILE_128, 1};
   double least = 1e300;
   auto offer = [&](Kind kind, int parts, double t) {
-    if (t < least) {
+    if (t < least && fits(kind, parts, m, n)) {
       least = t;
       best = Choice{kind, parts};
     }
   };
   // 4 KB a workgroup and block out of the caches
-  if (cdiv(n, 16) <= 65535 && cdiv(m, 16) < 1 << 22) offer(STRIP, 1, 2.8 + cdiv(m, 16) * cdiv(n, 16) * nb * (fast ? 0.00040 : 0.00048));
+  offer(STRIP, 1, 2.8 + cdiv(m, 16) * cdiv(n, 16) * nb * (fast ? 0.00040 : 0.00048));
   // One workgroup a CU takes `one` a column block, two together `two`.
   auto tiles = [&](Kind kind, int tn, double one, double two, double first, double next) {
     for (const int parts : {1, 2, 4, 8}) {
@@ -892,9 +909,11 @@ Choice choose(int64_t m, int64_t n, int64_t k, bool fast) {
   return best;
 }
 
-template <bool A5, bool B5, bool FAST, int TM, int TN, int WM, int WN, int KG, int SPREAD>
+template <Kind KIND, bool A5, bool B5, bool FAST, int WM, int WN, int SPREAD>
 void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
-  const dim3 grid((unsigned)(cdiv(g.m, TM) * cdiv(g.n, TN)), (unsigned)parts);
+  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, KG = SHAPE[KIND].halves;
+  static_assert(SHAPE[KIND].threads == 64 * WM * WN * KG, "");
+  const dim3 grid((unsigned)workgroups(KIND, g.m, g.n), (unsigned)parts);
   GemmArgs h = g;
   if (parts > 1) {
     h.alpha = 1.0f;
@@ -913,7 +932,7 @@ void tile_launch(const GemmArgs &g, int parts, float *ws, hipStream_t st) {
 }
 
 template <bool A5, bool B5, bool FAST> void strip_launch(const GemmArgs &g, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(g.m, 16), (unsigned)cdiv(g.n, 16));
+  const dim3 grid((unsigned)workgroups(STRIP, g.m, g.n), (unsigned)cdiv(g.n, 16));
   if (g.a.shift) strip_kernel<A5, B5, FAST, true><<<grid, 512, 0, st>>>(g);
   else strip_kernel<A5, B5, FAST, false><<<grid, 512, 0, st>>>(g);
 }
@@ -922,13 +941,13 @@ template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, float
   const Choice c = choose(g.m, g.n, g.k, FAST);
   switch (c.kind) {
     case STRIP: return strip_launch<A5, B5, FAST>(g, st);
-    case TILE_64: return tile_launch<A5, B5, FAST, 128, 64, 4, 2, 1, 0>(g, c.parts, ws, st);
-    case TILE_64K: return tile_launch<A5, B5, FAST, 128, 64, 2, 2, 2, 0>(g, c.parts, ws, st);
-    case TILE_128: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 1, 3>(g, c.parts, ws, st);
-    case TILE_128W: return tile_launch<A5, B5, FAST, 128, 128, 2, 4, 1, 0>(g, c.parts, ws, st);
-    case TILE_128K: return tile_launch<A5, B5, FAST, 128, 128, 2, 2, 2, FAST ? 0 : 3>(g, c.parts, ws, st);
+    case TILE_64: return tile_launch<TILE_64, A5, B5, FAST, 4, 2, 0>(g, c.parts, ws, st);
+    case TILE_64K: return tile_launch<TILE_64K, A5, B5, FAST, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<TILE_128, A5, B5, FAST, 2, 2, 3>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<TILE_128W, A5, B5, FAST, 2, 4, 0>(g, c.parts, ws, st);
+    case TILE_128K: return tile_launch<TILE_128K, A5, B5, FAST, 2, 2, FAST ? 0 : 3>(g, c.parts, ws, st);
     case TILE_256:
-      if constexpr (FAST) return tile_launch<A5, B5, FAST, 256, 256, 2, 4, 1, 2>(g, c.parts, ws, st);
+      if constexpr (FAST) return tile_launch<TILE_256, A5, B5, FAST, 2, 4, 2>(g, c.parts, ws, st);
   }
 }
 
@@ -984,7 +1003,7 @@ tlr_status block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_t ro
   if (block != 1 && block != QB) return fail(TLR_ERR_INVALID_ARG, "block_quantize: blocks are 1 or 128 rows high");
   if (rows < 0 || k < 0 || rows > SIZE_LIM || k > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_quantize: size out of range");
   if ((rows + QB - 1) / QB > 65535) return fail(TLR_ERR_INVALID_ARG, "block_quantize: too many rows");
-  if (((rows + QB - 1) / QB) * ((k + QB - 1) / QB) > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_quantize: too many tiles");
+  if (((rows + QB - 1) / QB) * ((k + QB - 1) / QB) >= TILE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_quantize: too many tiles");
   if (ldx < std::max<int64_t>(1, k)) return fail(TLR_ERR_INVALID_ARG, "block_quantize: leading dimension of X too small");
   if (rows == 0 || k == 0) return TLR_OK;
   if (!codes && !codes_t) return fail(TLR_ERR_INVALID_ARG, "block_quantize: no result wanted");
@@ -1020,12 +1039,28 @@ tlr_status block_gemm_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes) 
   // a tile's rows past the end are still an int
   if (m < 0 || n < 0 || k < 0 || m > PRODUCT_LIM || n > PRODUCT_LIM || k > SIZE_LIM)
     return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: size out of range");
+  if (cdiv(m, 128) * cdiv(n, 128) >= TILE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_gemm: too many tiles for a launch");
   *bytes = 0;
   if (m > 0 && n > 0 && k > 0)
     for (const bool fast : {false, true}) {
       const Choice c = choose(m, n, k, fast);
       if (c.parts > 1) *bytes = std::max(*bytes, sizeof(float) * (size_t)c.parts * m * n);
     }
+  return TLR_OK;
+}
+
+tlr_status block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out) {
+  if (!out) return fail(TLR_ERR_INVALID_ARG, "block_gemm_plan: null output");
+  if (flags & ~TLR_BLOCK_FAST) return fail(TLR_ERR_INVALID_ARG, "block_gemm_plan: unknown flags");
+  size_t most = 0;
+  const tlr_status st = block_gemm_workspace(m, n, k, &most);      // its checks
+  if (st != TLR_OK) return st;
+  *out = tlr_block_gemm_choice{};
+  if (m == 0 || n == 0 || k == 0) return TLR_OK;
+  const Choice c = choose(m, n, k, (flags & TLR_BLOCK_FAST) != 0);
+  const Shape &s = SHAPE[c.kind];
+  const int64_t x = workgroups(c.kind, m, n), y = c.kind == STRIP ? cdiv(n, 16) : 1;
+  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, s.halves, c.parts, 0, x, y};
   return TLR_OK;
 }
 

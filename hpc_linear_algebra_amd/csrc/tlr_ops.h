@@ -11,6 +11,7 @@ tlr_status block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_t ro
                           int64_t ldx, void *codes, int64_t ldq, float *scales, int64_t lds, void *codes_t,
                           int64_t ldq_t, float *scales_t, int64_t lds_t, void *stream);
 tlr_status block_gemm_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes);
+tlr_status block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out);
 tlr_status block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alpha, const tlr_block_matrix *A,
                       const tlr_block_matrix *B, double beta, void *C, int64_t ldc, uint32_t flags, void *ws,
                       size_t ws_bytes, void *stream);

@@ -33,7 +33,7 @@ EXPORTED = [
     "tlr_gemm_execute", "tlr_gemm_execute_noalloc", "tlr_expand", "tlr_compress_workspace_bytes",
     "tlr_compress", "tlr_compress_profile", "tlr_compress_profile_read", "tlr_plan_profile",
     "tlr_plan_profile_read", "tlr_dense_gemm", "tlr_block_quantize", "tlr_block_gemm_workspace_bytes",
-    "tlr_block_gemm", "tlr_moe_workspace_bytes", "tlr_moe_init", "tlr_moe",
+    "tlr_block_gemm_plan", "tlr_block_gemm", "tlr_moe_workspace_bytes", "tlr_moe_init", "tlr_moe",
     "tlr_status_string", "tlr_last_error", "tlr_version",
 ]
 
@@ -60,6 +60,11 @@ class tlr_plan_summary(ctypes.Structure):
 class tlr_block_matrix(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("ld", c_int64), ("lds", c_int64),
                 ("block", c_int32), ("fmt", c_int32)]
+
+
+class tlr_block_gemm_choice(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("cols", c_int32), ("threads", c_int32), ("halves", c_int32), ("parts", c_int32),
+                ("reserved", c_int32), ("grid_x", c_int64), ("grid_y", c_int64)]
 
 
 class tlr_moe_layer(ctypes.Structure):
@@ -117,6 +122,7 @@ def lib():
     L.tlr_block_quantize.argtypes = [c_int32, c_int32, c_int32, c_int64, c_int64, P, c_int64, P, c_int64, P, c_int64,
                                      P, c_int64, P, c_int64, P]
     L.tlr_block_gemm_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+    L.tlr_block_gemm_plan.argtypes = [c_int64, c_int64, c_int64, c_uint32, POINTER(tlr_block_gemm_choice)]
     L.tlr_block_gemm.argtypes = [c_int32, c_int64, c_int64, c_int64, c_double, POINTER(tlr_block_matrix),
                                  POINTER(tlr_block_matrix), c_double, P, c_int64, c_uint32, P, c_size_t, P]
     L.tlr_moe_workspace_bytes.argtypes = [POINTER(tlr_moe_layer), c_int32, POINTER(c_size_t)]
@@ -346,6 +352,12 @@ def tlr_block_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
     out = c_size_t()
     _check(lib().tlr_block_gemm_workspace_bytes(m, n, k, ctypes.byref(out)), "tlr_block_gemm_workspace_bytes")
     return int(out.value)
+
+
+def tlr_block_gemm_plan(m: int, n: int, k: int, flags: int = 0) -> tlr_block_gemm_choice:
+    out = tlr_block_gemm_choice()
+    _check(lib().tlr_block_gemm_plan(m, n, k, flags, ctypes.byref(out)), "tlr_block_gemm_plan")
+    return out
 
 
 def tlr_block_gemm(dtype, m: int, n: int, k: int, alpha: float, A: tlr_block_matrix, B: tlr_block_matrix, beta: float,

@@ -485,6 +485,7 @@ typedef struct {
  *           bytes k .. k rounded up to 16 of each row are written as zero.
  *   codes_t, ldq_t, scales_t, lds_t  the k x rows result of X^T (blocks of X^T),
  *           likewise.
+ * rows up to 65535 * 128, k up to 2^31 - 1, less than 2^24 tiles of 128 x 128.
  * No workspace.  Errors: TLR_ERR_INVALID_ARG, TLR_ERR_UNSUPPORTED (TLR_F64),
  * TLR_ERR_HIP.
  */
@@ -522,11 +523,23 @@ tlr_status tlr_block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_
  * codes propagate.  The product of two scales has to be a finite float.
  *   workspace  device, tlr_block_gemm_workspace_bytes (may be 0: then NULL is
  *              fine), 256-byte aligned; its contents need not be cleared.
- * m and n up to 2^31 - 512, ld < 2^22.
+ * m and n up to 2^31 - 512 with less than 2^24 tiles of 128 x 128 in C; ld < 2^22.
  * Errors: TLR_ERR_INVALID_ARG (unknown flags among it), TLR_ERR_UNSUPPORTED (dt TLR_F64),
  * TLR_ERR_WORKSPACE, TLR_ERR_HIP.
  */
 tlr_status tlr_block_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t *bytes_out);
+
+/* What tlr_block_gemm launches for these sizes (zeros where it launches no
+ * product): workgroups of `threads` threads, each `rows` x `cols` of C, in a grid
+ * of grid_x x (grid_y * parts); `halves` 2: two halves of a workgroup's waves take
+ * alternate column blocks; `parts` > 1: as many pieces of the contraction, added
+ * by a second launch.  Depends on the arguments alone. */
+typedef struct {
+  int32_t rows, cols, threads, halves, parts, reserved;
+  int64_t grid_x, grid_y;
+} tlr_block_gemm_choice;
+tlr_status tlr_block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out);
+
 tlr_status tlr_block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alpha,
                           const tlr_block_matrix *A, const tlr_block_matrix *B, double beta, void *C,
                           int64_t ldc, uint32_t flags, void *workspace, size_t workspace_bytes,

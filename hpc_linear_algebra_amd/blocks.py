@@ -42,7 +42,9 @@ def binding():
     return _binding
 
 
-_gemm_workspace = functools.lru_cache(4096)(T.tlr_block_gemm_workspace_bytes)      # of the sizes alone
+@functools.lru_cache(4096)
+def _gemm_workspace(m: int, n: int, k: int, flags: int) -> int:
+    return int(T.tlr_block_gemm_plan(m, n, k, flags).workspace)
 
 
 class BlockScaled:
@@ -138,8 +140,9 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
             raise ValueError("gemm: beta needs an out to add to")
     elif tuple(out.shape) != (n, m) or out.dtype not in _DT or out.device != device or (m > 1 and out.stride(1) != 1):
         raise ValueError(f"gemm: out has to be a ({n}, {m}) float32, float16 or bfloat16 tensor with contiguous rows")
+    flags = T.TLR_BLOCK_FAST if fast else 0
     got = binding().gemm(A.codes, A.scales, A.block, B.codes, B.scales, B.block, m, n, A.k, alpha, beta, out, _NEW[dtype],
-                         T.TLR_BLOCK_FAST if fast else 0, _gemm_workspace(m, n, A.k))
+                         flags, _gemm_workspace(m, n, A.k, flags) if alpha != 0.0 else 0)
     if type(got) is int:
         T._check(got, "tlr_block_gemm")
     return got

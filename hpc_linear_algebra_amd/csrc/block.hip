@@ -937,8 +937,7 @@ template <bool A5, bool B5, bool FAST> void strip_launch(const GemmArgs &g, hipS
   else strip_kernel<A5, B5, FAST, false><<<grid, 512, 0, st>>>(g);
 }
 
-template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, float *ws, hipStream_t st) {
-  const Choice c = choose(g.m, g.n, g.k, FAST);
+template <bool A5, bool B5, bool FAST> void gemm_launch(const GemmArgs &g, const Choice &c, float *ws, hipStream_t st) {
   switch (c.kind) {
     case STRIP: return strip_launch<A5, B5, FAST>(g, st);
     case TILE_64: return tile_launch<TILE_64, A5, B5, FAST, 4, 2, 0>(g, c.parts, ws, st);
@@ -960,6 +959,17 @@ tlr_status launched(const char *what) {
 }
 
 constexpr int64_t SIZE_LIM = 0x7fffffff, PRODUCT_LIM = SIZE_LIM - 511, LD_LIM = (int64_t)1 << 22;
+
+// Sizes of a product; a tile's rows past the end are still an int.
+tlr_status check_sizes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 0 || m > PRODUCT_LIM || n > PRODUCT_LIM || k > SIZE_LIM)
+    return fail(TLR_ERR_INVALID_ARG, "block_gemm: size out of range");
+  if (cdiv(m, 128) * cdiv(n, 128) >= TILE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_gemm: too many tiles for a launch");
+  return TLR_OK;
+}
+
+// Workspace of a product in parts.
+size_t parts_bytes(const Choice &c, int64_t m, int64_t n) { return c.parts > 1 ? sizeof(float) * (size_t)c.parts * m * n : 0; }
 
 // Checks one result of the quantizer: rows x k codes with blocks of `block` rows.
 tlr_status check_result(const char *name, int block, int64_t rows, int64_t k, const void *codes, int64_t ld,
@@ -1036,31 +1046,25 @@ tlr_status block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_t ro
 
 tlr_status block_gemm_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes) {
   if (!bytes) return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: null output");
-  // a tile's rows past the end are still an int
-  if (m < 0 || n < 0 || k < 0 || m > PRODUCT_LIM || n > PRODUCT_LIM || k > SIZE_LIM)
-    return fail(TLR_ERR_INVALID_ARG, "block_gemm_workspace_bytes: size out of range");
-  if (cdiv(m, 128) * cdiv(n, 128) >= TILE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_gemm: too many tiles for a launch");
+  const tlr_status st = check_sizes(m, n, k);
+  if (st != TLR_OK) return st;
   *bytes = 0;
   if (m > 0 && n > 0 && k > 0)
-    for (const bool fast : {false, true}) {
-      const Choice c = choose(m, n, k, fast);
-      if (c.parts > 1) *bytes = std::max(*bytes, sizeof(float) * (size_t)c.parts * m * n);
-    }
+    for (const bool fast : {false, true}) *bytes = std::max(*bytes, parts_bytes(choose(m, n, k, fast), m, n));
   return TLR_OK;
 }
 
 tlr_status block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out) {
   if (!out) return fail(TLR_ERR_INVALID_ARG, "block_gemm_plan: null output");
   if (flags & ~TLR_BLOCK_FAST) return fail(TLR_ERR_INVALID_ARG, "block_gemm_plan: unknown flags");
-  size_t most = 0;
-  const tlr_status st = block_gemm_workspace(m, n, k, &most);      // its checks
+  const tlr_status st = check_sizes(m, n, k);
   if (st != TLR_OK) return st;
   *out = tlr_block_gemm_choice{};
   if (m == 0 || n == 0 || k == 0) return TLR_OK;
   const Choice c = choose(m, n, k, (flags & TLR_BLOCK_FAST) != 0);
   const Shape &s = SHAPE[c.kind];
   const int64_t x = workgroups(c.kind, m, n), y = c.kind == STRIP ? cdiv(n, 16) : 1;
-  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, s.halves, c.parts, 0, x, y};
+  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, s.halves, c.parts, 0, x, y, parts_bytes(c, m, n)};
   return TLR_OK;
 }
 
@@ -1070,15 +1074,16 @@ tlr_status block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alph
   if (dt == TLR_F64) return fail(TLR_ERR_UNSUPPORTED, "block_gemm: C of type TLR_F64 is not provided");
   if (dt != TLR_F32 && dt != TLR_F16 && dt != TLR_BF16) return fail(TLR_ERR_INVALID_ARG, "block_gemm: bad dtype of C");
   if (flags & ~TLR_BLOCK_FAST) return fail(TLR_ERR_INVALID_ARG, "block_gemm: unknown flags");
-  size_t need = 0;
-  tlr_status st = block_gemm_workspace(m, n, k, &need);
+  tlr_status st = check_sizes(m, n, k);
   if (st != TLR_OK) return st;
   if (ldc < std::max<int64_t>(1, m) || ldc > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, "block_gemm: ldc out of range");
   if (m == 0 || n == 0) return TLR_OK;
-  if (need > 0 && (!ws || !aligned(ws, 256))) return fail(TLR_ERR_INVALID_ARG, "block_gemm: null or misaligned workspace");
-  if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "block_gemm: workspace too small");
   GemmArgs g{};
   const bool product = k > 0 && alpha != 0.0;
+  const Choice choice = product ? choose(m, n, k, (flags & TLR_BLOCK_FAST) != 0) : Choice{STRIP, 1};
+  const size_t need = parts_bytes(choice, m, n);
+  if (need > 0 && (!ws || !aligned(ws, 256))) return fail(TLR_ERR_INVALID_ARG, "block_gemm: null or misaligned workspace");
+  if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "block_gemm: workspace too small");
   if (product) {
     if ((st = check_operand("A", A, m, k, &g.a)) != TLR_OK) return st;
     if ((st = check_operand("B", B, n, k, &g.b)) != TLR_OK) return st;
@@ -1102,11 +1107,11 @@ tlr_status block_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, double alph
   float *part = static_cast<float *>(ws);
   const bool a5 = A->fmt == TLR_E5M2, b5 = B->fmt == TLR_E5M2;
   if (flags & TLR_BLOCK_FAST) {
-    if (a5) b5 ? gemm_launch<true, true, true>(g, part, hs) : gemm_launch<true, false, true>(g, part, hs);
-    else b5 ? gemm_launch<false, true, true>(g, part, hs) : gemm_launch<false, false, true>(g, part, hs);
+    if (a5) b5 ? gemm_launch<true, true, true>(g, choice, part, hs) : gemm_launch<true, false, true>(g, choice, part, hs);
+    else b5 ? gemm_launch<false, true, true>(g, choice, part, hs) : gemm_launch<false, false, true>(g, choice, part, hs);
   } else {
-    if (a5) b5 ? gemm_launch<true, true, false>(g, part, hs) : gemm_launch<true, false, false>(g, part, hs);
-    else b5 ? gemm_launch<false, true, false>(g, part, hs) : gemm_launch<false, false, false>(g, part, hs);
+    if (a5) b5 ? gemm_launch<true, true, false>(g, choice, part, hs) : gemm_launch<true, false, false>(g, choice, part, hs);
+    else b5 ? gemm_launch<false, true, false>(g, choice, part, hs) : gemm_launch<false, false, false>(g, choice, part, hs);
   }
   return launched("block_gemm");
 }

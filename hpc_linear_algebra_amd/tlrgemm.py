@@ -64,7 +64,7 @@ class tlr_block_matrix(ctypes.Structure):
 
 class tlr_block_gemm_choice(ctypes.Structure):
     _fields_ = [("rows", c_int32), ("cols", c_int32), ("threads", c_int32), ("halves", c_int32), ("parts", c_int32),
-                ("reserved", c_int32), ("grid_x", c_int64), ("grid_y", c_int64)]
+                ("reserved", c_int32), ("grid_x", c_int64), ("grid_y", c_int64), ("workspace", c_size_t)]
 
 
 class tlr_moe_layer(ctypes.Structure):

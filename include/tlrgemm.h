@@ -521,8 +521,10 @@ tlr_status tlr_block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_
  * blocks of 1 row along the tokens.  Any block height on either side.
  * beta == 0 never reads C; alpha == 0 reads neither A nor B.  NaN scales and
  * codes propagate.  The product of two scales has to be a finite float.
- *   workspace  device, tlr_block_gemm_workspace_bytes (may be 0: then NULL is
- *              fine), 256-byte aligned; its contents need not be cleared.
+ *   workspace  device, 256-byte aligned, its contents need not be cleared; what
+ *              the call takes (tlr_block_gemm_plan; none where alpha == 0), or
+ *              tlr_block_gemm_workspace_bytes, the larger of both modes.  NULL
+ *              is fine where that is 0.
  * m and n up to 2^31 - 512 with less than 2^24 tiles of 128 x 128 in C; ld < 2^22.
  * Errors: TLR_ERR_INVALID_ARG (unknown flags among it), TLR_ERR_UNSUPPORTED (dt TLR_F64),
  * TLR_ERR_WORKSPACE, TLR_ERR_HIP.
@@ -537,6 +539,7 @@ tlr_status tlr_block_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, size_
 typedef struct {
   int32_t rows, cols, threads, halves, parts, reserved;
   int64_t grid_x, grid_y;
+  size_t workspace;        /* bytes */
 } tlr_block_gemm_choice;
 tlr_status tlr_block_gemm_plan(int64_t m, int64_t n, int64_t k, uint32_t flags, tlr_block_gemm_choice *out);
 

@@ -482,13 +482,13 @@ __device__ __forceinline__ u4 buffer(const void *p, int32_t bytes) {
 // Loads from a lane's offset in a descriptor, moved by the uniform `by`, straight
 // into LDS: lane l writes its 16 (4) bytes at lds + 16 (4) l.  Written out, with
 // no register for a result, since the compiler, where it issues them, has LDS
-// reads wait for them; the stage loop does the waiting.  Nothing else here uses
-// m0.
+// reads wait for them; the stage loop does the waiting.  The LDS address goes in
+// m0, as an operand in that register: the compiler sets it.
 __device__ __forceinline__ void to_lds16(u4 b, uint32_t at, uint32_t by, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" : : "s"(lds), "v"(at), "s"(b), "s"(by) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" : : "{m0}"(lds), "v"(at), "s"(b), "s"(by) : "memory");
 }
 __device__ __forceinline__ void to_lds4(u4 b, uint32_t at, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(lds), "v"(at), "s"(b) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(at), "s"(b) : "memory");
 }
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 __device__ __forceinline__ uint32_t lds_address(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_byte *)p; }

@@ -35,9 +35,13 @@ constexpr int FEW = 256;                  // assignments that an expert's workgr
 constexpr int MAX_SPLITS = 4;             // workgroups that share a router tile's columns
 constexpr int ROUTED = 32, BLOCKS = 64;   // counters: 0.. router groups, ROUTED all groups, BLOCKS.. row blocks of y
 
-// The 16-bit type of x, y and the products.
+// The 16-bit type of x, y and the products.  LOW: what the lower of the two
+// numbers that stand for silu(g) u is multiplied with.  Half precision ends at
+// 2^-24 and would cut the sum of the two there; with 2^11 it is cut at 2^-35, and
+// the largest remainder, 16 beside 65504, still fits.
 template <typename H> struct Num;
 template <> struct Num<_Float16> {
+  static constexpr float LOW = 0x1p11f;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f4 mma(u4 a, u4 b, f4 c) {
@@ -48,6 +52,7 @@ template <> struct Num<_Float16> {
   }
 };
 template <> struct Num<__bf16> {
+  static constexpr float LOW = 1.0f;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f4 mma(u4 a, u4 b, f4 c) {
@@ -76,7 +81,7 @@ struct MoeArgs {
   double *logits;           // splits x tokens x experts: parts of the router product
   int32_t splits;
   int32_t sorted;           // the experts' workgroups take their assignments from the router's tables
-  uint16_t *hi, *lo;        // tokens*topk x inter: silu(g) u as hi + lo
+  uint16_t *hi, *lo;        // tokens*topk x inter: silu(g) u as hi + lo / LOW
   float *part;              // tokens*topk x hidden: the experts' outputs
 };
 
@@ -388,9 +393,12 @@ template <typename H, bool W8, int RTILE, int NJ, bool TWO> struct Group {
   __device__ __forceinline__ void add(f4 (&acc)[RTILE][NJ]) const {
 #pragma unroll
     for (int i = 0; i < RTILE; ++i) {
-      f4 d[NJ];
+      f4 d[NJ], low[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) d[j] = W8 ? f4{0, 0, 0, 0} : acc[i][j];
+      for (int j = 0; j < NJ; ++j) {
+        d[j] = W8 ? f4{0, 0, 0, 0} : acc[i][j];
+        low[j] = f4{0, 0, 0, 0};
+      }
 #pragma unroll
       for (int b = 0; b < SUB; ++b) {
         u4 f[2];
@@ -409,17 +417,22 @@ template <typename H, bool W8, int RTILE, int NJ, bool TWO> struct Group {
           d[j] = Num<H>::mma(f[0], x[j][b][0], d[j]);
           d[j] = Num<H>::mma(f[1], x[j][b][1], d[j]);
           if constexpr (TWO) {
-            d[j] = Num<H>::mma(f[0], x2[j][b][0], d[j]);
-            d[j] = Num<H>::mma(f[1], x2[j][b][1], d[j]);
+            f4 &l = Num<H>::LOW == 1.0f ? d[j] : low[j];
+            l = Num<H>::mma(f[0], x2[j][b][0], l);
+            l = Num<H>::mma(f[1], x2[j][b][1], l);
           }
         }
       }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j) {
+        if constexpr (TWO && Num<H>::LOW != 1.0f)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) d[j][v] = __builtin_fmaf(low[j][v], 1.0f / Num<H>::LOW, d[j][v]);
         if constexpr (W8)
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(s[i], d[j][v], acc[i][j][v]);
         else acc[i][j] = d[j];
+      }
     }
   }
 };
@@ -448,13 +461,13 @@ __device__ __forceinline__ void multiply(f4 (&acc)[RTILE][NJ], const uint8_t *co
   }
 }
 
-// silu(g) u as a sum of two numbers of the type: one would round the sum that
-// the down product takes to 8 or 11 bits.
+// silu(g) u as a sum hi + lo / LOW of two numbers of the type: one would round the
+// sum that the down product takes to 8 or 11 bits, two keep 16 or 22.
 template <typename H> __device__ __forceinline__ void put_act(const MoeArgs &a, int64_t at, float g, float u) {
   const float v = g / (1.0f + expf(-g)) * u;
   const H hi = (H)v;
   const float rest = v - (float)hi;
-  const H lo = (H)(__builtin_isfinite(rest) ? rest : 0.0f);     // beyond the type's range hi is infinite
+  const H lo = (H)(__builtin_isfinite(rest) ? rest * Num<H>::LOW : 0.0f);     // beyond the type's range hi is infinite
   a.hi[at] = __builtin_bit_cast(uint16_t, hi);
   a.lo[at] = __builtin_bit_cast(uint16_t, lo);
 }
@@ -754,7 +767,7 @@ template <typename H, bool W8> __global__ __launch_bounds__(256) void down_one_k
     floats16<H, false>(hi, x);
     floats16<H, false>(lo, l);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] += l[i];      // exact: lo ends where the float that both were cut from did
+    for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(l[i], 1.0f / Num<H>::LOW, x[i]);      // exact: lo ends where the float that both were cut from did
 #pragma unroll
     for (int r = 0; r < ONE_ROWS; ++r) {
       float y[16], d = 0.0f;

@@ -573,8 +573,9 @@ typedef struct {
  *   lower index; NaN above all numbers), in decreasing order;
  *   y = sum over the chosen e of prob_e down_e (silu(gate_e x) * (up_e x)),
  *   sums in float, silu(g) u carried to the down product as a sum of two
- *   numbers of type dt (in half precision it must stay within its range, as
- *   the TLR products' intermediates), y rounded once.
+ *   numbers of type dt: 16 bits of it for bfloat16, 22 for half precision, where
+ *   it must stay below 65520, as the TLR products' intermediates, and is cut at
+ *   2^-35.  y rounded once.
  *   X, Y     token t at element t*ldx, t*ldy (>= hidden); X rows 16-byte aligned
  *            (ldx a multiple of 8), Y any alignment.
  *   ids      device int32, tokens x topk: the chosen experts; weights: float,

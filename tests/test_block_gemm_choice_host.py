@@ -3,6 +3,7 @@ import random
 
 import pytest
 
+import block_gemm_shapes
 from hpc_linear_algebra_amd import tlrgemm as T
 
 FAST = T.TLR_BLOCK_FAST
@@ -84,3 +85,20 @@ def test_a_call_needs_the_workspace_of_its_own_mode_and_only_for_a_product():
     assert e.value.status == T.TLR_ERR_WORKSPACE
     with pytest.raises(T.TLRError, match="A: null"):
         call(1.0, 0, 0x10000, exact.workspace)
+
+
+@pytest.mark.parametrize("flags,shapes", [(0, block_gemm_shapes.EXACT), (FAST, block_gemm_shapes.FAST)])
+def test_the_shapes_that_stand_for_each_kernel_take_it_and_leave_none_out(flags, shapes):
+    """The tests on the GPU run these shapes: a kernel that another choice of constants brings in needs one."""
+    def kind(m, n, k):
+        c = T.tlr_block_gemm_plan(m, n, k, flags)
+        return c.rows, c.cols, c.threads, c.halves, c.parts
+
+    for want, shape in shapes.items():
+        assert kind(*shape) == want, shape
+    rng = random.Random(2)
+    seen = set()
+    for _ in range(150000):
+        m, n = (int(2 ** rng.uniform(0, 15.5)) for _ in range(2))
+        seen.add(kind(m, n, int(2 ** rng.uniform(4, 15.5))))
+    assert seen <= set(shapes), seen - set(shapes)

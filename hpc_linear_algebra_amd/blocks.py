@@ -131,6 +131,9 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
     For results in 16 bits whose operands allow it."""
     if A.k != B.k:
         raise ValueError(f"gemm: contraction lengths differ ({A.k} and {B.k})")
+    new = _NEW.get(dtype)
+    if new is None:
+        raise ValueError(f"gemm: dtype is f32, f16 or bf16, not {dtype!r}")
     device = A.codes.device
     if B.codes.device != device:
         raise ValueError("gemm: operands on different devices")
@@ -141,7 +144,7 @@ def gemm(A: BlockScaled, B: BlockScaled, out: Optional[torch.Tensor] = None, alp
     elif tuple(out.shape) != (n, m) or out.dtype not in _DT or out.device != device or (m > 1 and out.stride(1) != 1):
         raise ValueError(f"gemm: out has to be a ({n}, {m}) float32, float16 or bfloat16 tensor with contiguous rows")
     flags = T.TLR_BLOCK_FAST if fast else 0
-    got = binding().gemm(A.codes, A.scales, A.block, B.codes, B.scales, B.block, m, n, A.k, alpha, beta, out, _NEW[dtype],
+    got = binding().gemm(A.codes, A.scales, A.block, B.codes, B.scales, B.block, m, n, A.k, alpha, beta, out, new,
                          flags, _gemm_workspace(m, n, A.k, flags) if alpha != 0.0 else 0)
     if type(got) is int:
         T._check(got, "tlr_block_gemm")

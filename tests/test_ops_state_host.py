@@ -107,3 +107,10 @@ def test_a_layer_refuses_what_requires_a_gradient():
     layer._trained = True
     with pytest.raises(RuntimeError, match="no backward"):
         layer(x.detach())
+
+
+def test_an_unknown_result_type_is_an_argument_error():
+    q = made()
+    for bad in ("f64", "e4m3", "float32", None, 3):
+        with pytest.raises(ValueError, match="dtype"):
+            blocks.gemm(q, q, dtype=bad)

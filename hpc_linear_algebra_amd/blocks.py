@@ -104,7 +104,9 @@ def quantize(x: torch.Tensor, block: int = 1, fmt: str = "e4m3", straight: bool 
     x is a 2-d float32, float16 or bfloat16 tensor whose rows are contiguous
     (any row stride).  block 1: a scale for every 128 entries of a row of the
     result; block 128: one for every 128 x 128 tile.  Codes and scales carry no
-    gradient, whatever x does: linear is the differentiable function."""
+    gradient, whatever x does: linear is the differentiable function.  A result's
+    codes and scales are views of one allocation, codes first: keeping or saving
+    either keeps or saves both; ``clone()`` one to part them."""
     f8 = _FMT.get(fmt)
     if f8 is None or block not in (1, BLOCK) or not (straight or transposed):
         raise ValueError("quantize: fmt is e4m3 or e5m2, block 1 or 128, and a result has to be wanted")

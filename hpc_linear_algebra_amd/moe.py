@@ -99,7 +99,9 @@ class MoELayer:
 
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(y, ids, weights) of x (tokens, hidden): the layer's output in x's
-        type, the chosen experts (int32) and their probabilities (float32)."""
+        type, the chosen experts (int32) and their probabilities (float32).  ids
+        and weights are views of one allocation: keeping or saving either keeps or
+        saves both."""
         if torch.is_grad_enabled() and (x.requires_grad or self._trained):
             raise RuntimeError("MoELayer has no backward pass: call it under torch.no_grad() or on detached tensors")
         if x.device != self.device:

@@ -520,7 +520,9 @@ tlr_status tlr_block_quantize(tlr_dtype dt, tlr_dtype fmt, int32_t block, int64_
  * codes of W (blocks of 128 rows), its weight gradient two matrices with
  * blocks of 1 row along the tokens.  Any block height on either side.
  * beta == 0 never reads C; alpha == 0 reads neither A nor B.  NaN scales and
- * codes propagate.  The product of two scales has to be a finite float.
+ * codes propagate.  The product of two scales is a float of its own: it has to be
+ * finite, and loses bits below 2^-126 (e4m3 blocks on both sides that reach no
+ * more than about 5e-17).
  *   workspace  device, 256-byte aligned, its contents need not be cleared; what
  *              the call takes (tlr_block_gemm_plan; none where alpha == 0), or
  *              tlr_block_gemm_workspace_bytes, the larger of both modes.  NULL

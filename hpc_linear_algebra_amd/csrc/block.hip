@@ -563,8 +563,8 @@ template <int ROWS, int T, bool IS_A> struct Panel {
 // 128 x 128 tiles on four waves 243 with three, 259 at once; 2501 x 1111 x 1747 on
 // eight waves 19.0 spread, 17.7 at once.
 //
-// What bounds 8192^3 (455 us, 2.4 PFLOP/s, 88% of the library's product without blocks):
-// the matrix cores are busy 53% of the clocks.  Timing copies: matrix instructions
+// What bounds 8192^3 (451 us, 2.4 PFLOP/s, 89% of the library's product without blocks):
+// the matrix cores are busy 62% of the clocks.  Timing copies (at 460 us as built): matrix instructions
 // and barriers alone 319 us, the scaled additions add 48, the loads 94 (alone they
 // take 377; two, three or four stages of them in flight make no difference, nor do
 // odd strides), the fragment reads from LDS 10.

@@ -10,9 +10,9 @@
 // tokens, which stay in L2) and the tokens of one expert as the columns.
 // 8-bit weights are widened to the 16-bit type in registers, exactly, and
 // their scale is applied to each block's float sum.  64 tokens of 128 experts
-// (2048, 1024, top 8, bf16): gate/up 178 us for 1.06 GB (5.9 TB/s), down 90 us
-// for 0.53 GB; 13 tokens of 96 experts (2064, 1168, top 6, e4m3): 52 and 32 us
-// for 263 and 131 MB.
+// (2048, 1024, top 8, bf16): gate/up 179 - 185 us for 1.06 GB (5.7 - 5.9 TB/s), down
+// 90 - 94 us for 0.53 GB; 13 tokens of 96 experts (2064, 1168, top 6, e4m3): 52 and
+// 32 us for 263 and 131 MB.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -32,7 +32,7 @@ def train(steps: int = 30, tokens: int = 512, width: int = 512, features: int = 
         with torch.no_grad():
             w -= 0.2 * features * w.grad
             w.grad = None
-        losses.append(float(loss))
+        losses.append(float(loss.detach()))
     return w.detach(), losses
 
 

@@ -41,7 +41,8 @@ class MoELayer:
 
     Calls share the layer's workspace, which is cleared on the stream that is
     current when the layer is made: making it and calling it run in the order of
-    one stream, or with events between them.
+    one stream, or with events between them.  Called on another stream than that,
+    the layer has to live until the call's work has ended.
 
     There is no backward pass: where gradients are on, an x or weights that
     require one are refused.

@@ -8,7 +8,8 @@ around tlr_block_quantize and tlr_block_gemm, include/tlrgemm.h).
     dx = blocks.gemm(W8t, dy8, fast=True)                       # dy W
     dW = blocks.gemm(x8t, dy8t, dtype="f32")                    # dy^T x
 
-``linear`` wraps these three products as one differentiable function.  Every
+``linear`` wraps these three products as one differentiable function; ``gated``
+is the activation between two of them, its input kept in 8 bits as well.  Every
 call runs on torch's current stream of the operands' device.
 """
 from __future__ import annotations
@@ -38,7 +39,10 @@ def binding():
     except ImportError as e:
         raise RuntimeError("the extension module is not built: python -m hpc_linear_algebra_amd.build") from e
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value   # noqa: E731
-    _binding.connect(address(lib.tlr_block_quantize), address(lib.tlr_block_gemm), address(lib.tlr_moe))
+    _binding.connect(*(address(getattr(lib, name)) for name in (
+        "tlr_block_quantize", "tlr_block_gemm", "tlr_moe", "tlr_row_quantize", "tlr_row_gemm_workspace_bytes", "tlr_row_gemm",
+        "tlr_expert_sort_workspace_bytes", "tlr_expert_sort", "tlr_expert_gather", "tlr_expert_combine",
+        "tlr_expert_combine_grad", "tlr_gated", "tlr_gated_grad")))
     return _binding
 
 
@@ -213,3 +217,55 @@ def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3", fast: bool 
     if grad_fmt not in FORMATS:
         raise ValueError("linear: grad_fmt is e4m3 or e5m2")
     return _Linear.apply(x, w, grad_fmt, fast)
+
+
+def gated_forward(x: torch.Tensor, keep: bool = True):
+    """(y, codes, scales) of a 2-d x: y = silu(gate) * up, and x as int8 codes
+    (rows, 2, inter rounded up to 16) with a float32 scale for every 128 of them
+    (rows, 2, ceil(inter/128)), gate first; None unless ``keep``.  The scale is the
+    largest magnitude over 127.  Codes and scales are views of one allocation."""
+    got = binding().gated(x, keep)
+    if type(got) is int:
+        T._check(got, "tlr_gated")
+    return got
+
+
+def gated_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """The gradient of gated_forward's x, in dy's type, taken at the values that
+    the codes and scales stand for."""
+    got = binding().gated_grad(dy, codes, scales)
+    if type(got) is int:
+        T._check(got, "tlr_gated_grad")
+    return got
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x):
+        y, codes, scales = gated_forward(_rows(x))
+        ctx.save_for_backward(codes, scales)
+        ctx.shape = x.shape
+        return y.reshape(*x.shape[:-1], y.shape[1])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        return gated_backward(_rows(dy), *ctx.saved_tensors).reshape(ctx.shape)
+
+
+def gated(x: torch.Tensor) -> torch.Tensor:
+    """silu(gate) * up for x (..., 2*inter) whose last dimension holds `inter`
+    gate entries, then `inter` up entries: (..., inter), in x's type.
+
+    Where x requires a gradient it is kept for the backward pass as int8 codes with
+    one scale for every 128 entries, a byte an entry in place of x; the gradient is
+    that at the values the codes stand for (off by at most the block's largest
+    magnitude / 254).  A block that holds an infinity or a NaN has NaN gradients.
+    No double backward.  In a captured graph take torch.autograd.grad, or leaves that
+    no live eager graph holds: their accumulation belongs to its stream."""
+    if x.dim() < 1 or x.shape[-1] % 2:
+        raise ValueError("gated: x is (..., 2*inter)")
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _Gated.apply(x)
+    y = gated_forward(_rows(x), keep=False)[0]
+    return y.reshape(*x.shape[:-1], y.shape[1])

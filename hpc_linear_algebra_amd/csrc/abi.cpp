@@ -298,6 +298,74 @@ tlr_status tlr_moe(const tlr_moe_layer *layer, int32_t tokens, const void *X, in
   TLR_GUARD({ return tlr::moe(layer, tokens, X, ldx, Y, ldy, ids, weights, workspace, workspace_bytes, stream); })
 }
 
+tlr_status tlr_row_quantize(tlr_dtype dt, int64_t rows, int64_t k, const void *X, int64_t x_rows, int64_t ldx,
+                            const int32_t *index, void *codes, int64_t ldq, float *scales, void *stream) {
+  TLR_GUARD({ return tlr::row_quantize(dt, rows, k, X, x_rows, ldx, index, codes, ldq, scales, stream); })
+}
+
+tlr_status tlr_row_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes_out) {
+  TLR_GUARD({
+    if (!bytes_out) return tlr::fail(TLR_ERR_INVALID_ARG, "row_gemm_workspace_bytes: null output");
+    tlr_block_gemm_choice c;
+    const tlr_status st = tlr::row_gemm_plan(m, n, k, groups, &c);
+    if (st == TLR_OK) *bytes_out = c.workspace;
+    return st;
+  })
+}
+
+tlr_status tlr_row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_block_gemm_choice *out) {
+  TLR_GUARD({ return tlr::row_gemm_plan(m, n, k, groups, out); })
+}
+
+tlr_status tlr_row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A,
+                        const tlr_row_matrix *B, const tlr_row_groups *groups, void *C, int64_t ldc,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+  TLR_GUARD({ return tlr::row_gemm(dt, m, n, k, A, B, groups, C, ldc, workspace, workspace_bytes, stream); })
+}
+
+tlr_status tlr_expert_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts, size_t *bytes_out) {
+  TLR_GUARD({ return tlr::expert_sort_workspace(tokens, topk, experts, bytes_out); })
+}
+
+tlr_status tlr_expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t experts, const void *ids,
+                           int32_t *offsets, int32_t *place, int32_t *rows, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  TLR_GUARD({
+    return tlr::expert_sort(id_bytes, tokens, topk, experts, ids, offsets, place, rows, workspace, workspace_bytes,
+                            stream);
+  })
+}
+
+tlr_status tlr_expert_gather(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *X, int64_t ldx,
+                             const int32_t *place, const int32_t *end, void *Y, int64_t ldy, void *stream) {
+  TLR_GUARD({ return tlr::expert_gather(dt, tokens, topk, hidden, X, ldx, place, end, Y, ldy, stream); })
+}
+
+tlr_status tlr_expert_combine(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *Y, int64_t ldy,
+                              const int32_t *place, const int32_t *end, const float *weights, void *out, int64_t ldo,
+                              void *stream) {
+  TLR_GUARD({ return tlr::expert_combine(dt, tokens, topk, hidden, Y, ldy, place, end, weights, out, ldo, stream); })
+}
+
+tlr_status tlr_expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *dout,
+                                   int64_t ldd, const void *Y, int64_t ldy, const int32_t *place, const int32_t *end,
+                                   const float *weights, void *dY, int64_t lddy, float *dweights, void *stream) {
+  TLR_GUARD({
+    return tlr::expert_combine_grad(dt, tokens, topk, hidden, dout, ldd, Y, ldy, place, end, weights, dY, lddy,
+                                    dweights, stream);
+  })
+}
+
+tlr_status tlr_gated(tlr_dtype dt, int64_t rows, int64_t inter, const void *X, int64_t ldx, void *Y, int64_t ldy,
+                     void *codes, int64_t ldq, float *scales, int64_t lds, void *stream) {
+  TLR_GUARD({ return tlr::gated(dt, rows, inter, X, ldx, Y, ldy, codes, ldq, scales, lds, stream); })
+}
+
+tlr_status tlr_gated_grad(tlr_dtype dt, int64_t rows, int64_t inter, const void *dY, int64_t lddy, const void *codes,
+                          int64_t ldq, const float *scales, int64_t lds, void *dX, int64_t lddx, void *stream) {
+  TLR_GUARD({ return tlr::gated_grad(dt, rows, inter, dY, lddy, codes, ldq, scales, lds, dX, lddx, stream); })
+}
+
 const char *tlr_status_string(tlr_status s) {
   switch (s) {
     case TLR_OK: return "TLR_OK";

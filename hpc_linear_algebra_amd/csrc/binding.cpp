@@ -17,6 +17,16 @@ namespace {
 decltype(&tlr_block_quantize) quantize_entry = nullptr;
 decltype(&tlr_block_gemm) gemm_entry = nullptr;
 decltype(&tlr_moe) moe_entry = nullptr;
+decltype(&tlr_row_quantize) row_quantize_entry = nullptr;
+decltype(&tlr_row_gemm_workspace_bytes) row_gemm_bytes_entry = nullptr;
+decltype(&tlr_row_gemm) row_gemm_entry = nullptr;
+decltype(&tlr_expert_sort_workspace_bytes) sort_bytes_entry = nullptr;
+decltype(&tlr_expert_sort) sort_entry = nullptr;
+decltype(&tlr_expert_gather) gather_entry = nullptr;
+decltype(&tlr_expert_combine) combine_entry = nullptr;
+decltype(&tlr_expert_combine_grad) combine_grad_entry = nullptr;
+decltype(&tlr_gated) gated_entry = nullptr;
+decltype(&tlr_gated_grad) gated_grad_entry = nullptr;
 
 // TLR_* of a tensor's type, -1 for types that are not X's or C's.
 int code_of(const at::Tensor &t) {
@@ -35,12 +45,24 @@ PyObject *value_error(const char *text) {
   return nullptr;
 }
 
-// connect(addresses of tlr_block_quantize, tlr_block_gemm, tlr_moe)
+template <typename F> void take(F &entry, PyObject *address) { entry = reinterpret_cast<F>(PyLong_AsVoidPtr(address)); }
+
+// connect(addresses of the entries above, in their order)
 PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  if (n != 3) return value_error("connect: 3 addresses");
-  quantize_entry = reinterpret_cast<decltype(quantize_entry)>(PyLong_AsVoidPtr(args[0]));
-  gemm_entry = reinterpret_cast<decltype(gemm_entry)>(PyLong_AsVoidPtr(args[1]));
-  moe_entry = reinterpret_cast<decltype(moe_entry)>(PyLong_AsVoidPtr(args[2]));
+  if (n != 13) return value_error("connect: 13 addresses");
+  take(quantize_entry, args[0]);
+  take(gemm_entry, args[1]);
+  take(moe_entry, args[2]);
+  take(row_quantize_entry, args[3]);
+  take(row_gemm_bytes_entry, args[4]);
+  take(row_gemm_entry, args[5]);
+  take(sort_bytes_entry, args[6]);
+  take(sort_entry, args[7]);
+  take(gather_entry, args[8]);
+  take(combine_entry, args[9]);
+  take(combine_grad_entry, args[10]);
+  take(gated_entry, args[11]);
+  take(gated_grad_entry, args[12]);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -205,12 +227,368 @@ PyObject *moe(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-PyMethodDef methods[] = {
-    {"connect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(connect)), METH_FASTCALL, nullptr},
-    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize)), METH_FASTCALL, nullptr},
-    {"gemm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm)), METH_FASTCALL, nullptr},
-    {"moe", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(moe)), METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+// ---- 8-bit integers with a scale for each row ----------------------------------------------------------
+
+// Stride between the rows of a matrix whose rows are contiguous.
+int64_t row_stride(const at::Tensor &x) {
+  return x.size(0) > 1 ? x.stride(0) : std::max<int64_t>({x.stride(0), x.size(1), 1});
+}
+
+// x, or a copy of it where its rows overlap or are not contiguous.
+at::Tensor with_rows(const at::Tensor &x) {
+  const bool fine = (x.size(1) <= 1 || x.stride(1) == 1) && (x.size(0) <= 1 || x.stride(0) >= x.size(1));
+  return fine ? x : x.clone(at::MemoryFormat::Contiguous);
+}
+
+at::ScalarType type_of(long code) { return code == TLR_F32 ? at::kFloat : code == TLR_F16 ? at::kHalf : at::kBFloat16; }
+
+PyObject *tuple_of(std::initializer_list<at::Tensor> t) {
+  PyObject *out = PyTuple_New((Py_ssize_t)t.size());
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor &x : t) PyTuple_SET_ITEM(out, i++, wrap(x));
+  return out;
+}
+
+// Codes (rows, ld) and scales (rows) in one allocation, the scales behind the codes.
+struct RowResult {
+  at::Tensor codes, scales;
+  RowResult(int64_t rows, int64_t k, const at::Device &d) {
+    const int64_t ld = (k + 15) / 16 * 16, scales_at = (rows * ld + 255) / 256 * 256;
+    codes = at::empty({scales_at + 4 * rows}, at::TensorOptions().dtype(at::kChar).device(d));
+    scales = beside(codes, at::kFloat, scales_at, rows, 1);
+    scales.unsafeGetTensorImpl()->set_sizes_contiguous({rows});
+    codes.unsafeGetTensorImpl()->set_sizes_contiguous({rows, ld});
+  }
+};
+
+const char *quantizable(const at::Tensor &x) {
+  return code_of(x) < 0 || x.dim() != 2 || !x.is_cuda() ? "quantize: a 2-d float32, float16 or bfloat16 tensor on a GPU is needed" : nullptr;
+}
+
+tlr_status quantize_rows(const at::Tensor &x, const int32_t *index, int64_t rows, const RowResult &r) {
+  return row_quantize_entry((tlr_dtype)code_of(x), rows, x.size(1), x.data_ptr(), x.size(0), row_stride(x), index,
+                            r.codes.data_ptr(), r.codes.size(1), static_cast<float *>(r.scales.data_ptr()), stream_of(x.device()));
+}
+
+// row_quantize(x, rows or None) -> (codes, scales) or a status
+PyObject *row_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2 || !THPVariable_Check(args[0])) return value_error("quantize: a tensor and rows");
+  at::Tensor x = THPVariable_Unpack(args[0]), index;
+  if (const char *wrong = quantizable(x)) return value_error(wrong);
+  if (args[1] != Py_None) {
+    if (!THPVariable_Check(args[1])) return value_error("quantize: rows is a tensor");
+    index = THPVariable_Unpack(args[1]);
+    if (index.scalar_type() != at::kInt || index.dim() != 1 || index.device() != x.device())
+      return value_error("quantize: rows is a 1-d int32 tensor on x's device");
+  }
+  const c10::DeviceGuard guard(x.device());
+  x = with_rows(x);
+  if (index.defined()) index = index.contiguous();
+  const int64_t rows = index.defined() ? index.size(0) : x.size(0);
+  const RowResult r(rows, x.size(1), x.device());
+  const tlr_status st = quantize_rows(x, index.defined() ? static_cast<const int32_t *>(index.data_ptr()) : nullptr, rows, r);
+  return st == TLR_OK ? tuple_of({r.codes, r.scales}) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// An operand of a product: the last two dimensions of codes, the last one of scales; null, or what is wrong.
+const char *row_operand(const at::Tensor &codes, const at::Tensor &scales, int64_t k, tlr_row_matrix *x) {
+  const int64_t d = codes.dim();
+  if ((d != 2 && d != 3) || codes.scalar_type() != at::kChar) return "codes: an int8 tensor of 2 or 3 dimensions is needed";
+  if (scales.dim() != d - 1 || scales.scalar_type() != at::kFloat || scales.device() != codes.device())
+    return "scales: a float32 tensor on the codes' device, a scale for each row, is needed";
+  for (int64_t i = 0; i < d - 1; ++i)
+    if (scales.size(i) != codes.size(i)) return "scales: one for each row of codes is needed";
+  const int64_t rows = codes.size(d - 2), wide = codes.size(d - 1);
+  if (k < 0 || wide < k || (wide > 1 && codes.stride(d - 1) != 1)) return "codes: contiguous rows of k entries are needed";
+  if (rows > 1 && scales.stride(d - 2) != 1) return "scales: contiguous rows are needed";
+  x->ld = k == 0 ? 0 : rows > 1 ? codes.stride(d - 2) : (wide + 15) / 16 * 16;
+  if (codes.numel() > 0 && k > 0) {
+    const int64_t last = codes.storage_offset() + (d == 3 ? (codes.size(0) - 1) * codes.stride(0) : 0) + (rows - 1) * x->ld;
+    if (last + (k + 15) / 16 * 16 > (int64_t)codes.storage().nbytes()) return "codes: every row has to be readable up to a multiple of 16 entries";
+  }
+  x->codes = codes.data_ptr();
+  x->scales = static_cast<const float *>(scales.data_ptr());
+  return nullptr;
+}
+
+// The product into c, with what it needs of workspace.
+tlr_status multiply(const at::Tensor &c, int64_t m, int64_t n, int64_t k, const tlr_row_matrix &A, const tlr_row_matrix &B,
+                    const tlr_row_groups *groups) {
+  size_t bytes = 0;
+  tlr_status st = row_gemm_bytes_entry(m, n, k, groups ? groups->count : 0, &bytes);
+  if (st != TLR_OK) return st;
+  at::Tensor ws;
+  if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(c.device()));
+  return row_gemm_entry((tlr_dtype)code_of(c), m, n, k, &A, &B, groups, c.data_ptr(), row_stride(c),
+                        bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream_of(c.device()));
+}
+
+// row_gemm(A's codes, scales, B's codes, scales, k, offsets or None, out or None, type of a new one) -> out or a status
+PyObject *row_gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  if (n_args != 8) return value_error("gemm: 8 arguments");
+  for (const int i : {0, 1, 2, 3})
+    if (!THPVariable_Check(args[i])) return value_error("gemm: codes and scales are tensors");
+  for (const int i : {5, 6})
+    if (args[i] != Py_None && !THPVariable_Check(args[i])) return value_error("gemm: offsets and out are tensors");
+  const int64_t k = PyLong_AsLongLong(args[4]);
+  const long type = PyLong_AsLong(args[7]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor &a_codes = THPVariable_Unpack(args[0]), &b_codes = THPVariable_Unpack(args[2]);
+  tlr_row_matrix A{}, B{};
+  if (const char *wrong = row_operand(a_codes, THPVariable_Unpack(args[1]), k, &A)) return value_error(wrong);
+  if (const char *wrong = row_operand(b_codes, THPVariable_Unpack(args[3]), k, &B)) return value_error(wrong);
+  const at::Device device = b_codes.device();
+  if (a_codes.device() != device || !device.is_cuda()) return value_error("gemm: operands on one GPU are needed");
+  if (b_codes.dim() != 2) return value_error("gemm: B's codes have 2 dimensions");
+  const c10::DeviceGuard guard(device);
+  const bool grouped = args[5] != Py_None;
+  if ((a_codes.dim() == 3) != grouped) return value_error("gemm: offsets belong to an A with a matrix for each group");
+  tlr_row_groups groups{};
+  at::Tensor offsets;
+  if (grouped) {
+    offsets = THPVariable_Unpack(args[5]);
+    if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.device() != device || offsets.size(0) != a_codes.size(0) + 1)
+      return value_error("gemm: offsets is a 1-d int32 tensor on the operands' device, one entry more than groups");
+    offsets = offsets.contiguous();
+    groups = tlr_row_groups{static_cast<const int32_t *>(offsets.data_ptr()), a_codes.stride(0), THPVariable_Unpack(args[1]).stride(0),
+                            (int32_t)std::min<int64_t>(a_codes.size(0), 0x7fffffff), args[6] == Py_None};
+  }
+  const int64_t m = a_codes.size(-2), n = b_codes.size(0);
+  const bool grad = c10::GradMode::is_enabled();
+  if (grad && (THPVariable_Unpack(args[1]).requires_grad() || THPVariable_Unpack(args[3]).requires_grad()))
+    return value_error("gemm: scales that require a gradient would get none");
+  at::Tensor c;
+  if (args[6] == Py_None) {
+    c = at::empty({n, m}, at::TensorOptions().device(device).dtype(type_of(type)));
+  } else {
+    c = THPVariable_Unpack(args[6]);
+    if (c.dim() != 2 || c.size(0) != n || c.size(1) != m || code_of(c) < 0 || c.device() != device || (m > 1 && c.stride(1) != 1))
+      return value_error("gemm: out has to be a (B's rows, A's rows) float32, float16 or bfloat16 tensor with contiguous rows");
+    if (grad && c.requires_grad()) return value_error("gemm: an out that requires a gradient would get none");
+    if (!c.is_inference()) c.unsafeGetTensorImpl()->bump_version();      // written in place, as autograd sees it
+  }
+  const tlr_status st = multiply(c, m, n, k, A, B, grouped ? &groups : nullptr);
+  return st == TLR_OK ? wrap(c) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// row_linear(x, W's codes, scales, k) -> (rows of x, rows of W) or a status: x quantized and multiplied in one call
+PyObject *row_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4) return value_error("linear: 4 arguments");
+  for (const int i : {0, 1, 2})
+    if (!THPVariable_Check(args[i])) return value_error("linear: x, codes and scales are tensors");
+  at::Tensor x = THPVariable_Unpack(args[0]);
+  const at::Tensor &codes = THPVariable_Unpack(args[1]);
+  const int64_t k = PyLong_AsLongLong(args[3]);
+  if (PyErr_Occurred()) return nullptr;
+  if (const char *wrong = quantizable(x)) return value_error(wrong);
+  tlr_row_matrix A{};
+  if (const char *wrong = row_operand(codes, THPVariable_Unpack(args[2]), k, &A)) return value_error(wrong);
+  if (codes.dim() != 2 || codes.device() != x.device() || x.size(1) != k) return value_error("linear: x is (..., k) on the device of a weight of 2 dimensions");
+  if (c10::GradMode::is_enabled() && THPVariable_Unpack(args[2]).requires_grad()) return value_error("linear: scales that require a gradient would get none");
+  const c10::DeviceGuard guard(x.device());
+  x = with_rows(x);
+  const RowResult r(x.size(0), k, x.device());
+  tlr_status st = quantize_rows(x, nullptr, x.size(0), r);
+  if (st != TLR_OK) return PyLong_FromLong(st);
+  const at::Tensor c = at::empty({x.size(0), codes.size(0)}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+  const tlr_row_matrix B{r.codes.data_ptr(), static_cast<const float *>(r.scales.data_ptr()), r.codes.size(1)};
+  st = multiply(c, codes.size(0), x.size(0), k, A, B, nullptr);
+  return st == TLR_OK ? wrap(c) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// ---- tokens sorted by expert ---------------------------------------------------------------------------
+
+// sort(ids, experts) -> (offsets, place, rows), views of one allocation, or a status
+PyObject *sort(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2 || !THPVariable_Check(args[0])) return value_error("sort: a tensor and a number");
+  at::Tensor ids = THPVariable_Unpack(args[0]);
+  const long experts = PyLong_AsLong(args[1]);
+  if (PyErr_Occurred()) return nullptr;
+  if (ids.dim() != 2 || !ids.is_cuda() || (ids.scalar_type() != at::kInt && ids.scalar_type() != at::kLong))
+    return value_error("sort: ids is a (tokens, topk) int32 or int64 tensor on a GPU");
+  if (experts < 1 || experts > 1024 || ids.size(1) < 1 || ids.size(1) > 64) return value_error("sort: experts are 1 .. 1024, topk 1 .. 64");
+  const c10::DeviceGuard guard(ids.device());
+  ids = ids.contiguous();
+  const int64_t tokens = ids.size(0), topk = ids.size(1), all = tokens * topk;
+  size_t bytes = 0;
+  tlr_status st = sort_bytes_entry(tokens, (int32_t)topk, (int32_t)experts, &bytes);
+  if (st != TLR_OK) return PyLong_FromLong(st);
+  const at::TensorOptions on = at::TensorOptions().device(ids.device()).dtype(at::kInt);
+  const at::Tensor offsets = at::empty({experts + 1 + 2 * all + (int64_t)bytes / 4}, on);
+  const at::Tensor place = beside(offsets, at::kInt, 4 * (experts + 1), tokens, topk), rows = beside(offsets, at::kInt, 4 * (experts + 1 + all), all, 1);
+  rows.unsafeGetTensorImpl()->set_sizes_contiguous({all});
+  auto *p = static_cast<int32_t *>(offsets.data_ptr());
+  offsets.unsafeGetTensorImpl()->set_sizes_contiguous({experts + 1});
+  st = sort_entry(ids.scalar_type() == at::kInt ? 4 : 8, tokens, (int32_t)topk, (int32_t)experts, ids.data_ptr(), p, p + experts + 1,
+                  p + experts + 1 + all, bytes ? p + experts + 1 + 2 * all : nullptr, bytes, stream_of(ids.device()));
+  return st == TLR_OK ? tuple_of({offsets, place, rows}) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// What the operators on sorted rows take of a sort: place (tokens, topk) and the first row of no expert.
+struct Order {
+  at::Tensor place, offsets;
+  int64_t tokens = 0, topk = 0;
+  const int32_t *at = nullptr, *end = nullptr;
+  const char *wrong = nullptr;
+  Order(PyObject *p, PyObject *o, const at::Device &d) {
+    wrong = "an order as moe.sort gives it, on the operands' device, is needed";
+    if (!THPVariable_Check(p) || !THPVariable_Check(o)) return;
+    place = THPVariable_Unpack(p);
+    offsets = THPVariable_Unpack(o);
+    if (place.scalar_type() != at::kInt || place.dim() != 2 || place.device() != d || !place.is_contiguous()) return;
+    if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.size(0) < 2 || offsets.device() != d || !offsets.is_contiguous()) return;
+    tokens = place.size(0);
+    topk = place.size(1);
+    at = static_cast<const int32_t *>(place.data_ptr());
+    end = static_cast<const int32_t *>(offsets.data_ptr()) + offsets.size(0) - 1;
+    wrong = nullptr;
+  }
+};
+
+const char *rows_of(const at::Tensor &x, int64_t rows) {
+  return code_of(x) < 0 || x.dim() != 2 || !x.is_cuda() || x.size(0) != rows ? "2-d float32, float16 or bfloat16 tensors on a GPU, of the order's rows, are needed" : nullptr;
+}
+
+// gather(x, place, offsets) -> sorted rows or a status
+PyObject *gather(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3 || !THPVariable_Check(args[0])) return value_error("gather: 3 tensors");
+  at::Tensor x = THPVariable_Unpack(args[0]);
+  const Order o(args[1], args[2], x.device());
+  if (o.wrong) return value_error(o.wrong);
+  if (const char *wrong = rows_of(x, o.tokens)) return value_error(wrong);
+  const c10::DeviceGuard guard(x.device());
+  x = with_rows(x);
+  const at::Tensor y = at::empty({o.tokens * o.topk, x.size(1)}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+  const tlr_status st = gather_entry((tlr_dtype)code_of(x), o.tokens, (int32_t)o.topk, x.size(1), x.data_ptr(), row_stride(x), o.at, o.end,
+                                     y.data_ptr(), row_stride(y), stream_of(x.device()));
+  return st == TLR_OK ? wrap(y) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+const char *weights_of(const at::Tensor &w, const Order &o, const at::Device &d) {
+  return w.scalar_type() != at::kFloat || w.dim() != 2 || w.size(0) != o.tokens || w.size(1) != o.topk || w.device() != d
+             ? "weights: a float32 (tokens, topk) tensor on the operands' device is needed" : nullptr;
+}
+
+// combine(y, weights or None, place, offsets) -> a row for each token or a status
+PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4 || !THPVariable_Check(args[0]) || !(args[1] == Py_None || THPVariable_Check(args[1]))) return value_error("combine: 4 tensors");
+  at::Tensor y = THPVariable_Unpack(args[0]), w;
+  const Order o(args[2], args[3], y.device());
+  if (o.wrong) return value_error(o.wrong);
+  if (const char *wrong = rows_of(y, o.tokens * o.topk)) return value_error(wrong);
+  const c10::DeviceGuard guard(y.device());
+  if (args[1] != Py_None) {
+    w = THPVariable_Unpack(args[1]);
+    if (const char *wrong = weights_of(w, o, y.device())) return value_error(wrong);
+    w = w.contiguous();
+  }
+  y = with_rows(y);
+  const at::Tensor out = at::empty({o.tokens, y.size(1)}, at::TensorOptions().device(y.device()).dtype(y.scalar_type()));
+  const tlr_status st = combine_entry((tlr_dtype)code_of(y), o.tokens, (int32_t)o.topk, y.size(1), y.data_ptr(), row_stride(y), o.at, o.end,
+                                      w.defined() ? static_cast<const float *>(w.data_ptr()) : nullptr, out.data_ptr(), row_stride(out),
+                                      stream_of(y.device()));
+  return st == TLR_OK ? wrap(out) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// combine_grad(dout, y, weights, place, offsets, dy wanted, dweights wanted) -> (dy or None, dweights or None) or a status
+PyObject *combine_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7) return value_error("combine_grad: 7 arguments");
+  for (const int i : {0, 1, 2})
+    if (!THPVariable_Check(args[i])) return value_error("combine_grad: dout, y and weights are tensors");
+  at::Tensor dout = THPVariable_Unpack(args[0]), y = THPVariable_Unpack(args[1]), w = THPVariable_Unpack(args[2]), dy, dw;
+  const int want_y = PyObject_IsTrue(args[5]), want_w = PyObject_IsTrue(args[6]);
+  const at::Device d = dout.device();
+  const Order o(args[3], args[4], d);
+  if (o.wrong) return value_error(o.wrong);
+  if (const char *wrong = rows_of(dout, o.tokens)) return value_error(wrong);
+  if (const char *wrong = rows_of(y, o.tokens * o.topk)) return value_error(wrong);
+  if (const char *wrong = weights_of(w, o, d)) return value_error(wrong);
+  if (y.device() != d || y.scalar_type() != dout.scalar_type() || y.size(1) != dout.size(1))
+    return value_error("combine_grad: y and dout of one type, width and device are needed");
+  const c10::DeviceGuard guard(d);
+  dout = with_rows(dout);
+  y = with_rows(y);
+  w = w.contiguous();
+  if (want_y) dy = at::empty({y.size(0), y.size(1)}, at::TensorOptions().device(d).dtype(y.scalar_type()));
+  if (want_w) dw = at::empty({o.tokens, o.topk}, at::TensorOptions().device(d).dtype(at::kFloat));
+  const tlr_status st = combine_grad_entry((tlr_dtype)code_of(y), o.tokens, (int32_t)o.topk, y.size(1), dout.data_ptr(), row_stride(dout),
+                                           y.data_ptr(), row_stride(y), o.at, o.end, static_cast<const float *>(w.data_ptr()),
+                                           want_y ? dy.data_ptr() : nullptr, want_y ? row_stride(dy) : y.size(1),
+                                           want_w ? static_cast<float *>(dw.data_ptr()) : nullptr, stream_of(d));
+  return st == TLR_OK ? tuple_of({dy, dw}) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// ---- gated activation -----------------------------------------------------------------------------------
+
+// gated(x, keep) -> (y, codes, scales) or a status; codes (rows, 2, ld) and scales (rows, 2, blocks), in one allocation,
+// None unless kept
+PyObject *gated(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2 || !THPVariable_Check(args[0])) return value_error("gated: a tensor and a truth value");
+  at::Tensor x = THPVariable_Unpack(args[0]), codes, scales;
+  const int keep = PyObject_IsTrue(args[1]);
+  if (code_of(x) < 0 || x.dim() != 2 || !x.is_cuda() || x.size(1) % 2 != 0)
+    return value_error("gated: a float32, float16 or bfloat16 tensor on a GPU with rows of two halves is needed");
+  const c10::DeviceGuard guard(x.device());
+  x = with_rows(x);
+  const int64_t rows = x.size(0), inter = x.size(1) / 2, ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
+  const at::Tensor y = at::empty({rows, inter}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+  if (keep) {
+    const int64_t scales_at = (2 * rows * ld + 255) / 256 * 256;
+    codes = at::empty({scales_at + 8 * rows * nq}, at::TensorOptions().dtype(at::kChar).device(x.device()));
+    scales = beside(codes, at::kFloat, scales_at, 2 * rows, nq);
+    scales.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, nq});
+    codes.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, ld});
+  }
+  const tlr_status st = gated_entry((tlr_dtype)code_of(x), rows, inter, x.data_ptr(), row_stride(x), y.data_ptr(), row_stride(y),
+                                    keep ? codes.data_ptr() : nullptr, ld, keep ? static_cast<float *>(scales.data_ptr()) : nullptr, nq,
+                                    stream_of(x.device()));
+  return st == TLR_OK ? tuple_of({y, codes, scales}) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// gated_grad(dy, codes, scales) -> dx or a status
+PyObject *gated_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3) return value_error("gated_grad: 3 tensors");
+  for (const int i : {0, 1, 2})
+    if (!THPVariable_Check(args[i])) return value_error("gated_grad: 3 tensors");
+  at::Tensor dy = THPVariable_Unpack(args[0]);
+  const at::Tensor &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]);
+  if (code_of(dy) < 0 || dy.dim() != 2 || !dy.is_cuda()) return value_error("gated_grad: dy is a 2-d float32, float16 or bfloat16 tensor on a GPU");
+  const int64_t rows = dy.size(0), inter = dy.size(1), ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
+  if (codes.scalar_type() != at::kChar || codes.sizes() != at::IntArrayRef({rows, 2, ld}) || !codes.is_contiguous() || codes.device() != dy.device() ||
+      scales.scalar_type() != at::kFloat || scales.sizes() != at::IntArrayRef({rows, 2, nq}) || !scales.is_contiguous() || scales.device() != dy.device())
+    return value_error("gated_grad: codes and scales as gated gives them, of dy's rows, are needed");
+  const c10::DeviceGuard guard(dy.device());
+  dy = with_rows(dy);
+  const at::Tensor dx = at::empty({rows, 2 * inter}, at::TensorOptions().device(dy.device()).dtype(dy.scalar_type()));
+  const tlr_status st = gated_grad_entry((tlr_dtype)code_of(dy), rows, inter, dy.data_ptr(), row_stride(dy), codes.data_ptr(), ld,
+                                         static_cast<const float *>(scales.data_ptr()), nq, dx.data_ptr(), row_stride(dx), stream_of(dy.device()));
+  return st == TLR_OK ? wrap(dx) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {METHOD(connect), METHOD(quantize), METHOD(gemm), METHOD(moe), METHOD(row_quantize), METHOD(row_gemm),
+                         METHOD(row_linear), METHOD(sort), METHOD(gather), METHOD(combine), METHOD(combine_grad), METHOD(gated),
+                         METHOD(gated_grad), {nullptr, nullptr, 0, nullptr}};
+#undef METHOD
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

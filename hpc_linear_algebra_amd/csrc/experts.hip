@@ -1,0 +1,431 @@
+// Tokens sorted by expert and back, with weights, and the gradients, for gfx950.
+//
+// A router gives each token `topk` assignments to experts.  The sort gives each
+// assignment a row, so that every expert's rows are consecutive and in the order
+// of their tokens (a counting sort; no atomics on results, so the same inputs give
+// the same rows).  gather copies a token to its rows, combine adds its rows with
+// the router's weights; the gradient of one is the other:
+//   gather   xs[p(t,s)] = x[t]                  dx[t] = sum_s dxs[p(t,s)]
+//   combine  out[t] = sum_s w[t,s] y[p(t,s)]    dy[p(t,s)] = w[t,s] dout[t],
+//                                               dw[t,s] = <dout[t], y[p(t,s)]>
+// Assignments to no expert have the rows behind the last expert's: they are filled
+// with zeros and never read.  All of it moves each row once, bound by HBM; sums
+// are in float, in the order of s.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <string>
+
+#include "int8.h"
+#include "tlr_ops.h"
+
+namespace tlr {
+
+namespace {
+
+// ---- sort --------------------------------------------------------------------------------------------
+
+constexpr int MOST_EXPERTS = 1024, MOST_TOPK = 64;
+constexpr int WAVES = 16, EACH = 4, PART = WAVES * 64 * EACH;      // assignments of a workgroup
+
+struct SortArgs {
+  const void *ids;
+  int32_t *offsets, *place, *rows;
+  int32_t *counts;          // (parts, experts + 1), where there are several parts
+  int32_t n, topk, experts, parts;
+};
+
+// The expert of an assignment; `experts` for none.
+template <typename ID> __device__ __forceinline__ int expert_of(const SortArgs &a, int i) {
+  const ID e = static_cast<const ID *>(a.ids)[i];
+  return e >= 0 && e < (ID)a.experts ? (int)e : a.experts;
+}
+
+// How many assignments of its part each expert has.
+template <typename ID> __global__ __launch_bounds__(1024) void count_kernel(SortArgs a) {
+  __shared__ int32_t hist[MOST_EXPERTS + 1];
+  for (int e = threadIdx.x; e <= a.experts; e += 1024) hist[e] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < EACH; ++c) {
+    const int64_t i = (int64_t)blockIdx.x * PART + c * 1024 + threadIdx.x;
+    if (i < a.n) atomicAdd(&hist[expert_of<ID>(a, (int)i)], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.experts; e += 1024) a.counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
+}
+
+// Rows of a part's assignments.  A wave takes 64 consecutive ones at a time: which
+// lanes share an expert follows from one ballot for each bit of its number, and a
+// lane's rank is the number of such lanes before it, added to the wave's count so
+// far.  Ranks, counts of the waves before, counts of the parts before and the
+// experts' first rows add up to the row.
+template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortArgs a) {
+  __shared__ int32_t hist[WAVES][MOST_EXPERTS + 1];
+  __shared__ int32_t sums[WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t first = (int64_t)blockIdx.x * PART + wave * 64 * EACH + lane;
+  int e[EACH], rank[EACH];
+#pragma unroll
+  for (int c = 0; c < EACH; ++c) e[c] = first + 64 * c < a.n ? expert_of<ID>(a, (int)(first + 64 * c)) : -1;
+  for (int x = lane; x <= a.experts; x += 64) hist[wave][x] = 0;
+  const int bits = 32 - __builtin_clz(a.experts);
+#pragma unroll
+  for (int c = 0; c < EACH; ++c) {
+    uint64_t same = __ballot(e[c] >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const bool on = (e[c] >> b) & 1;
+      const uint64_t m = __ballot(on);
+      same &= on ? m : ~m;
+    }
+    const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
+    asm volatile("" ::: "memory");
+    if (e[c] >= 0) {
+      const int so_far = hist[wave][e[c]];
+      asm volatile("" ::: "memory");
+      rank[c] = so_far + before;
+      if (before == 0) hist[wave][e[c]] = so_far + __builtin_popcountll(same);
+    }
+    asm volatile("" ::: "memory");
+  }
+  __syncthreads();
+  // thread x: expert x (the last column, of no expert, is thread 0's as well)
+  auto column = [&](int x, int &before, int &all) {
+    before = all = 0;
+    int part = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const int v = hist[w][x];
+      hist[w][x] = part;
+      part += v;
+    }
+    if (a.parts == 1) {
+      all = part;
+      return;
+    }
+    for (int p = 0; p < a.parts; ++p) {
+      const int v = a.counts[(int64_t)p * (a.experts + 1) + x];
+      before += p < (int)blockIdx.x ? v : 0;
+      all += v;
+    }
+  };
+  int before = 0, all = 0;
+  if (tid < a.experts) column(tid, before, all);
+  int scan = all;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(scan, d);
+    if (lane >= d) scan += v;
+  }
+  if (lane == 63) sums[wave] = scan;
+  __syncthreads();
+  int total = 0, start = scan - all;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w < wave) start += sums[w];
+    total += sums[w];
+  }
+  if (tid < a.experts) {
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) hist[w][tid] += start + before;
+    if (blockIdx.x == 0) a.offsets[tid] = start;
+  }
+  if (tid == 0) {
+    int none_before, none;
+    column(a.experts, none_before, none);
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) hist[w][a.experts] += total + none_before;
+    if (blockIdx.x == 0) a.offsets[a.experts] = total;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < EACH; ++c)
+    if (e[c] >= 0) {
+      const int i = (int)(first + 64 * c), p = hist[wave][e[c]] + rank[c];
+      a.place[i] = p;
+      a.rows[p] = e[c] < a.experts ? i / a.topk : -1;
+    }
+}
+
+// ---- rows --------------------------------------------------------------------------------------------
+
+struct RowArgs {
+  const void *x;            // gather: tokens; combine: rows; gradient: tokens (dout)
+  void *y;                  // gather: rows; combine: tokens; gradient: rows (dy)
+  const void *rows;         // gradient: the rows that were combined
+  int64_t ldx, ldy, ldr;
+  const int32_t *place, *end;
+  const float *weights;
+  float *dweights;
+  int32_t tokens, topk, hidden, chunks;
+};
+
+// An assignment's row; -1 if none is its own.  Nothing but 0 .. tokens * topk - 1
+// is used as one, whatever stands in `place`.
+__device__ __forceinline__ int row_of(const RowArgs &a, int64_t i, int end) {
+  const int p = a.place[i];
+  return p >= 0 && p < end ? p : -1;
+}
+__device__ __forceinline__ int end_of(const RowArgs &a) { return min(*a.end, a.tokens * a.topk); }
+
+// 16 bytes of a row, the last ones fewer.
+__device__ __forceinline__ void copy_out(char *p, u4 v, int left) {
+  if (left >= 16) __builtin_memcpy(p, &v, 16);
+  else
+    for (int h = 0; 2 * h < left; ++h) reinterpret_cast<uint16_t *>(p)[h] = (uint16_t)(v[h >> 1] >> (16 * (h & 1)));
+}
+
+// A wave takes 1024 bytes of a token's row and writes them topk times (sizes in bytes).
+__global__ __launch_bounds__(256) void gather_kernel(RowArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tasks = (int64_t)a.tokens * a.chunks, all = (int64_t)a.tokens * a.topk;
+  const int end = end_of(a);
+  for (int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); task < tasks; task += (int64_t)gridDim.x * 4) {
+    const int64_t t = task / a.chunks;
+    const int at = (int)(task - t * a.chunks) * 1024 + lane * 16, left = a.hidden - at;
+    if (left <= 0) continue;
+    const char *p = static_cast<const char *>(a.x) + t * a.ldx + at;
+    u4 v = u4{0, 0, 0, 0};
+    if (left >= 16) __builtin_memcpy(&v, p, 16);
+    else
+      for (int h = 0; 2 * h < left; ++h) v[h >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[h] << (16 * (h & 1));
+    for (int s = 0; s < a.topk; ++s) {
+      const int row = a.place[t * a.topk + s];
+      if (row < 0 || row >= all) continue;
+      copy_out(static_cast<char *>(a.y) + row * a.ldy + at, row < end ? v : u4{0, 0, 0, 0}, left);
+    }
+  }
+}
+
+// A wave adds 512 entries of a token's rows.
+template <typename T> __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tasks = (int64_t)a.tokens * a.chunks;
+  const int end = end_of(a);
+  for (int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); task < tasks; task += (int64_t)gridDim.x * 4) {
+    const int64_t t = task / a.chunks;
+    const int at = (int)(task - t * a.chunks) * 512 + lane * 8, left = a.hidden - at;
+    if (left <= 0) continue;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < a.topk; ++s) {
+      const int row = row_of(a, t * a.topk + s, end);
+      if (row < 0) continue;
+      const float w = a.weights ? a.weights[t * a.topk + s] : 1.0f;
+      float v[8];
+      get8(static_cast<const T *>(a.x) + row * a.ldx + at, left, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w, v[e], sum[e]);
+    }
+    put8(static_cast<T *>(a.y) + t * a.ldy + at, left, sum);
+  }
+}
+
+// A workgroup takes a token: dout is read once for eight of its rows, which take
+// w dout and give their dot products with it.
+template <typename T> __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
+  constexpr int G = 8;
+  __shared__ float part[4][G];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int end = end_of(a);
+  const int64_t all = (int64_t)a.tokens * a.topk;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const T *d = static_cast<const T *>(a.x) + t * a.ldx;
+    for (int s0 = 0; s0 < a.topk; s0 += G) {
+      int row[G];
+      float w[G], dot[G];
+#pragma unroll
+      for (int s = 0; s < G; ++s) {
+        row[s] = s0 + s < a.topk ? a.place[t * a.topk + s0 + s] : -1;
+        if (row[s] >= all) row[s] = -1;
+        w[s] = row[s] >= 0 && row[s] < end ? a.weights[t * a.topk + s0 + s] : 0.0f;
+        dot[s] = 0.0f;
+      }
+      for (int at = tid * 8; at < a.hidden; at += 2048) {
+        const int left = a.hidden - at;
+        float v[8];
+        get8(d + at, left, v);
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+          if (row[s] < 0) continue;
+          const bool real = row[s] < end;
+          if (a.rows && real) {
+            float y[8];
+            get8(static_cast<const T *>(a.rows) + row[s] * a.ldr + at, left, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[s] = __builtin_fmaf(v[e], y[e], dot[s]);
+          }
+          if (a.y) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = real ? w[s] * v[e] : 0.0f;
+            put8(static_cast<T *>(a.y) + row[s] * a.ldy + at, left, o);
+          }
+        }
+      }
+      if (!a.dweights) continue;
+#pragma unroll
+      for (int s = 0; s < G; ++s) {
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) dot[s] += __shfl_xor(dot[s], x);
+        if (lane == 0) part[wave][s] = dot[s];
+      }
+      __syncthreads();
+      if (tid < G && s0 + tid < a.topk) a.dweights[t * a.topk + s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      __syncthreads();
+    }
+  }
+}
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t SIZE_LIM = 0x7fffffff, MOST = 1 << 24;      // assignments
+
+tlr_status launched(const char *what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(TLR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+  return TLR_OK;
+}
+
+tlr_status check_counts(const std::string &w, int64_t tokens, int32_t topk) {
+  if (topk < 1 || topk > MOST_TOPK) return fail(TLR_ERR_INVALID_ARG, w + "topk is 1 .. 64");
+  if (tokens < 0 || tokens > SIZE_LIM || tokens * topk > MOST) return fail(TLR_ERR_INVALID_ARG, w + "too many tokens");
+  return TLR_OK;
+}
+
+int64_t parts_of(int64_t n) { return std::max<int64_t>(1, (n + PART - 1) / PART); }
+
+// What the operators on rows check; sets the sizes.
+tlr_status check_rows(const char *name, tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const int32_t *place,
+                      const int32_t *end, RowArgs *a) {
+  const std::string w = std::string(name) + ": ";
+  if (dt == TLR_F64) return fail(TLR_ERR_UNSUPPORTED, w + "TLR_F64 is not provided");
+  if (dt != TLR_F32 && dt != TLR_F16 && dt != TLR_BF16) return fail(TLR_ERR_INVALID_ARG, w + "bad dtype");
+  const tlr_status st = check_counts(w, tokens, topk);
+  if (st != TLR_OK) return st;
+  if (hidden < 0 || hidden > 1 << 24) return fail(TLR_ERR_INVALID_ARG, w + "hidden out of range");
+  if (tokens > 0 && hidden > 0 && (!place || !end || !aligned(place, 4) || !aligned(end, 4)))
+    return fail(TLR_ERR_INVALID_ARG, w + "null or misaligned place or end");
+  a->place = place;
+  a->end = end;
+  a->tokens = (int32_t)tokens;
+  a->topk = topk;
+  a->hidden = (int32_t)hidden;
+  return TLR_OK;
+}
+
+tlr_status check_matrix(const char *what, tlr_dtype dt, const void *p, int64_t ld, int64_t hidden) {
+  if (ld < hidden || ld > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, std::string(what) + ": leading dimension out of range");
+  if (!p || !aligned(p, dt == TLR_F32 ? 4 : 2)) return fail(TLR_ERR_INVALID_ARG, std::string(what) + ": null or misaligned");
+  return TLR_OK;
+}
+
+unsigned wave_grid(int64_t tasks) { return (unsigned)std::min<int64_t>((tasks + 3) / 4, 1 << 22); }
+
+}  // namespace
+
+tlr_status expert_sort_workspace(int64_t tokens, int32_t topk, int32_t experts, size_t *bytes) {
+  if (!bytes) return fail(TLR_ERR_INVALID_ARG, "expert_sort_workspace_bytes: null output");
+  const tlr_status st = check_counts("expert_sort_workspace_bytes: ", tokens, topk);
+  if (st != TLR_OK) return st;
+  if (experts < 1 || experts > MOST_EXPERTS) return fail(TLR_ERR_INVALID_ARG, "expert_sort_workspace_bytes: experts are 1 .. 1024");
+  const int64_t parts = parts_of(tokens * topk);
+  *bytes = parts > 1 ? sizeof(int32_t) * (size_t)parts * (experts + 1) : 0;
+  return TLR_OK;
+}
+
+tlr_status expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t experts, const void *ids, int32_t *offsets,
+                       int32_t *place, int32_t *rows, void *ws, size_t ws_bytes, void *stream) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(TLR_ERR_INVALID_ARG, "expert_sort: ids have 4 or 8 bytes");
+  size_t need = 0;
+  const tlr_status st = expert_sort_workspace(tokens, topk, experts, &need);
+  if (st != TLR_OK) return st;
+  const int64_t n = tokens * topk;
+  if (!offsets || !aligned(offsets, 4)) return fail(TLR_ERR_INVALID_ARG, "expert_sort: null or misaligned offsets");
+  if (n > 0 && (!ids || !aligned(ids, id_bytes) || !place || !aligned(place, 4) || !rows || !aligned(rows, 4)))
+    return fail(TLR_ERR_INVALID_ARG, "expert_sort: null or misaligned ids, place or rows");
+  if (need > 0 && (!ws || !aligned(ws, 4))) return fail(TLR_ERR_INVALID_ARG, "expert_sort: null or misaligned workspace");
+  if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "expert_sort: workspace too small");
+  const SortArgs a{ids, offsets, place, rows, static_cast<int32_t *>(ws), (int32_t)n, topk, experts, (int32_t)parts_of(n)};
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (id_bytes == 4) {
+    if (a.parts > 1) count_kernel<int32_t><<<a.parts, 1024, 0, hs>>>(a);
+    sort_kernel<int32_t><<<a.parts, 1024, 0, hs>>>(a);
+  } else {
+    if (a.parts > 1) count_kernel<int64_t><<<a.parts, 1024, 0, hs>>>(a);
+    sort_kernel<int64_t><<<a.parts, 1024, 0, hs>>>(a);
+  }
+  return launched("expert_sort");
+}
+
+tlr_status expert_gather(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *X, int64_t ldx,
+                         const int32_t *place, const int32_t *end, void *Y, int64_t ldy, void *stream) {
+  RowArgs a{};
+  tlr_status st = check_rows("expert_gather", dt, tokens, topk, hidden, place, end, &a);
+  if (st != TLR_OK || tokens == 0 || hidden == 0) return st;
+  if ((st = check_matrix("expert_gather: X", dt, X, ldx, hidden)) != TLR_OK) return st;
+  if ((st = check_matrix("expert_gather: Y", dt, Y, ldy, hidden)) != TLR_OK) return st;
+  const int es = dt == TLR_F32 ? 4 : 2;
+  a.x = X;
+  a.ldx = ldx * es;
+  a.y = Y;
+  a.ldy = ldy * es;
+  a.hidden *= es;
+  a.chunks = (a.hidden + 1023) / 1024;
+  gather_kernel<<<wave_grid(tokens * a.chunks), 256, 0, static_cast<hipStream_t>(stream)>>>(a);
+  return launched("expert_gather");
+}
+
+tlr_status expert_combine(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *Y, int64_t ldy,
+                          const int32_t *place, const int32_t *end, const float *weights, void *out, int64_t ldo, void *stream) {
+  RowArgs a{};
+  tlr_status st = check_rows("expert_combine", dt, tokens, topk, hidden, place, end, &a);
+  if (st != TLR_OK || tokens == 0 || hidden == 0) return st;
+  if ((st = check_matrix("expert_combine: Y", dt, Y, ldy, hidden)) != TLR_OK) return st;
+  if ((st = check_matrix("expert_combine: out", dt, out, ldo, hidden)) != TLR_OK) return st;
+  if (!aligned(weights, 4)) return fail(TLR_ERR_INVALID_ARG, "expert_combine: misaligned weights");
+  a.x = Y;
+  a.ldx = ldy;
+  a.y = out;
+  a.ldy = ldo;
+  a.weights = weights;
+  a.chunks = (a.hidden + 511) / 512;
+  const unsigned grid = wave_grid(tokens * a.chunks);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (dt == TLR_F32) combine_kernel<float><<<grid, 256, 0, hs>>>(a);
+  else if (dt == TLR_F16) combine_kernel<_Float16><<<grid, 256, 0, hs>>>(a);
+  else combine_kernel<__bf16><<<grid, 256, 0, hs>>>(a);
+  return launched("expert_combine");
+}
+
+tlr_status expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *dout, int64_t ldd,
+                               const void *Y, int64_t ldy, const int32_t *place, const int32_t *end, const float *weights,
+                               void *dY, int64_t lddy, float *dweights, void *stream) {
+  RowArgs a{};
+  tlr_status st = check_rows("expert_combine_grad", dt, tokens, topk, hidden, place, end, &a);
+  if (st != TLR_OK || tokens == 0) return st;
+  if (!dY && !dweights) return TLR_OK;
+  if (hidden > 0 && (st = check_matrix("expert_combine_grad: dout", dt, dout, ldd, hidden)) != TLR_OK) return st;
+  if (hidden > 0 && dY && (st = check_matrix("expert_combine_grad: dY", dt, dY, lddy, hidden)) != TLR_OK) return st;
+  if (hidden > 0 && dweights && (st = check_matrix("expert_combine_grad: Y", dt, Y, ldy, hidden)) != TLR_OK) return st;
+  if (!weights || !aligned(weights, 4)) return fail(TLR_ERR_INVALID_ARG, "expert_combine_grad: null or misaligned weights");
+  if (!aligned(dweights, 4)) return fail(TLR_ERR_INVALID_ARG, "expert_combine_grad: misaligned dweights");
+  if (!place || !end || !aligned(place, 4) || !aligned(end, 4))
+    return fail(TLR_ERR_INVALID_ARG, "expert_combine_grad: null or misaligned place or end");
+  a.x = dout;
+  a.ldx = ldd;
+  a.y = dY;
+  a.ldy = lddy;
+  a.rows = dweights ? Y : nullptr;
+  a.ldr = ldy;
+  a.weights = weights;
+  a.dweights = dweights;
+  const unsigned grid = (unsigned)std::min<int64_t>(tokens, 1 << 20);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (dt == TLR_F32) combine_grad_kernel<float><<<grid, 256, 0, hs>>>(a);
+  else if (dt == TLR_F16) combine_grad_kernel<_Float16><<<grid, 256, 0, hs>>>(a);
+  else combine_grad_kernel<__bf16><<<grid, 256, 0, hs>>>(a);
+  return launched("expert_combine_grad");
+}
+
+}  // namespace tlr

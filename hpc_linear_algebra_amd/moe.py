@@ -1,18 +1,30 @@
-"""A mixture-of-experts layer for a few tokens (torch plumbing around tlr_moe,
-include/tlrgemm.h): router, softmax, top-k, gated experts (silu), weighted sum.
+"""Mixtures of experts (torch plumbing around tlr_moe and tlr_expert_*,
+include/tlrgemm.h).
+
+MoELayer is a whole layer for a few tokens: router, softmax, top-k, gated experts
+(silu), weighted sum.  For any number of tokens, trained ones among them:
+
+    order = moe.sort(ids, experts)              # a row for each choice, by expert
+    xs = moe.gather(x, order)                   # tokens to their rows; differentiable
+    ...                                         # each expert on its rows
+    out = moe.combine(y, weights, order)        # rows back to tokens; differentiable
+
+and Int8Experts, which runs the experts between the two on 8-bit integers.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
 from . import tlrgemm as T
-from .blocks import binding, quantize
+from . import int8
+from .blocks import binding, gated, quantize
 
 MAX_TOKENS = 256
 _DT = {torch.float16: T.TLR_F16, torch.bfloat16: T.TLR_BF16}
+_NAME = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 
 
 def quantize_experts(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -111,3 +123,125 @@ class MoELayer:
         if type(got) is int:
             T._check(got, "tlr_moe")
         return got
+
+
+class Order(NamedTuple):
+    """Assignments of tokens to experts, sorted by expert.
+
+    offsets  (experts + 1,) int32: expert e has rows offsets[e] .. offsets[e+1] - 1;
+             rows from offsets[-1] on belong to none
+    place    (tokens, topk) int32: the row of each assignment
+    rows     (tokens * topk,) int32: the token of each row, -1 for rows of no expert
+    """
+    offsets: torch.Tensor
+    place: torch.Tensor
+    rows: torch.Tensor
+
+
+def sort(ids: torch.Tensor, experts: int) -> Order:
+    """A row for each assignment ids (tokens, topk), int32 or int64: by expert, those
+    of one expert in the order of the tokens, those to no expert (an id that is none
+    of 0 .. experts - 1: padding, experts elsewhere) last.  The results are views of
+    one allocation.  Up to 1024 experts, topk up to 64, 2^24 assignments."""
+    got = binding().sort(ids, experts)
+    if type(got) is int:
+        T._check(got, "tlr_expert_sort")
+    return Order(*got)
+
+
+def _gather(x: torch.Tensor, place: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    got = binding().gather(x, place, offsets)
+    if type(got) is int:
+        T._check(got, "tlr_expert_gather")
+    return got
+
+
+def _combine(y: torch.Tensor, weights: Optional[torch.Tensor], place: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    got = binding().combine(y, weights, place, offsets)
+    if type(got) is int:
+        T._check(got, "tlr_expert_combine")
+    return got
+
+
+class _Gather(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, place, offsets):
+        ctx.save_for_backward(place, offsets)
+        return _gather(x, place, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxs):
+        return _combine(dxs, None, *ctx.saved_tensors), None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, place, offsets):
+        ctx.save_for_backward(y, weights, place, offsets)
+        return _combine(y, weights, place, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        got = binding().combine_grad(dout, *ctx.saved_tensors, *ctx.needs_input_grad[:2])
+        if type(got) is int:
+            T._check(got, "tlr_expert_combine_grad")
+        return (*got, None, None)
+
+
+def gather(x: torch.Tensor, order: Order) -> torch.Tensor:
+    """Each token x (tokens, hidden) at the rows of its assignments, (tokens * topk,
+    hidden); rows of no expert are zeros.  The gradient of a token is the sum of its
+    rows', in float, rounded once, in the order of its assignments; rows of no expert
+    add nothing.  No double backward."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _Gather.apply(x, order.place, order.offsets)
+    return _gather(x, order.place, order.offsets)
+
+
+def combine(y: torch.Tensor, weights: Optional[torch.Tensor], order: Order) -> torch.Tensor:
+    """The rows y (tokens * topk, hidden) of each token's assignments added with its
+    weights (tokens, topk), float32 (None: 1): (tokens, hidden) in y's type, sums in
+    float in the order of the assignments.  Rows of no expert are not read.  Gradients
+    of y (zeros for rows of no expert) and of the weights.  No double backward."""
+    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
+        if weights is None:
+            weights = torch.ones(order.place.shape, device=y.device)
+        return _Combine.apply(y, weights, order.place, order.offsets)
+    return _combine(y, weights, order.place, order.offsets)
+
+
+class Int8Experts:
+    """Gated experts (silu) on 8-bit integers, for any number of tokens.
+
+    gate_up  int8.RowScaled (experts, 2*inter, hidden): inter gate rows, then inter
+             up rows, a scale for each
+    down     int8.RowScaled (experts, hidden, inter)
+
+    A call sorts the tokens by expert, quantizes them on the way to their rows,
+    multiplies each expert's rows with its weights, and the same for the gated
+    results; every product rounds to x's type.  No backward pass.
+    """
+
+    def __init__(self, gate_up: int8.RowScaled, down: int8.RowScaled):
+        if gate_up.codes.dim() != 3 or down.codes.dim() != 3:
+            raise ValueError("Int8Experts: weights are (experts, rows, k)")
+        experts, hidden, inter = gate_up.codes.shape[0], gate_up.k, down.k
+        if gate_up.rows != 2 * inter or down.rows != hidden or down.codes.shape[0] != experts:
+            raise ValueError("Int8Experts: gate_up is (experts, 2*inter, hidden) and down (experts, hidden, inter)")
+        self.gate_up, self.down, self.experts, self.hidden = gate_up, down, experts, hidden
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+        """The experts' outputs for x (tokens, hidden), added with the router's
+        weights (tokens, topk), float32, for its choices ids; in x's type."""
+        if torch.is_grad_enabled() and (x.requires_grad or weights.requires_grad):
+            raise RuntimeError("Int8Experts has no backward pass: call it under torch.no_grad() or on detached tensors")
+        if x.dim() != 2 or x.shape[1] != self.hidden or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+            raise ValueError(f"Int8Experts: x is (tokens, {self.hidden}) and ids (tokens, topk)")
+        dtype = _NAME.get(x.dtype)
+        if dtype is None:
+            raise ValueError("Int8Experts: x is float32, float16 or bfloat16")
+        order = sort(ids, self.experts)
+        h = gated(int8.gemm(self.gate_up, int8.quantize(x, rows=order.rows), offsets=order.offsets, dtype=dtype))
+        return combine(int8.gemm(self.down, int8.quantize(h), offsets=order.offsets, dtype=dtype), weights, order)

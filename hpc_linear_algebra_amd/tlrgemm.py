@@ -34,6 +34,9 @@ EXPORTED = [
     "tlr_compress", "tlr_compress_profile", "tlr_compress_profile_read", "tlr_plan_profile",
     "tlr_plan_profile_read", "tlr_dense_gemm", "tlr_block_quantize", "tlr_block_gemm_workspace_bytes",
     "tlr_block_gemm_plan", "tlr_block_gemm", "tlr_moe_workspace_bytes", "tlr_moe_init", "tlr_moe",
+    "tlr_row_quantize", "tlr_row_gemm_workspace_bytes", "tlr_row_gemm_plan", "tlr_row_gemm",
+    "tlr_expert_sort_workspace_bytes", "tlr_expert_sort", "tlr_expert_gather", "tlr_expert_combine",
+    "tlr_expert_combine_grad", "tlr_gated", "tlr_gated_grad",
     "tlr_status_string", "tlr_last_error", "tlr_version",
 ]
 
@@ -72,6 +75,15 @@ class tlr_moe_layer(ctypes.Structure):
                 ("dt", c_int32), ("wdt", c_int32), ("normalize", c_int32), ("reserved", c_int32),
                 ("router", c_void_p), ("gate_up", c_void_p), ("down", c_void_p),
                 ("gate_up_scales", c_void_p), ("down_scales", c_void_p)]
+
+
+class tlr_row_matrix(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("ld", c_int64)]
+
+
+class tlr_row_groups(ctypes.Structure):
+    _fields_ = [("offsets", c_void_p), ("code_step", c_int64), ("scale_step", c_int64), ("count", c_int32),
+                ("clear", c_int32)]
 
 
 class TLRError(RuntimeError):
@@ -128,6 +140,19 @@ def lib():
     L.tlr_moe_workspace_bytes.argtypes = [POINTER(tlr_moe_layer), c_int32, POINTER(c_size_t)]
     L.tlr_moe_init.argtypes = [POINTER(tlr_moe_layer), P, c_size_t, P]
     L.tlr_moe.argtypes = [POINTER(tlr_moe_layer), c_int32, P, c_int64, P, c_int64, P, P, P, c_size_t, P]
+    L.tlr_row_quantize.argtypes = [c_int32, c_int64, c_int64, P, c_int64, c_int64, P, P, c_int64, P, P]
+    L.tlr_row_gemm_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, c_int32, POINTER(c_size_t)]
+    L.tlr_row_gemm_plan.argtypes = [c_int64, c_int64, c_int64, c_int32, POINTER(tlr_block_gemm_choice)]
+    L.tlr_row_gemm.argtypes = [c_int32, c_int64, c_int64, c_int64, POINTER(tlr_row_matrix), POINTER(tlr_row_matrix),
+                               POINTER(tlr_row_groups), P, c_int64, P, c_size_t, P]
+    L.tlr_expert_sort_workspace_bytes.argtypes = [c_int64, c_int32, c_int32, POINTER(c_size_t)]
+    L.tlr_expert_sort.argtypes = [c_int32, c_int64, c_int32, c_int32, P, P, P, P, P, c_size_t, P]
+    L.tlr_expert_gather.argtypes = [c_int32, c_int64, c_int32, c_int64, P, c_int64, P, P, P, c_int64, P]
+    L.tlr_expert_combine.argtypes = [c_int32, c_int64, c_int32, c_int64, P, c_int64, P, P, P, P, c_int64, P]
+    L.tlr_expert_combine_grad.argtypes = [c_int32, c_int64, c_int32, c_int64, P, c_int64, P, c_int64, P, P, P, P,
+                                          c_int64, P, P]
+    L.tlr_gated.argtypes = [c_int32, c_int64, c_int64, P, c_int64, P, c_int64, P, c_int64, P, c_int64, P]
+    L.tlr_gated_grad.argtypes = [c_int32, c_int64, c_int64, P, c_int64, P, c_int64, P, c_int64, P, c_int64, P]
     for name in EXPORTED[:-3]:
         getattr(L, name).restype = c_int32
     L.tlr_status_string.argtypes = [c_int32]
@@ -383,6 +408,83 @@ def tlr_moe(layer: tlr_moe_layer, tokens: int, X: int, ldx: int, Y: int, ldy: in
     st = lib().tlr_moe(ctypes.byref(layer), tokens, X or None, ldx, Y or None, ldy, ids or None, weights or None,
                        workspace or None, workspace_bytes, stream or None)
     _check(st, "tlr_moe")
+
+
+def tlr_row_quantize(dtype, rows: int, k: int, X: int, x_rows: int, ldx: int, index: int, codes: int, ldq: int,
+                     scales: int, stream: int = 0):
+    st = lib().tlr_row_quantize(_dt(dtype), rows, k, X or None, x_rows, ldx, index or None, codes or None, ldq,
+                                scales or None, stream or None)
+    _check(st, "tlr_row_quantize")
+
+
+def tlr_row_gemm_workspace_bytes(m: int, n: int, k: int, groups: int = 0) -> int:
+    out = c_size_t()
+    _check(lib().tlr_row_gemm_workspace_bytes(m, n, k, groups, ctypes.byref(out)), "tlr_row_gemm_workspace_bytes")
+    return int(out.value)
+
+
+def tlr_row_gemm_plan(m: int, n: int, k: int, groups: int = 0) -> tlr_block_gemm_choice:
+    out = tlr_block_gemm_choice()
+    _check(lib().tlr_row_gemm_plan(m, n, k, groups, ctypes.byref(out)), "tlr_row_gemm_plan")
+    return out
+
+
+def tlr_row_gemm(dtype, m: int, n: int, k: int, A: tlr_row_matrix, B: tlr_row_matrix, C: int, ldc: int,
+                 groups: Optional[tlr_row_groups] = None, workspace: int = 0, workspace_bytes: int = 0, stream: int = 0):
+    st = lib().tlr_row_gemm(_dt(dtype), m, n, k, ctypes.byref(A), ctypes.byref(B),
+                            ctypes.byref(groups) if groups is not None else None, C or None, ldc, workspace or None,
+                            workspace_bytes, stream or None)
+    _check(st, "tlr_row_gemm")
+
+
+def tlr_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    out = c_size_t()
+    _check(lib().tlr_expert_sort_workspace_bytes(tokens, topk, experts, ctypes.byref(out)),
+           "tlr_expert_sort_workspace_bytes")
+    return int(out.value)
+
+
+def tlr_expert_sort(id_bytes: int, tokens: int, topk: int, experts: int, ids: int, offsets: int, place: int, rows: int,
+                    workspace: int = 0, workspace_bytes: int = 0, stream: int = 0):
+    st = lib().tlr_expert_sort(id_bytes, tokens, topk, experts, ids or None, offsets or None, place or None,
+                               rows or None, workspace or None, workspace_bytes, stream or None)
+    _check(st, "tlr_expert_sort")
+
+
+def tlr_expert_gather(dtype, tokens: int, topk: int, hidden: int, X: int, ldx: int, place: int, end: int, Y: int,
+                      ldy: int, stream: int = 0):
+    st = lib().tlr_expert_gather(_dt(dtype), tokens, topk, hidden, X or None, ldx, place or None, end or None, Y or None,
+                                 ldy, stream or None)
+    _check(st, "tlr_expert_gather")
+
+
+def tlr_expert_combine(dtype, tokens: int, topk: int, hidden: int, Y: int, ldy: int, place: int, end: int, weights: int,
+                       out: int, ldo: int, stream: int = 0):
+    st = lib().tlr_expert_combine(_dt(dtype), tokens, topk, hidden, Y or None, ldy, place or None, end or None,
+                                  weights or None, out or None, ldo, stream or None)
+    _check(st, "tlr_expert_combine")
+
+
+def tlr_expert_combine_grad(dtype, tokens: int, topk: int, hidden: int, dout: int, ldd: int, Y: int, ldy: int,
+                            place: int, end: int, weights: int, dY: int, lddy: int, dweights: int, stream: int = 0):
+    st = lib().tlr_expert_combine_grad(_dt(dtype), tokens, topk, hidden, dout or None, ldd, Y or None, ldy,
+                                       place or None, end or None, weights or None, dY or None, lddy, dweights or None,
+                                       stream or None)
+    _check(st, "tlr_expert_combine_grad")
+
+
+def tlr_gated(dtype, rows: int, inter: int, X: int, ldx: int, Y: int, ldy: int, codes: int = 0, ldq: int = 0,
+              scales: int = 0, lds: int = 0, stream: int = 0):
+    st = lib().tlr_gated(_dt(dtype), rows, inter, X or None, ldx, Y or None, ldy, codes or None, ldq, scales or None,
+                         lds, stream or None)
+    _check(st, "tlr_gated")
+
+
+def tlr_gated_grad(dtype, rows: int, inter: int, dY: int, lddy: int, codes: int, ldq: int, scales: int, lds: int,
+                   dX: int, lddx: int, stream: int = 0):
+    st = lib().tlr_gated_grad(_dt(dtype), rows, inter, dY or None, lddy, codes or None, ldq, scales or None, lds,
+                              dX or None, lddx, stream or None)
+    _check(st, "tlr_gated_grad")
 
 
 def tlr_status_string(s: int) -> str:

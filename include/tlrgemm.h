@@ -593,6 +593,148 @@ tlr_status tlr_moe(const tlr_moe_layer *layer, int32_t tokens, const void *X, in
                    int64_t ldy, int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ---- 8-bit integers with a scale for each row --------------------------------
+ *
+ * A matrix X of `rows` rows and k columns as 8-bit integers with one float scale
+ * for each row: X[i,c] ~ scale(i) * code[i,c].  A weight has a row for each output
+ * channel, a batch of activations one for each token.
+ *   codes   int8, code (i,c) at byte i*ld + c: ld >= k, ld a multiple of 16, codes
+ *           16-byte aligned, and every row readable up to k rounded up to 16 (what
+ *           stands there after column k is never used).
+ *   scales  the scale of row i at scales[i].
+ */
+typedef struct {
+  const void *codes;
+  const float *scales;
+  int64_t ld;
+} tlr_row_matrix;
+
+/*
+ * tlr_row_quantize: codes and scales of X, or of rows picked from it.
+ *   s(i) = max(float(a / 127), 2^-100), a the row's largest magnitude;
+ *   code = float(x / s) rounded to an integer, ties to even (-127 .. 127).
+ *   A row that holds an infinity or a NaN gets a NaN scale and zero codes.
+ *   dt      TLR_F32, TLR_F16 or TLR_BF16 (X); X[i,c] at element i*ldx + c,
+ *           ldx >= k, any alignment of the element type.
+ *   index   NULL: row r of the result is row r of X, which has as many (x_rows).
+ *           Otherwise device int32, `rows` of them: row r is row index[r] of X, of
+ *           zeros (scale 2^-100) where index[r] is none of 0 .. x_rows - 1.
+ *   codes, ldq, scales   the rows x k result; bytes k .. k rounded up to 16 of each
+ *           row are written as zero.
+ * k up to 2^30.  No workspace.  Errors: TLR_ERR_INVALID_ARG, TLR_ERR_UNSUPPORTED
+ * (TLR_F64), TLR_ERR_HIP.
+ */
+tlr_status tlr_row_quantize(tlr_dtype dt, int64_t rows, int64_t k, const void *X, int64_t x_rows, int64_t ldx,
+                            const int32_t *index, void *codes, int64_t ldq, float *scales, void *stream);
+
+/* Rows of B in consecutive groups, each with an A of its own: rows
+ * offsets[g] .. offsets[g + 1] - 1 take the codes at A->codes + g*code_step (bytes,
+ * a multiple of 16) with the scales at A->scales + g*scale_step (floats).  offsets is
+ * device memory, count + 1 int32 in ascending order from 0 to at most n (others are
+ * cut to 0 .. n; groups that end before they begin are empty). */
+typedef struct {
+  const int32_t *offsets;
+  int64_t code_step, scale_step;
+  int32_t count;           /* 1 .. 1024 */
+  int32_t clear;           /* columns of C behind the last group: 0 left as they are, 1 set to zero */
+} tlr_row_groups;
+
+/*
+ * tlr_row_gemm: C = A B^T for row-scaled A (m rows: channels) and B (n rows:
+ * tokens) with k columns each:
+ *   C[i,j] = (float(sum over c of a[i,c] b[j,c]) * sB(j)) * sA(i), rounded to C's
+ *   type once.  The sum is exact (32-bit integers); its product with sB(j) is a
+ *   float of its own and has to be finite.
+ * C (m x n) is column-major with leading dimension ldc >= m and of type dt
+ * (TLR_F32, TLR_F16, TLR_BF16), any alignment of that type: a linear layer y = x W^T
+ * has A = W, B = x, and C row-major over (token, feature).
+ *   groups     NULL, or B's rows in groups with an A each (A's other fields hold
+ *              for all of them).
+ *   workspace  device, 16-byte aligned, not cleared: tlr_row_gemm_workspace_bytes
+ *              for the same sizes.  NULL is fine where that is 0.
+ * k up to 131071 (TLR_ERR_UNSUPPORTED above), m and n up to 2^31 - 512 with less than
+ * 2^24 tiles of 128 x 128 in C (a group's last tile counts whole); ld < 2^22.
+ * Errors: TLR_ERR_INVALID_ARG, TLR_ERR_UNSUPPORTED, TLR_ERR_WORKSPACE, TLR_ERR_HIP.
+ */
+tlr_status tlr_row_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t *bytes_out);
+
+/* What tlr_row_gemm launches for these sizes (groups 0: none), as
+ * tlr_block_gemm_plan. */
+tlr_status tlr_row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_block_gemm_choice *out);
+
+tlr_status tlr_row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A,
+                        const tlr_row_matrix *B, const tlr_row_groups *groups, void *C, int64_t ldc,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- tokens sorted by expert ------------------------------------------------- */
+
+/*
+ * tlr_expert_sort: a row for each of the tokens * topk assignments ids[t,s], such
+ * that each expert's rows are consecutive, in the order of the assignments.
+ *   ids      device, tokens x topk, int32 or int64 (id_bytes 4 or 8).  An id that is
+ *            none of 0 .. experts - 1 belongs to no expert: its rows come last.
+ *   offsets  device, experts + 1 int32: expert e has rows offsets[e] .. offsets[e+1]
+ *            - 1; rows from offsets[experts] on belong to none.
+ *   place    device, tokens x topk int32: the row of each assignment.
+ *   rows     device, tokens * topk int32: the token of each row, -1 for rows of no
+ *            expert.
+ *   workspace  device, 4-byte aligned, not cleared: tlr_expert_sort_workspace_bytes.
+ * experts 1 .. 1024, topk 1 .. 64, at most 2^24 assignments.
+ * Errors: TLR_ERR_INVALID_ARG, TLR_ERR_WORKSPACE, TLR_ERR_HIP.
+ */
+tlr_status tlr_expert_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts, size_t *bytes_out);
+tlr_status tlr_expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t experts, const void *ids,
+                           int32_t *offsets, int32_t *place, int32_t *rows, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * Rows of `hidden` entries to the sorted order and back.  dt is TLR_F32, TLR_F16 or
+ * TLR_BF16; leading dimensions are at least hidden, any alignment of the type.
+ * place as tlr_expert_sort leaves it (values out of range are skipped), end the
+ * device address of the first row of no expert (offsets + experts).
+ *   gather        Y[place[t,s]] = X[t]; rows of no expert become zeros.
+ *   combine       out[t] = sum over s of weights[t,s] Y[place[t,s]], in float in the
+ *                 order of s and rounded once; weights NULL: 1.  Rows of no expert
+ *                 are not read and add nothing.  With weights NULL it is the
+ *                 gradient of gather.
+ *   combine_grad  dY[place[t,s]] = weights[t,s] dout[t] (zeros for rows of no
+ *                 expert), dweights[t,s] = sum over c of dout[t,c] Y[place[t,s],c]
+ *                 (0 for those).  dY or dweights may be NULL; without dweights Y
+ *                 is not read.
+ * hidden up to 2^24, tokens and topk as for the sort.
+ * Errors: TLR_ERR_INVALID_ARG, TLR_ERR_UNSUPPORTED (TLR_F64), TLR_ERR_HIP.
+ */
+tlr_status tlr_expert_gather(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *X, int64_t ldx,
+                             const int32_t *place, const int32_t *end, void *Y, int64_t ldy, void *stream);
+tlr_status tlr_expert_combine(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *Y, int64_t ldy,
+                              const int32_t *place, const int32_t *end, const float *weights, void *out, int64_t ldo,
+                              void *stream);
+tlr_status tlr_expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const void *dout,
+                                   int64_t ldd, const void *Y, int64_t ldy, const int32_t *place, const int32_t *end,
+                                   const float *weights, void *dY, int64_t lddy, float *dweights, void *stream);
+
+/* ---- gated activation with an 8-bit checkpoint -------------------------------- */
+
+/*
+ * tlr_gated: Y = silu(g) u for rows of X that hold `inter` entries of g, then as many
+ * of u; silu(g) = g / (1 + exp(-g)), in float, Y rounded once.
+ *   codes, ldq, scales, lds   NULL, or where the row is kept for the backward pass:
+ *           int8 codes of g at codes + 2*i*ldq and of u at codes + (2*i + 1)*ldq,
+ *           one scale for every 128 of them (the last ones fewer) at scales + 2*i*lds
+ *           and scales + (2*i + 1)*lds.  Scale and codes as tlr_row_quantize's, a
+ *           block of 128 in place of a row.  ldq >= inter, a multiple of 16, codes
+ *           16-byte aligned; lds >= ceil(inter / 128).
+ * tlr_gated_grad: the gradient at the values g', u' that the codes stand for:
+ *   dX = (dY u' s (1 + g' (1 - s)), dY g' s), s = 1 / (1 + exp(-g')), rounded once.
+ * dt is TLR_F32, TLR_F16 or TLR_BF16 for X, Y and their gradients, any alignment of
+ * it; rows * ceil(inter / 128) < 2^31.
+ * Errors: TLR_ERR_INVALID_ARG, TLR_ERR_UNSUPPORTED (TLR_F64), TLR_ERR_HIP.
+ */
+tlr_status tlr_gated(tlr_dtype dt, int64_t rows, int64_t inter, const void *X, int64_t ldx, void *Y, int64_t ldy,
+                     void *codes, int64_t ldq, float *scales, int64_t lds, void *stream);
+tlr_status tlr_gated_grad(tlr_dtype dt, int64_t rows, int64_t inter, const void *dY, int64_t lddy, const void *codes,
+                          int64_t ldq, const float *scales, int64_t lds, void *dX, int64_t lddx, void *stream);
+
 /* Static description of a status code (plumbing; the pages define no error
  * handling). */
 const char *tlr_status_string(tlr_status s);

@@ -1,0 +1,278 @@
+"""Tokens sorted by expert and back, with weights, and the gradients, against plain loops in 64 bits."""
+import pytest
+import torch
+
+from hpc_linear_algebra_amd import moe
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}            # half a step, relative
+LEAST = {"f32": 2.0 ** -149, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}
+EPS = 2.0 ** -24                                                            # half a step of a float sum
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def plain_sort(ids, experts):
+    lists = [[] for _ in range(experts + 1)]
+    for a, e in enumerate(ids.reshape(-1).tolist()):
+        lists[e if 0 <= e < experts else experts].append(a)
+    offsets = [0]
+    for one in lists[:-1]:
+        offsets.append(offsets[-1] + len(one))
+    order = [a for one in lists for a in one]
+    place = torch.empty(len(order), dtype=torch.int32)
+    place[torch.tensor(order, dtype=torch.int64)] = torch.arange(len(order), dtype=torch.int32)
+    topk = ids.shape[1]
+    rows = torch.tensor([a // topk for a in order], dtype=torch.int32)
+    rows[offsets[-1]:] = -1
+    return torch.tensor(offsets, dtype=torch.int32), place.reshape(ids.shape), rows
+
+
+def same_order(order, ids, experts):
+    for got, want in zip(order, plain_sort(ids, experts)):
+        assert got.dtype == torch.int32 and torch.equal(got.cpu(), want)
+
+
+def choose(g, tokens, topk, experts, dropped):
+    ids = torch.randint(0, experts, (tokens, topk), generator=g)
+    if dropped:
+        gone = torch.rand(tokens, topk, generator=g) < 0.3
+        ids[gone] = torch.randint(-5, 0, (int(gone.sum()),), generator=g)
+        ids[torch.rand(tokens, topk, generator=g) < 0.05] = experts
+    return ids
+
+
+SORTS = [(0, 1, 1), (1, 1, 1), (1, 8, 64), (1, 64, 1024), (5, 3, 2), (63, 1, 7), (64, 1, 8), (65, 2, 9), (300, 4, 31), (512, 8, 64),
+         (513, 8, 65), (1000, 6, 1000), (700, 6, 1024), (2049, 8, 128), (9000, 8, 3), (5000, 7, 1024), (40000, 8, 257)]
+
+
+@pytest.mark.parametrize("dropped", [False, True])
+@pytest.mark.parametrize("tokens,topk,experts", SORTS)
+def test_sort(tokens, topk, experts, dropped):
+    ids = choose(gen(tokens + topk), tokens, topk, experts, dropped)
+    same_order(moe.sort(ids.int().cuda(), experts), ids, experts)
+    same_order(moe.sort(ids.cuda(), experts), ids, experts)
+
+
+def test_sort_one_expert_takes_all_or_none():
+    for n in (100, 10000):
+        for e in (0, 5, 7):
+            ids = torch.full((n, 2), e)
+            same_order(moe.sort(ids.cuda(), 8), ids, 8)
+        for e in (-1, 8, 2 ** 40, -2 ** 40):
+            ids = torch.full((n, 2), e)
+            same_order(moe.sort(ids.cuda(), 8), ids, 8)
+        ids = torch.full((n, 2), -2 ** 31)
+        same_order(moe.sort(ids.int().cuda(), 8), ids, 8)
+        ids[::3] = 2 ** 31 - 1
+        same_order(moe.sort(ids.int().cuda(), 8), ids, 8)
+
+
+def test_sort_strided_ids():
+    ids = choose(gen(1), 50, 6, 9, True)
+    same_order(moe.sort(ids.cuda()[::2, ::3], 9), ids[::2, ::3], 9)
+    same_order(moe.sort(ids.cuda().t(), 9), ids.t(), 9)
+
+
+def values(g, dtype, *shape):
+    return torch.randn(*shape, generator=g).to(DT[dtype])
+
+
+ROWS = [(1, 1, 1, 1), (1, 8, 64, 2048), (3, 2, 4, 7), (17, 6, 9, 130), (40, 3, 5, 511), (33, 9, 17, 513), (20, 8, 16, 1024), (9, 17, 40, 1037),
+        (130, 4, 8, 2050), (7, 2, 3, 5000), (300, 2, 1, 64), (64, 5, 6, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dropped", [False, True])
+@pytest.mark.parametrize("tokens,topk,experts,hidden", ROWS)
+def test_rows_and_gradients(tokens, topk, experts, hidden, dropped, dtype):
+    g = gen(tokens + topk + hidden)
+    ids = choose(g, tokens, topk, experts, dropped)
+    all_ = tokens * topk
+    x, y = values(g, dtype, tokens, hidden), values(g, dtype, all_, hidden)
+    w = torch.randn(tokens, topk, generator=g)
+    dxs, dout = values(g, dtype, all_, hidden), values(g, dtype, tokens, hidden)
+    order = moe.sort(ids.cuda(), experts)
+    offsets, place, _ = plain_sort(ids, experts)
+    end = int(offsets[-1])
+    y_dev = y.cuda()
+    if hidden:
+        y_dev[end:] = float("nan")                     # rows of no expert are not read
+    leaves = [t.requires_grad_() for t in (x.cuda(), y_dev, w.cuda())]
+    xs, out = moe.gather(leaves[0], order), moe.combine(leaves[1], leaves[2], order)
+    dx, dy, dw = torch.autograd.grad([xs, out], leaves, [dxs.cuda(), dout.cuda()])
+    assert xs.dtype == out.dtype == dx.dtype == dy.dtype == DT[dtype] and dw.dtype == torch.float32
+
+    real = (place < end).unsqueeze(2)
+    at = place.long()
+    want = torch.zeros(all_, hidden, dtype=torch.float64)
+    want[at] = torch.where(real, x.double().unsqueeze(1), 0.0)
+    assert torch.equal(xs.detach().cpu().double(), want)
+    pick = torch.where(real, y.double()[at], 0.0)
+
+    def check(got, want, terms, count):
+        # `count` float additions, each off by at most half a step of the sum of the magnitudes, and the last rounding
+        bound = HALF[dtype] * want.abs() * (1 + count * EPS) + 1.01 * count * EPS * terms + LEAST[dtype]
+        assert bool(((got.detach().cpu().double() - want).abs() <= bound).all())
+
+    t = pick * w.double().unsqueeze(2)
+    check(out, t.sum(dim=1), t.abs().sum(dim=1), topk)
+    t = torch.where(real, dxs.double()[at], 0.0)
+    check(dx, t.sum(dim=1), t.abs().sum(dim=1), topk)
+    want = torch.zeros(all_, hidden, dtype=torch.float64)
+    want[at] = torch.where(real, dout.double().unsqueeze(1) * w.double().unsqueeze(2), 0.0)
+    check(dy, want, want.abs(), 1)
+    t = pick * dout.double().unsqueeze(1)
+    # a lane's entries one after another, then 6 + 2 additions
+    count = 8 * -(-hidden // 2048) + 8 if hidden else 0
+    bound = 1.01 * count * EPS * t.abs().sum(dim=2) + LEAST["f32"]
+    assert bool(((dw.cpu().double() - t.sum(dim=2)).abs() <= bound).all())
+    # without gradients: the same values
+    with torch.no_grad():
+        assert torch.equal(moe.gather(leaves[0], order), xs) and torch.equal(moe.combine(leaves[1], leaves[2], order), out)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_one_gradient_alone(which):
+    g = gen(5)
+    ids = choose(g, 30, 4, 6, True)
+    order = moe.sort(ids.cuda(), 6)
+    y, w, dout = values(g, "f32", 120, 90).cuda(), torch.rand(30, 4, generator=g).cuda(), values(g, "f32", 30, 90).cuda()
+    both = torch.autograd.grad(moe.combine(y.requires_grad_(), w.requires_grad_(), order), [y, w], dout)
+    leaves = [y.detach(), w.detach()]
+    leaves[which].requires_grad_()
+    one, = torch.autograd.grad(moe.combine(*leaves, order), [leaves[which]], dout)
+    assert torch.equal(one, both[which])
+
+
+def test_without_weights_and_gradcheck():
+    """combine without weights is the sum, and each gradient the difference quotient of the function."""
+    g = gen(6)
+    ids = choose(g, 12, 3, 5, True)
+    order = moe.sort(ids.cuda(), 5)
+    y = values(g, "f32", 36, 20).cuda()
+    assert torch.equal(moe.combine(y, None, order), moe.combine(y, torch.ones(12, 3, device="cuda"), order))
+    y.requires_grad_()
+    a, = torch.autograd.grad(moe.combine(y, None, order).square().sum(), [y])
+    b, = torch.autograd.grad(moe.combine(y, torch.ones(12, 3, device="cuda"), order).square().sum(), [y])
+    assert torch.equal(a, b)
+    # both operators are linear in each operand: a difference over a step of 1 is the derivative, up to float sums of
+    # 4 terms of size 4 at most (x, y, w, steps in -2 .. 2 in quarters: exact in float)
+    quarters = lambda *s: (torch.randint(-8, 9, s, generator=g) / 4.0).cuda()   # noqa: E731
+    x, y, w = quarters(12, 20), quarters(36, 20), quarters(12, 3)
+    ux, uy, uw = quarters(12, 20), quarters(36, 20), quarters(12, 3)
+    cx, cy = quarters(36, 20), quarters(12, 20)
+    leaves = [t.requires_grad_() for t in (x, y, w)]
+    dx, dy, dw = torch.autograd.grad([moe.gather(x, order), moe.combine(y, w, order)], leaves, [cx, cy])
+    with torch.no_grad():
+        step = lambda f, a, u, c: ((f(a + u) - f(a)) * c).sum()   # noqa: E731
+        assert float(step(lambda v: moe.gather(v, order), x, ux, cx)) == float((dx * ux).sum())
+        assert float(step(lambda v: moe.combine(v, w, order), y, uy, cy)) == float((dy * uy).sum())
+        assert float(step(lambda v: moe.combine(y, v, order), w, uw, cy)) == float((dw * uw).sum())
+
+
+def test_strides_and_expanded_gradients():
+    g = gen(7)
+    ids = choose(g, 21, 4, 6, True)
+    order = moe.sort(ids.cuda(), 6)
+    x, y, w = values(g, "bf16", 21, 77).cuda(), values(g, "bf16", 84, 77).cuda(), torch.rand(21, 4, generator=g).cuda()
+    xs, out = moe.gather(x, order), moe.combine(y, w, order)
+
+    def odd(t):                                # rows at an odd offset, with gaps
+        big = torch.zeros(t.shape[0], t.shape[1] + 6, dtype=t.dtype, device="cuda")
+        big[:, 3:3 + t.shape[1]] = t
+        return big[:, 3:3 + t.shape[1]]
+
+    assert torch.equal(moe.gather(odd(x), order), xs) and torch.equal(moe.combine(odd(y), odd(w), order), out)
+    assert torch.equal(moe.gather(x.t().contiguous().t(), order), xs)
+    assert torch.equal(moe.combine(y.t().contiguous().t(), w.t().contiguous().t(), order), out)
+    row = x[:1].expand(21, 77)
+    assert torch.equal(moe.gather(row, order), moe.gather(row.contiguous(), order))
+    leaves = [t.requires_grad_() for t in (x, y, w)]
+    total = moe.gather(x, order).float().sum() + moe.combine(y, w, order).float().sum()        # expanded gradients
+    got = torch.autograd.grad(total, leaves)
+    want = torch.autograd.grad([moe.gather(x, order), moe.combine(y, w, order)], leaves,
+                               [torch.ones_like(xs), torch.ones_like(out)])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_infinities_travel_and_stay_apart():
+    ids = torch.tensor([[0, 1], [1, -1], [0, 2]])
+    order = moe.sort(ids.cuda(), 3)
+    x = torch.tensor([[1.0, float("inf")], [float("nan"), 2.0], [-float("inf"), 3.0]])
+    xs = moe.gather(x.cuda(), order).cpu()
+    assert torch.equal(xs.nan_to_num(9.0, 8.0, 7.0), x[torch.tensor([0, 2, 0, 1, 2, 1])].nan_to_num(9.0, 8.0, 7.0) *
+                       torch.tensor([[1.0]] * 5 + [[0.0]]))
+    w = torch.tensor([[0.5, 0.5], [1.0, float("nan")], [1.0, 1.0]])            # the weight of no expert is not used
+    out = moe.combine(xs.cuda(), w.cuda(), order).cpu()
+    assert out[0].tolist() == [1.0, float("inf")] and torch.isnan(out[1, 0]) and out[1, 1] == 2.0
+
+
+def test_places_out_of_range_are_skipped():
+    place = torch.tensor([[0, 99], [-1, 2], [2 ** 31 - 1, -2 ** 31]], dtype=torch.int32, device="cuda")
+    for end in (3, 100, -4):
+        order = moe.Order(torch.tensor([0, end], dtype=torch.int32, device="cuda"), place, None)
+        y = torch.arange(1.0, 13.0, device="cuda").reshape(6, 2)
+        live = end > 2
+        want = [[1.0, 2.0], [5.0, 6.0], [0.0, 0.0]] if live else [[0.0, 0.0]] * 3
+        assert moe.combine(y, None, order).tolist() == want
+        xs = moe.gather(torch.ones(3, 2, device="cuda"), order)
+        assert xs[0].tolist() == [float(live)] * 2 and xs[2].tolist() == [float(live)] * 2
+        w = torch.ones(3, 2, device="cuda", requires_grad=True)
+        dw, = torch.autograd.grad(moe.combine(y, w, order), [w], torch.ones(3, 2, device="cuda"))
+        assert dw.tolist() == ([[3.0, 0.0], [0.0, 11.0], [0.0, 0.0]] if live else [[0.0, 0.0]] * 3)
+
+
+def test_far_rows():
+    """Rows whose offset passes 2^32 bytes."""
+    tokens, topk, hidden = 70000, 2, 16384
+    ids = torch.arange(tokens * topk, device="cuda").reshape(tokens, topk) % 5
+    order = moe.sort(ids, 5)
+    x = torch.empty(tokens, hidden, dtype=torch.bfloat16, device="cuda")
+    x.copy_((torch.arange(tokens, device="cuda") % 251).unsqueeze(1))
+    x[:, -1] = 3.0
+    xs = moe.gather(x, order)
+    token = order.rows.long()
+    assert torch.equal(xs[:, 0].float(), (token % 251).float()) and (xs[:, -1] == 3.0).all()
+    assert torch.equal(xs[:, 9000].float(), (token % 251).float())
+    w = torch.full((tokens, topk), 0.5, device="cuda")
+    out = moe.combine(xs, w, order)
+    assert torch.equal(out, x)
+
+
+def test_same_inputs_same_bits_on_streams_and_in_graphs():
+    g = gen(8)
+    tokens, topk, experts, hidden = 3000, 4, 33, 260
+    ids = choose(g, tokens, topk, experts, True).cuda()
+    x, y, w = values(g, "bf16", tokens, hidden).cuda(), values(g, "bf16", tokens * topk, hidden).cuda(), torch.rand(tokens, topk, generator=g).cuda()
+    cx, cy = torch.randn_like(y), torch.randn_like(x)
+
+    def run():
+        leaves = [t.detach().requires_grad_() for t in (x, y, w)]
+        order = moe.sort(ids, experts)
+        xs, out = moe.gather(leaves[0], order), moe.combine(leaves[1], leaves[2], order)
+        return [*order, xs.detach(), out.detach(), *torch.autograd.grad([xs, out], leaves, [cx, cy])]
+
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    keep = ids.clone()
+    for i in range(3):
+        ids.copy_((keep * (i + 1)) % experts)
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))

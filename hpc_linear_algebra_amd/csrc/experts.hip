@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "int8.h"
 #include "tlr_ops.h"
@@ -27,7 +28,7 @@ namespace {
 // ---- sort --------------------------------------------------------------------------------------------
 
 constexpr int MOST_EXPERTS = 1024, MOST_TOPK = 64;
-constexpr int WAVES = 16, EACH = 4, PART = WAVES * 64 * EACH;      // assignments of a workgroup
+constexpr int PART = 4096;        // assignments of a workgroup, where there are several
 
 struct SortArgs {
   const void *ids;
@@ -45,27 +46,32 @@ template <typename ID> __device__ __forceinline__ int expert_of(const SortArgs &
 // How many assignments of its part each expert has.
 template <typename ID> __global__ __launch_bounds__(1024) void count_kernel(SortArgs a) {
   __shared__ int32_t hist[MOST_EXPERTS + 1];
-  for (int e = threadIdx.x; e <= a.experts; e += 1024) hist[e] = 0;
+  int e[PART / 1024];
+#pragma unroll
+  for (int c = 0; c < PART / 1024; ++c) {
+    const int64_t i = (int64_t)blockIdx.x * PART + c * 1024 + threadIdx.x;
+    e[c] = i < a.n ? expert_of<ID>(a, (int)i) : -1;
+  }
+  for (int x = threadIdx.x; x <= a.experts; x += 1024) hist[x] = 0;
   __syncthreads();
 #pragma unroll
-  for (int c = 0; c < EACH; ++c) {
-    const int64_t i = (int64_t)blockIdx.x * PART + c * 1024 + threadIdx.x;
-    if (i < a.n) atomicAdd(&hist[expert_of<ID>(a, (int)i)], 1);
-  }
+  for (int c = 0; c < PART / 1024; ++c)
+    if (e[c] >= 0) atomicAdd(&hist[e[c]], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e <= a.experts; e += 1024) a.counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
+  for (int x = threadIdx.x; x <= a.experts; x += 1024) a.counts[(int64_t)blockIdx.x * (a.experts + 1) + x] = hist[x];
 }
 
-// Rows of a part's assignments.  A wave takes 64 consecutive ones at a time: which
-// lanes share an expert follows from one ballot for each bit of its number, and a
-// lane's rank is the number of such lanes before it, added to the wave's count so
-// far.  Ranks, counts of the waves before, counts of the parts before and the
-// experts' first rows add up to the row.
-template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortArgs a) {
-  __shared__ int32_t hist[WAVES][MOST_EXPERTS + 1];
-  __shared__ int32_t sums[WAVES];
+// Rows of a part's assignments, EACH for each of W waves' threads.  A wave takes 64
+// consecutive ones at a time: which lanes share an expert follows from one ballot for
+// each bit of its number, and a lane's rank is the number of such lanes before it,
+// added to the wave's count so far.  Ranks, counts of the waves before, counts of the
+// parts before and the experts' first rows add up to the row.
+template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) void sort_kernel(SortArgs a) {
+  constexpr int MOST = W == 16 ? MOST_EXPERTS : 64 * W;
+  __shared__ int32_t hist[W][MOST + 1];
+  __shared__ int32_t sums[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t first = (int64_t)blockIdx.x * PART + wave * 64 * EACH + lane;
+  const int64_t first = (int64_t)blockIdx.x * (64 * W * EACH) + wave * 64 * EACH + lane;
   int e[EACH], rank[EACH];
 #pragma unroll
   for (int c = 0; c < EACH; ++c) e[c] = first + 64 * c < a.n ? expert_of<ID>(a, (int)(first + 64 * c)) : -1;
@@ -80,7 +86,7 @@ template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortA
       same &= on ? m : ~m;
     }
     const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
-    asm volatile("" ::: "memory");
+    asm volatile("" ::: "memory");        // the wave's LDS accesses stay in this order
     if (e[c] >= 0) {
       const int so_far = hist[wave][e[c]];
       asm volatile("" ::: "memory");
@@ -95,7 +101,7 @@ template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortA
     before = all = 0;
     int part = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
+    for (int w = 0; w < W; ++w) {
       const int v = hist[w][x];
       hist[w][x] = part;
       part += v;
@@ -104,10 +110,15 @@ template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortA
       all = part;
       return;
     }
-    for (int p = 0; p < a.parts; ++p) {
-      const int v = a.counts[(int64_t)p * (a.experts + 1) + x];
-      before += p < (int)blockIdx.x ? v : 0;
-      all += v;
+    for (int p0 = 0; p0 < a.parts; p0 += 16) {        // 16 loads in flight
+      int v[16];
+#pragma unroll
+      for (int p = 0; p < 16; ++p) v[p] = a.counts[(int64_t)min(p0 + p, a.parts - 1) * (a.experts + 1) + x];
+#pragma unroll
+      for (int p = 0; p < 16; ++p) {
+        before += p0 + p < (int)blockIdx.x ? v[p] : 0;
+        all += p0 + p < a.parts ? v[p] : 0;
+      }
     }
   };
   int before = 0, all = 0;
@@ -122,20 +133,20 @@ template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortA
   __syncthreads();
   int total = 0, start = scan - all;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < wave) start += sums[w];
     total += sums[w];
   }
   if (tid < a.experts) {
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) hist[w][tid] += start + before;
+    for (int w = 0; w < W; ++w) hist[w][tid] += start + before;
     if (blockIdx.x == 0) a.offsets[tid] = start;
   }
   if (tid == 0) {
     int none_before, none;
     column(a.experts, none_before, none);
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) hist[w][a.experts] += total + none_before;
+    for (int w = 0; w < W; ++w) hist[w][a.experts] += total + none_before;
     if (blockIdx.x == 0) a.offsets[a.experts] = total;
   }
   __syncthreads();
@@ -146,6 +157,20 @@ template <typename ID> __global__ __launch_bounds__(1024) void sort_kernel(SortA
       a.place[i] = p;
       a.rows[p] = e[c] < a.experts ? i / a.topk : -1;
     }
+}
+
+// Up to 8192 assignments are sorted by one workgroup, as few waves as hold them.
+constexpr int64_t ONE = 8192;
+int64_t parts_of(int64_t n) { return n <= ONE ? 1 : (n + PART - 1) / PART; }
+
+template <typename ID> void sort_launch(const SortArgs &a, hipStream_t st) {
+  if (a.parts > 1) {
+    count_kernel<ID><<<a.parts, 1024, 0, st>>>(a);
+    sort_kernel<ID, 16, 4><<<a.parts, 1024, 0, st>>>(a);
+  } else if (a.n <= 256 && a.experts <= 256) sort_kernel<ID, 4, 1><<<1, 256, 0, st>>>(a);
+  else if (a.n <= 1024 && a.experts <= 256) sort_kernel<ID, 4, 4><<<1, 256, 0, st>>>(a);
+  else if (a.n <= 4096) sort_kernel<ID, 16, 4><<<1, 1024, 0, st>>>(a);
+  else sort_kernel<ID, 16, 8><<<1, 1024, 0, st>>>(a);
 }
 
 // ---- rows --------------------------------------------------------------------------------------------
@@ -169,15 +194,10 @@ __device__ __forceinline__ int row_of(const RowArgs &a, int64_t i, int end) {
 }
 __device__ __forceinline__ int end_of(const RowArgs &a) { return min(*a.end, a.tokens * a.topk); }
 
-// 16 bytes of a row, the last ones fewer.
-__device__ __forceinline__ void copy_out(char *p, u4 v, int left) {
-  if (left >= 16) __builtin_memcpy(p, &v, 16);
-  else
-    for (int h = 0; 2 * h < left; ++h) reinterpret_cast<uint16_t *>(p)[h] = (uint16_t)(v[h >> 1] >> (16 * (h & 1)));
-}
-
-// A wave takes 1024 bytes of a token's row and writes them topk times (sizes in bytes).
-__global__ __launch_bounds__(256) void gather_kernel(RowArgs a) {
+// A wave takes 1024 bytes of a token's row and writes them topk times (sizes in
+// bytes).  PAST: past the caches, for results that do not fit there (8192 tokens to 8
+// rows of 8 KB: 103 us, through them 118).
+template <bool PAST> __global__ __launch_bounds__(256) void gather_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t tasks = (int64_t)a.tokens * a.chunks, all = (int64_t)a.tokens * a.topk;
   const int end = end_of(a);
@@ -187,18 +207,45 @@ __global__ __launch_bounds__(256) void gather_kernel(RowArgs a) {
     if (left <= 0) continue;
     const char *p = static_cast<const char *>(a.x) + t * a.ldx + at;
     u4 v = u4{0, 0, 0, 0};
-    if (left >= 16) __builtin_memcpy(&v, p, 16);
+    if (left >= 16) v = get16<false>(p);
     else
-      for (int h = 0; 2 * h < left; ++h) v[h >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[h] << (16 * (h & 1));
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (2 * h < left) v[h >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[h] << (16 * (h & 1));
     for (int s = 0; s < a.topk; ++s) {
       const int row = a.place[t * a.topk + s];
       if (row < 0 || row >= all) continue;
-      copy_out(static_cast<char *>(a.y) + row * a.ldy + at, row < end ? v : u4{0, 0, 0, 0}, left);
+      char *y = static_cast<char *>(a.y) + row * a.ldy + at;
+      const u4 o = row < end ? v : u4{0, 0, 0, 0};
+      if (left >= 16) put16<PAST>(y, o);
+      else
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (2 * h < left) reinterpret_cast<uint16_t *>(y)[h] = (uint16_t)(o[h >> 1] >> (16 * (h & 1)));
     }
   }
 }
 
-// A wave adds 512 entries of a token's rows.
+// Calls f with N = MOST or, for the last ones, 4, 2, 1 (as a type) and the first of as many assignments, until topk are
+// covered.
+template <int MOST, typename F> __device__ __forceinline__ void in_groups(int topk, F f) {
+  int s = 0;
+  for (; s + MOST <= topk; s += MOST) f(std::integral_constant<int, MOST>{}, s);
+  if (MOST > 4 && s + 4 <= topk) {
+    f(std::integral_constant<int, 4>{}, s);
+    s += 4;
+  }
+  if (s + 2 <= topk) {
+    f(std::integral_constant<int, 2>{}, s);
+    s += 2;
+  }
+  if (s < topk) f(std::integral_constant<int, 1>{}, s);
+}
+
+// A wave adds 512 entries of a token's rows, the loads of up to eight rows in flight.
+// Rows are read past the caches (8192 tokens of 8 x 4096: 139 us, through them 168;
+// 1000 of 6 x 2048: 8.0 and 10.4).  Rows of no expert are replaced by row 0 for the
+// load and left out of the sum.
 template <typename T> __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t tasks = (int64_t)a.tokens * a.chunks;
@@ -207,73 +254,87 @@ template <typename T> __global__ __launch_bounds__(256) void combine_kernel(RowA
     const int64_t t = task / a.chunks;
     const int at = (int)(task - t * a.chunks) * 512 + lane * 8, left = a.hidden - at;
     if (left <= 0) continue;
+    const T *x = static_cast<const T *>(a.x) + at;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < a.topk; ++s) {
-      const int row = row_of(a, t * a.topk + s, end);
-      if (row < 0) continue;
-      const float w = a.weights ? a.weights[t * a.topk + s] : 1.0f;
-      float v[8];
-      get8(static_cast<const T *>(a.x) + row * a.ldx + at, left, v);
+    in_groups<8>(a.topk, [&](auto n, int s0) {
+      constexpr int N = decltype(n)::value;
+      int row[N];
+      float w[N], v[N][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w, v[e], sum[e]);
-    }
+      for (int s = 0; s < N; ++s) {
+        row[s] = row_of(a, t * a.topk + s0 + s, end);
+        w[s] = a.weights ? a.weights[t * a.topk + s0 + s] : 1.0f;
+      }
+#pragma unroll
+      for (int s = 0; s < N; ++s) get8<true>(x + max(row[s], 0) * a.ldx, left, v[s]);
+#pragma unroll
+      for (int s = 0; s < N; ++s)
+        if (row[s] >= 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w[s], v[s][e], sum[e]);
+    });
     put8(static_cast<T *>(a.y) + t * a.ldy + at, left, sum);
   }
 }
 
-// A workgroup takes a token: dout is read once for eight of its rows, which take
-// w dout and give their dot products with it.
-template <typename T> __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
-  constexpr int G = 8;
-  __shared__ float part[4][G];
+// A workgroup takes a token: four of its rows at a time take w dout and give their dot
+// products with it; dout comes from the caches again for the next four.  8192 tokens of
+// 8 x 4096: 232 us with reads and writes of rows past the caches, 252 with eight rows at
+// a time, 313 with those through the caches.
+template <typename T, bool PAST> __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
+  __shared__ float part[4][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int end = end_of(a);
   const int64_t all = (int64_t)a.tokens * a.topk;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const T *d = static_cast<const T *>(a.x) + t * a.ldx;
-    for (int s0 = 0; s0 < a.topk; s0 += G) {
-      int row[G];
-      float w[G], dot[G];
+    in_groups<4>(a.topk, [&](auto n, int s0) {
+      constexpr int N = decltype(n)::value;
+      int row[N];               // -1: nothing to write
+      bool real[N];
+      float w[N], dot[N];
 #pragma unroll
-      for (int s = 0; s < G; ++s) {
-        row[s] = s0 + s < a.topk ? a.place[t * a.topk + s0 + s] : -1;
-        if (row[s] >= all) row[s] = -1;
-        w[s] = row[s] >= 0 && row[s] < end ? a.weights[t * a.topk + s0 + s] : 0.0f;
+      for (int s = 0; s < N; ++s) {
+        row[s] = a.place[t * a.topk + s0 + s];
+        if (row[s] < 0 || row[s] >= all) row[s] = -1;
+        real[s] = row[s] >= 0 && row[s] < end;
+        w[s] = a.weights[t * a.topk + s0 + s];
         dot[s] = 0.0f;
       }
       for (int at = tid * 8; at < a.hidden; at += 2048) {
         const int left = a.hidden - at;
-        float v[8];
+        float v[8], y[N][8];
         get8(d + at, left, v);
+        if (a.rows) {
 #pragma unroll
-        for (int s = 0; s < G; ++s) {
-          if (row[s] < 0) continue;
-          const bool real = row[s] < end;
-          if (a.rows && real) {
-            float y[8];
-            get8(static_cast<const T *>(a.rows) + row[s] * a.ldr + at, left, y);
+          for (int s = 0; s < N; ++s) get8<true>(static_cast<const T *>(a.rows) + (real[s] ? row[s] : 0) * a.ldr + at, left, y[s]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot[s] = __builtin_fmaf(v[e], y[e], dot[s]);
-          }
-          if (a.y) {
-            float o[8];
+          for (int s = 0; s < N; ++s)
+            if (real[s])
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = real ? w[s] * v[e] : 0.0f;
-            put8(static_cast<T *>(a.y) + row[s] * a.ldy + at, left, o);
-          }
+              for (int e = 0; e < 8; ++e) dot[s] = __builtin_fmaf(v[e], y[s][e], dot[s]);
         }
-      }
-      if (!a.dweights) continue;
+        if (a.y)
 #pragma unroll
-      for (int s = 0; s < G; ++s) {
+          for (int s = 0; s < N; ++s)
+            if (row[s] >= 0) {
+              float o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = real[s] ? w[s] * v[e] : 0.0f;
+              put8<PAST>(static_cast<T *>(a.y) + row[s] * a.ldy + at, left, o);
+            }
+      }
+      if (!a.dweights) return;
+#pragma unroll
+      for (int s = 0; s < N; ++s) {
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) dot[s] += __shfl_xor(dot[s], x);
         if (lane == 0) part[wave][s] = dot[s];
       }
       __syncthreads();
-      if (tid < G && s0 + tid < a.topk) a.dweights[t * a.topk + s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+      if (tid < N) a.dweights[t * a.topk + s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
       __syncthreads();
-    }
+    });
   }
 }
 
@@ -292,8 +353,6 @@ tlr_status check_counts(const std::string &w, int64_t tokens, int32_t topk) {
   if (tokens < 0 || tokens > SIZE_LIM || tokens * topk > MOST) return fail(TLR_ERR_INVALID_ARG, w + "too many tokens");
   return TLR_OK;
 }
-
-int64_t parts_of(int64_t n) { return std::max<int64_t>(1, (n + PART - 1) / PART); }
 
 // What the operators on rows check; sets the sizes.
 tlr_status check_rows(const char *name, tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hidden, const int32_t *place,
@@ -318,6 +377,14 @@ tlr_status check_matrix(const char *what, tlr_dtype dt, const void *p, int64_t l
   if (ld < hidden || ld > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, std::string(what) + ": leading dimension out of range");
   if (!p || !aligned(p, dt == TLR_F32 ? 4 : 2)) return fail(TLR_ERR_INVALID_ARG, std::string(what) + ": null or misaligned");
   return TLR_OK;
+}
+
+// Results that fit into the caches are left there for their reader.
+bool past_caches(int64_t bytes) { return bytes >= (int64_t)1 << 26; }
+
+template <typename T> void combine_grad_launch(const RowArgs &a, unsigned grid, hipStream_t st) {
+  if (past_caches((int64_t)sizeof(T) * a.tokens * a.topk * a.hidden)) combine_grad_kernel<T, true><<<grid, 256, 0, st>>>(a);
+  else combine_grad_kernel<T, false><<<grid, 256, 0, st>>>(a);
 }
 
 unsigned wave_grid(int64_t tasks) { return (unsigned)std::min<int64_t>((tasks + 3) / 4, 1 << 22); }
@@ -348,13 +415,8 @@ tlr_status expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t e
   if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "expert_sort: workspace too small");
   const SortArgs a{ids, offsets, place, rows, static_cast<int32_t *>(ws), (int32_t)n, topk, experts, (int32_t)parts_of(n)};
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (id_bytes == 4) {
-    if (a.parts > 1) count_kernel<int32_t><<<a.parts, 1024, 0, hs>>>(a);
-    sort_kernel<int32_t><<<a.parts, 1024, 0, hs>>>(a);
-  } else {
-    if (a.parts > 1) count_kernel<int64_t><<<a.parts, 1024, 0, hs>>>(a);
-    sort_kernel<int64_t><<<a.parts, 1024, 0, hs>>>(a);
-  }
+  if (id_bytes == 4) sort_launch<int32_t>(a, hs);
+  else sort_launch<int64_t>(a, hs);
   return launched("expert_sort");
 }
 
@@ -372,7 +434,10 @@ tlr_status expert_gather(tlr_dtype dt, int64_t tokens, int32_t topk, int64_t hid
   a.ldy = ldy * es;
   a.hidden *= es;
   a.chunks = (a.hidden + 1023) / 1024;
-  gather_kernel<<<wave_grid(tokens * a.chunks), 256, 0, static_cast<hipStream_t>(stream)>>>(a);
+  const unsigned grid = wave_grid(tokens * a.chunks);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (past_caches(tokens * topk * a.hidden)) gather_kernel<true><<<grid, 256, 0, hs>>>(a);
+  else gather_kernel<false><<<grid, 256, 0, hs>>>(a);
   return launched("expert_gather");
 }
 
@@ -422,9 +487,9 @@ tlr_status expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, int64
   a.dweights = dweights;
   const unsigned grid = (unsigned)std::min<int64_t>(tokens, 1 << 20);
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (dt == TLR_F32) combine_grad_kernel<float><<<grid, 256, 0, hs>>>(a);
-  else if (dt == TLR_F16) combine_grad_kernel<_Float16><<<grid, 256, 0, hs>>>(a);
-  else combine_grad_kernel<__bf16><<<grid, 256, 0, hs>>>(a);
+  if (dt == TLR_F32) combine_grad_launch<float>(a, grid, hs);
+  else if (dt == TLR_F16) combine_grad_launch<_Float16>(a, grid, hs);
+  else combine_grad_launch<__bf16>(a, grid, hs);
   return launched("expert_combine_grad");
 }
 

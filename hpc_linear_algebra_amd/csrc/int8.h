@@ -38,12 +38,27 @@ __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(_Float16 x) { return (float)x; }
 __device__ __forceinline__ float widen(__bf16 x) { return b2f(__builtin_bit_cast(uint16_t, x)); }
 
-// Eight consecutive elements at any alignment of their type (one or two 16-byte
-// loads; the hardware takes them unaligned); zeros at or past `left`.
-template <typename T> __device__ __forceinline__ void get8(const T *p, int64_t left, float (&v)[8]) {
+// 16 bytes at any alignment of 2 (the hardware takes them), past the caches if PAST.
+typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <bool PAST> __device__ __forceinline__ u4 get16(const void *p) {
+  const u4_any *q = static_cast<const u4_any *>(p);
+  if constexpr (PAST) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <bool PAST> __device__ __forceinline__ void put16(void *p, u4 v) {
+  u4_any *q = static_cast<u4_any *>(p);
+  if constexpr (PAST) __builtin_nontemporal_store((u4_any)v, q);
+  else *q = v;
+}
+
+// Eight consecutive elements as floats; zeros at or past `left`.
+template <bool PAST = false, typename T> __device__ __forceinline__ void get8(const T *p, int64_t left, float (&v)[8]) {
   if (left >= 8) {
     T x[8];
-    __builtin_memcpy(x, p, sizeof x);
+    u4 w[sizeof x / 16];
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof x / 16); ++i) w[i] = get16<PAST>(reinterpret_cast<const char *>(p) + 16 * i);
+    __builtin_memcpy(x, w, sizeof x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = widen(x[e]);
   } else {
@@ -53,12 +68,15 @@ template <typename T> __device__ __forceinline__ void get8(const T *p, int64_t l
 }
 
 // Eight floats rounded to consecutive elements, those before `left`.
-template <typename T> __device__ __forceinline__ void put8(T *p, int64_t left, const float (&v)[8]) {
+template <bool PAST = false, typename T> __device__ __forceinline__ void put8(T *p, int64_t left, const float (&v)[8]) {
   if (left >= 8) {
     T x[8];
+    u4 w[sizeof x / 16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = (T)v[e];
-    __builtin_memcpy(p, x, sizeof x);
+    __builtin_memcpy(w, x, sizeof x);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof x / 16); ++i) put16<PAST>(reinterpret_cast<char *>(p) + 16 * i, w[i]);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -193,6 +193,15 @@ __device__ __forceinline__ void store8(const RowGemmArgs &g, int i, int j, const
   else put8(static_cast<__bf16 *>(g.c) + at, g.m - i, v);
 }
 
+// Eight consecutive sums of a column, those before `left`.
+__device__ __forceinline__ void put_sums(int *p, int left, const int (&v)[8]) {
+  if (left >= 8) __builtin_memcpy(p, v, 32);
+  else
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) p[e] = v[e];
+}
+
 // Few columns or little work: a workgroup computes 16 rows of A against 16 rows of
 // B, its eight waves taking every eighth block of 128 columns; fragments come
 // straight from global memory, and the partial sums meet in LDS.
@@ -267,16 +276,24 @@ template <bool GROUPED> __global__ __launch_bounds__(512, 4) void strip_kernel(R
   }
 }
 
-// C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16; the codes of two
-// blocks of 128 columns in LDS, one read while the other is loaded.
-template <bool GROUPED, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(RowGemmArgs g) {
-  constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
+// C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16.  KG 2: two such
+// halves of waves take every other block of 128 columns and add their sums at the
+// end, which halves the barriers of a long contraction.
+//
+// Two stages of KG blocks each in LDS.  A wave goes through a stage row tile by row
+// tile; with the last one's matrix instructions under way it waits for the next
+// stage and reads its first fragments: one barrier a stage, and the matrix cores have
+// work on both sides of it.  The stage after that is loaded into the buffer that is
+// then used up, SPREAD pieces under each row tile's matrix instructions, or all at
+// once (SPREAD 0), which a short stage needs.
+template <bool GROUPED, int TM, int TN, int WM, int WN, int KG, int SPREAD>
+__global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(RowGemmArgs g) {
+  constexpr int T = 64 * WM * WN * KG, RI = TM / WM / 16, CJ = TN / WN / 16;
   static_assert(RI % 2 == 0, "");
-  constexpr int AT_B = TM * QB, STAGE = (TM + TN) * QB;
+  constexpr int AT_B = TM * QB, BLOCK = (TM + TN) * QB, STAGE = KG * BLOCK;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, q = lane >> 4, kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
 
   // tile of this workgroup: workgroups go to the 8 XCDs in turn; each XCD takes
   // a contiguous part of the tiles, which run down 8 row tiles at a time
@@ -284,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   {
     const int tm = (g.m + TM - 1) / TM, tn = GROUPED ? count_pieces<TN>(g) : (g.n + TN - 1) / TN, all = tm * tn;
     const int id = blockIdx.x, x = id & 7, part = all >> 3, more = all & 7;
-    if ((id >> 3) >= part + (x < more)) return;
+    if (GROUPED && (id >> 3) >= part + (x < more)) return;
     const int t = x * part + min(x, more) + (id >> 3);
     const int width = 8 * tn, band = t / width, h = min(8, tm - 8 * band), in = t - band * width;
     mt = 8 * band + in % h;
@@ -300,63 +317,154 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     zero = rows.group == g.groups;
     take_group(g, zero ? Rows{rows.first, rows.end, 0} : rows);
   }
+  Panel<TM, T, true> pa;
+  Panel<TN, T, false> pb;
+  pa.init(g.a, m0, g.k, tid);
+  pb.init(g.b, n0, g.k, tid);
+  // The stage of blocks kb, kb + 1, .., in LOADS pieces.
+  constexpr int NA = Panel<TM, T, true>::N, PIECES = NA + Panel<TN, T, false>::N, LOADS = KG * PIECES;
+  auto load = [&](int piece, int kb, uint32_t to) {
+    kb += piece / PIECES;
+    to += piece / PIECES * BLOCK;
+    piece %= PIECES;
+    if (piece < NA) pa.load(piece, kb, to, wave);
+    else pb.load(piece - NA, kb, to + AT_B, wave);
+  };
+
   i4 acc[RI][CJ];
 #pragma unroll
   for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < CJ; ++j) acc[i][j] = i4{0, 0, 0, 0};
 
-  Panel<TM, T, true> pa;
-  Panel<TN, T, false> pb;
-  pa.init(g.a, m0, g.k, tid);
-  pb.init(g.b, n0, g.k, tid);
+  // Fragment addresses.  Row tile i = 2h + p: lane r holds block row
+  // 32 h + 8 (r / 4) + 4 p + r % 4, so that the two tiles of a pair leave 8
+  // consecutive rows of C in one lane.
   const int ar = wm * (TM / WM) + 8 * (r >> 2) + (r & 3), br = wn * (TN / WN) + r;
   const int aat = ar * QB + 16 * (q ^ a_key(ar)), bat = AT_B + br * QB + 16 * (q ^ b_key(br));
+  i4 x[2][2], b[CJ][2];       // of row tile i (mod 2) and of the stage's columns
+  auto read_a = [&](const uint8_t *l, int i) {
+    const int o = (i >> 1) * 32 * QB + (i & 1) * 4 * QB;
+    x[i & 1][0] = *reinterpret_cast<const i4 *>(l + aat + o);
+    x[i & 1][1] = *reinterpret_cast<const i4 *>(l + (aat ^ 64) + o);
+  };
+  auto read_b = [&](const uint8_t *l) {
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) {
+      b[j][0] = *reinterpret_cast<const i4 *>(l + bat + 16 * QB * j);
+      b[j][1] = *reinterpret_cast<const i4 *>(l + (bat ^ 64) + 16 * QB * j);
+    }
+  };
   auto meet = [&]() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+
+  // This workgroup's blocks: all, or the part of grid y.  Stage 0 is its last one to
+  // KG, the very last of which may be cut at column k; stage i > 0 is the KG from
+  // kb0 + (i - 1) KG on.
   const int blocks = zero ? 0 : (g.k + QB - 1) / QB;
-  const uint32_t base = lds_address(lds);
-  if (blocks > 0) {
-    pa.load_last(blocks - 1, base, wave, true);
-    pb.load_last(blocks - 1, base + AT_B, wave, true);
-    meet();
-    if (g.k & (QB - 1)) {
-      pa.cut(g.k & (QB - 1), lds, tid);
-      pb.cut(g.k & (QB - 1), lds + AT_B, tid);
+  const int kb0 = (int)((int64_t)blocks * blockIdx.y / gridDim.y);
+  const int mine = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
+  if (mine > 0) {
+    const int nb = (mine + KG - 1) / KG, last = mine - (nb - 1) * KG;      // stages; blocks of stage 0
+    const bool cut = (g.k & (QB - 1)) != 0 && kb0 + mine == blocks;
+    const uint32_t base = lds_address(lds);
+#pragma unroll
+    for (int c = 0; c < KG; ++c) {
+      const int kb = c < last ? kb0 + mine - last + c : 0;
+      pa.load_last(kb, base + c * BLOCK, wave, c < last);
+      pb.load_last(kb, base + c * BLOCK + AT_B, wave, c < last);
+    }
+    auto load_all = [&](int kb, uint32_t to) {
+#pragma unroll
+      for (int c = 0; c < LOADS; ++c) load(c, kb, to);
+    };
+    if (SPREAD == 0 && nb > 1) {
+      load_all(kb0, base + STAGE);
+      static_assert(LOADS < 16, "");
+      __builtin_amdgcn_s_waitcnt(LOADS | 0xf << 8 | 7 << 4);     // stage 1 is still under way
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    } else {
       meet();
     }
-  }
-  int now = 0;
-  for (int kb = 0; kb < blocks; ++kb) {
-    if (kb + 1 < blocks) {
-#pragma unroll
-      for (int i = 0; i < pa.N; ++i) pa.load(i, kb, base + (STAGE - now), wave);
-#pragma unroll
-      for (int i = 0; i < pb.N; ++i) pb.load(i, kb, base + (STAGE - now) + AT_B, wave);
+    if (cut) {                // zeros in one operand are enough: integers have no NaN
+      pb.cut(g.k & (QB - 1), lds + (last - 1) * BLOCK + AT_B, tid);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);      // LDS only
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
     }
-    const uint8_t *l = lds + now;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i4 b[CJ];
-#pragma unroll
-      for (int j = 0; j < CJ; ++j) b[j] = *reinterpret_cast<const i4 *>(l + (bat ^ 64 * h) + 16 * QB * j);
+    read_b(lds + kg * BLOCK);
+    read_a(lds + kg * BLOCK, 0);
+    // All products of a stage, that of block kb loaded meanwhile.
+    auto row_tiles = [&](const uint8_t *l, auto live, int kb, uint32_t to) {
+      static_assert(SPREAD == 0 || SPREAD * RI >= LOADS, "");
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
-        const i4 a = *reinterpret_cast<const i4 *>(l + (aat ^ 64 * h) + (i >> 1) * 32 * QB + (i & 1) * 4 * QB);
+        if (i + 1 < RI) read_a(l, i + 1);
 #pragma unroll
-        for (int j = 0; j < CJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[j], acc[i][j], 0, 0, 0);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i & 1][h], b[j][h], acc[i][j], 0, 0, 0);
+        if constexpr (decltype(live)::value)
+#pragma unroll
+          for (int c = 0; c < SPREAD; ++c)
+            if (i * SPREAD + c < LOADS) load(i * SPREAD + c, kb, to);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    int now = 0, next = STAGE;
+    for (int stage = 0; stage < nb - 1; ++stage) {
+      row_tiles(lds + now + kg * BLOCK, std::true_type{}, kb0 + stage * KG, base + next);
+      meet();
+      if (SPREAD == 0 && stage + 2 < nb) load_all(kb0 + (stage + 1) * KG, base + now);
+      read_b(lds + next + kg * BLOCK);
+      read_a(lds + next + kg * BLOCK, 0);
+      const int t = now;
+      now = next;
+      next = t;
     }
-    meet();
-    now = STAGE - now;
+    row_tiles(lds + now + kg * BLOCK, std::false_type{}, 0, 0);
+  }
+  if constexpr (KG == 2) {                // the second half's sums to the first half
+    static_assert(WM * WN * RI * CJ * 1024 <= 2 * STAGE, "");
+    i4 *sums = reinterpret_cast<i4 *>(lds) + (wave % (WM * WN)) * RI * CJ * 64 + lane;
+    __syncthreads();
+    if (kg == 1)
+#pragma unroll
+      for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) sums[(i * CJ + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) acc[i][j] += sums[(i * CJ + j) * 64];
   }
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
   const int row0 = m0 + wm * (TM / WM), col0 = n0 + wn * (TN / WN);
+  if (!GROUPED && gridDim.y > 1) {        // a part's sums
+    int *part = static_cast<int *>(g.c) + (int64_t)blockIdx.y * g.m * g.n;
+#pragma unroll
+    for (int h = 0; h < RI / 2; ++h)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        const int row = row0 + 32 * h + 8 * q, col = col0 + 16 * j + r;
+        if (row < g.m && col < g.n) {
+          int v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = acc[2 * h + (e >> 2)][j][e & 3];
+          put_sums(part + (int64_t)col * g.m + row, g.m - row, v);
+        }
+      }
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < RI / 2; ++h) {
     const int row = row0 + 32 * h + 8 * q;
@@ -378,32 +486,122 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   }
 }
 
+// C from PARTS m x n matrices of sums: a thread takes 8 consecutive rows of a column.
+template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(RowGemmArgs g, const int *part) {
+  const int up = (g.m + 7) / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int j = (int)(at / up), i = 8 * (int)(at - (int64_t)j * up), left = g.m - i;
+  if (j >= g.n) return;
+  const int *p = part + (int64_t)j * g.m + i;
+  const int64_t step = (int64_t)g.m * g.n;
+  int x[PARTS][8];
+#pragma unroll
+  for (int z = 0; z < PARTS; ++z) {
+    if (left >= 8) __builtin_memcpy(x[z], p + z * step, 32);
+    else
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[z][e] = e < left ? p[z * step + e] : 0;
+  }
+  float sa[8], v[8];
+  get8(g.a.scales + i, left, sa);
+  const float sb = g.b.scales[j];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    int sum = 0;
+#pragma unroll
+    for (int z = 0; z < PARTS; ++z) sum += x[z][e];
+    v[e] = (float)sum * sb * sa[e];
+  }
+  store8(g, i, j, v);
+}
+
 // ---- which kernel ------------------------------------------------------------------------------------
+
+enum Kind { STRIP, TILE_64, TILE_64K, TILE_128, TILE_128W, TILE_128K, TILE_256 };
+struct Shape {
+  int rows, cols, threads;  // of C and of the workgroup that computes them
+  int halves;               // of its waves, which share the blocks of the contraction
+};
+constexpr Shape SHAPE[] = {{16, 16, 512, 1},   {128, 64, 512, 1},  {128, 64, 512, 2}, {128, 128, 256, 1},
+                           {128, 128, 512, 1}, {128, 128, 512, 2}, {256, 256, 512, 1}};
+struct Choice {
+  Kind kind;
+  int parts;                // of the contraction, with a launch that adds them if more than one
+};
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-enum Kind { STRIP, TILE_128 };
-struct Shape {
-  int rows, cols, threads;
-};
-constexpr Shape SHAPE[] = {{16, 16, 512}, {128, 128, 256}};
-
-constexpr int64_t THREAD_LIM = (int64_t)1 << 32;
-
-// Pieces of B's rows at most: each group ends with a piece that may be short, and so do the rows behind the last.
+// Pieces of B's rows at most: each group ends with a piece that may be short, and so
+// do the rows behind the last.
 int64_t most_pieces(Kind kind, int64_t n, int32_t groups) {
   const int64_t tn = SHAPE[kind].cols;
   return groups ? std::min(n, (n + (groups + 1) * (tn - 1)) / tn) : cdiv(n, tn);
 }
-bool fits(Kind kind, int64_t m, int64_t n, int32_t groups) {
-  const int64_t p = most_pieces(kind, n, groups);
-  return kind == STRIP ? cdiv(m, 16) * 512 < THREAD_LIM && p <= 65535 : cdiv(m, SHAPE[kind].rows) * p * SHAPE[kind].threads < THREAD_LIM;
+
+// A launch has less than 2^32 threads along x.  128 x 128 tiles of four waves fit
+// whatever the others do, where a result has less than 2^24 of them.
+constexpr int64_t THREAD_LIM = (int64_t)1 << 32, TILE_LIM = (int64_t)1 << 24;
+int64_t workgroups(Kind kind, int64_t m, int64_t n, int32_t groups) {
+  return kind == STRIP ? cdiv(m, 16) : cdiv(m, SHAPE[kind].rows) * most_pieces(kind, n, groups);      // along x
+}
+bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
+  return workgroups(kind, m, n, groups) * SHAPE[kind].threads < THREAD_LIM && (kind != STRIP || most_pieces(STRIP, n, groups) <= 65535) &&
+         (parts == 1 || cdiv(m, 8) * n < THREAD_LIM - 256);
 }
 
-Kind choose(int64_t m, int64_t n, int64_t, int32_t groups) {
-  const int64_t each = groups ? cdiv(n, groups) : n;
-  return each <= 32 && fits(STRIP, m, n, groups) ? STRIP : TILE_128;
+// The kernel with the least estimated time (us).  The estimates are fits to measured
+// times (graph replays, 16-bit C) of every kernel at 36 products and 14 of groups; the
+// choice costs 1.2% against the best of them, 19% at most.  Some of them, the kernel
+// chosen first:
+//   4608 x 37 x 2568     strip 8.6, 128 x 64 tiles in four parts 9.3, 128 x 128 14
+//   8192 x 33 x 8192     128 x 64 in two halves and four parts 17.7, strip 41
+//   2501 x 1111 x 1747   128 x 128 on eight waves 15.3, on four 16.4, 128 x 64 22
+//   2000 x 1000 x 8000   128 x 64 in two halves 33, 128 x 128 in two halves 44
+//   2048 x 4096 x 2048   128 x 128 on four waves 22.5, on eight 27
+//   4096 x 4096 x 4096   256 x 256 62, 128 x 128 on four waves 77
+//   64 groups, 28672 rows, 2816 x 2048   256 x 256 265, 128 x 128 303
+//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 21, strip 32
+Choice choose(int64_t m, int64_t n, int64_t k, int32_t groups) {
+  const double nb = (double)std::max<int64_t>(1, cdiv(k, QB));
+  // Groups that have rows, where each row falls into one of them; the weights they
+  // read, MB; pieces of tn rows of B, half a piece more for each group.
+  const double reached = groups ? groups * (1.0 - std::exp(-(double)n / groups)) : 1.0;
+  const double weights = groups ? reached * (double)m * (double)k * 1e-6 : 0.0;
+  auto pieces = [&](int tn) { return groups ? std::max(reached, (double)n / tn + 0.5 * reached) : (double)cdiv(n, tn); };
+  Choice best{TILE_128, 1};
+  double least = 1e300;
+  // `rate`: what the kernel reads of weights, TB/s
+  auto offer = [&](Kind kind, int parts, double rate, double t) {
+    if (groups) t = std::max(t, 3.0 + weights / rate);
+    if (t < least && fits(kind, parts, m, n, groups)) {
+      least = t;
+      best = Choice{kind, parts};
+    }
+  };
+  // 2 KB of A a workgroup and block, and as many rows of B as there are up to 16
+  offer(STRIP, 1, 3.6, 2.4 + cdiv(m, 16) * pieces(16) * nb * (1.8e-4 + 1e-5 * std::min(16.0, n / reached)) + 0.05 * nb);
+  // One workgroup a CU takes `one` a block, `pair` of them together `two`.
+  auto tiles = [&](Kind kind, int tn, int pair, double rate, double one, double two, double first, double next) {
+    for (const int parts : {1, 2, 4, 8}) {
+      if (parts > 1 && (nb < 4 * parts || groups)) break;
+      const double t = (double)cdiv(m, SHAPE[kind].rows) * pieces(tn) * parts;
+      const double rounds = std::ceil(t / (256 * pair)), rest = t - 256 * pair * (rounds - 1);
+      double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
+      if (parts > 1) us += 2.8 + parts * (0.1 + (double)m * (double)n * 2.1e-6);
+      offer(kind, parts, rate, us);
+      if (kind == TILE_256) break;
+    }
+  };
+  tiles(TILE_64, 64, 2, 4.3, 0.475, 1.265, 2.6, 3.0);
+  tiles(TILE_128W, 128, 2, 4.0, 0.6, 1.38, 3.9, 7.2);
+  tiles(TILE_128, 128, 2, 5.6, 0.645, 1.0, 4.3, 8.5);
+  tiles(TILE_64K, 64, 2, 4.8, 0.39, 1.02, 3.85, 4.7);
+  tiles(TILE_128K, 128, 1, 4.4, 0.53, 0.53, 5.5, 6.0);
+  tiles(TILE_256, 256, 1, 4.6, 1.46, 1.46, 10.6, 14.0);
+  return best;
 }
+
+size_t parts_bytes(const Choice &c, int64_t m, int64_t n) { return c.parts > 1 ? sizeof(int) * (size_t)c.parts * m * n : 0; }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -420,7 +618,7 @@ tlr_status check_sizes(int64_t m, int64_t n, int64_t k, int32_t groups) {
   if (m < 0 || n < 0 || k < 0 || m > PRODUCT_LIM || n > PRODUCT_LIM) return fail(TLR_ERR_INVALID_ARG, "row_gemm: size out of range");
   if (k > K_LIM) return fail(TLR_ERR_UNSUPPORTED, "row_gemm: 32-bit sums hold 131071 columns at most");
   if (groups < 0 || groups > MOST_GROUPS) return fail(TLR_ERR_INVALID_ARG, "row_gemm: groups are 1 .. 1024");
-  if (!fits(TILE_128, m, n, groups)) return fail(TLR_ERR_INVALID_ARG, "row_gemm: too many tiles for a launch");
+  if (cdiv(m, 128) * most_pieces(TILE_128, n, groups) >= TILE_LIM) return fail(TLR_ERR_INVALID_ARG, "row_gemm: too many tiles for a launch");
   return TLR_OK;
 }
 
@@ -434,12 +632,36 @@ tlr_status check_operand(const char *name, const tlr_row_matrix *x, int64_t rows
   return TLR_OK;
 }
 
-template <Kind KIND, int WM, int WN> void tile_launch(const RowGemmArgs &g, hipStream_t st) {
-  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols;
-  static_assert(SHAPE[KIND].threads == 64 * WM * WN, "");
-  const unsigned grid = (unsigned)(cdiv(g.m, TM) * most_pieces(KIND, g.n, g.offsets ? g.groups : 0));
-  if (g.offsets) tile_kernel<true, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
-  else tile_kernel<false, TM, TN, WM, WN><<<grid, 64 * WM * WN, 0, st>>>(g);
+template <Kind KIND, int WM, int WN, int SPREAD> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
+  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, KG = SHAPE[KIND].halves, T = 64 * WM * WN * KG;
+  static_assert(SHAPE[KIND].threads == T, "");
+  const dim3 grid((unsigned)workgroups(KIND, g.m, g.n, g.groups), (unsigned)parts);
+  if (g.groups) return tile_kernel<true, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(g);
+  if (parts == 1) return tile_kernel<false, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(g);
+  RowGemmArgs h = g;
+  h.c = ws;
+  tile_kernel<false, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(h);
+  const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
+  if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
+  else if (parts == 4) parts_kernel<4><<<sum, 256, 0, st>>>(g, ws);
+  else parts_kernel<8><<<sum, 256, 0, st>>>(g, ws);
+}
+
+void gemm_launch(const RowGemmArgs &g, const Choice &c, int *ws, hipStream_t st) {
+  switch (c.kind) {
+    case STRIP: {
+      const dim3 grid((unsigned)workgroups(STRIP, g.m, g.n, g.groups), (unsigned)most_pieces(STRIP, g.n, g.groups));
+      if (g.groups) strip_kernel<true><<<grid, 512, 0, st>>>(g);
+      else strip_kernel<false><<<grid, 512, 0, st>>>(g);
+      return;
+    }
+    case TILE_64: return tile_launch<TILE_64, 4, 2, 0>(g, c.parts, ws, st);
+    case TILE_64K: return tile_launch<TILE_64K, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<TILE_128, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<TILE_128W, 2, 4, 0>(g, c.parts, ws, st);
+    case TILE_128K: return tile_launch<TILE_128K, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_256: return tile_launch<TILE_256, 2, 4, 2>(g, c.parts, ws, st);
+  }
 }
 
 }  // namespace
@@ -471,10 +693,10 @@ tlr_status row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_bl
   if (st != TLR_OK) return st;
   *out = tlr_block_gemm_choice{};
   if (m == 0 || n == 0) return TLR_OK;
-  const Kind c = choose(m, n, k, groups);
-  const Shape &s = SHAPE[c];
-  const int64_t p = most_pieces(c, n, groups);
-  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, 1, 1, 0, c == STRIP ? cdiv(m, 16) : cdiv(m, s.rows) * p, c == STRIP ? p : 1, 0};
+  const Choice c = choose(m, n, k, groups);
+  const Shape &s = SHAPE[c.kind];
+  const int64_t y = c.kind == STRIP ? most_pieces(STRIP, n, groups) : 1;
+  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, s.halves, c.parts, 0, workgroups(c.kind, m, n, groups), y, parts_bytes(c, m, n)};
   return TLR_OK;
 }
 
@@ -501,20 +723,17 @@ tlr_status row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row
   if ((st = check_operand("A", A, m, k, &g.a)) != TLR_OK) return st;
   if ((st = check_operand("B", B, n, k, &g.b)) != TLR_OK) return st;
   if (!C || !aligned(C, dt == TLR_F32 ? 4 : 2)) return fail(TLR_ERR_INVALID_ARG, "row_gemm: null or misaligned C");
+  const Choice choice = choose(m, n, k, g.groups);
+  const size_t need = parts_bytes(choice, m, n);
+  if (need > 0 && (!ws || !aligned(ws, 16))) return fail(TLR_ERR_INVALID_ARG, "row_gemm: null or misaligned workspace");
+  if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "row_gemm: workspace too small");
   g.m = (int32_t)m;
   g.n = (int32_t)n;
   g.k = (int32_t)k;
   g.c = C;
   g.ldc = ldc;
   g.dt = dt;
-  hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (choose(m, n, k, g.groups) == STRIP) {
-    const dim3 grid((unsigned)cdiv(m, 16), (unsigned)most_pieces(STRIP, n, g.groups));
-    if (groups) strip_kernel<true><<<grid, 512, 0, hs>>>(g);
-    else strip_kernel<false><<<grid, 512, 0, hs>>>(g);
-  } else {
-    tile_launch<TILE_128, 2, 2>(g, hs);
-  }
+  gemm_launch(g, choice, static_cast<int *>(ws), static_cast<hipStream_t>(stream));
   return launched("row_gemm");
 }
 

@@ -41,8 +41,8 @@ def binding():
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value   # noqa: E731
     _binding.connect(*(address(getattr(lib, name)) for name in (
         "tlr_block_quantize", "tlr_block_gemm", "tlr_moe", "tlr_row_quantize", "tlr_row_gemm_workspace_bytes", "tlr_row_gemm",
-        "tlr_expert_sort_workspace_bytes", "tlr_expert_sort", "tlr_expert_gather", "tlr_expert_combine",
-        "tlr_expert_combine_grad", "tlr_gated", "tlr_gated_grad")))
+        "tlr_row_linear_workspace_bytes", "tlr_row_linear", "tlr_expert_sort_workspace_bytes", "tlr_expert_sort",
+        "tlr_expert_gather", "tlr_expert_combine", "tlr_expert_combine_grad", "tlr_gated", "tlr_gated_grad")))
     return _binding
 
 
@@ -219,12 +219,12 @@ def linear(x: torch.Tensor, w: torch.Tensor, grad_fmt: str = "e4m3", fast: bool 
     return _Linear.apply(x, w, grad_fmt, fast)
 
 
-def gated_forward(x: torch.Tensor, keep: bool = True):
+def gated_forward(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y, codes, scales) of a 2-d x: y = silu(gate) * up, and x as int8 codes
     (rows, 2, inter rounded up to 16) with a float32 scale for every 128 of them
-    (rows, 2, ceil(inter/128)), gate first; None unless ``keep``.  The scale is the
-    largest magnitude over 127.  Codes and scales are views of one allocation."""
-    got = binding().gated(x, keep)
+    (rows, 2, ceil(inter/128)), gate first.  The scale is the largest magnitude over
+    127.  Codes and scales are views of one allocation."""
+    got = binding().gated_forward(x)
     if type(got) is int:
         T._check(got, "tlr_gated")
     return got
@@ -233,24 +233,10 @@ def gated_forward(x: torch.Tensor, keep: bool = True):
 def gated_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
     """The gradient of gated_forward's x, in dy's type, taken at the values that
     the codes and scales stand for."""
-    got = binding().gated_grad(dy, codes, scales)
+    got = binding().gated_backward(dy, codes, scales)
     if type(got) is int:
         T._check(got, "tlr_gated_grad")
     return got
-
-
-class _Gated(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x):
-        y, codes, scales = gated_forward(_rows(x))
-        ctx.save_for_backward(codes, scales)
-        ctx.shape = x.shape
-        return y.reshape(*x.shape[:-1], y.shape[1])
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        return gated_backward(_rows(dy), *ctx.saved_tensors).reshape(ctx.shape)
 
 
 def gated(x: torch.Tensor) -> torch.Tensor:
@@ -263,9 +249,7 @@ def gated(x: torch.Tensor) -> torch.Tensor:
     magnitude / 254).  A block that holds an infinity or a NaN has NaN gradients.
     No double backward.  In a captured graph take torch.autograd.grad, or leaves that
     no live eager graph holds: their accumulation belongs to its stream."""
-    if x.dim() < 1 or x.shape[-1] % 2:
-        raise ValueError("gated: x is (..., 2*inter)")
-    if torch.is_grad_enabled() and x.requires_grad:
-        return _Gated.apply(x)
-    y = gated_forward(_rows(x), keep=False)[0]
-    return y.reshape(*x.shape[:-1], y.shape[1])
+    got = binding().gated(x)
+    if type(got) is int:
+        T._check(got, "tlr_gated")
+    return got

@@ -323,6 +323,15 @@ tlr_status tlr_row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr
   TLR_GUARD({ return tlr::row_gemm(dt, m, n, k, A, B, groups, C, ldc, workspace, workspace_bytes, stream); })
 }
 
+tlr_status tlr_row_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t *bytes_out) {
+  TLR_GUARD({ return tlr::row_linear_workspace(m, n, k, bytes_out); })
+}
+
+tlr_status tlr_row_linear(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const void *X,
+                          int64_t ldx, void *C, int64_t ldc, void *workspace, size_t workspace_bytes, void *stream) {
+  TLR_GUARD({ return tlr::row_linear(dt, m, n, k, A, X, ldx, C, ldc, workspace, workspace_bytes, stream); })
+}
+
 tlr_status tlr_expert_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts, size_t *bytes_out) {
   TLR_GUARD({ return tlr::expert_sort_workspace(tokens, topk, experts, bytes_out); })
 }

@@ -8,7 +8,13 @@
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <stdexcept>
+#include <string>
+#include <vector>
 
 #include "tlrgemm.h"
 
@@ -20,6 +26,8 @@ decltype(&tlr_moe) moe_entry = nullptr;
 decltype(&tlr_row_quantize) row_quantize_entry = nullptr;
 decltype(&tlr_row_gemm_workspace_bytes) row_gemm_bytes_entry = nullptr;
 decltype(&tlr_row_gemm) row_gemm_entry = nullptr;
+decltype(&tlr_row_linear_workspace_bytes) row_linear_bytes_entry = nullptr;
+decltype(&tlr_row_linear) row_linear_entry = nullptr;
 decltype(&tlr_expert_sort_workspace_bytes) sort_bytes_entry = nullptr;
 decltype(&tlr_expert_sort) sort_entry = nullptr;
 decltype(&tlr_expert_gather) gather_entry = nullptr;
@@ -49,20 +57,22 @@ template <typename F> void take(F &entry, PyObject *address) { entry = reinterpr
 
 // connect(addresses of the entries above, in their order)
 PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  if (n != 13) return value_error("connect: 13 addresses");
+  if (n != 15) return value_error("connect: 15 addresses");
   take(quantize_entry, args[0]);
   take(gemm_entry, args[1]);
   take(moe_entry, args[2]);
   take(row_quantize_entry, args[3]);
   take(row_gemm_bytes_entry, args[4]);
   take(row_gemm_entry, args[5]);
-  take(sort_bytes_entry, args[6]);
-  take(sort_entry, args[7]);
-  take(gather_entry, args[8]);
-  take(combine_entry, args[9]);
-  take(combine_grad_entry, args[10]);
-  take(gated_entry, args[11]);
-  take(gated_grad_entry, args[12]);
+  take(row_linear_bytes_entry, args[6]);
+  take(row_linear_entry, args[7]);
+  take(sort_bytes_entry, args[8]);
+  take(sort_entry, args[9]);
+  take(gather_entry, args[10]);
+  take(combine_entry, args[11]);
+  take(combine_grad_entry, args[12]);
+  take(gated_entry, args[13]);
+  take(gated_grad_entry, args[14]);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -376,30 +386,54 @@ PyObject *row_gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   END_HANDLE_TH_ERRORS
 }
 
-// row_linear(x, W's codes, scales, k) -> (rows of x, rows of W) or a status: x quantized and multiplied in one call
+// x (..., cols) as a matrix with contiguous rows.
+at::Tensor as_matrix(const at::Tensor &x) {
+  if (x.dim() == 2) return with_rows(x);
+  int64_t rows = 1;
+  for (int64_t i = 0; i + 1 < x.dim(); ++i) rows *= x.size(i);
+  return with_rows(x.reshape({rows, x.size(-1)}));
+}
+
+// Sizes of x with another last one.
+std::vector<int64_t> sizes_with(const at::Tensor &x, int64_t last) {
+  std::vector<int64_t> s = x.sizes().vec();
+  s.back() = last;
+  return s;
+}
+
+// row_linear(x, W's codes, scales, k) -> (..., rows of W) or a status: x (..., k) quantized and multiplied in one call
 PyObject *row_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 4) return value_error("linear: 4 arguments");
   for (const int i : {0, 1, 2})
     if (!THPVariable_Check(args[i])) return value_error("linear: x, codes and scales are tensors");
-  at::Tensor x = THPVariable_Unpack(args[0]);
+  at::Tensor x = THPVariable_Unpack(args[0]), ws;
   const at::Tensor &codes = THPVariable_Unpack(args[1]);
   const int64_t k = PyLong_AsLongLong(args[3]);
   if (PyErr_Occurred()) return nullptr;
-  if (const char *wrong = quantizable(x)) return value_error(wrong);
+  const bool grad = c10::GradMode::is_enabled();
+  if (grad && x.requires_grad()) {
+    PyErr_SetString(PyExc_RuntimeError, "int8.linear has no backward pass: call it under torch.no_grad() or on detached tensors");
+    return nullptr;
+  }
+  if (code_of(x) < 0 || x.dim() < 1 || !x.is_cuda()) return value_error("linear: a float32, float16 or bfloat16 x on a GPU is needed");
   tlr_row_matrix A{};
   if (const char *wrong = row_operand(codes, THPVariable_Unpack(args[2]), k, &A)) return value_error(wrong);
-  if (codes.dim() != 2 || codes.device() != x.device() || x.size(1) != k) return value_error("linear: x is (..., k) on the device of a weight of 2 dimensions");
-  if (c10::GradMode::is_enabled() && THPVariable_Unpack(args[2]).requires_grad()) return value_error("linear: scales that require a gradient would get none");
+  if (codes.dim() != 2 || codes.device() != x.device() || x.size(-1) != k) return value_error("linear: x is (..., k) on the device of a weight of 2 dimensions");
+  if (grad && THPVariable_Unpack(args[2]).requires_grad()) return value_error("linear: scales that require a gradient would get none");
   const c10::DeviceGuard guard(x.device());
-  x = with_rows(x);
-  const RowResult r(x.size(0), k, x.device());
-  tlr_status st = quantize_rows(x, nullptr, x.size(0), r);
+  const at::Tensor given = x;
+  x = as_matrix(x);
+  const int64_t m = codes.size(0), tokens = x.size(0);
+  const at::Tensor c = at::empty({tokens, m}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+  size_t bytes = 0;
+  tlr_status st = row_linear_bytes_entry(m, tokens, k, &bytes);
   if (st != TLR_OK) return PyLong_FromLong(st);
-  const at::Tensor c = at::empty({x.size(0), codes.size(0)}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
-  const tlr_row_matrix B{r.codes.data_ptr(), static_cast<const float *>(r.scales.data_ptr()), r.codes.size(1)};
-  st = multiply(c, codes.size(0), x.size(0), k, A, B, nullptr);
-  return st == TLR_OK ? wrap(c) : PyLong_FromLong(st);
+  if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(x.device()));
+  st = row_linear_entry((tlr_dtype)code_of(x), m, tokens, k, &A, x.data_ptr(), row_stride(x), c.data_ptr(), row_stride(c),
+                        bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream_of(x.device()));
+  if (st != TLR_OK) return PyLong_FromLong(st);
+  return wrap(given.dim() == 2 ? c : c.view(sizes_with(given, m)));
   END_HANDLE_TH_ERRORS
 }
 
@@ -433,24 +467,100 @@ PyObject *sort(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A call of the library that failed within an operator of autograd.  The Python call returns its status; from a backward
+// pass it arrives as a RuntimeError.
+struct Failed : std::runtime_error {
+  tlr_status status;
+  explicit Failed(tlr_status st) : std::runtime_error("a tlr_* call failed with status " + std::to_string(st)), status(st) {}
+};
+void must(tlr_status st) {
+  if (st != TLR_OK) throw Failed(st);
+}
+
+// Gradients that have none themselves: where a graph of the backward pass is made, differentiating it is an error.
+torch::autograd::variable_list once(const char *name, torch::autograd::variable_list grads) {
+  bool any = false;
+  for (const at::Tensor &g : grads) any = any || g.defined();
+  if (!c10::GradMode::is_enabled() || !any) return grads;
+  torch::autograd::variable_list leaves;
+  for (const at::Tensor &g : grads) leaves.push_back(g.defined() ? g.detach().requires_grad_() : g);
+  auto end = std::make_shared<torch::autograd::DelayedError>(std::string(name) + " has no second derivative", (int)grads.size());
+  return (*end)(std::move(leaves));
+}
+
 // What the operators on sorted rows take of a sort: place (tokens, topk) and the first row of no expert.
 struct Order {
   at::Tensor place, offsets;
-  int64_t tokens = 0, topk = 0;
-  const int32_t *at = nullptr, *end = nullptr;
-  const char *wrong = nullptr;
-  Order(PyObject *p, PyObject *o, const at::Device &d) {
-    wrong = "an order as moe.sort gives it, on the operands' device, is needed";
-    if (!THPVariable_Check(p) || !THPVariable_Check(o)) return;
-    place = THPVariable_Unpack(p);
-    offsets = THPVariable_Unpack(o);
-    if (place.scalar_type() != at::kInt || place.dim() != 2 || place.device() != d || !place.is_contiguous()) return;
-    if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.size(0) < 2 || offsets.device() != d || !offsets.is_contiguous()) return;
-    tokens = place.size(0);
-    topk = place.size(1);
-    at = static_cast<const int32_t *>(place.data_ptr());
-    end = static_cast<const int32_t *>(offsets.data_ptr()) + offsets.size(0) - 1;
-    wrong = nullptr;
+  Order(const at::Tensor &p, const at::Tensor &o) : place(p), offsets(o) {}
+  int64_t tokens() const { return place.size(0); }
+  int64_t topk() const { return place.size(1); }
+  const int32_t *at() const { return static_cast<const int32_t *>(place.data_ptr()); }
+  const int32_t *end() const { return static_cast<const int32_t *>(offsets.data_ptr()) + offsets.size(0) - 1; }
+};
+
+const char *not_an_order(PyObject *p, PyObject *o, const at::Device &d) {
+  const char *wrong = "an order as moe.sort gives it, on the operands' device, is needed";
+  if (!THPVariable_Check(p) || !THPVariable_Check(o)) return wrong;
+  const at::Tensor &place = THPVariable_Unpack(p), &offsets = THPVariable_Unpack(o);
+  if (place.scalar_type() != at::kInt || place.dim() != 2 || place.device() != d || !place.is_contiguous()) return wrong;
+  if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.size(0) < 2 || offsets.device() != d || !offsets.is_contiguous()) return wrong;
+  return nullptr;
+}
+
+at::Tensor like(const at::Tensor &x, int64_t rows, int64_t cols) {
+  return at::empty({rows, cols}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+}
+
+at::Tensor gather_rows(at::Tensor x, const Order &o) {
+  const c10::DeviceGuard guard(x.device());
+  x = with_rows(x);
+  const at::Tensor y = like(x, o.tokens() * o.topk(), x.size(1));
+  must(gather_entry((tlr_dtype)code_of(x), o.tokens(), (int32_t)o.topk(), x.size(1), x.data_ptr(), row_stride(x), o.at(), o.end(),
+                    y.data_ptr(), row_stride(y), stream_of(x.device())));
+  return y;
+}
+
+// weights undefined: 1
+at::Tensor combine_rows(at::Tensor y, at::Tensor w, const Order &o) {
+  const c10::DeviceGuard guard(y.device());
+  y = with_rows(y);
+  if (w.defined()) w = w.contiguous();
+  const at::Tensor out = like(y, o.tokens(), y.size(1));
+  must(combine_entry((tlr_dtype)code_of(y), o.tokens(), (int32_t)o.topk(), y.size(1), y.data_ptr(), row_stride(y), o.at(), o.end(),
+                     w.defined() ? static_cast<const float *>(w.data_ptr()) : nullptr, out.data_ptr(), row_stride(out), stream_of(y.device())));
+  return out;
+}
+
+struct Gather : torch::autograd::Function<Gather> {
+  static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &x, const at::Tensor &place, const at::Tensor &offsets) {
+    ctx->save_for_backward({place, offsets});
+    return gather_rows(x, Order(place, offsets));
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, const torch::autograd::variable_list &grads) {
+    const auto saved = ctx->get_saved_variables();
+    return once("gather", {combine_rows(grads[0], at::Tensor(), Order(saved[0], saved[1])), at::Tensor(), at::Tensor()});
+  }
+};
+
+struct Combine : torch::autograd::Function<Combine> {
+  static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &y, const at::Tensor &w, const at::Tensor &place,
+                            const at::Tensor &offsets) {
+    ctx->save_for_backward({y, w, place, offsets});
+    return combine_rows(y, w, Order(place, offsets));
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, const torch::autograd::variable_list &grads) {
+    const auto saved = ctx->get_saved_variables();
+    const Order o(saved[2], saved[3]);
+    const c10::DeviceGuard guard(grads[0].device());
+    const at::Tensor dout = with_rows(grads[0]), y = with_rows(saved[0]), w = saved[1].contiguous();
+    at::Tensor dy, dw;
+    if (ctx->needs_input_grad(0)) dy = like(y, y.size(0), y.size(1));
+    if (ctx->needs_input_grad(1)) dw = like(w, o.tokens(), o.topk());
+    must(combine_grad_entry((tlr_dtype)code_of(y), o.tokens(), (int32_t)o.topk(), y.size(1), dout.data_ptr(), row_stride(dout), y.data_ptr(),
+                            row_stride(y), o.at(), o.end(), static_cast<const float *>(w.data_ptr()), dy.defined() ? dy.data_ptr() : nullptr,
+                            dy.defined() ? row_stride(dy) : y.size(1), dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr,
+                            stream_of(dout.device())));
+    return once("combine", {dy, dw, at::Tensor(), at::Tensor()});
   }
 };
 
@@ -458,136 +568,155 @@ const char *rows_of(const at::Tensor &x, int64_t rows) {
   return code_of(x) < 0 || x.dim() != 2 || !x.is_cuda() || x.size(0) != rows ? "2-d float32, float16 or bfloat16 tensors on a GPU, of the order's rows, are needed" : nullptr;
 }
 
-// gather(x, place, offsets) -> sorted rows or a status
+// gather(x, place, offsets) -> sorted rows or a status; with their gradient where x has one
 PyObject *gather(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 3 || !THPVariable_Check(args[0])) return value_error("gather: 3 tensors");
-  at::Tensor x = THPVariable_Unpack(args[0]);
-  const Order o(args[1], args[2], x.device());
-  if (o.wrong) return value_error(o.wrong);
-  if (const char *wrong = rows_of(x, o.tokens)) return value_error(wrong);
-  const c10::DeviceGuard guard(x.device());
-  x = with_rows(x);
-  const at::Tensor y = at::empty({o.tokens * o.topk, x.size(1)}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
-  const tlr_status st = gather_entry((tlr_dtype)code_of(x), o.tokens, (int32_t)o.topk, x.size(1), x.data_ptr(), row_stride(x), o.at, o.end,
-                                     y.data_ptr(), row_stride(y), stream_of(x.device()));
-  return st == TLR_OK ? wrap(y) : PyLong_FromLong(st);
+  const at::Tensor &x = THPVariable_Unpack(args[0]);
+  if (const char *wrong = not_an_order(args[1], args[2], x.device())) return value_error(wrong);
+  const Order o(THPVariable_Unpack(args[1]), THPVariable_Unpack(args[2]));
+  if (const char *wrong = rows_of(x, o.tokens())) return value_error(wrong);
+  try {
+    if (c10::GradMode::is_enabled() && x.requires_grad()) return wrap(Gather::apply(x, o.place, o.offsets));
+    return wrap(gather_rows(x, o));
+  } catch (const Failed &f) {
+    return PyLong_FromLong(f.status);
+  }
   END_HANDLE_TH_ERRORS
 }
 
-const char *weights_of(const at::Tensor &w, const Order &o, const at::Device &d) {
-  return w.scalar_type() != at::kFloat || w.dim() != 2 || w.size(0) != o.tokens || w.size(1) != o.topk || w.device() != d
-             ? "weights: a float32 (tokens, topk) tensor on the operands' device is needed" : nullptr;
-}
-
-// combine(y, weights or None, place, offsets) -> a row for each token or a status
+// combine(y, weights or None, place, offsets) -> a row for each token or a status; with gradients where y or weights have one
 PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 4 || !THPVariable_Check(args[0]) || !(args[1] == Py_None || THPVariable_Check(args[1]))) return value_error("combine: 4 tensors");
-  at::Tensor y = THPVariable_Unpack(args[0]), w;
-  const Order o(args[2], args[3], y.device());
-  if (o.wrong) return value_error(o.wrong);
-  if (const char *wrong = rows_of(y, o.tokens * o.topk)) return value_error(wrong);
-  const c10::DeviceGuard guard(y.device());
+  const at::Tensor &y = THPVariable_Unpack(args[0]);
+  at::Tensor w;
+  if (const char *wrong = not_an_order(args[2], args[3], y.device())) return value_error(wrong);
+  const Order o(THPVariable_Unpack(args[2]), THPVariable_Unpack(args[3]));
+  if (const char *wrong = rows_of(y, o.tokens() * o.topk())) return value_error(wrong);
   if (args[1] != Py_None) {
     w = THPVariable_Unpack(args[1]);
-    if (const char *wrong = weights_of(w, o, y.device())) return value_error(wrong);
-    w = w.contiguous();
+    if (w.scalar_type() != at::kFloat || w.dim() != 2 || w.size(0) != o.tokens() || w.size(1) != o.topk() || w.device() != y.device())
+      return value_error("weights: a float32 (tokens, topk) tensor on the operands' device is needed");
   }
-  y = with_rows(y);
-  const at::Tensor out = at::empty({o.tokens, y.size(1)}, at::TensorOptions().device(y.device()).dtype(y.scalar_type()));
-  const tlr_status st = combine_entry((tlr_dtype)code_of(y), o.tokens, (int32_t)o.topk, y.size(1), y.data_ptr(), row_stride(y), o.at, o.end,
-                                      w.defined() ? static_cast<const float *>(w.data_ptr()) : nullptr, out.data_ptr(), row_stride(out),
-                                      stream_of(y.device()));
-  return st == TLR_OK ? wrap(out) : PyLong_FromLong(st);
-  END_HANDLE_TH_ERRORS
-}
-
-// combine_grad(dout, y, weights, place, offsets, dy wanted, dweights wanted) -> (dy or None, dweights or None) or a status
-PyObject *combine_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  if (n != 7) return value_error("combine_grad: 7 arguments");
-  for (const int i : {0, 1, 2})
-    if (!THPVariable_Check(args[i])) return value_error("combine_grad: dout, y and weights are tensors");
-  at::Tensor dout = THPVariable_Unpack(args[0]), y = THPVariable_Unpack(args[1]), w = THPVariable_Unpack(args[2]), dy, dw;
-  const int want_y = PyObject_IsTrue(args[5]), want_w = PyObject_IsTrue(args[6]);
-  const at::Device d = dout.device();
-  const Order o(args[3], args[4], d);
-  if (o.wrong) return value_error(o.wrong);
-  if (const char *wrong = rows_of(dout, o.tokens)) return value_error(wrong);
-  if (const char *wrong = rows_of(y, o.tokens * o.topk)) return value_error(wrong);
-  if (const char *wrong = weights_of(w, o, d)) return value_error(wrong);
-  if (y.device() != d || y.scalar_type() != dout.scalar_type() || y.size(1) != dout.size(1))
-    return value_error("combine_grad: y and dout of one type, width and device are needed");
-  const c10::DeviceGuard guard(d);
-  dout = with_rows(dout);
-  y = with_rows(y);
-  w = w.contiguous();
-  if (want_y) dy = at::empty({y.size(0), y.size(1)}, at::TensorOptions().device(d).dtype(y.scalar_type()));
-  if (want_w) dw = at::empty({o.tokens, o.topk}, at::TensorOptions().device(d).dtype(at::kFloat));
-  const tlr_status st = combine_grad_entry((tlr_dtype)code_of(y), o.tokens, (int32_t)o.topk, y.size(1), dout.data_ptr(), row_stride(dout),
-                                           y.data_ptr(), row_stride(y), o.at, o.end, static_cast<const float *>(w.data_ptr()),
-                                           want_y ? dy.data_ptr() : nullptr, want_y ? row_stride(dy) : y.size(1),
-                                           want_w ? static_cast<float *>(dw.data_ptr()) : nullptr, stream_of(d));
-  return st == TLR_OK ? tuple_of({dy, dw}) : PyLong_FromLong(st);
+  try {
+    if (c10::GradMode::is_enabled() && (y.requires_grad() || (w.defined() && w.requires_grad()))) {
+      if (!w.defined()) {
+        const c10::DeviceGuard guard(y.device());
+        w = at::ones({o.tokens(), o.topk()}, at::TensorOptions().device(y.device()).dtype(at::kFloat));
+      }
+      return wrap(Combine::apply(y, w, o.place, o.offsets));
+    }
+    return wrap(combine_rows(y, w, o));
+  } catch (const Failed &f) {
+    return PyLong_FromLong(f.status);
+  }
   END_HANDLE_TH_ERRORS
 }
 
 // ---- gated activation -----------------------------------------------------------------------------------
 
-// gated(x, keep) -> (y, codes, scales) or a status; codes (rows, 2, ld) and scales (rows, 2, blocks), in one allocation,
-// None unless kept
-PyObject *gated(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  if (n != 2 || !THPVariable_Check(args[0])) return value_error("gated: a tensor and a truth value");
-  at::Tensor x = THPVariable_Unpack(args[0]), codes, scales;
-  const int keep = PyObject_IsTrue(args[1]);
-  if (code_of(x) < 0 || x.dim() != 2 || !x.is_cuda() || x.size(1) % 2 != 0)
-    return value_error("gated: a float32, float16 or bfloat16 tensor on a GPU with rows of two halves is needed");
-  const c10::DeviceGuard guard(x.device());
-  x = with_rows(x);
-  const int64_t rows = x.size(0), inter = x.size(1) / 2, ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
-  const at::Tensor y = at::empty({rows, inter}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
-  if (keep) {
-    const int64_t scales_at = (2 * rows * ld + 255) / 256 * 256;
-    codes = at::empty({scales_at + 8 * rows * nq}, at::TensorOptions().dtype(at::kChar).device(x.device()));
-    scales = beside(codes, at::kFloat, scales_at, 2 * rows, nq);
-    scales.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, nq});
-    codes.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, ld});
+// y (rows, inter) of x (rows, 2 inter); with codes (rows, 2, ld) and scales (rows, 2, blocks), in one allocation, if kept.
+struct GatedResult {
+  at::Tensor y, codes, scales;
+  GatedResult(const at::Tensor &x, bool keep) {
+    const c10::DeviceGuard guard(x.device());
+    const int64_t rows = x.size(0), inter = x.size(1) / 2, ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
+    y = like(x, rows, inter);
+    if (keep) {
+      const int64_t scales_at = (2 * rows * ld + 255) / 256 * 256;
+      codes = at::empty({scales_at + 8 * rows * nq}, at::TensorOptions().dtype(at::kChar).device(x.device()));
+      scales = beside(codes, at::kFloat, scales_at, 2 * rows, nq);
+      scales.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, nq});
+      codes.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, ld});
+    }
+    must(gated_entry((tlr_dtype)code_of(x), rows, inter, x.data_ptr(), row_stride(x), y.data_ptr(), row_stride(y),
+                     keep ? codes.data_ptr() : nullptr, ld, keep ? static_cast<float *>(scales.data_ptr()) : nullptr, nq, stream_of(x.device())));
   }
-  const tlr_status st = gated_entry((tlr_dtype)code_of(x), rows, inter, x.data_ptr(), row_stride(x), y.data_ptr(), row_stride(y),
-                                    keep ? codes.data_ptr() : nullptr, ld, keep ? static_cast<float *>(scales.data_ptr()) : nullptr, nq,
-                                    stream_of(x.device()));
-  return st == TLR_OK ? tuple_of({y, codes, scales}) : PyLong_FromLong(st);
+};
+
+at::Tensor gated_rows_grad(const at::Tensor &dy, const at::Tensor &codes, const at::Tensor &scales) {
+  const c10::DeviceGuard guard(dy.device());
+  const int64_t rows = dy.size(0), inter = dy.size(1);
+  const at::Tensor dx = like(dy, rows, 2 * inter);
+  must(gated_grad_entry((tlr_dtype)code_of(dy), rows, inter, dy.data_ptr(), row_stride(dy), codes.data_ptr(), codes.size(2),
+                        static_cast<const float *>(scales.data_ptr()), scales.size(2), dx.data_ptr(), row_stride(dx), stream_of(dy.device())));
+  return dx;
+}
+
+struct Gated : torch::autograd::Function<Gated> {
+  static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &x) {
+    const GatedResult r(as_matrix(x), true);
+    ctx->save_for_backward({r.codes, r.scales});
+    return x.dim() == 2 ? r.y : r.y.view(sizes_with(x, r.y.size(1)));
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, const torch::autograd::variable_list &grads) {
+    const auto saved = ctx->get_saved_variables();
+    const c10::DeviceGuard guard(grads[0].device());
+    const at::Tensor dx = gated_rows_grad(as_matrix(grads[0]), saved[0], saved[1]);
+    return once("gated", {grads[0].dim() == 2 ? dx : dx.view(sizes_with(grads[0], dx.size(1)))});
+  }
+};
+
+bool gateable(const at::Tensor &x) { return code_of(x) >= 0 && x.is_cuda() && x.dim() >= 1 && x.size(-1) % 2 == 0; }
+const char *const NOT_GATEABLE = "gated: a float32, float16 or bfloat16 tensor (..., 2*inter) on a GPU is needed";
+
+// gated(x) -> y or a status; with its gradient where x has one
+PyObject *gated(PyObject *, PyObject *x_) {
+  HANDLE_TH_ERRORS
+  if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_))) return value_error(NOT_GATEABLE);
+  const at::Tensor &x = THPVariable_Unpack(x_);
+  const c10::DeviceGuard guard(x.device());
+  try {
+    if (c10::GradMode::is_enabled() && x.requires_grad()) return wrap(Gated::apply(x));
+    const GatedResult r(as_matrix(x), false);
+    return wrap(x.dim() == 2 ? r.y : r.y.view(sizes_with(x, r.y.size(1))));
+  } catch (const Failed &f) {
+    return PyLong_FromLong(f.status);
+  }
   END_HANDLE_TH_ERRORS
 }
 
-// gated_grad(dy, codes, scales) -> dx or a status
-PyObject *gated_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+// gated_forward(x of 2 dimensions) -> (y, codes, scales) or a status
+PyObject *gated_forward(PyObject *, PyObject *x_) {
   HANDLE_TH_ERRORS
-  if (n != 3) return value_error("gated_grad: 3 tensors");
+  if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_)) || THPVariable_Unpack(x_).dim() != 2) return value_error(NOT_GATEABLE);
+  const at::Tensor &x = THPVariable_Unpack(x_);
+  const c10::DeviceGuard guard(x.device());
+  try {
+    const GatedResult r(with_rows(x), true);
+    return tuple_of({r.y, r.codes, r.scales});
+  } catch (const Failed &f) {
+    return PyLong_FromLong(f.status);
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// gated_backward(dy, codes, scales) -> dx or a status
+PyObject *gated_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3) return value_error("gated_backward: 3 tensors");
   for (const int i : {0, 1, 2})
-    if (!THPVariable_Check(args[i])) return value_error("gated_grad: 3 tensors");
-  at::Tensor dy = THPVariable_Unpack(args[0]);
-  const at::Tensor &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]);
-  if (code_of(dy) < 0 || dy.dim() != 2 || !dy.is_cuda()) return value_error("gated_grad: dy is a 2-d float32, float16 or bfloat16 tensor on a GPU");
+    if (!THPVariable_Check(args[i])) return value_error("gated_backward: 3 tensors");
+  const at::Tensor &dy = THPVariable_Unpack(args[0]), &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]);
+  if (code_of(dy) < 0 || dy.dim() != 2 || !dy.is_cuda()) return value_error("gated_backward: dy is a 2-d float32, float16 or bfloat16 tensor on a GPU");
   const int64_t rows = dy.size(0), inter = dy.size(1), ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
   if (codes.scalar_type() != at::kChar || codes.sizes() != at::IntArrayRef({rows, 2, ld}) || !codes.is_contiguous() || codes.device() != dy.device() ||
       scales.scalar_type() != at::kFloat || scales.sizes() != at::IntArrayRef({rows, 2, nq}) || !scales.is_contiguous() || scales.device() != dy.device())
-    return value_error("gated_grad: codes and scales as gated gives them, of dy's rows, are needed");
+    return value_error("gated_backward: codes and scales as gated_forward gives them, of dy's rows, are needed");
   const c10::DeviceGuard guard(dy.device());
-  dy = with_rows(dy);
-  const at::Tensor dx = at::empty({rows, 2 * inter}, at::TensorOptions().device(dy.device()).dtype(dy.scalar_type()));
-  const tlr_status st = gated_grad_entry((tlr_dtype)code_of(dy), rows, inter, dy.data_ptr(), row_stride(dy), codes.data_ptr(), ld,
-                                         static_cast<const float *>(scales.data_ptr()), nq, dx.data_ptr(), row_stride(dx), stream_of(dy.device()));
-  return st == TLR_OK ? wrap(dx) : PyLong_FromLong(st);
+  try {
+    return wrap(gated_rows_grad(with_rows(dy), codes, scales));
+  } catch (const Failed &f) {
+    return PyLong_FromLong(f.status);
+  }
   END_HANDLE_TH_ERRORS
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(connect), METHOD(quantize), METHOD(gemm), METHOD(moe), METHOD(row_quantize), METHOD(row_gemm),
-                         METHOD(row_linear), METHOD(sort), METHOD(gather), METHOD(combine), METHOD(combine_grad), METHOD(gated),
-                         METHOD(gated_grad), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(row_linear), METHOD(sort), METHOD(gather), METHOD(combine), {"gated", gated, METH_O, nullptr},
+                         {"gated_forward", gated_forward, METH_O, nullptr}, METHOD(gated_backward), {nullptr, nullptr, 0, nullptr}};
 #undef METHOD
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

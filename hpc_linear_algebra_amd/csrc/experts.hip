@@ -256,23 +256,29 @@ template <typename T> __global__ __launch_bounds__(256) void combine_kernel(RowA
     if (left <= 0) continue;
     const T *x = static_cast<const T *>(a.x) + at;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    in_groups<8>(a.topk, [&](auto n, int s0) {
+    auto add = [&](auto whole, auto n, int s0) {
       constexpr int N = decltype(n)::value;
       int row[N];
-      float w[N], v[N][8];
+      float w[N];
+      Eight<T> v[N];
 #pragma unroll
       for (int s = 0; s < N; ++s) {
         row[s] = row_of(a, t * a.topk + s0 + s, end);
         w[s] = a.weights ? a.weights[t * a.topk + s0 + s] : 1.0f;
       }
 #pragma unroll
-      for (int s = 0; s < N; ++s) get8<true>(x + max(row[s], 0) * a.ldx, left, v[s]);
+      for (int s = 0; s < N; ++s) v[s].template load<decltype(whole)::value, true>(x + max(row[s], 0) * a.ldx, left);
 #pragma unroll
       for (int s = 0; s < N; ++s)
-        if (row[s] >= 0)
+        if (row[s] >= 0) {
+          float y[8];
+          v[s].get(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w[s], v[s][e], sum[e]);
-    });
+          for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w[s], y[e], sum[e]);
+        }
+    };
+    if (left >= 8) in_groups<8>(a.topk, [&](auto n, int s0) { add(std::true_type{}, n, s0); });
+    else in_groups<8>(a.topk, [&](auto n, int s0) { add(std::false_type{}, n, s0); });
     put8(static_cast<T *>(a.y) + t * a.ldy + at, left, sum);
   }
 }
@@ -303,17 +309,27 @@ template <typename T, bool PAST> __global__ __launch_bounds__(256) void combine_
       }
       for (int at = tid * 8; at < a.hidden; at += 2048) {
         const int left = a.hidden - at;
-        float v[8], y[N][8];
-        get8(d + at, left, v);
-        if (a.rows) {
+        Eight<T> x, y[N];
+        auto load = [&](auto whole) {
+          constexpr bool WHOLE = decltype(whole)::value;
+          x.template load<WHOLE>(d + at, left);
+          if (a.rows)
 #pragma unroll
-          for (int s = 0; s < N; ++s) get8<true>(static_cast<const T *>(a.rows) + (real[s] ? row[s] : 0) * a.ldr + at, left, y[s]);
+            for (int s = 0; s < N; ++s) y[s].template load<WHOLE, true>(static_cast<const T *>(a.rows) + (real[s] ? row[s] : 0) * a.ldr + at, left);
+        };
+        if (left >= 8) load(std::true_type{});
+        else load(std::false_type{});
+        float v[8];
+        x.get(v);
+        if (a.rows)
 #pragma unroll
           for (int s = 0; s < N; ++s)
-            if (real[s])
+            if (real[s]) {
+              float r[8];
+              y[s].get(r);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dot[s] = __builtin_fmaf(v[e], y[s][e], dot[s]);
-        }
+              for (int e = 0; e < 8; ++e) dot[s] = __builtin_fmaf(v[e], r[e], dot[s]);
+            }
         if (a.y)
 #pragma unroll
           for (int s = 0; s < N; ++s)

@@ -51,9 +51,17 @@ template <typename T, bool KEEP> __global__ __launch_bounds__(256) void gated_ke
     const int64_t row = task / a.nq;
     const int q = (int)(task % a.nq), col = q * QB + 8 * c, left = a.inter - col;
     const T *x = static_cast<const T *>(a.x) + row * a.ldx + col;
+    Eight<T> xg, xu;
+    if (left >= 8) {
+      xg.template load<true>(x, left);
+      xu.template load<true>(x + a.inter, left);
+    } else {
+      xg.template load<false>(x, left);
+      xu.template load<false>(x + a.inter, left);
+    }
     float g[8], u[8], y[8];
-    get8(x, left, g);
-    get8(x + a.inter, left, u);
+    xg.get(g);
+    xu.get(u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = g[e] * sigmoid(g[e]).s * u[e];
     put8(static_cast<T *>(a.y) + row * a.ldy + col, left, y);

@@ -51,20 +51,36 @@ template <bool PAST> __device__ __forceinline__ void put16(void *p, u4 v) {
   else *q = v;
 }
 
-// Eight consecutive elements as floats; zeros at or past `left`.
-template <bool PAST = false, typename T> __device__ __forceinline__ void get8(const T *p, int64_t left, float (&v)[8]) {
-  if (left >= 8) {
-    T x[8];
-    u4 w[sizeof x / 16];
+// Eight consecutive elements as they are.  WHOLE: all of them are there; otherwise
+// zeros at or past `left`, element by element.  Several of them go under one branch on
+// that: loads under a branch each wait for one another.
+template <typename T> struct Eight {
+  u4 w[sizeof(T) / 2];
+  template <bool WHOLE, bool PAST = false> __device__ __forceinline__ void load(const T *p, int64_t left) {
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof x / 16); ++i) w[i] = get16<PAST>(reinterpret_cast<const char *>(p) + 16 * i);
+      for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = get16<PAST>(reinterpret_cast<const char *>(p) + 16 * i);
+    } else {
+      T x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < left ? p[e] : (T)0.0f;
+      __builtin_memcpy(w, x, sizeof x);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    T x[8];
     __builtin_memcpy(x, w, sizeof x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = widen(x[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? widen(p[e]) : 0.0f;
   }
+};
+
+// Eight consecutive elements as floats; zeros at or past `left`.
+template <typename T> __device__ __forceinline__ void get8(const T *p, int64_t left, float (&v)[8]) {
+  Eight<T> x;
+  if (left >= 8) x.template load<true>(p, left);
+  else x.template load<false>(p, left);
+  x.get(v);
 }
 
 // Eight floats rounded to consecutive elements, those before `left`.

@@ -56,8 +56,18 @@ template <typename T, int W, int U> __global__ __launch_bounds__(256) void row_q
     float v[U > 0 ? U : 1][8];
     uint32_t m = 0;
     if constexpr (U > 0) {
+      Eight<T> in[U];
+      if (k >= 8) {             // all loads at once, from the row's end where there is nothing else
 #pragma unroll
-      for (int u = 0; u < U; ++u) get8(x + at + u * STEP, k - at - u * STEP, v[u]);
+        for (int u = 0; u < U; ++u) in[u].template load<true>(x + min(at + u * STEP, k - 8), 8);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int left = k - at - u * STEP;
+        if (left <= 0) in[u] = Eight<T>{};
+        else if (left < 8) in[u].template load<false>(x + at + u * STEP, left);
+        in[u].get(v[u]);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -273,6 +283,100 @@ template <bool GROUPED> __global__ __launch_bounds__(512, 4) void strip_kernel(R
 #pragma unroll
     for (int w = 0; w < W; ++w) v += part[w][i & 3][(i >> 2) * 16 + j];
     if (m0 + i < g.m && n0 + j < g.n) store_one(g, m0 + i, n0 + j, zero ? 0.0f : (float)v * g.b.scales[n0 + j] * g.a.scales[m0 + i]);
+  }
+}
+
+// A few tokens, quantized by every workgroup for itself: codes and scales stand in LDS,
+// and the strip's product follows, its first weights under way while x is read.  One
+// launch where quantizer and product are two: 8192 x 1 x 4096 7.0 us, 9.5 (the product
+// alone 6.8); 8192 x 4 x 4096 10.0, 10.4; 4096 x 8 x 2048 5.5, 6.2.  Beyond four vectors
+// of x a lane the work of all workgroups costs more than the launch (2048 x 5 x 3000
+// 6.6, 6.2).
+constexpr int FEW_TOKENS = 8, FEW = 16384;       // tokens, and entries of all of them
+__host__ __device__ constexpr int few_waves(int64_t n) { return n == 1 ? 8 : n == 2 ? 4 : n <= 4 ? 2 : 1; }     // for each token
+template <typename T> __global__ __launch_bounds__(512, 4) void few_kernel(RowGemmArgs g, const void *xp, int64_t ldx) {
+  constexpr int W = 8, AHEAD = 4, MOST = FEW_TOKENS;       // eight waves, as many as tokens at most
+  __shared__ __attribute__((aligned(16))) uint8_t codes[FEW + MOST * QB];
+  __shared__ int part[W][4][64];
+  __shared__ uint32_t top[W];
+  __shared__ float scale[MOST];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4, m0 = blockIdx.x * 16;
+  const uint8_t *arow = g.a.codes + (int64_t)min(m0 + r, g.m - 1) * g.a.ld + 16 * q;
+  const int blocks = (g.k + QB - 1) / QB, full = g.k / QB, ld = blocks * QB;      // rows of whole blocks in LDS, zeros behind column k
+  u4 ahead[AHEAD][2];
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kb = wave + u * W;
+      ahead[u][h] = kb < full ? *reinterpret_cast<const u4 *>(arow + kb * QB + 64 * h) : u4{0, 0, 0, 0};
+    }
+  // the waves share the tokens: eight, four, two or one of them for each
+  const int waves = few_waves(g.n), j = wave / waves, step = 512 * waves, at = 512 * (wave % waves) + 8 * lane;
+  const T *x = static_cast<const T *>(xp) + min(j, g.n - 1) * ldx;
+  float v[8];
+  if (j < g.n) {
+    uint32_t m = 0;
+    for (int c = at; c < g.k; c += step) {
+      get8(x + c, g.k - c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, mag(v[e]));
+    }
+    m = max64(m);
+    if (lane == 0) top[wave] = m;
+  }
+  __syncthreads();
+  if (j < g.n) {
+    uint32_t m = top[wave];
+    for (int w = 0; w < waves; ++w) m = max(m, top[j * waves + w]);
+    const float s = int8_scale(m), inverse = 1.0f / s;
+    if (at == 0) scale[j] = s;
+    for (int c = at; c < ld; c += step) {
+      if (ld > step || c >= g.k) get8(x + min(c, g.k), g.k - c, v);
+      *reinterpret_cast<u2 *>(codes + j * ld + c) = int8_codes8(v, s, inverse);
+    }
+  }
+  __syncthreads();
+  i4 acc = i4{0, 0, 0, 0};
+  const uint8_t *brow = codes + min(r, g.n - 1) * ld + 16 * q;
+  auto add = [&](int kb, const u4 (&x)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, x[h]), *reinterpret_cast<const i4 *>(brow + kb * QB + 64 * h), acc, 0, 0, 0);
+  };
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u)
+    if (wave + u * W < full) add(wave + u * W, ahead[u]);
+  int kb = wave + AHEAD * W;
+  for (; kb + (AHEAD - 1) * W < full; kb += AHEAD * W) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ahead[u][h] = *reinterpret_cast<const u4 *>(arow + (kb + u * W) * QB + 64 * h);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) add(kb + u * W, ahead[u]);
+  }
+  for (; kb < full; kb += W) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ahead[0][h] = *reinterpret_cast<const u4 *>(arow + kb * QB + 64 * h);
+    add(kb, ahead[0]);
+  }
+  if (full < blocks && wave == full % W) {                // the cut block
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ahead[0][h] = load16(arow + full * QB - 16 * q, 16 * q + 64 * h, g.k - full * QB);
+    add(full, ahead[0]);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[v];
+  __syncthreads();
+  if (tid < 256) {
+    const int i = tid & 15, j = tid >> 4;
+    int v = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += part[w][i & 3][(i >> 2) * 16 + j];
+    if (m0 + i < g.m && j < g.n) store_one(g, m0 + i, j, (float)v * scale[j] * g.a.scales[m0 + i]);
   }
 }
 
@@ -561,7 +665,7 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 //   4096 x 4096 x 4096   256 x 256 62, 128 x 128 on four waves 77
 //   64 groups, 28672 rows, 2816 x 2048   256 x 256 265, 128 x 128 303
 //   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 21, strip 32
-Choice choose(int64_t m, int64_t n, int64_t k, int32_t groups) {
+Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
   const double nb = (double)std::max<int64_t>(1, cdiv(k, QB));
   // Groups that have rows, where each row falls into one of them; the weights they
   // read, MB; pieces of tn rows of B, half a piece more for each group.
@@ -601,6 +705,20 @@ Choice choose(int64_t m, int64_t n, int64_t k, int32_t groups) {
   return best;
 }
 
+// A call asks for its workspace and then for its launch: the last answer is kept.
+Choice choose(int64_t m, int64_t n, int64_t k, int32_t groups) {
+  thread_local int64_t of[4] = {-1, -1, -1, -1};
+  thread_local Choice last;
+  if (of[0] != m || of[1] != n || of[2] != k || of[3] != groups) {
+    last = least_estimate(m, n, k, groups);
+    of[0] = m;
+    of[1] = n;
+    of[2] = k;
+    of[3] = groups;
+  }
+  return last;
+}
+
 size_t parts_bytes(const Choice &c, int64_t m, int64_t n) { return c.parts > 1 ? sizeof(int) * (size_t)c.parts * m * n : 0; }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -623,13 +741,56 @@ tlr_status check_sizes(int64_t m, int64_t n, int64_t k, int32_t groups) {
 }
 
 tlr_status check_operand(const char *name, const tlr_row_matrix *x, int64_t rows, int64_t k, Operand *o) {
-  const std::string w = std::string("row_gemm: ") + name;
+  const std::string w = name;
   if (!x || (!x->codes && k > 0) || !x->scales) return fail(TLR_ERR_INVALID_ARG, w + ": null matrix, codes or scales");
   if (x->ld % 16 != 0 || !aligned(x->codes, 16)) return fail(TLR_ERR_INVALID_ARG, w + ": codes and their rows must be 16-byte aligned");
   if (x->ld < k || x->ld >= LD_LIM) return fail(TLR_ERR_INVALID_ARG, w + ": leading dimension out of range");
   if (!aligned(x->scales, 4)) return fail(TLR_ERR_INVALID_ARG, w + ": misaligned scales");
   *o = Operand{static_cast<const uint8_t *>(x->codes), x->scales, x->ld, (int32_t)rows};
   return TLR_OK;
+}
+
+// What products of x or of its codes check alike, and set.
+tlr_status product_args(const char *name, tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, void *C, int64_t ldc,
+                        RowGemmArgs *g) {
+  const std::string w = std::string(name) + ": ";
+  if (dt == TLR_F64) return fail(TLR_ERR_UNSUPPORTED, w + "TLR_F64 is not provided");
+  if (dt != TLR_F32 && dt != TLR_F16 && dt != TLR_BF16) return fail(TLR_ERR_INVALID_ARG, w + "bad dtype");
+  if (ldc < std::max<int64_t>(1, m) || ldc > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, w + "ldc out of range");
+  if (m == 0 || n == 0) return TLR_OK;
+  const tlr_status st = check_operand((w + "A").c_str(), A, m, k, &g->a);
+  if (st != TLR_OK) return st;
+  if (!C || !aligned(C, dt == TLR_F32 ? 4 : 2)) return fail(TLR_ERR_INVALID_ARG, w + "null or misaligned C");
+  g->m = (int32_t)m;
+  g->n = (int32_t)n;
+  g->k = (int32_t)k;
+  g->c = C;
+  g->ldc = ldc;
+  g->dt = dt;
+  return TLR_OK;
+}
+
+// A linear layer's call: where the codes of x (rows of ld bytes), its scales and a
+// product's parts stand in the workspace.  A few tokens take one launch and no
+// workspace, where the product is a strip's.
+struct LinearParts {
+  Choice choice;
+  bool few;
+  int64_t ld;
+  size_t scales, parts, bytes;
+};
+LinearParts linear_parts(int64_t m, int64_t n, int64_t k) {
+  LinearParts p{};
+  if (m == 0 || n == 0) return p;
+  p.choice = choose(m, n, k, 0);
+  p.few = p.choice.kind == STRIP && n <= FEW_TOKENS && k <= 4 * 512 * few_waves(n);
+  if (p.few) return p;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  p.ld = (k + 15) & ~(int64_t)15;
+  p.scales = up((size_t)n * p.ld);
+  p.parts = p.scales + up(sizeof(float) * (size_t)n);
+  p.bytes = p.parts + parts_bytes(p.choice, m, n);
+  return p;
 }
 
 template <Kind KIND, int WM, int WN, int SPREAD> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
@@ -702,12 +863,9 @@ tlr_status row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_bl
 
 tlr_status row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const tlr_row_matrix *B,
                     const tlr_row_groups *groups, void *C, int64_t ldc, void *ws, size_t ws_bytes, void *stream) {
-  if (dt == TLR_F64) return fail(TLR_ERR_UNSUPPORTED, "row_gemm: C of type TLR_F64 is not provided");
-  if (dt != TLR_F32 && dt != TLR_F16 && dt != TLR_BF16) return fail(TLR_ERR_INVALID_ARG, "row_gemm: bad dtype of C");
+  RowGemmArgs g{};
   tlr_status st = check_sizes(m, n, k, groups ? std::max(groups->count, 1) : 0);
   if (st != TLR_OK) return st;
-  if (ldc < std::max<int64_t>(1, m) || ldc > SIZE_LIM) return fail(TLR_ERR_INVALID_ARG, "row_gemm: ldc out of range");
-  RowGemmArgs g{};
   if (groups) {
     if (groups->count < 1) return fail(TLR_ERR_INVALID_ARG, "row_gemm: groups are 1 .. 1024");
     if (!groups->offsets || !aligned(groups->offsets, 4)) return fail(TLR_ERR_INVALID_ARG, "row_gemm: null or misaligned offsets");
@@ -719,22 +877,52 @@ tlr_status row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row
     g.groups = groups->count;
     g.clear = groups->clear;
   }
-  if (m == 0 || n == 0) return TLR_OK;
-  if ((st = check_operand("A", A, m, k, &g.a)) != TLR_OK) return st;
-  if ((st = check_operand("B", B, n, k, &g.b)) != TLR_OK) return st;
-  if (!C || !aligned(C, dt == TLR_F32 ? 4 : 2)) return fail(TLR_ERR_INVALID_ARG, "row_gemm: null or misaligned C");
+  if ((st = product_args("row_gemm", dt, m, n, k, A, C, ldc, &g)) != TLR_OK || m == 0 || n == 0) return st;
+  if ((st = check_operand("row_gemm: B", B, n, k, &g.b)) != TLR_OK) return st;
   const Choice choice = choose(m, n, k, g.groups);
   const size_t need = parts_bytes(choice, m, n);
   if (need > 0 && (!ws || !aligned(ws, 16))) return fail(TLR_ERR_INVALID_ARG, "row_gemm: null or misaligned workspace");
   if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "row_gemm: workspace too small");
-  g.m = (int32_t)m;
-  g.n = (int32_t)n;
-  g.k = (int32_t)k;
-  g.c = C;
-  g.ldc = ldc;
-  g.dt = dt;
   gemm_launch(g, choice, static_cast<int *>(ws), static_cast<hipStream_t>(stream));
   return launched("row_gemm");
+}
+
+tlr_status row_linear_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes) {
+  if (!bytes) return fail(TLR_ERR_INVALID_ARG, "row_linear_workspace_bytes: null output");
+  const tlr_status st = check_sizes(m, n, k, 0);
+  if (st == TLR_OK) *bytes = linear_parts(m, n, k).bytes;
+  return st;
+}
+
+tlr_status row_linear(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const void *X, int64_t ldx, void *C,
+                      int64_t ldc, void *ws, size_t ws_bytes, void *stream) {
+  RowGemmArgs g{};
+  tlr_status st = check_sizes(m, n, k, 0);
+  if (st != TLR_OK) return st;
+  if ((st = product_args("row_linear", dt, m, n, k, A, C, ldc, &g)) != TLR_OK) return st;
+  if (ldx < std::max<int64_t>(1, k)) return fail(TLR_ERR_INVALID_ARG, "row_linear: leading dimension of X too small");
+  if (m == 0 || n == 0) return TLR_OK;
+  if (k > 0 && (!X || !aligned(X, dt == TLR_F32 ? 4 : 2))) return fail(TLR_ERR_INVALID_ARG, "row_linear: null or misaligned X");
+  const LinearParts p = linear_parts(m, n, k);
+  if (p.bytes > 0 && (!ws || !aligned(ws, 256))) return fail(TLR_ERR_INVALID_ARG, "row_linear: null or misaligned workspace");
+  if (ws_bytes < p.bytes) return fail(TLR_ERR_WORKSPACE, "row_linear: workspace too small");
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (p.few) {
+    const unsigned grid = (unsigned)cdiv(m, 16);
+    if (dt == TLR_F32) few_kernel<float><<<grid, 512, 0, hs>>>(g, X, ldx);
+    else if (dt == TLR_F16) few_kernel<_Float16><<<grid, 512, 0, hs>>>(g, X, ldx);
+    else few_kernel<__bf16><<<grid, 512, 0, hs>>>(g, X, ldx);
+    return launched("row_linear");
+  }
+  uint8_t *codes = static_cast<uint8_t *>(ws);
+  float *scales = reinterpret_cast<float *>(codes + p.scales);
+  g.b = Operand{codes, scales, p.ld, (int32_t)n};
+  const RowQuantArgs a{X, n, n, ldx, p.ld, nullptr, codes, scales, (int32_t)k};
+  if (dt == TLR_F32) row_quantize_launch<float>(a, hs);
+  else if (dt == TLR_F16) row_quantize_launch<_Float16>(a, hs);
+  else row_quantize_launch<__bf16>(a, hs);
+  gemm_launch(g, p.choice, reinterpret_cast<int *>(codes + p.parts), hs);
+  return launched("row_linear");
 }
 
 }  // namespace tlr

@@ -24,6 +24,9 @@ tlr_status row_quantize(tlr_dtype dt, int64_t rows, int64_t k, const void *X, in
 tlr_status row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_block_gemm_choice *out);
 tlr_status row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const tlr_row_matrix *B,
                     const tlr_row_groups *groups, void *C, int64_t ldc, void *ws, size_t ws_bytes, void *stream);
+tlr_status row_linear_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes);
+tlr_status row_linear(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const void *X, int64_t ldx, void *C,
+                      int64_t ldc, void *ws, size_t ws_bytes, void *stream);
 tlr_status expert_sort_workspace(int64_t tokens, int32_t topk, int32_t experts, size_t *bytes);
 tlr_status expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t experts, const void *ids, int32_t *offsets,
                        int32_t *place, int32_t *rows, void *ws, size_t ws_bytes, void *stream);

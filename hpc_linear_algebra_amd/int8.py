@@ -105,12 +105,7 @@ def linear(x: torch.Tensor, w: RowScaled) -> torch.Tensor:
     """x W^T for x (..., k) in float32, float16 or bfloat16, quantized with a scale
     for each token, and a weight of 2 dimensions; in x's type.  There is no backward
     pass: where gradients are on, an x that requires one is refused."""
-    if torch.is_grad_enabled() and x.requires_grad:
-        raise RuntimeError("int8.linear has no backward pass: call it under torch.no_grad() or on detached tensors")
-    if x.dim() < 1 or x.shape[-1] != w.k:
-        raise ValueError(f"linear: x is (..., {w.k})")
-    flat = x if x.dim() == 2 else _rows(x)
-    got = binding().row_linear(flat, w.codes, w.scales, w.k)
+    got = binding().row_linear(x, w.codes, w.scales, w.k)
     if type(got) is int:
-        T._check(got, "tlr_row_gemm")
-    return got if x.dim() == 2 else got.reshape(*x.shape[:-1], got.shape[1])
+        T._check(got, "tlr_row_linear")
+    return got

@@ -149,55 +149,15 @@ def sort(ids: torch.Tensor, experts: int) -> Order:
     return Order(*got)
 
 
-def _gather(x: torch.Tensor, place: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
-    got = binding().gather(x, place, offsets)
-    if type(got) is int:
-        T._check(got, "tlr_expert_gather")
-    return got
-
-
-def _combine(y: torch.Tensor, weights: Optional[torch.Tensor], place: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
-    got = binding().combine(y, weights, place, offsets)
-    if type(got) is int:
-        T._check(got, "tlr_expert_combine")
-    return got
-
-
-class _Gather(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, place, offsets):
-        ctx.save_for_backward(place, offsets)
-        return _gather(x, place, offsets)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dxs):
-        return _combine(dxs, None, *ctx.saved_tensors), None, None
-
-
-class _Combine(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, y, weights, place, offsets):
-        ctx.save_for_backward(y, weights, place, offsets)
-        return _combine(y, weights, place, offsets)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dout):
-        got = binding().combine_grad(dout, *ctx.saved_tensors, *ctx.needs_input_grad[:2])
-        if type(got) is int:
-            T._check(got, "tlr_expert_combine_grad")
-        return (*got, None, None)
-
-
 def gather(x: torch.Tensor, order: Order) -> torch.Tensor:
     """Each token x (tokens, hidden) at the rows of its assignments, (tokens * topk,
     hidden); rows of no expert are zeros.  The gradient of a token is the sum of its
     rows', in float, rounded once, in the order of its assignments; rows of no expert
     add nothing.  No double backward."""
-    if torch.is_grad_enabled() and x.requires_grad:
-        return _Gather.apply(x, order.place, order.offsets)
-    return _gather(x, order.place, order.offsets)
+    got = binding().gather(x, order.place, order.offsets)
+    if type(got) is int:
+        T._check(got, "tlr_expert_gather")
+    return got
 
 
 def combine(y: torch.Tensor, weights: Optional[torch.Tensor], order: Order) -> torch.Tensor:
@@ -205,11 +165,10 @@ def combine(y: torch.Tensor, weights: Optional[torch.Tensor], order: Order) -> t
     weights (tokens, topk), float32 (None: 1): (tokens, hidden) in y's type, sums in
     float in the order of the assignments.  Rows of no expert are not read.  Gradients
     of y (zeros for rows of no expert) and of the weights.  No double backward."""
-    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
-        if weights is None:
-            weights = torch.ones(order.place.shape, device=y.device)
-        return _Combine.apply(y, weights, order.place, order.offsets)
-    return _combine(y, weights, order.place, order.offsets)
+    got = binding().combine(y, weights, order.place, order.offsets)
+    if type(got) is int:
+        T._check(got, "tlr_expert_combine")
+    return got
 
 
 class Int8Experts:

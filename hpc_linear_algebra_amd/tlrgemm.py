@@ -35,6 +35,7 @@ EXPORTED = [
     "tlr_plan_profile_read", "tlr_dense_gemm", "tlr_block_quantize", "tlr_block_gemm_workspace_bytes",
     "tlr_block_gemm_plan", "tlr_block_gemm", "tlr_moe_workspace_bytes", "tlr_moe_init", "tlr_moe",
     "tlr_row_quantize", "tlr_row_gemm_workspace_bytes", "tlr_row_gemm_plan", "tlr_row_gemm",
+    "tlr_row_linear_workspace_bytes", "tlr_row_linear",
     "tlr_expert_sort_workspace_bytes", "tlr_expert_sort", "tlr_expert_gather", "tlr_expert_combine",
     "tlr_expert_combine_grad", "tlr_gated", "tlr_gated_grad",
     "tlr_status_string", "tlr_last_error", "tlr_version",
@@ -145,6 +146,9 @@ def lib():
     L.tlr_row_gemm_plan.argtypes = [c_int64, c_int64, c_int64, c_int32, POINTER(tlr_block_gemm_choice)]
     L.tlr_row_gemm.argtypes = [c_int32, c_int64, c_int64, c_int64, POINTER(tlr_row_matrix), POINTER(tlr_row_matrix),
                                POINTER(tlr_row_groups), P, c_int64, P, c_size_t, P]
+    L.tlr_row_linear_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, POINTER(c_size_t)]
+    L.tlr_row_linear.argtypes = [c_int32, c_int64, c_int64, c_int64, POINTER(tlr_row_matrix), P, c_int64, P, c_int64, P,
+                                 c_size_t, P]
     L.tlr_expert_sort_workspace_bytes.argtypes = [c_int64, c_int32, c_int32, POINTER(c_size_t)]
     L.tlr_expert_sort.argtypes = [c_int32, c_int64, c_int32, c_int32, P, P, P, P, P, c_size_t, P]
     L.tlr_expert_gather.argtypes = [c_int32, c_int64, c_int32, c_int64, P, c_int64, P, P, P, c_int64, P]
@@ -435,6 +439,19 @@ def tlr_row_gemm(dtype, m: int, n: int, k: int, A: tlr_row_matrix, B: tlr_row_ma
                             ctypes.byref(groups) if groups is not None else None, C or None, ldc, workspace or None,
                             workspace_bytes, stream or None)
     _check(st, "tlr_row_gemm")
+
+
+def tlr_row_linear_workspace_bytes(m: int, n: int, k: int) -> int:
+    out = c_size_t()
+    _check(lib().tlr_row_linear_workspace_bytes(m, n, k, ctypes.byref(out)), "tlr_row_linear_workspace_bytes")
+    return int(out.value)
+
+
+def tlr_row_linear(dtype, m: int, n: int, k: int, A: tlr_row_matrix, X: int, ldx: int, C: int, ldc: int,
+                   workspace: int = 0, workspace_bytes: int = 0, stream: int = 0):
+    st = lib().tlr_row_linear(_dt(dtype), m, n, k, ctypes.byref(A), X or None, ldx, C or None, ldc, workspace or None,
+                              workspace_bytes, stream or None)
+    _check(st, "tlr_row_linear")
 
 
 def tlr_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:

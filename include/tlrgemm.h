@@ -666,6 +666,17 @@ tlr_status tlr_row_gemm(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr
                         const tlr_row_matrix *B, const tlr_row_groups *groups, void *C, int64_t ldc,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * tlr_row_linear: the same product with B = X (n rows of k entries of type dt, X[j,c]
+ * at element j*ldx + c, any alignment of the type), quantized within the call as
+ * tlr_row_quantize does: one launch for a few tokens, two or three for more.  C has X's
+ * type.
+ *   workspace  device, 256-byte aligned, not cleared: tlr_row_linear_workspace_bytes.
+ */
+tlr_status tlr_row_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t *bytes_out);
+tlr_status tlr_row_linear(tlr_dtype dt, int64_t m, int64_t n, int64_t k, const tlr_row_matrix *A, const void *X,
+                          int64_t ldx, void *C, int64_t ldc, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- tokens sorted by expert ------------------------------------------------- */
 
 /*

@@ -188,9 +188,17 @@ def test_far_rows():
 
 def test_memory_kept_for_the_backward_pass():
     x = torch.randn(512, 2048, device="cuda").bfloat16().requires_grad_()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
     y = blocks.gated(x)
-    saved = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in y.grad_fn.saved_tensors}
-    assert sum(saved.values()) == 512 * 2048 + 512 * 2 * 8 * 4
+    assert torch.cuda.memory_allocated() - before == y.numel() * 2 + 512 * 2048 + 512 * 2 * 8 * 4
+
+
+def test_no_second_derivative():
+    x = torch.randn(4, 32, device="cuda", requires_grad=True)
+    dx, = torch.autograd.grad(blocks.gated(x).sum(), [x], create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        dx.sum().backward()
 
 
 def test_streams_and_graphs():

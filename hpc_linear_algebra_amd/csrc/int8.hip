@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t max64(uint32_t x) {
 
 // A row is read once into the registers of W waves, U vectors of 8 entries a lane
 // (U 0: too long for them, read twice).  One wave: four rows a workgroup.
-template <typename T, int W, int U> __global__ __launch_bounds__(256) void row_quantize_kernel(RowQuantArgs a) {
+template <typename T, int W, int U, bool PAST> __global__ __launch_bounds__(256) void row_quantize_kernel(RowQuantArgs a) {
   __shared__ uint32_t top[4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int STEP = W * 512;
@@ -92,7 +92,12 @@ template <typename T, int W, int U> __global__ __launch_bounds__(256) void row_q
     if constexpr (U > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (at + u * STEP < up) *reinterpret_cast<u2 *>(out + at + u * STEP) = int8_codes8(v[u], s, q);
+        if (at + u * STEP < up) {
+          u2 *to = reinterpret_cast<u2 *>(out + at + u * STEP);
+          const u2 w = int8_codes8(v[u], s, q);
+          if constexpr (PAST) __builtin_nontemporal_store(w, to);
+          else *to = w;
+        }
     } else {
       for (int c = at; c < up; c += STEP) {
         get8(x + c, k - c, v[0]);
@@ -102,13 +107,21 @@ template <typename T, int W, int U> __global__ __launch_bounds__(256) void row_q
   }
 }
 
-template <typename T> void row_quantize_launch(const RowQuantArgs &a, hipStream_t st) {
+// Results that fit into the caches are left there for their reader (8192 x 2048 past
+// them 8.4 us, through them 9.9; 32768 x 2048 28.7 and 30.0).  A few rows of up to 2048
+// entries go to a workgroup each (96: 2.6 us, a wave each 2.8).
+template <typename T, bool PAST> void row_quantize_launch(const RowQuantArgs &a, hipStream_t st) {
   const unsigned one = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 1 << 22), all = (unsigned)std::min<int64_t>(a.rows, 1 << 22);
-  if (a.k <= 512) row_quantize_kernel<T, 1, 1><<<one, 256, 0, st>>>(a);
-  else if (a.k <= 2048) row_quantize_kernel<T, 1, 4><<<one, 256, 0, st>>>(a);
-  else if (a.k <= 4096) row_quantize_kernel<T, 4, 2><<<all, 256, 0, st>>>(a);
-  else if (a.k <= 8192) row_quantize_kernel<T, 4, 4><<<all, 256, 0, st>>>(a);
-  else row_quantize_kernel<T, 4, 0><<<all, 256, 0, st>>>(a);
+  if (a.k <= 512) row_quantize_kernel<T, 1, 1, PAST><<<one, 256, 0, st>>>(a);
+  else if (a.k <= 2048 && a.rows < 512) row_quantize_kernel<T, 4, 1, false><<<all, 256, 0, st>>>(a);
+  else if (a.k <= 2048) row_quantize_kernel<T, 1, 4, PAST><<<one, 256, 0, st>>>(a);
+  else if (a.k <= 4096) row_quantize_kernel<T, 4, 2, PAST><<<all, 256, 0, st>>>(a);
+  else if (a.k <= 8192) row_quantize_kernel<T, 4, 4, PAST><<<all, 256, 0, st>>>(a);
+  else row_quantize_kernel<T, 4, 0, false><<<all, 256, 0, st>>>(a);
+}
+template <typename T> void row_quantize_launch(const RowQuantArgs &a, hipStream_t st) {
+  if (a.rows * a.k >= (int64_t)1 << 24) row_quantize_launch<T, true>(a, st);
+  else row_quantize_launch<T, false>(a, st);
 }
 
 // ---- product -----------------------------------------------------------------------------------------
@@ -380,24 +393,25 @@ template <typename T> __global__ __launch_bounds__(512, 4) void few_kernel(RowGe
   }
 }
 
-// C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16.  KG 2: two such
-// halves of waves take every other block of 128 columns and add their sums at the
-// end, which halves the barriers of a long contraction.
-//
-// Two stages of KG blocks each in LDS.  A wave goes through a stage row tile by row
-// tile; with the last one's matrix instructions under way it waits for the next
+// C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16; blocks of 128
+// columns pass through a ring of NS stages in LDS.  A wave goes through a stage row tile
+// by row tile; with the last one's matrix instructions under way it waits for the next
 // stage and reads its first fragments: one barrier a stage, and the matrix cores have
-// work on both sides of it.  The stage after that is loaded into the buffer that is
-// then used up, SPREAD pieces under each row tile's matrix instructions, or all at
-// once (SPREAD 0), which a short stage needs.
-template <bool GROUPED, int TM, int TN, int WM, int WN, int KG, int SPREAD>
-__global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(RowGemmArgs g) {
-  constexpr int T = 64 * WM * WN * KG, RI = TM / WM / 16, CJ = TN / WN / 16;
-  static_assert(RI % 2 == 0, "");
-  constexpr int AT_B = TM * QB, BLOCK = (TM + TN) * QB, STAGE = KG * BLOCK;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+// work on both sides of it.  The buffer that is then used up takes the stage NS further
+// on, at once (SPREAD 0), or, with two stages, SPREAD pieces under each row tile's matrix
+// instructions, which a long stage likes better (8192^3 in 256 x 256 tiles 427 us, at
+// once 437).  A short stage is computed faster than its loads arrive: with three of them
+// 2000 x 1000 x 8000 in 128 x 64 tiles takes 27.6 us, with two 42, with four 27.7;
+// 2501 x 1111 x 1747 in 128 x 128 on eight waves 13.6, 15.0, 13.8.  128 x 128 on four
+// waves keep two, so that two workgroups fit a CU: 2048 x 4096 x 2048 22, with three 34.
+template <bool GROUPED, int TM, int TN, int WM, int WN, int NS, int SPREAD>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(RowGemmArgs g) {
+  constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
+  static_assert(RI % 2 == 0 && (SPREAD == 0 || NS == 2), "");
+  constexpr int AT_B = TM * QB, STAGE = (TM + TN) * QB;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, q = lane >> 4, kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
+  const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
 
   // tile of this workgroup: workgroups go to the 8 XCDs in turn; each XCD takes
   // a contiguous part of the tiles, which run down 8 row tiles at a time
@@ -425,14 +439,15 @@ __global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_
   Panel<TN, T, false> pb;
   pa.init(g.a, m0, g.k, tid);
   pb.init(g.b, n0, g.k, tid);
-  // The stage of blocks kb, kb + 1, .., in LOADS pieces.
-  constexpr int NA = Panel<TM, T, true>::N, PIECES = NA + Panel<TN, T, false>::N, LOADS = KG * PIECES;
+  // The stage of block kb, in LOADS pieces.
+  constexpr int NA = Panel<TM, T, true>::N, LOADS = NA + Panel<TN, T, false>::N;
   auto load = [&](int piece, int kb, uint32_t to) {
-    kb += piece / PIECES;
-    to += piece / PIECES * BLOCK;
-    piece %= PIECES;
     if (piece < NA) pa.load(piece, kb, to, wave);
     else pb.load(piece - NA, kb, to + AT_B, wave);
+  };
+  auto load_all = [&](int kb, uint32_t to) {
+#pragma unroll
+    for (int c = 0; c < LOADS; ++c) load(c, kb, to);
   };
 
   i4 acc[RI][CJ];
@@ -459,52 +474,45 @@ __global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_
       b[j][1] = *reinterpret_cast<const i4 *>(l + (bat ^ 64) + 16 * QB * j);
     }
   };
-  auto meet = [&]() {
+  // All waves, once this one has at most LEFT loads under way and no LDS access.
+  auto meet = [&](auto left) {
+    constexpr int LEFT = decltype(left)::value;
+    static_assert(LEFT < 64, "");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT >> 4) << 14 | 7 << 4);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  constexpr std::integral_constant<int, 0> ALL{};
 
-  // This workgroup's blocks: all, or the part of grid y.  Stage 0 is its last one to
-  // KG, the very last of which may be cut at column k; stage i > 0 is the KG from
-  // kb0 + (i - 1) KG on.
+  // This workgroup's blocks: all, or the part of grid y.  Stage 0 is its last one, which
+  // may be cut at column k; stage i > 0 is block kb0 + i - 1.
   const int blocks = zero ? 0 : (g.k + QB - 1) / QB;
   const int kb0 = (int)((int64_t)blocks * blockIdx.y / gridDim.y);
-  const int mine = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
-  if (mine > 0) {
-    const int nb = (mine + KG - 1) / KG, last = mine - (nb - 1) * KG;      // stages; blocks of stage 0
-    const bool cut = (g.k & (QB - 1)) != 0 && kb0 + mine == blocks;
+  const int nb = (int)((int64_t)blocks * (blockIdx.y + 1) / gridDim.y) - kb0;
+  if (nb > 0) {
     const uint32_t base = lds_address(lds);
+    pa.load_last(kb0 + nb - 1, base, wave, true);
+    pb.load_last(kb0 + nb - 1, base + AT_B, wave, true);
+    if (SPREAD == 0 && nb >= NS) {
 #pragma unroll
-    for (int c = 0; c < KG; ++c) {
-      const int kb = c < last ? kb0 + mine - last + c : 0;
-      pa.load_last(kb, base + c * BLOCK, wave, c < last);
-      pb.load_last(kb, base + c * BLOCK + AT_B, wave, c < last);
-    }
-    auto load_all = [&](int kb, uint32_t to) {
-#pragma unroll
-      for (int c = 0; c < LOADS; ++c) load(c, kb, to);
-    };
-    if (SPREAD == 0 && nb > 1) {
-      load_all(kb0, base + STAGE);
-      static_assert(LOADS < 16, "");
-      __builtin_amdgcn_s_waitcnt(LOADS | 0xf << 8 | 7 << 4);     // stage 1 is still under way
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+      for (int s = 1; s < NS; ++s) load_all(kb0 + s - 1, base + s * STAGE);
+      meet(std::integral_constant<int, (NS - 1) * LOADS>{});
     } else {
-      meet();
+      if (SPREAD == 0)
+        for (int s = 1; s < nb; ++s) load_all(kb0 + s - 1, base + s * STAGE);
+      meet(ALL);
     }
-    if (cut) {                // zeros in one operand are enough: integers have no NaN
-      pb.cut(g.k & (QB - 1), lds + (last - 1) * BLOCK + AT_B, tid);
+    if ((g.k & (QB - 1)) != 0 && kb0 + nb == blocks) {      // zeros in one operand are enough: integers have no NaN
+      pb.cut(g.k & (QB - 1), lds + AT_B, tid);
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);      // LDS only
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
-    read_b(lds + kg * BLOCK);
-    read_a(lds + kg * BLOCK, 0);
-    // All products of a stage, that of block kb loaded meanwhile.
+    read_b(lds);
+    read_a(lds, 0);
+    // All products of a stage, with SPREAD that of block kb loaded meanwhile.
     auto row_tiles = [&](const uint8_t *l, auto live, int kb, uint32_t to) {
       static_assert(SPREAD == 0 || SPREAD * RI >= LOADS, "");
 #pragma unroll
@@ -523,32 +531,17 @@ __global__ __launch_bounds__(64 * WM * WN * KG) __attribute__((amdgpu_waves_per_
     };
     int now = 0, next = STAGE;
     for (int stage = 0; stage < nb - 1; ++stage) {
-      row_tiles(lds + now + kg * BLOCK, std::true_type{}, kb0 + stage * KG, base + next);
-      meet();
-      if (SPREAD == 0 && stage + 2 < nb) load_all(kb0 + (stage + 1) * KG, base + now);
-      read_b(lds + next + kg * BLOCK);
-      read_a(lds + next + kg * BLOCK, 0);
-      const int t = now;
+      row_tiles(lds + now, std::true_type{}, kb0 + stage, base + next);
+      // stages under way: up to stage + NS - 1, of which the next one is needed
+      if (NS > 2 && stage + NS <= nb) meet(std::integral_constant<int, (NS - 2) * LOADS>{});
+      else meet(ALL);
+      if (SPREAD == 0 && stage + NS < nb) load_all(kb0 + stage + NS - 1, base + now);
+      read_b(lds + next);
+      read_a(lds + next, 0);
       now = next;
-      next = t;
+      next = next == (NS - 1) * STAGE ? 0 : next + STAGE;
     }
-    row_tiles(lds + now + kg * BLOCK, std::false_type{}, 0, 0);
-  }
-  if constexpr (KG == 2) {                // the second half's sums to the first half
-    static_assert(WM * WN * RI * CJ * 1024 <= 2 * STAGE, "");
-    i4 *sums = reinterpret_cast<i4 *>(lds) + (wave % (WM * WN)) * RI * CJ * 64 + lane;
-    __syncthreads();
-    if (kg == 1)
-#pragma unroll
-      for (int i = 0; i < RI; ++i)
-#pragma unroll
-        for (int j = 0; j < CJ; ++j) sums[(i * CJ + j) * 64] = acc[i][j];
-    __syncthreads();
-    if (kg == 1) return;
-#pragma unroll
-    for (int i = 0; i < RI; ++i)
-#pragma unroll
-      for (int j = 0; j < CJ; ++j) acc[i][j] += sums[(i * CJ + j) * 64];
+    row_tiles(lds + now, std::false_type{}, 0, 0);
   }
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
@@ -621,13 +614,11 @@ template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(RowGemm
 
 // ---- which kernel ------------------------------------------------------------------------------------
 
-enum Kind { STRIP, TILE_64, TILE_64K, TILE_128, TILE_128W, TILE_128K, TILE_256 };
+enum Kind { STRIP, TILE_64, TILE_128, TILE_128W, TILE_256 };
 struct Shape {
   int rows, cols, threads;  // of C and of the workgroup that computes them
-  int halves;               // of its waves, which share the blocks of the contraction
 };
-constexpr Shape SHAPE[] = {{16, 16, 512, 1},   {128, 64, 512, 1},  {128, 64, 512, 2}, {128, 128, 256, 1},
-                           {128, 128, 512, 1}, {128, 128, 512, 2}, {256, 256, 512, 1}};
+constexpr Shape SHAPE[] = {{16, 16, 512}, {128, 64, 512}, {128, 128, 256}, {128, 128, 512}, {256, 256, 512}};
 struct Choice {
   Kind kind;
   int parts;                // of the contraction, with a launch that adds them if more than one
@@ -655,16 +646,17 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 
 // The kernel with the least estimated time (us).  The estimates are fits to measured
 // times (graph replays, 16-bit C) of every kernel at 36 products and 14 of groups; the
-// choice costs 1.2% against the best of them, 19% at most.  Some of them, the kernel
+// choice costs 0.5% against the best of them, 18% at most.  Some of them, the kernel
 // chosen first:
-//   4608 x 37 x 2568     strip 8.6, 128 x 64 tiles in four parts 9.3, 128 x 128 14
-//   8192 x 33 x 8192     128 x 64 in two halves and four parts 17.7, strip 41
-//   2501 x 1111 x 1747   128 x 128 on eight waves 15.3, on four 16.4, 128 x 64 22
-//   2000 x 1000 x 8000   128 x 64 in two halves 33, 128 x 128 in two halves 44
-//   2048 x 4096 x 2048   128 x 128 on four waves 22.5, on eight 27
+//   4608 x 37 x 2568     strip 8.6, 128 x 64 tiles in two parts 9.5, 128 x 128 14
+//   8192 x 33 x 8192     128 x 64 in four parts 17, strip 41
+//   2501 x 1111 x 1747   128 x 128 on eight waves 13.6, on four 16.4, 128 x 64 18
+//   2000 x 1000 x 8000   128 x 64 28, 128 x 128 on eight waves 35
+//   2048 x 4096 x 2048   128 x 128 on four waves 22, on eight 25
 //   4096 x 4096 x 4096   256 x 256 62, 128 x 128 on four waves 77
-//   64 groups, 28672 rows, 2816 x 2048   256 x 256 265, 128 x 128 303
-//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 21, strip 32
+//   64 groups, 28672 rows, 2816 x 2048   256 x 256 260, 128 x 128 282
+//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 21, 128 x 64 23, strip 32
+//   64 groups, 40 rows, 1024 x 4096      128 x 64 19, 128 x 128 on four waves 25
 Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
   const double nb = (double)std::max<int64_t>(1, cdiv(k, QB));
   // Groups that have rows, where each row falls into one of them; the weights they
@@ -683,25 +675,24 @@ Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
     }
   };
   // 2 KB of A a workgroup and block, and as many rows of B as there are up to 16
-  offer(STRIP, 1, 3.6, 2.4 + cdiv(m, 16) * pieces(16) * nb * (1.8e-4 + 1e-5 * std::min(16.0, n / reached)) + 0.05 * nb);
-  // One workgroup a CU takes `one` a block, `pair` of them together `two`.
-  auto tiles = [&](Kind kind, int tn, int pair, double rate, double one, double two, double first, double next) {
+  offer(STRIP, 1, 3.6, 2.4 + cdiv(m, 16) * pieces(16) * nb * (1.8e-4 + 1.1e-5 * std::min(16.0, n / reached)) + 0.05 * nb);
+  // One workgroup a CU takes `one` a block, `pair` of them together `two`.  Four waves a
+  // CU keep too few loads under way for weights out of HBM.
+  auto tiles = [&](Kind kind, int pair, double rate, double one, double two, double first, double next) {
     for (const int parts : {1, 2, 4, 8}) {
       if (parts > 1 && (nb < 4 * parts || groups)) break;
-      const double t = (double)cdiv(m, SHAPE[kind].rows) * pieces(tn) * parts;
+      const double t = (double)cdiv(m, SHAPE[kind].rows) * pieces(SHAPE[kind].cols) * parts;
       const double rounds = std::ceil(t / (256 * pair)), rest = t - 256 * pair * (rounds - 1);
       double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
       if (parts > 1) us += 2.8 + parts * (0.1 + (double)m * (double)n * 2.1e-6);
-      offer(kind, parts, rate, us);
+      offer(kind, parts, kind == TILE_128 && t < 384 ? 4.4 : rate, us);
       if (kind == TILE_256) break;
     }
   };
-  tiles(TILE_64, 64, 2, 4.3, 0.475, 1.265, 2.6, 3.0);
-  tiles(TILE_128W, 128, 2, 4.0, 0.6, 1.38, 3.9, 7.2);
-  tiles(TILE_128, 128, 2, 5.6, 0.645, 1.0, 4.3, 8.5);
-  tiles(TILE_64K, 64, 2, 4.8, 0.39, 1.02, 3.85, 4.7);
-  tiles(TILE_128K, 128, 1, 4.4, 0.53, 0.53, 5.5, 6.0);
-  tiles(TILE_256, 256, 1, 4.6, 1.46, 1.46, 10.6, 14.0);
+  tiles(TILE_64, 2, 5.0, 0.31, 0.875, 3.8, 4.6);
+  tiles(TILE_128W, 1, 4.8, 0.51, 0.575, 4.2, 4.5);
+  tiles(TILE_128, 2, 5.6, 0.635, 0.95, 4.3, 8.5);
+  tiles(TILE_256, 1, 4.6, 1.45, 1.45, 10.5, 13.4);
   return best;
 }
 
@@ -793,15 +784,15 @@ LinearParts linear_parts(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-template <Kind KIND, int WM, int WN, int SPREAD> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
-  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, KG = SHAPE[KIND].halves, T = 64 * WM * WN * KG;
+template <Kind KIND, int WM, int WN, int NS, int SPREAD> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
+  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, T = 64 * WM * WN;
   static_assert(SHAPE[KIND].threads == T, "");
   const dim3 grid((unsigned)workgroups(KIND, g.m, g.n, g.groups), (unsigned)parts);
-  if (g.groups) return tile_kernel<true, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(g);
-  if (parts == 1) return tile_kernel<false, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(g);
+  if (g.groups) return tile_kernel<true, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(g);
+  if (parts == 1) return tile_kernel<false, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(g);
   RowGemmArgs h = g;
   h.c = ws;
-  tile_kernel<false, TM, TN, WM, WN, KG, SPREAD><<<grid, T, 0, st>>>(h);
+  tile_kernel<false, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(h);
   const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
   if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
   else if (parts == 4) parts_kernel<4><<<sum, 256, 0, st>>>(g, ws);
@@ -816,12 +807,10 @@ void gemm_launch(const RowGemmArgs &g, const Choice &c, int *ws, hipStream_t st)
       else strip_kernel<false><<<grid, 512, 0, st>>>(g);
       return;
     }
-    case TILE_64: return tile_launch<TILE_64, 4, 2, 0>(g, c.parts, ws, st);
-    case TILE_64K: return tile_launch<TILE_64K, 2, 2, 0>(g, c.parts, ws, st);
-    case TILE_128: return tile_launch<TILE_128, 2, 2, 0>(g, c.parts, ws, st);
-    case TILE_128W: return tile_launch<TILE_128W, 2, 4, 0>(g, c.parts, ws, st);
-    case TILE_128K: return tile_launch<TILE_128K, 2, 2, 0>(g, c.parts, ws, st);
-    case TILE_256: return tile_launch<TILE_256, 2, 4, 2>(g, c.parts, ws, st);
+    case TILE_64: return tile_launch<TILE_64, 4, 2, 3, 0>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<TILE_128, 2, 2, 2, 0>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<TILE_128W, 2, 4, 3, 0>(g, c.parts, ws, st);
+    case TILE_256: return tile_launch<TILE_256, 2, 4, 2, 2>(g, c.parts, ws, st);
   }
 }
 
@@ -857,7 +846,7 @@ tlr_status row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_bl
   const Choice c = choose(m, n, k, groups);
   const Shape &s = SHAPE[c.kind];
   const int64_t y = c.kind == STRIP ? most_pieces(STRIP, n, groups) : 1;
-  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, s.halves, c.parts, 0, workgroups(c.kind, m, n, groups), y, parts_bytes(c, m, n)};
+  *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, 1, c.parts, 0, workgroups(c.kind, m, n, groups), y, parts_bytes(c, m, n)};
   return TLR_OK;
 }
 

@@ -28,13 +28,13 @@ namespace {
 // ---- sort --------------------------------------------------------------------------------------------
 
 constexpr int MOST_EXPERTS = 1024, MOST_TOPK = 64;
-constexpr int PART = 4096;        // assignments of a workgroup, where there are several
 
 struct SortArgs {
   const void *ids;
   int32_t *offsets, *place, *rows;
-  int32_t *counts;          // (parts, experts + 1), where there are several parts
+  int32_t *counts;          // (parts, experts + 1), and a row of totals behind them
   int32_t n, topk, experts, parts;
+  int32_t scanned;          // counts: of the parts before, and the totals
 };
 
 // The expert of an assignment; `experts` for none.
@@ -43,29 +43,66 @@ template <typename ID> __device__ __forceinline__ int expert_of(const SortArgs &
   return e >= 0 && e < (ID)a.experts ? (int)e : a.experts;
 }
 
-// How many assignments of its part each expert has.
-template <typename ID> __global__ __launch_bounds__(1024) void count_kernel(SortArgs a) {
+// The lanes whose e (-1: none) is this lane's, by one ballot for each bit.
+__device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
+  uint64_t same = __ballot(e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (e >> b) & 1;
+    const uint64_t m = __ballot(on);
+    same &= on ? m : ~m;
+  }
+  return same;
+}
+
+// How many assignments of its part each expert has: the first lane of an expert adds
+// for the others.
+template <typename ID, int EACH> __global__ __launch_bounds__(1024) void count_kernel(SortArgs a) {
   __shared__ int32_t hist[MOST_EXPERTS + 1];
-  int e[PART / 1024];
+  const int lane = threadIdx.x & 63, bits = 32 - __builtin_clz(a.experts);
+  int e[EACH];
 #pragma unroll
-  for (int c = 0; c < PART / 1024; ++c) {
-    const int64_t i = (int64_t)blockIdx.x * PART + c * 1024 + threadIdx.x;
+  for (int c = 0; c < EACH; ++c) {
+    const int64_t i = ((int64_t)blockIdx.x * EACH + c) * 1024 + threadIdx.x;
     e[c] = i < a.n ? expert_of<ID>(a, (int)i) : -1;
   }
   for (int x = threadIdx.x; x <= a.experts; x += 1024) hist[x] = 0;
   __syncthreads();
 #pragma unroll
-  for (int c = 0; c < PART / 1024; ++c)
-    if (e[c] >= 0) atomicAdd(&hist[e[c]], 1);
+  for (int c = 0; c < EACH; ++c) {
+    const uint64_t same = same_lanes(e[c], bits);
+    if (e[c] >= 0 && (same & ((1ull << lane) - 1)) == 0) atomicAdd(&hist[e[c]], __builtin_popcountll(same));
+  }
   __syncthreads();
   for (int x = threadIdx.x; x <= a.experts; x += 1024) a.counts[(int64_t)blockIdx.x * (a.experts + 1) + x] = hist[x];
 }
 
+// Counts of many parts to those of the parts before each, and the totals: a workgroup
+// takes 64 experts, a wave every sixteenth of the parts.
+__global__ __launch_bounds__(1024) void scan_kernel(SortArgs a) {
+  __shared__ int32_t sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, x = blockIdx.x * 64 + lane, row = a.experts + 1;
+  const int each = (a.parts + 15) / 16, from = min(wave * each, a.parts), to = min(from + each, a.parts);
+  int sum = 0;
+  if (x < row)
+#pragma unroll 8
+    for (int p = from; p < to; ++p) sum += a.counts[(int64_t)p * row + x];
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (x >= row) return;
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += sums[w][lane];
+  for (int p = from; p < to; ++p) {
+    const int v = a.counts[(int64_t)p * row + x];
+    a.counts[(int64_t)p * row + x] = before;
+    before += v;
+  }
+  if (wave == 15) a.counts[(int64_t)a.parts * row + x] = before;
+}
+
 // Rows of a part's assignments, EACH for each of W waves' threads.  A wave takes 64
-// consecutive ones at a time: which lanes share an expert follows from one ballot for
-// each bit of its number, and a lane's rank is the number of such lanes before it,
-// added to the wave's count so far.  Ranks, counts of the waves before, counts of the
-// parts before and the experts' first rows add up to the row.
+// consecutive ones at a time: a lane's rank is the number of lanes before it with its
+// expert, added to the wave's count so far.  Ranks, counts of the waves before, counts
+// of the parts before and the experts' first rows add up to the row.
 template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) void sort_kernel(SortArgs a) {
   constexpr int MOST = W == 16 ? MOST_EXPERTS : 64 * W;
   __shared__ int32_t hist[W][MOST + 1];
@@ -79,12 +116,7 @@ template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) voi
   const int bits = 32 - __builtin_clz(a.experts);
 #pragma unroll
   for (int c = 0; c < EACH; ++c) {
-    uint64_t same = __ballot(e[c] >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const bool on = (e[c] >> b) & 1;
-      const uint64_t m = __ballot(on);
-      same &= on ? m : ~m;
-    }
+    const uint64_t same = same_lanes(e[c], bits);
     const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
     asm volatile("" ::: "memory");        // the wave's LDS accesses stay in this order
     if (e[c] >= 0) {
@@ -106,18 +138,23 @@ template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) voi
       hist[w][x] = part;
       part += v;
     }
+    const int32_t *counts = a.counts + x;
+    const int64_t row = a.experts + 1;
     if (a.parts == 1) {
       all = part;
-      return;
-    }
-    for (int p0 = 0; p0 < a.parts; p0 += 16) {        // 16 loads in flight
-      int v[16];
+    } else if (a.scanned) {
+      before = counts[blockIdx.x * row];
+      all = counts[a.parts * row];
+    } else {
+      for (int p0 = 0; p0 < a.parts; p0 += 16) {        // 16 loads in flight
+        int v[16];
 #pragma unroll
-      for (int p = 0; p < 16; ++p) v[p] = a.counts[(int64_t)min(p0 + p, a.parts - 1) * (a.experts + 1) + x];
+        for (int p = 0; p < 16; ++p) v[p] = counts[min(p0 + p, a.parts - 1) * row];
 #pragma unroll
-      for (int p = 0; p < 16; ++p) {
-        before += p0 + p < (int)blockIdx.x ? v[p] : 0;
-        all += p0 + p < a.parts ? v[p] : 0;
+        for (int p = 0; p < 16; ++p) {
+          before += p0 + p < (int)blockIdx.x ? v[p] : 0;
+          all += p0 + p < a.parts ? v[p] : 0;
+        }
       }
     }
   };
@@ -159,18 +196,23 @@ template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) voi
     }
 }
 
-// Up to 8192 assignments are sorted by one workgroup, as few waves as hold them.
-constexpr int64_t ONE = 8192;
-int64_t parts_of(int64_t n) { return n <= ONE ? 1 : (n + PART - 1) / PART; }
+// One workgroup sorts up to ONE assignments; more go in parts of 1024 or, from FINE on, of
+// 4096, and beyond SUMMED parts their counts are summed by a launch of its own.
+constexpr int64_t ONE = 4096, FINE = 65536, SUMMED = 64;
+int64_t part_of(int64_t n) { return n <= FINE ? 1024 : 4096; }
+int64_t parts_of(int64_t n) { return n <= ONE ? 1 : (n + part_of(n) - 1) / part_of(n); }
 
 template <typename ID> void sort_launch(const SortArgs &a, hipStream_t st) {
   if (a.parts > 1) {
-    count_kernel<ID><<<a.parts, 1024, 0, st>>>(a);
-    sort_kernel<ID, 16, 4><<<a.parts, 1024, 0, st>>>(a);
+    const bool fine = a.n <= FINE;
+    if (fine) count_kernel<ID, 1><<<a.parts, 1024, 0, st>>>(a);
+    else count_kernel<ID, 4><<<a.parts, 1024, 0, st>>>(a);
+    if (a.scanned) scan_kernel<<<a.experts / 64 + 1, 1024, 0, st>>>(a);
+    if (fine) sort_kernel<ID, 16, 1><<<a.parts, 1024, 0, st>>>(a);
+    else sort_kernel<ID, 16, 4><<<a.parts, 1024, 0, st>>>(a);
   } else if (a.n <= 256 && a.experts <= 256) sort_kernel<ID, 4, 1><<<1, 256, 0, st>>>(a);
   else if (a.n <= 1024 && a.experts <= 256) sort_kernel<ID, 4, 4><<<1, 256, 0, st>>>(a);
-  else if (a.n <= 4096) sort_kernel<ID, 16, 4><<<1, 1024, 0, st>>>(a);
-  else sort_kernel<ID, 16, 8><<<1, 1024, 0, st>>>(a);
+  else sort_kernel<ID, 16, 4><<<1, 1024, 0, st>>>(a);
 }
 
 // ---- rows --------------------------------------------------------------------------------------------
@@ -413,7 +455,7 @@ tlr_status expert_sort_workspace(int64_t tokens, int32_t topk, int32_t experts, 
   if (st != TLR_OK) return st;
   if (experts < 1 || experts > MOST_EXPERTS) return fail(TLR_ERR_INVALID_ARG, "expert_sort_workspace_bytes: experts are 1 .. 1024");
   const int64_t parts = parts_of(tokens * topk);
-  *bytes = parts > 1 ? sizeof(int32_t) * (size_t)parts * (experts + 1) : 0;
+  *bytes = parts > 1 ? sizeof(int32_t) * (size_t)(parts + 1) * (experts + 1) : 0;
   return TLR_OK;
 }
 
@@ -429,7 +471,7 @@ tlr_status expert_sort(int32_t id_bytes, int64_t tokens, int32_t topk, int32_t e
     return fail(TLR_ERR_INVALID_ARG, "expert_sort: null or misaligned ids, place or rows");
   if (need > 0 && (!ws || !aligned(ws, 4))) return fail(TLR_ERR_INVALID_ARG, "expert_sort: null or misaligned workspace");
   if (ws_bytes < need) return fail(TLR_ERR_WORKSPACE, "expert_sort: workspace too small");
-  const SortArgs a{ids, offsets, place, rows, static_cast<int32_t *>(ws), (int32_t)n, topk, experts, (int32_t)parts_of(n)};
+  const SortArgs a{ids, offsets, place, rows, static_cast<int32_t *>(ws), (int32_t)n, topk, experts, (int32_t)parts_of(n), parts_of(n) > SUMMED};
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (id_bytes == 4) sort_launch<int32_t>(a, hs);
   else sort_launch<int64_t>(a, hs);

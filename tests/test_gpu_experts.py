@@ -47,7 +47,7 @@ def choose(g, tokens, topk, experts, dropped):
 
 
 SORTS = [(0, 1, 1), (1, 1, 1), (1, 8, 64), (1, 64, 1024), (5, 3, 2), (63, 1, 7), (64, 1, 8), (65, 2, 9), (300, 4, 31), (512, 8, 64),
-         (513, 8, 65), (1000, 6, 1000), (700, 6, 1024), (2049, 8, 128), (9000, 8, 3), (5000, 7, 1024), (40000, 8, 257)]
+         (513, 8, 65), (1000, 6, 1000), (700, 6, 1024), (2049, 8, 128), (9000, 8, 3), (5000, 7, 1024), (40000, 8, 257), (65536, 1, 64), (65537, 1, 64), (8193, 8, 1000), (33000, 8, 64)]
 
 
 @pytest.mark.parametrize("dropped", [False, True])

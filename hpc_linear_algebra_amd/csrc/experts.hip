@@ -192,7 +192,8 @@ template <typename ID, int W, int EACH> __global__ __launch_bounds__(64 * W) voi
     if (e[c] >= 0) {
       const int i = (int)(first + 64 * c), p = hist[wave][e[c]] + rank[c];
       a.place[i] = p;
-      a.rows[p] = e[c] < a.experts ? i / a.topk : -1;
+      // always in range, unless ids were written between the launches
+      if ((uint32_t)p < (uint32_t)a.n) a.rows[p] = e[c] < a.experts ? i / a.topk : -1;
     }
 }
 

@@ -185,8 +185,11 @@ template <int TN> __device__ __forceinline__ Rows find_piece(const RowGemmArgs &
     const uint64_t past = __ballot(at < upto);
     if (past) {
       const int l = __builtin_ctzll(past);
-      const int start = __builtin_amdgcn_readlane(upto - mine, l);
-      return Rows{__builtin_amdgcn_readlane(lo, l) + (at - start) * TN, __builtin_amdgcn_readlane(hi, l), e0 + l};
+      const int start = __builtin_amdgcn_readlane(upto - mine, l), from = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
+      const int first = from + (at - start) * TN;
+      // always so, unless groups that overlap have more pieces than an int counts
+      if (first >= from && first < end) return Rows{first, end, e0 + l};
+      return Rows{0, 0, -1};
     }
     before = __builtin_amdgcn_readlane(upto, 63);
   }
@@ -424,6 +427,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     const int width = 8 * tn, band = t / width, h = min(8, tm - 8 * band), in = t - band * width;
     mt = 8 * band + in % h;
     nt = in / h;
+    if (GROUPED && (mt < 0 || mt >= tm)) return;      // as in find_piece
   }
   const int m0 = mt * TM;
   int n0 = nt * TN;

@@ -566,25 +566,62 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
       }
     return;
   }
+  // C goes through LDS, a column's TM entries in a row, 16-byte pieces XOR-placed, so
+  // that whole stretches of its columns are stored, past the caches: 64 groups, 28672
+  // rows, 2816 x 2048 in 256 x 256 tiles 251 us, through the caches 257, straight from the
+  // registers, 64 bytes of a column at a time, 265; 2501 x 1111 x 1747 in 128 x 128 on
+  // four waves 12.8, 13.2 and 15.7.
+  auto store = [&](auto element) {
+    typedef decltype(element) E;
+    constexpr int WIDE = sizeof(E) / 2, PIECES = WIDE * TM / 8;       // pieces of 8 entries; of a column
+    constexpr int PASSES = (int)sizeof(E) * TM * TN > NS * STAGE ? 2 : 1, JS = CJ / PASSES, COLS = T / PIECES;
+    static_assert((int)sizeof(E) * TM * TN <= PASSES * NS * STAGE && CJ % PASSES == 0, "");
 #pragma unroll
-  for (int h = 0; h < RI / 2; ++h) {
-    const int row = row0 + 32 * h + 8 * q;
-    if (row < g.m) {
-      float sa[8];
-      get8(g.a.scales + row, g.m - row, sa);
+    for (int pass = 0; pass < PASSES; ++pass) {
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < CJ; ++j) {
-        const int col = col0 + 16 * j + r;
-        if (col < g.n) {
-          const float sb = g.b.scales[col];
-          float v[8];
+      for (int h = 0; h < RI / 2; ++h) {
+        const int row = wm * (TM / WM) + 32 * h + 8 * q;
+        float sa[8];
+        get8(g.a.scales + m0 + row, g.m - m0 - row, sa);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e];
-          store8(g, row, col, v);
+        for (int jj = 0; jj < JS; ++jj) {
+          const int at = 16 * (wn * JS + jj) + r, j = pass * JS + jj;      // column in LDS
+          const float sb = g.b.scales[min(col0 + 16 * j + r, g.n - 1)];
+          E v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (E)(zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e]);
+          u4 w[WIDE];
+          __builtin_memcpy(w, v, sizeof v);
+#pragma unroll
+          for (int p = 0; p < WIDE; ++p) *reinterpret_cast<u4 *>(lds + at * 16 * PIECES + 16 * ((WIDE * (row >> 3) + p) ^ (at & 15))) = w[p];
+        }
+      }
+      __syncthreads();
+      constexpr int N = 8 / WIDE;                   // entries of a piece
+      const int piece = tid % PIECES, row = m0 + N * piece;
+#pragma unroll 4
+      for (int at = tid / PIECES; at < TN / PASSES; at += COLS) {
+        const int col = n0 + at / (16 * JS) * (TN / WN) + 16 * JS * pass + at % (16 * JS);
+        if (col < g.n && row < g.m) {
+          const u4 w = *reinterpret_cast<const u4 *>(lds + at * 16 * PIECES + 16 * (piece ^ (at & 15)));
+          E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
+          if (row + N <= g.m) {
+            put16<true>(to, w);
+          } else {
+            E v[N];
+            __builtin_memcpy(v, &w, 16);
+#pragma unroll
+            for (int e = 0; e < N - 1; ++e)
+              if (row + e < g.m) to[e] = v[e];
+          }
         }
       }
     }
-  }
+  };
+  if (g.dt == TLR_F32) store(float{});
+  else if (g.dt == TLR_F16) store((_Float16)0.0f);
+  else store((__bf16)0.0f);
 }
 
 // C from PARTS m x n matrices of sums: a thread takes 8 consecutive rows of a column.
@@ -650,17 +687,17 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 
 // The kernel with the least estimated time (us).  The estimates are fits to measured
 // times (graph replays, 16-bit C) of every kernel at 36 products and 14 of groups; the
-// choice costs 0.5% against the best of them, 18% at most.  Some of them, the kernel
+// choice costs 0.6% against the best of them, 22% at most.  Some of them, the kernel
 // chosen first:
-//   4608 x 37 x 2568     strip 8.6, 128 x 64 tiles in two parts 9.5, 128 x 128 14
+//   4608 x 37 x 2568     strip 8.5, 128 x 64 tiles 9.8, in four parts 9.1, 128 x 128 13
 //   8192 x 33 x 8192     128 x 64 in four parts 17, strip 41
-//   2501 x 1111 x 1747   128 x 128 on eight waves 13.6, on four 16.4, 128 x 64 18
-//   2000 x 1000 x 8000   128 x 64 28, 128 x 128 on eight waves 35
-//   2048 x 4096 x 2048   128 x 128 on four waves 22, on eight 25
-//   4096 x 4096 x 4096   256 x 256 62, 128 x 128 on four waves 77
-//   64 groups, 28672 rows, 2816 x 2048   256 x 256 260, 128 x 128 282
-//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 21, 128 x 64 23, strip 32
-//   64 groups, 40 rows, 1024 x 4096      128 x 64 19, 128 x 128 on four waves 25
+//   2501 x 1111 x 1747   128 x 128 on eight waves 12.0, on four 12.8, 128 x 64 16
+//   2000 x 1000 x 8000   128 x 64 28, 128 x 128 on eight waves 34
+//   2048 x 4096 x 2048   128 x 128 on four waves 19, on eight 24
+//   4096 x 4096 x 4096   256 x 256 57, 128 x 128 on four waves 64
+//   64 groups, 28672 rows, 2816 x 2048   256 x 256 244, 128 x 128 262
+//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 23, 128 x 64 24, strip 31
+//   64 groups, 40 rows, 1024 x 4096      128 x 64 20, 128 x 128 on four waves 26
 Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
   const double nb = (double)std::max<int64_t>(1, cdiv(k, QB));
   // Groups that have rows, where each row falls into one of them; the weights they
@@ -690,13 +727,13 @@ Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
       double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
       if (parts > 1) us += 2.8 + parts * (0.1 + (double)m * (double)n * 2.1e-6);
       offer(kind, parts, kind == TILE_128 && t < 384 ? 4.4 : rate, us);
-      if (kind == TILE_256) break;
+      if (kind == TILE_256 || (kind == TILE_128 && parts == 2)) break;
     }
   };
-  tiles(TILE_64, 2, 5.0, 0.31, 0.875, 3.8, 4.6);
-  tiles(TILE_128W, 1, 4.8, 0.51, 0.575, 4.2, 4.5);
-  tiles(TILE_128, 2, 5.6, 0.635, 0.95, 4.3, 8.5);
-  tiles(TILE_256, 1, 4.6, 1.45, 1.45, 10.5, 13.4);
+  tiles(TILE_64, 2, 5.0, 0.313, 0.866, 3.6, 4.5);
+  tiles(TILE_128W, 1, 4.8, 0.503, 0.61, 3.9, 4.1);
+  tiles(TILE_128, 2, 5.6, 0.627, 0.95, 3.5, 8.0);
+  tiles(TILE_256, 1, 4.6, 1.45, 1.45, 7.3, 11.4);
   return best;
 }
 

@@ -151,15 +151,6 @@ struct Rows {
   int group;                // -1: nothing to do; `groups`: zeros
 };
 
-// The `at`-th piece of TN rows, counted through the groups; `total` pieces there are.
-// Offsets out of order or range give empty or shorter groups.
-template <int TN> __device__ __forceinline__ int pieces(const RowGemmArgs &g, int e, int &lo, int &hi) {
-  const int first = e <= g.groups ? min(max(g.offsets[e], 0), g.n) : g.n;
-  const int next = e < g.groups ? min(max(g.offsets[e + 1], 0), g.n) : e == g.groups && g.clear ? g.n : 0;
-  lo = first;
-  hi = max(first, next);
-  return (hi - lo + TN - 1) / TN;
-}
 __device__ __forceinline__ int scan64(int x, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -168,33 +159,59 @@ __device__ __forceinline__ int scan64(int x, int lane) {
   }
   return x;
 }
-template <int TN> __device__ __forceinline__ int count_pieces(const RowGemmArgs &g) {
-  const int lane = threadIdx.x & 63;
-  int total = 0, lo, hi;
-  for (int e0 = 0; e0 <= g.groups; e0 += 64) total += pieces<TN>(g, e0 + lane, lo, hi);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-  return __builtin_amdgcn_readfirstlane(total);
-}
-template <int TN> __device__ __forceinline__ Rows find_piece(const RowGemmArgs &g, int at) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 <= g.groups; e0 += 64) {
-    int lo, hi;
-    const int mine = pieces<TN>(g, e0 + lane, lo, hi), upto = before + scan64(mine, lane);
-    const uint64_t past = __ballot(at < upto);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int start = __builtin_amdgcn_readlane(upto - mine, l), from = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
-      const int first = from + (at - start) * TN;
-      // always so, unless groups that overlap have more pieces than an int counts
-      if (first >= from && first < end) return Rows{first, end, e0 + l};
-      return Rows{0, 0, -1};
-    }
-    before = __builtin_amdgcn_readlane(upto, 63);
+
+// Pieces of TN rows, counted through the groups, those of the rows behind the last group
+// (to be zeroed) at the end.  A lane has one of 64 groups; with more of them they are
+// gone through again to find a piece.  Offsets out of order or range give empty or
+// shorter groups.
+template <int TN> struct Pieces {
+  const RowGemmArgs &g;
+  int lane, lo, hi, mine, upto;         // of the lane's group in the 64 looked at last
+  int in_groups, behind, total;
+  __device__ __forceinline__ void look(int e0, int before) {
+    const int e = e0 + lane;
+    lo = e < g.groups ? min(max(g.offsets[e], 0), g.n) : 0;
+    hi = e < g.groups ? max(lo, min(max(g.offsets[e + 1], 0), g.n)) : 0;
+    mine = (hi - lo + TN - 1) / TN;
+    upto = before + scan64(mine, lane);
   }
-  return Rows{0, 0, -1};
-}
+  __device__ __forceinline__ Pieces(const RowGemmArgs &args) : g(args), lane(threadIdx.x & 63) {
+    behind = g.clear ? min(max(g.offsets[g.groups], 0), g.n) : g.n;
+    in_groups = 0;
+    for (int e0 = 0; e0 < g.groups; e0 += 64) {
+      look(e0, in_groups);
+      in_groups = __builtin_amdgcn_readlane(upto, 63);
+    }
+    total = in_groups + (g.n - behind + TN - 1) / TN;
+  }
+  __device__ __forceinline__ Rows find(int at) {
+    if (at >= in_groups) {
+      const int first = behind + (at - in_groups) * TN;
+      return first >= behind && first < g.n ? Rows{first, g.n, g.groups} : Rows{0, 0, -1};
+    }
+    int e0 = 0, before = 0;
+    if (g.groups > 64) look(0, 0);
+    while (true) {
+      const uint64_t past = __ballot(at < upto);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        const int start = __builtin_amdgcn_readlane(upto - mine, l), from = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
+        const int first = from + (at - start) * TN;
+        // always so, unless groups that overlap have more pieces than an int counts
+        return first >= from && first < end ? Rows{first, end, e0 + l} : Rows{0, 0, -1};
+      }
+      before = __builtin_amdgcn_readlane(upto, 63);
+      e0 += 64;
+      if (e0 >= g.groups) return Rows{0, 0, -1};
+      look(e0, before);
+    }
+  }
+};
+
+template <int TN> struct Whole {
+  int total;
+  __device__ __forceinline__ Whole(const RowGemmArgs &g) : total((g.n + TN - 1) / TN) {}
+};
 
 // A's codes and scales for a group.
 __device__ __forceinline__ void take_group(RowGemmArgs &g, const Rows &r) {
@@ -240,7 +257,7 @@ template <bool GROUPED> __global__ __launch_bounds__(512, 4) void strip_kernel(R
   int n0 = blockIdx.y * 16;
   bool zero = false;
   if constexpr (GROUPED) {
-    const Rows rows = find_piece<16>(g, blockIdx.y);
+    const Rows rows = Pieces<16>(g).find(blockIdx.y);
     if (rows.group < 0) return;
     n0 = rows.first;
     zero = rows.group == g.groups;
@@ -418,27 +435,27 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 
   // tile of this workgroup: workgroups go to the 8 XCDs in turn; each XCD takes
   // a contiguous part of the tiles, which run down 8 row tiles at a time
-  int mt, nt;
+  int mt, nt, n0;
+  bool zero = false;
   {
-    const int tm = (g.m + TM - 1) / TM, tn = GROUPED ? count_pieces<TN>(g) : (g.n + TN - 1) / TN, all = tm * tn;
+    std::conditional_t<GROUPED, Pieces<TN>, Whole<TN>> pieces(g);
+    const int tm = (g.m + TM - 1) / TM, tn = pieces.total, all = tm * tn;
     const int id = blockIdx.x, x = id & 7, part = all >> 3, more = all & 7;
     if (GROUPED && (id >> 3) >= part + (x < more)) return;
     const int t = x * part + min(x, more) + (id >> 3);
     const int width = 8 * tn, band = t / width, h = min(8, tm - 8 * band), in = t - band * width;
     mt = 8 * band + in % h;
     nt = in / h;
-    if (GROUPED && (mt < 0 || mt >= tm)) return;      // as in find_piece
+    n0 = nt * TN;
+    if constexpr (GROUPED) {
+      const Rows rows = pieces.find(nt);
+      if (rows.group < 0 || mt < 0 || mt >= tm) return;      // the latter as in find
+      n0 = rows.first;
+      zero = rows.group == g.groups;
+      take_group(g, zero ? Rows{rows.first, rows.end, 0} : rows);
+    }
   }
   const int m0 = mt * TM;
-  int n0 = nt * TN;
-  bool zero = false;
-  if constexpr (GROUPED) {
-    const Rows rows = find_piece<TN>(g, nt);
-    if (rows.group < 0) return;
-    n0 = rows.first;
-    zero = rows.group == g.groups;
-    take_group(g, zero ? Rows{rows.first, rows.end, 0} : rows);
-  }
   Panel<TM, T, true> pa;
   Panel<TN, T, false> pb;
   pa.init(g.a, m0, g.k, tid);

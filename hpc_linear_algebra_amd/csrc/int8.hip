@@ -245,86 +245,85 @@ __device__ __forceinline__ void put_sums(int *p, int left, const int (&v)[8]) {
       if (e < left) p[e] = v[e];
 }
 
-// Few columns or little work: a workgroup computes 16 rows of A against 16 rows of
-// B, its eight waves taking every eighth block of 128 columns; fragments come
-// straight from global memory, and the partial sums meet in LDS.
-template <bool GROUPED> __global__ __launch_bounds__(512, 4) void strip_kernel(RowGemmArgs g) {
-  constexpr int W = 8, UNROLL = 4;
-  __shared__ int part[W][4][64];
+// Few columns or little work: a workgroup computes 16 rows of A against 16 NJ rows of
+// B, its eight waves taking every eighth block of 128 columns; fragments come straight
+// from global memory, UNROLL blocks of a wave at once (whole or not: those behind the
+// last are zeros), and the partial sums meet in LDS.
+template <bool GROUPED, int NJ> __global__ __launch_bounds__(512, 4) void strip_kernel(RowGemmArgs g) {
+  constexpr int W = 8, UNROLL = 2, TN = 16 * NJ;
+  __shared__ int part[W][4 * NJ][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int m0 = blockIdx.x * 16;
-  int n0 = blockIdx.y * 16;
+  int n0 = blockIdx.y * TN;
   bool zero = false;
   if constexpr (GROUPED) {
-    const Rows rows = Pieces<16>(g).find(blockIdx.y);
+    const Rows rows = Pieces<TN>(g).find(blockIdx.y);
     if (rows.group < 0) return;
     n0 = rows.first;
     zero = rows.group == g.groups;
     take_group(g, zero ? Rows{rows.first, rows.end, 0} : rows);
   }
   const uint8_t *arow = g.a.codes + (int64_t)min(m0 + r, g.m - 1) * g.a.ld + 16 * q;
-  const uint8_t *brow = g.b.codes + (int64_t)min(n0 + r, g.n - 1) * g.b.ld + 16 * q;
-  i4 acc = i4{0, 0, 0, 0};
-  struct Block {
-    u4 a[2], b[2];
-  };
-  auto load = [&](int kb, Block &x) {
-    const int64_t c = (int64_t)kb * QB;
+  const uint8_t *brow[NJ];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x.a[h] = *reinterpret_cast<const u4 *>(arow + c + 64 * h);
-      x.b[h] = *reinterpret_cast<const u4 *>(brow + c + 64 * h);
+  for (int j = 0; j < NJ; ++j) brow[j] = g.b.codes + (int64_t)min(n0 + 16 * j + r, g.n - 1) * g.b.ld + 16 * q;
+  i4 acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[j] = i4{0, 0, 0, 0};
+  const int full = zero ? 0 : g.k / QB, blocks = zero ? 0 : (g.k + QB - 1) / QB;
+  for (int kb = wave; kb < blocks; kb += UNROLL * W) {
+    u4 a[UNROLL][2], b[UNROLL][NJ][2];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int at = kb + u * W;
+      const int64_t c = (int64_t)at * QB;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (at < full) {
+          a[u][h] = *reinterpret_cast<const u4 *>(arow + c + 64 * h);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) b[u][j][h] = *reinterpret_cast<const u4 *>(brow[j] + c + 64 * h);
+        } else {
+          // the cut block: zeros from column k on in one operand are enough
+          const bool cut = at < blocks && 16 * q + 64 * h < g.k - full * QB;
+          a[u][h] = at < blocks ? load16(arow + c - 16 * q, 16 * q + 64 * h, g.k - full * QB) : u4{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) b[u][j][h] = cut ? *reinterpret_cast<const u4 *>(brow[j] + c + 64 * h) : u4{0, 0, 0, 0};
+        }
+      }
     }
-  };
-  auto add = [&](const Block &x) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, x.a[h]), __builtin_bit_cast(i4, x.b[h]), acc, 0, 0, 0);
-  };
-  const int full = zero ? 0 : g.k / QB;
-  int kb = wave;
-  for (; kb + (UNROLL - 1) * W < full; kb += UNROLL * W) {
-    Block x[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) load(kb + u * W, x[u]);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) add(x[u]);
-  }
-  for (; kb < full; kb += W) {
-    Block x;
-    load(kb, x);
-    add(x);
-  }
-  if (!zero && kb == full && g.k > full * QB) {          // the cut block
-    Block x;
-    const int64_t o = (int64_t)full * QB - 16 * q;
+    for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x.a[h] = load16(arow + o, 16 * q + 64 * h, g.k - full * QB);
-      x.b[h] = load16(brow + o, 16 * q + 64 * h, g.k - full * QB);
-    }
-    add(x);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, a[u][h]), __builtin_bit_cast(i4, b[u][j][h]), acc[j], 0, 0, 0);
   }
 #pragma unroll
-  for (int v = 0; v < 4; ++v) part[wave][v][lane] = acc[v];
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) part[wave][4 * j + v][lane] = acc[j][v];
   __syncthreads();
-  if (threadIdx.x < 256) {
-    const int i = threadIdx.x & 15, j = threadIdx.x >> 4;      // row, column of the workgroup's block
-    int v = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += part[w][i & 3][(i >> 2) * 16 + j];
-    if (m0 + i < g.m && n0 + j < g.n) store_one(g, m0 + i, n0 + j, zero ? 0.0f : (float)v * g.b.scales[n0 + j] * g.a.scales[m0 + i]);
+  for (int j0 = 0; j0 < NJ; j0 += 2) {
+    const int i = threadIdx.x & 15, j = j0 + (threadIdx.x >> 8), c = threadIdx.x >> 4 & 15;      // row, strip and column of the workgroup's block
+    if (j < NJ) {
+      int v = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += part[w][4 * j + (i & 3)][(i >> 2) * 16 + c];
+      const int col = n0 + 16 * j + c;
+      if (m0 + i < g.m && col < g.n) store_one(g, m0 + i, col, zero ? 0.0f : (float)v * g.b.scales[col] * g.a.scales[m0 + i]);
+    }
   }
 }
 
 // A few tokens, quantized by every workgroup for itself: codes and scales stand in LDS,
 // and the strip's product follows, its first weights under way while x is read.  One
 // launch where quantizer and product are two: 8192 x 1 x 4096 7.0 us, 9.5 (the product
-// alone 6.8); 8192 x 4 x 4096 10.0, 10.4; 4096 x 8 x 2048 5.5, 6.2.  Beyond four vectors
-// of x a lane the work of all workgroups costs more than the launch (2048 x 5 x 3000
-// 6.6, 6.2).
+// alone 6.8); 8192 x 4 x 4096 10.0, 10.4; 4096 x 8 x 2048 5.5, 6.2.
 constexpr int FEW_TOKENS = 8, FEW = 16384;       // tokens, and entries of all of them
 __host__ __device__ constexpr int few_waves(int64_t n) { return n == 1 ? 8 : n == 2 ? 4 : n <= 4 ? 2 : 1; }     // for each token
 template <typename T> __global__ __launch_bounds__(512, 4) void few_kernel(RowGemmArgs g, const void *xp, int64_t ldx) {
@@ -672,11 +671,11 @@ template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(RowGemm
 
 // ---- which kernel ------------------------------------------------------------------------------------
 
-enum Kind { STRIP, TILE_64, TILE_128, TILE_128W, TILE_256 };
+enum Kind { STRIP, STRIP_2, TILE_64, TILE_128, TILE_128W, TILE_256 };
 struct Shape {
   int rows, cols, threads;  // of C and of the workgroup that computes them
 };
-constexpr Shape SHAPE[] = {{16, 16, 512}, {128, 64, 512}, {128, 128, 256}, {128, 128, 512}, {256, 256, 512}};
+constexpr Shape SHAPE[] = {{16, 16, 512}, {16, 32, 512}, {128, 64, 512}, {128, 128, 256}, {128, 128, 512}, {256, 256, 512}};
 struct Choice {
   Kind kind;
   int parts;                // of the contraction, with a launch that adds them if more than one
@@ -695,25 +694,26 @@ int64_t most_pieces(Kind kind, int64_t n, int32_t groups) {
 // whatever the others do, where a result has less than 2^24 of them.
 constexpr int64_t THREAD_LIM = (int64_t)1 << 32, TILE_LIM = (int64_t)1 << 24;
 int64_t workgroups(Kind kind, int64_t m, int64_t n, int32_t groups) {
-  return kind == STRIP ? cdiv(m, 16) : cdiv(m, SHAPE[kind].rows) * most_pieces(kind, n, groups);      // along x
+  return kind <= STRIP_2 ? cdiv(m, 16) : cdiv(m, SHAPE[kind].rows) * most_pieces(kind, n, groups);      // along x
 }
 bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
-  return workgroups(kind, m, n, groups) * SHAPE[kind].threads < THREAD_LIM && (kind != STRIP || most_pieces(STRIP, n, groups) <= 65535) &&
+  return workgroups(kind, m, n, groups) * SHAPE[kind].threads < THREAD_LIM && (kind > STRIP_2 || most_pieces(kind, n, groups) <= 65535) &&
          (parts == 1 || cdiv(m, 8) * n < THREAD_LIM - 256);
 }
 
 // The kernel with the least estimated time (us).  The estimates are fits to measured
 // times (graph replays, 16-bit C) of every kernel at 36 products and 14 of groups; the
-// choice costs 0.6% against the best of them, 22% at most.  Some of them, the kernel
+// choice costs 0.4% against the best of them, 9% at most.  Some of them, the kernel
 // chosen first:
-//   4608 x 37 x 2568     strip 8.5, 128 x 64 tiles 9.8, in four parts 9.1, 128 x 128 13
-//   8192 x 33 x 8192     128 x 64 in four parts 17, strip 41
+//   4608 x 37 x 2568     strip 8.5, of 32 columns 8.9, 128 x 64 tiles in four parts 9.1
+//   8192 x 24 x 2048     strip of 32 columns 7.5, of 16 9.5
+//   8192 x 33 x 8192     128 x 64 in four parts 16, strip of 32 columns 35
 //   2501 x 1111 x 1747   128 x 128 on eight waves 12.0, on four 12.8, 128 x 64 16
-//   2000 x 1000 x 8000   128 x 64 28, 128 x 128 on eight waves 34
+//   2000 x 1000 x 8000   128 x 64 27, 128 x 128 on eight waves 34
 //   2048 x 4096 x 2048   128 x 128 on four waves 19, on eight 24
 //   4096 x 4096 x 4096   256 x 256 57, 128 x 128 on four waves 64
-//   64 groups, 28672 rows, 2816 x 2048   256 x 256 244, 128 x 128 262
-//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 23, 128 x 64 24, strip 31
+//   64 groups, 28672 rows, 2816 x 2048   256 x 256 239, 128 x 128 248
+//   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 22, 128 x 64 24, strip 28
 //   64 groups, 40 rows, 1024 x 4096      128 x 64 20, 128 x 128 on four waves 26
 Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
   const double nb = (double)std::max<int64_t>(1, cdiv(k, QB));
@@ -732,8 +732,13 @@ Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
       best = Choice{kind, parts};
     }
   };
-  // 2 KB of A a workgroup and block, and as many rows of B as there are up to 16
-  offer(STRIP, 1, 3.6, 2.4 + cdiv(m, 16) * pieces(16) * nb * (1.8e-4 + 1.1e-5 * std::min(16.0, n / reached)) + 0.05 * nb);
+  // 2 KB of A a workgroup and block, and as many rows of B as there are up to the strip's
+  auto strips = [&](Kind kind, double first, double rows, double row, double next) {
+    const int tn = SHAPE[kind].cols;
+    offer(kind, 1, 4.2, first + cdiv(m, 16) * pieces(tn) * nb * (rows + row * std::min((double)tn, n / reached)) + next * nb);
+  };
+  strips(STRIP, 2.4, 1.75e-4, 1.0e-5, 0.058);
+  strips(STRIP_2, 2.55, 2.2e-4, 0.9e-5, 0.062);
   // One workgroup a CU takes `one` a block, `pair` of them together `two`.  Four waves a
   // CU keep too few loads under way for weights out of HBM.
   auto tiles = [&](Kind kind, int pair, double rate, double one, double two, double first, double next) {
@@ -747,10 +752,10 @@ Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
       if (kind == TILE_256 || (kind == TILE_128 && parts == 2)) break;
     }
   };
-  tiles(TILE_64, 2, 5.0, 0.313, 0.866, 3.6, 4.5);
-  tiles(TILE_128W, 1, 4.8, 0.503, 0.61, 3.9, 4.1);
-  tiles(TILE_128, 2, 5.6, 0.627, 0.95, 3.5, 8.0);
-  tiles(TILE_256, 1, 4.6, 1.45, 1.45, 7.3, 11.4);
+  tiles(TILE_64, 2, 5.0, 0.312, 0.865, 3.6, 4.4);
+  tiles(TILE_128W, 1, 4.8, 0.505, 0.65, 3.85, 4.0);
+  tiles(TILE_128, 2, 5.6, 0.62, 0.94, 3.8, 8.0);
+  tiles(TILE_256, 1, 4.6, 1.455, 1.455, 7.3, 11.6);
   return best;
 }
 
@@ -821,18 +826,28 @@ tlr_status product_args(const char *name, tlr_dtype dt, int64_t m, int64_t n, in
 
 // A linear layer's call: where the codes of x (rows of ld bytes), its scales and a
 // product's parts stand in the workspace.  A few tokens take one launch and no
-// workspace, where the product is a strip's.
+// workspace.
 struct LinearParts {
   Choice choice;
   bool few;
   int64_t ld;
   size_t scales, parts, bytes;
 };
+// Whether a linear layer's tokens are quantized in the product's launch: what they have to
+// fit into, and the work that its rounds of workgroups (512 at a time) repeat, which
+// costs more than the launch beyond 8 of the vectors of x a lane, with one more each for
+// the rest (65536 x 8 x 2048, eight rounds of four: 39 us, 26 with a launch of its own;
+// 32768 x 1 x 4096, four of one: 22.6 and 23.7).
+bool few_tokens(int64_t m, int64_t n, int64_t k) {
+  const int64_t vectors = cdiv(k, 512 * few_waves(n));
+  return n <= FEW_TOKENS && vectors <= 4 && cdiv(m, 16 * 512) * (1 + vectors) <= 8;
+}
+
 LinearParts linear_parts(int64_t m, int64_t n, int64_t k) {
   LinearParts p{};
   if (m == 0 || n == 0) return p;
   p.choice = choose(m, n, k, 0);
-  p.few = p.choice.kind == STRIP && n <= FEW_TOKENS && k <= 4 * 512 * few_waves(n);
+  p.few = few_tokens(m, n, k);
   if (p.few) return p;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.ld = (k + 15) & ~(int64_t)15;
@@ -857,14 +872,17 @@ template <Kind KIND, int WM, int WN, int NS, int SPREAD> void tile_launch(const 
   else parts_kernel<8><<<sum, 256, 0, st>>>(g, ws);
 }
 
+template <Kind KIND> void strip_launch(const RowGemmArgs &g, hipStream_t st) {
+  constexpr int NJ = SHAPE[KIND].cols / 16;
+  const dim3 grid((unsigned)workgroups(KIND, g.m, g.n, g.groups), (unsigned)most_pieces(KIND, g.n, g.groups));
+  if (g.groups) strip_kernel<true, NJ><<<grid, 512, 0, st>>>(g);
+  else strip_kernel<false, NJ><<<grid, 512, 0, st>>>(g);
+}
+
 void gemm_launch(const RowGemmArgs &g, const Choice &c, int *ws, hipStream_t st) {
   switch (c.kind) {
-    case STRIP: {
-      const dim3 grid((unsigned)workgroups(STRIP, g.m, g.n, g.groups), (unsigned)most_pieces(STRIP, g.n, g.groups));
-      if (g.groups) strip_kernel<true><<<grid, 512, 0, st>>>(g);
-      else strip_kernel<false><<<grid, 512, 0, st>>>(g);
-      return;
-    }
+    case STRIP: return strip_launch<STRIP>(g, st);
+    case STRIP_2: return strip_launch<STRIP_2>(g, st);
     case TILE_64: return tile_launch<TILE_64, 4, 2, 3, 0>(g, c.parts, ws, st);
     case TILE_128: return tile_launch<TILE_128, 2, 2, 2, 0>(g, c.parts, ws, st);
     case TILE_128W: return tile_launch<TILE_128W, 2, 4, 3, 0>(g, c.parts, ws, st);
@@ -903,7 +921,7 @@ tlr_status row_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t groups, tlr_bl
   if (m == 0 || n == 0) return TLR_OK;
   const Choice c = choose(m, n, k, groups);
   const Shape &s = SHAPE[c.kind];
-  const int64_t y = c.kind == STRIP ? most_pieces(STRIP, n, groups) : 1;
+  const int64_t y = c.kind <= STRIP_2 ? most_pieces(c.kind, n, groups) : 1;
   *out = tlr_block_gemm_choice{s.rows, s.cols, s.threads, 1, c.parts, 0, workgroups(c.kind, m, n, groups), y, parts_bytes(c, m, n)};
   return TLR_OK;
 }

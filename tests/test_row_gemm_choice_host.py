@@ -65,9 +65,14 @@ def test_workspaces():
     up = lambda x: -(-x // 256) * 256   # noqa: E731
     assert T.tlr_row_linear_workspace_bytes(m, n, k) == up(n * -(-k // 16) * 16) + up(4 * n) + c.workspace
     assert T.tlr_row_gemm_workspace_bytes(m, n, k, 3) == 0
+    def two_launches(m, n, k):
+        return up(n * -(-k // 16) * 16) + up(4 * n) + T.tlr_row_gemm_plan(m, n, k).workspace
+
     for tokens, most in ((1, 16384), (2, 8192), (3, 4096), (4, 4096), (5, 2048), (8, 2048)):
         assert T.tlr_row_linear_workspace_bytes(2048, tokens, most) == 0
-        assert T.tlr_row_linear_workspace_bytes(2048, tokens, most + 1) == up(tokens * (most + 16)) + 256
+        assert T.tlr_row_linear_workspace_bytes(2048, tokens, most + 1) == two_launches(2048, tokens, most + 1) > 0
+    assert T.tlr_row_linear_workspace_bytes(32768, 1, 4096) == 0             # four rounds of workgroups, a vector a lane
+    assert T.tlr_row_linear_workspace_bytes(32769, 1, 4096) == two_launches(32769, 1, 4096) > 0
     assert T.tlr_row_linear_workspace_bytes(2048, 9, 64) > 0
     assert T.tlr_row_linear_workspace_bytes(0, 9, 64) == T.tlr_row_linear_workspace_bytes(9, 0, 64) == 0
 

@@ -56,8 +56,8 @@ G = dict(dtype="bf16", m=64, n=8, k=40, A=matrix(), B=matrix(), C=A16, ldc=64)
     (dict(groups=groups(count=0)), BAD), (dict(groups=groups(count=1025)), BAD), (dict(groups=groups(offsets=0)), BAD),
     (dict(groups=groups(offsets=A16 + 2)), BAD), (dict(groups=groups(code_step=8)), BAD), (dict(groups=groups(code_step=-16)), BAD),
     (dict(groups=groups(scale_step=-1)), BAD), (dict(groups=groups(clear=2)), BAD),
-    (dict(m=324, n=418, k=4310, ldc=324, A=matrix(ld=4320), B=matrix(ld=4320)), BAD),                              # in parts: no workspace
-    (dict(m=324, n=418, k=4310, ldc=324, A=matrix(ld=4320), B=matrix(ld=4320), workspace=A16, workspace_bytes=64), SPACE),
+    (dict(m=362, n=548, k=4009, ldc=362, A=matrix(ld=4016), B=matrix(ld=4016)), BAD),                              # in parts: no workspace
+    (dict(m=362, n=548, k=4009, ldc=362, A=matrix(ld=4016), B=matrix(ld=4016), workspace=A16, workspace_bytes=64), SPACE),
     (dict(m=0), OK), (dict(n=0), OK), (dict(n=0, groups=groups()), OK)])
 def test_product_refusals(change, want):
     assert status(T.tlr_row_gemm, **dict(G, **change)) == want

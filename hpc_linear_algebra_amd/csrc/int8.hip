@@ -834,13 +834,12 @@ struct LinearParts {
   size_t scales, parts, bytes;
 };
 // Whether a linear layer's tokens are quantized in the product's launch: what they have to
-// fit into, and the work that its rounds of workgroups (512 at a time) repeat, which
-// costs more than the launch beyond 8 of the vectors of x a lane, with one more each for
-// the rest (65536 x 8 x 2048, eight rounds of four: 39 us, 26 with a launch of its own;
-// 32768 x 1 x 4096, four of one: 22.6 and 23.7).
+// fit into, and the work that its rounds of workgroups (512 at a time) repeat, 0.4 us for
+// each vector of x a lane and as much for the rest (8192 x 8 x 4096, eight vectors: 13.2
+// us, 11.3 with a launch of its own; 32768 x 1 x 4096, four rounds of one: 25.6 and 24.1).
 bool few_tokens(int64_t m, int64_t n, int64_t k) {
   const int64_t vectors = cdiv(k, 512 * few_waves(n));
-  return n <= FEW_TOKENS && vectors <= 4 && cdiv(m, 16 * 512) * (1 + vectors) <= 8;
+  return n <= FEW_TOKENS && vectors <= 4 && cdiv(m, 16 * 512) * (1 + vectors) <= 6;
 }
 
 LinearParts linear_parts(int64_t m, int64_t n, int64_t k) {

@@ -71,8 +71,8 @@ def test_workspaces():
     for tokens, most in ((1, 16384), (2, 8192), (3, 4096), (4, 4096), (5, 2048), (8, 2048)):
         assert T.tlr_row_linear_workspace_bytes(2048, tokens, most) == 0
         assert T.tlr_row_linear_workspace_bytes(2048, tokens, most + 1) == two_launches(2048, tokens, most + 1) > 0
-    assert T.tlr_row_linear_workspace_bytes(32768, 1, 4096) == 0             # four rounds of workgroups, a vector a lane
-    assert T.tlr_row_linear_workspace_bytes(32769, 1, 4096) == two_launches(32769, 1, 4096) > 0
+    assert T.tlr_row_linear_workspace_bytes(24576, 1, 4096) == 0             # three rounds of workgroups, a vector a lane
+    assert T.tlr_row_linear_workspace_bytes(24577, 1, 4096) == two_launches(24577, 1, 4096) > 0
     assert T.tlr_row_linear_workspace_bytes(2048, 9, 64) > 0
     assert T.tlr_row_linear_workspace_bytes(0, 9, 64) == T.tlr_row_linear_workspace_bytes(9, 0, 64) == 0
 

@@ -364,8 +364,10 @@ PyObject *row_gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
     if (offsets.scalar_type() != at::kInt || offsets.dim() != 1 || offsets.device() != device || offsets.size(0) != a_codes.size(0) + 1)
       return value_error("gemm: offsets is a 1-d int32 tensor on the operands' device, one entry more than groups");
     offsets = offsets.contiguous();
-    groups = tlr_row_groups{static_cast<const int32_t *>(offsets.data_ptr()), a_codes.stride(0), THPVariable_Unpack(args[1]).stride(0),
-                            (int32_t)std::min<int64_t>(a_codes.size(0), 0x7fffffff), args[6] == Py_None};
+    const bool one = a_codes.size(0) == 1;        // steps that no group takes, and strides of no codes, say nothing
+    groups = tlr_row_groups{static_cast<const int32_t *>(offsets.data_ptr()), one || k == 0 ? 0 : a_codes.stride(0),
+                            one ? 0 : THPVariable_Unpack(args[1]).stride(0), (int32_t)std::min<int64_t>(a_codes.size(0), 0x7fffffff),
+                            args[6] == Py_None};
   }
   const int64_t m = a_codes.size(-2), n = b_codes.size(0);
   const bool grad = c10::GradMode::is_enabled();

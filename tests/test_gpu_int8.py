@@ -205,6 +205,28 @@ def test_gemm_empty(m, n, k):
     assert got.shape == (n, m) and not got.any()
 
 
+@pytest.mark.parametrize("groups,m,n", [(1, 3, 4), (5, 1030, 40), (3, 7, 2)])
+def test_groups_of_no_columns(groups, m, n):
+    """Their codes have strides that are no multiple of 16."""
+    A = int8.RowScaled(torch.zeros(groups, m, 0, dtype=torch.int8, device="cuda"), torch.ones(groups, m, device="cuda"), 0)
+    B = int8.RowScaled(torch.zeros(n, 0, dtype=torch.int8, device="cuda"), torch.ones(n, device="cuda"), 0)
+    offsets = torch.tensor([0] * groups + [n - 1], dtype=torch.int32, device="cuda")
+    got = int8.gemm(A, B, offsets=offsets, dtype="f32")
+    assert got.shape == (n, m) and not got.any()
+
+
+def test_one_group_whatever_its_step():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    m, n, k = 20, 9, 48
+    a = torch.randint(-128, 128, (m, k), generator=g, dtype=torch.int8, device="cuda")
+    b = torch.randint(-128, 128, (n, k), generator=g, dtype=torch.int8, device="cuda")
+    sa, sb = torch.rand(m, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    offsets = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    A = int8.RowScaled(a.as_strided((1, m, k), (7, k, 1)), sa.as_strided((1, m), (3, 1)), k)
+    got = int8.gemm(A, int8.RowScaled(b, sb, k), offsets=offsets, dtype="f32")
+    assert torch.equal(got, int8.gemm(int8.RowScaled(a, sa, k), int8.RowScaled(b, sb, k), dtype="f32"))
+
+
 def grouped(a, sa, b, sb, k, offsets, m):
     want = torch.zeros(b.shape[0], m, dtype=torch.float64)
     for e in range(a.shape[0]):

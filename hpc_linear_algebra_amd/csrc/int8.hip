@@ -24,6 +24,8 @@ namespace {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
 
+constexpr int MOST_GROUPS = 1024;
+
 // ---- quantizer ---------------------------------------------------------------------------------------
 
 struct RowQuantArgs {
@@ -412,21 +414,85 @@ template <typename T> __global__ __launch_bounds__(512, 4) void few_kernel(RowGe
   }
 }
 
+// All waves of a workgroup, once this one has no LDS access under way; its loads go on.
+__device__ __forceinline__ void meet_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A tile's sums, scaled, to C, up to column `end`.  They go through LDS (ROOM bytes, in
+// passes if they need more), a column's TM entries in a row, 16-byte pieces XOR-placed, so
+// that whole stretches of C's columns are stored, past the caches: 2501 x 1111 x 1747 in
+// 128 x 128 on four waves 12.8 us, through the caches 13.2, straight from the registers,
+// 64 bytes of a column at a time, 15.7.  `rows(i, v)` gives the scales of the tile's rows i ..
+// i + 7, `column(j)` that of its column j; `before` runs before the first store.
+template <typename E, int TM, int TN, int WM, int WN, int ROOM, int RI, int CJ, typename ROWS, typename COLUMN, typename BEFORE>
+__device__ __forceinline__ void store_tile(const RowGemmArgs &g, const i4 (&acc)[RI][CJ], uint8_t *lds, int m0, int n0, int end, int tid, bool zero,
+                                           ROWS rows, COLUMN column, BEFORE before) {
+  constexpr int T = 64 * WM * WN, WIDE = sizeof(E) / 2, PIECES = WIDE * TM / 8;      // pieces of 8 entries; of a column
+  constexpr int SIZE = (int)sizeof(E) * TM * TN, PASSES = (SIZE + ROOM - 1) / ROOM, JS = CJ / PASSES, COLS = T / PIECES;
+  static_assert(CJ % PASSES == 0 && SIZE / PASSES <= ROOM, "");
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+#pragma unroll
+  for (int pass = 0; pass < PASSES; ++pass) {
+    meet_lds();
+#pragma unroll
+    for (int h = 0; h < RI / 2; ++h) {
+      const int row = wm * (TM / WM) + 32 * h + 8 * q;
+      float sa[8];
+      rows(row, sa);
+#pragma unroll
+      for (int jj = 0; jj < JS; ++jj) {
+        const int at = 16 * (wn * JS + jj) + r, j = pass * JS + jj;      // column in LDS
+        const float sb = column(wn * (TN / WN) + 16 * j + r);
+        E v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (E)(zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e]);
+        u4 w[WIDE];
+        __builtin_memcpy(w, v, sizeof v);
+#pragma unroll
+        for (int p = 0; p < WIDE; ++p) *reinterpret_cast<u4 *>(lds + at * 16 * PIECES + 16 * ((WIDE * (row >> 3) + p) ^ (at & 15))) = w[p];
+      }
+    }
+    if (pass == 0) before();
+    meet_lds();
+    constexpr int N = 8 / WIDE;                   // entries of a piece
+    const int piece = tid % PIECES, row = m0 + N * piece;
+#pragma unroll 4
+    for (int at = tid / PIECES; at < TN / PASSES; at += COLS) {
+      const int col = n0 + at / (16 * JS) * (TN / WN) + 16 * JS * pass + at % (16 * JS);
+      if (col < end && row < g.m) {
+        const u4 w = *reinterpret_cast<const u4 *>(lds + at * 16 * PIECES + 16 * (piece ^ (at & 15)));
+        E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
+        if (row + N <= g.m) {
+          put16<true>(to, w);
+        } else {
+          E v[N];
+          __builtin_memcpy(v, &w, 16);
+#pragma unroll
+          for (int e = 0; e < N - 1; ++e)
+            if (row + e < g.m) to[e] = v[e];
+        }
+      }
+    }
+  }
+}
+
 // C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16; blocks of 128
 // columns pass through a ring of NS stages in LDS.  A wave goes through a stage row tile
 // by row tile; with the last one's matrix instructions under way it waits for the next
 // stage and reads its first fragments: one barrier a stage, and the matrix cores have
 // work on both sides of it.  The buffer that is then used up takes the stage NS further
-// on, at once (SPREAD 0), or, with two stages, SPREAD pieces under each row tile's matrix
-// instructions, which a long stage likes better (8192^3 in 256 x 256 tiles 427 us, at
-// once 437).  A short stage is computed faster than its loads arrive: with three of them
+// on.  A short stage is computed faster than its loads arrive: with three of them
 // 2000 x 1000 x 8000 in 128 x 64 tiles takes 27.6 us, with two 42, with four 27.7;
 // 2501 x 1111 x 1747 in 128 x 128 on eight waves 13.6, 15.0, 13.8.  128 x 128 on four
 // waves keep two, so that two workgroups fit a CU: 2048 x 4096 x 2048 22, with three 34.
-template <bool GROUPED, int TM, int TN, int WM, int WN, int NS, int SPREAD>
+template <bool GROUPED, int TM, int TN, int WM, int WN, int NS>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(RowGemmArgs g) {
   constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16;
-  static_assert(RI % 2 == 0 && (SPREAD == 0 || NS == 2), "");
+  static_assert(RI % 2 == 0, "");
   constexpr int AT_B = TM * QB, STAGE = (TM + TN) * QB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[NS * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -514,27 +580,21 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     const uint32_t base = lds_address(lds);
     pa.load_last(kb0 + nb - 1, base, wave, true);
     pb.load_last(kb0 + nb - 1, base + AT_B, wave, true);
-    if (SPREAD == 0 && nb >= NS) {
+    if (nb >= NS) {
 #pragma unroll
       for (int s = 1; s < NS; ++s) load_all(kb0 + s - 1, base + s * STAGE);
       meet(std::integral_constant<int, (NS - 1) * LOADS>{});
     } else {
-      if (SPREAD == 0)
-        for (int s = 1; s < nb; ++s) load_all(kb0 + s - 1, base + s * STAGE);
+      for (int s = 1; s < nb; ++s) load_all(kb0 + s - 1, base + s * STAGE);
       meet(ALL);
     }
     if ((g.k & (QB - 1)) != 0 && kb0 + nb == blocks) {      // zeros in one operand are enough: integers have no NaN
       pb.cut(g.k & (QB - 1), lds + AT_B, tid);
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0xf | 3 << 14 | 7 << 4);      // LDS only
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+      meet_lds();
     }
     read_b(lds);
     read_a(lds, 0);
-    // All products of a stage, with SPREAD that of block kb loaded meanwhile.
-    auto row_tiles = [&](const uint8_t *l, auto live, int kb, uint32_t to) {
-      static_assert(SPREAD == 0 || SPREAD * RI >= LOADS, "");
+    auto row_tiles = [&](const uint8_t *l) {      // all products of a stage
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
         if (i + 1 < RI) read_a(l, i + 1);
@@ -542,26 +602,22 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < CJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i & 1][h], b[j][h], acc[i][j], 0, 0, 0);
-        if constexpr (decltype(live)::value)
-#pragma unroll
-          for (int c = 0; c < SPREAD; ++c)
-            if (i * SPREAD + c < LOADS) load(i * SPREAD + c, kb, to);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     int now = 0, next = STAGE;
     for (int stage = 0; stage < nb - 1; ++stage) {
-      row_tiles(lds + now, std::true_type{}, kb0 + stage, base + next);
+      row_tiles(lds + now);
       // stages under way: up to stage + NS - 1, of which the next one is needed
       if (NS > 2 && stage + NS <= nb) meet(std::integral_constant<int, (NS - 2) * LOADS>{});
       else meet(ALL);
-      if (SPREAD == 0 && stage + NS < nb) load_all(kb0 + stage + NS - 1, base + now);
+      if (stage + NS < nb) load_all(kb0 + stage + NS - 1, base + now);
       read_b(lds + next);
       read_a(lds + next, 0);
       now = next;
       next = next == (NS - 1) * STAGE ? 0 : next + STAGE;
     }
-    row_tiles(lds + now, std::false_type{}, 0, 0);
+    row_tiles(lds + now);
   }
 
   // lane (r, q): rows 32 h + 8 q .. + 7 of its columns
@@ -582,62 +638,214 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
       }
     return;
   }
-  // C goes through LDS, a column's TM entries in a row, 16-byte pieces XOR-placed, so
-  // that whole stretches of its columns are stored, past the caches: 64 groups, 28672
-  // rows, 2816 x 2048 in 256 x 256 tiles 251 us, through the caches 257, straight from the
-  // registers, 64 bytes of a column at a time, 265; 2501 x 1111 x 1747 in 128 x 128 on
-  // four waves 12.8, 13.2 and 15.7.
   auto store = [&](auto element) {
-    typedef decltype(element) E;
-    constexpr int WIDE = sizeof(E) / 2, PIECES = WIDE * TM / 8;       // pieces of 8 entries; of a column
-    constexpr int PASSES = (int)sizeof(E) * TM * TN > NS * STAGE ? 2 : 1, JS = CJ / PASSES, COLS = T / PIECES;
-    static_assert((int)sizeof(E) * TM * TN <= PASSES * NS * STAGE && CJ % PASSES == 0, "");
-#pragma unroll
-    for (int pass = 0; pass < PASSES; ++pass) {
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < RI / 2; ++h) {
-        const int row = wm * (TM / WM) + 32 * h + 8 * q;
-        float sa[8];
-        get8(g.a.scales + m0 + row, g.m - m0 - row, sa);
-#pragma unroll
-        for (int jj = 0; jj < JS; ++jj) {
-          const int at = 16 * (wn * JS + jj) + r, j = pass * JS + jj;      // column in LDS
-          const float sb = g.b.scales[min(col0 + 16 * j + r, g.n - 1)];
-          E v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = (E)(zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e]);
-          u4 w[WIDE];
-          __builtin_memcpy(w, v, sizeof v);
-#pragma unroll
-          for (int p = 0; p < WIDE; ++p) *reinterpret_cast<u4 *>(lds + at * 16 * PIECES + 16 * ((WIDE * (row >> 3) + p) ^ (at & 15))) = w[p];
-        }
-      }
-      __syncthreads();
-      constexpr int N = 8 / WIDE;                   // entries of a piece
-      const int piece = tid % PIECES, row = m0 + N * piece;
-#pragma unroll 4
-      for (int at = tid / PIECES; at < TN / PASSES; at += COLS) {
-        const int col = n0 + at / (16 * JS) * (TN / WN) + 16 * JS * pass + at % (16 * JS);
-        if (col < g.n && row < g.m) {
-          const u4 w = *reinterpret_cast<const u4 *>(lds + at * 16 * PIECES + 16 * (piece ^ (at & 15)));
-          E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
-          if (row + N <= g.m) {
-            put16<true>(to, w);
-          } else {
-            E v[N];
-            __builtin_memcpy(v, &w, 16);
-#pragma unroll
-            for (int e = 0; e < N - 1; ++e)
-              if (row + e < g.m) to[e] = v[e];
-          }
-        }
-      }
-    }
+    store_tile<decltype(element), TM, TN, WM, WN, NS * STAGE>(
+        g, acc, lds, m0, n0, g.n, tid, zero, [&](int i, float(&v)[8]) { get8(g.a.scales + m0 + i, g.m - m0 - i, v); },
+        [&](int j) { return g.b.scales[min(n0 + j, g.n - 1)]; }, [] {});
   };
   if (g.dt == TLR_F32) store(float{});
   else if (g.dt == TLR_F16) store((_Float16)0.0f);
   else store((__bf16)0.0f);
+}
+
+// Large products: one workgroup a CU goes through C tiles of TM x TN, its share of those
+// of its XCD.  As in tile_kernel, a ring of two stages in LDS and one barrier a stage; but
+// the stages of all its tiles are one sequence.  A tile's first stage and its scales are
+// loaded under the last stage of the tile before, and wait in LDS while that is stored
+// through the other buffer: 64 groups, 28672 rows, 2816 x 2048 in 256 x 256 tiles 231 us,
+// with a workgroup for each tile 265; 8192 x 16384 x 1024 137 and 152.  SPREAD loads of
+// the next stage follow each row tile's matrix instructions, which so long a stage likes
+// better than all of them at its start.  Groups' pieces are counted once, into LDS.
+template <bool GROUPED, int TM, int TN, int WM, int WN, int SPREAD>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void stream_kernel(RowGemmArgs g) {
+  constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16, NA = TM * 8 / T, NB = TN * 8 / T;
+  static_assert(RI % 2 == 0 && SPREAD * RI >= NA + NB, "");
+  constexpr int AT_B = TM * QB, STAGE = (TM + TN) * QB;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) float scales[2][TM + TN];       // of this tile's rows and columns, and the next one's
+  __shared__ int upto[GROUPED ? MOST_GROUPS : 1], begin[GROUPED ? MOST_GROUPS + 1 : 1];      // pieces up to and with a group; its rows
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+
+  int tn = (g.n + TN - 1) / TN;
+  if constexpr (GROUPED) {
+    if (wave == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 < g.groups; e0 += 64) {
+        const int e = e0 + lane;
+        const int lo = e < g.groups ? min(max(g.offsets[e], 0), g.n) : 0;
+        const int hi = e < g.groups ? max(lo, min(max(g.offsets[e + 1], 0), g.n)) : 0;
+        const int sum = before + scan64((hi - lo + TN - 1) / TN, lane);
+        if (e < g.groups) {
+          upto[e] = sum;
+          begin[e] = lo;
+        }
+        before = __builtin_amdgcn_readlane(sum, 63);
+      }
+      if (lane == 0) begin[g.groups] = min(max(g.offsets[g.groups], 0), g.n);
+    }
+    __syncthreads();
+    tn = __builtin_amdgcn_readfirstlane(upto[g.groups - 1]);
+  }
+  // Workgroups go to the 8 XCDs in turn; each XCD has a contiguous part of the tiles,
+  // which run down 8 row tiles at a time, and its workgroups take them in turn.
+  const int tm = (g.m + TM - 1) / TM, all = tm * tn, blocks = (g.k + QB - 1) / QB;
+  const int xcd = blockIdx.x & 7, peers = ((int)gridDim.x - xcd + 7) >> 3;
+  int t = xcd * (all >> 3) + min(xcd, all & 7);
+  const int end = t + (all >> 3) + (xcd < (all & 7) ? 1 : 0);
+  t += blockIdx.x >> 3;
+
+  struct Tile {
+    int m0, n0, n, group;     // n: end of the group's rows; m0 < 0: none
+  };
+  auto locate = [&](int at) {
+    Tile x{-1, 0, 0, 0};
+    if (at >= end) return x;
+    const int width = 8 * tn, band = at / width, h = min(8, tm - 8 * band), in = at - band * width, nt = in / h;
+    const int m0 = (8 * band + in % h) * TM;
+    if constexpr (!GROUPED) return Tile{m0, nt * TN, g.n, 0};
+    for (int e0 = 0; e0 < g.groups; e0 += 64) {
+      const uint64_t past = __ballot(nt < upto[min(e0 + lane, g.groups - 1)]);
+      if (past) {
+        const int e = e0 + __builtin_ctzll(past), lo = __builtin_amdgcn_readfirstlane(begin[e]);
+        const int first = lo + (nt - (e > 0 ? __builtin_amdgcn_readfirstlane(upto[e - 1]) : 0)) * TN;
+        const int last = max(lo, __builtin_amdgcn_readfirstlane(begin[e + 1]));
+        // always so, unless groups that overlap have more pieces than an int counts
+        if (first >= lo && first < last && m0 >= 0 && m0 < g.m) x = Tile{m0, first, last, e};
+        break;
+      }
+    }
+    return x;
+  };
+  // Where the loads of the next stage read: A's and B's first row and block, and bytes
+  // from there to the end of the last readable chunk (0: zeros).
+  const uint8_t *a_from = nullptr, *b_from = nullptr;
+  int32_t a_bytes = 0, b_bytes = 0;
+  auto aim = [&](const Tile &x, int kb) {
+    const int readable = ((g.k + 15) & ~15) - kb * QB;
+    a_from = g.a.codes + x.group * g.code_step + (int64_t)x.m0 * g.a.ld + kb * QB;
+    b_from = g.b.codes + (int64_t)x.n0 * g.b.ld + kb * QB;
+    a_bytes = x.m0 < 0 ? 0 : (min(TM, g.m - x.m0) - 1) * (int32_t)g.a.ld + readable;
+    b_bytes = x.m0 < 0 ? 0 : (min(TN, x.n - x.n0) - 1) * (int32_t)g.b.ld + readable;
+  };
+  const uint32_t base = lds_address(lds);
+  const int32_t a_step = (T / 8) * (int32_t)g.a.ld, b_step = (T / 8) * (int32_t)g.b.ld;
+  const uint32_t a_at = (uint32_t)(tid >> 3) * (uint32_t)g.a.ld + Panel<TM, T, true>::chunk(tid);
+  const uint32_t b_at = (uint32_t)(tid >> 3) * (uint32_t)g.b.ld + Panel<TN, T, false>::chunk(tid);
+  auto load = [&](int p, uint32_t to) {
+    if (p < NA) to_lds16(buffer(a_from + p * a_step, max(a_bytes - p * a_step, 0)), a_at, 0, to + (p * T + wave * 64) * 16);
+    else to_lds16(buffer(b_from + (p - NA) * b_step, max(b_bytes - (p - NA) * b_step, 0)), b_at, 0, to + AT_B + ((p - NA) * T + wave * 64) * 16);
+  };
+  const int ar = wm * (TM / WM) + 8 * (r >> 2) + (r & 3), br = wn * (TN / WN) + r;
+  const int aat = ar * QB + 16 * (q ^ a_key(ar)), bat = AT_B + br * QB + 16 * (q ^ b_key(br));
+  i4 x[2][2], b[CJ][2];       // fragments of row tile i (mod 2) and of the stage's columns
+  auto read_a = [&](const uint8_t *l, int i) {
+    const int o = (i >> 1) * 32 * QB + (i & 1) * 4 * QB;
+    x[i & 1][0] = *reinterpret_cast<const i4 *>(l + aat + o);
+    x[i & 1][1] = *reinterpret_cast<const i4 *>(l + (aat ^ 64) + o);
+  };
+  auto read_b = [&](const uint8_t *l) {
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) {
+      b[j][0] = *reinterpret_cast<const i4 *>(l + bat + 16 * QB * j);
+      b[j][1] = *reinterpret_cast<const i4 *>(l + (bat ^ 64) + 16 * QB * j);
+    }
+  };
+  auto meet = [&]() {         // nothing is under way
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto load_scales = [&](const Tile &x, int to) {
+    const bool of_a = wave < TM / 64;
+    const int first = of_a ? 0 : TM, have = x.m0 < 0 ? 0 : of_a ? min(TM, g.m - x.m0) : min(TN, x.n - x.n0);
+    const float *from = of_a ? g.a.scales + x.group * g.scale_step + x.m0 : g.b.scales + x.n0;
+    if (wave < (TM + TN) / 64) to_lds4(buffer(reinterpret_cast<const uint8_t *>(from), 4 * have), (tid - first) * 4, lds_address(reinterpret_cast<uint8_t *>(scales[to] + wave * 64)));
+  };
+
+  // A tile's first stage is its last block, the one cut at column k; stage i > 0 is block
+  // i - 1.
+  Tile now = locate(t);
+  int at = 0, turn = 0;       // LDS stage that is computed; scales of this tile
+  load_scales(now, 0);
+  if (blocks > 0) {
+    aim(now, blocks - 1);
+#pragma unroll
+    for (int p = 0; p < NA + NB; ++p) load(p, base);
+  }
+  meet();
+  for (; t < end; t += peers, turn ^= 1) {
+    const Tile next = locate(t + peers);
+    i4 acc[RI][CJ];
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) acc[i][j] = i4{0, 0, 0, 0};
+    if (blocks > 0 && (g.k & (QB - 1)) != 0) {      // zeros in one operand are enough: integers have no NaN
+      Panel<TN, T, false>::cut(g.k & (QB - 1), lds + at + AT_B, tid);
+      meet_lds();
+    }
+    if (blocks < 2) {
+      aim(next, blocks - 1);
+      load_scales(next, turn ^ 1);
+    } else {
+      aim(now, 0);
+    }
+    for (int stage = 0; stage < blocks; ++stage) {
+      const uint8_t *l = lds + at;
+      read_b(l);
+      read_a(l, 0);
+#pragma unroll
+      for (int i = 0; i < RI; ++i) {
+        if (i + 1 < RI) read_a(l, i + 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i & 1][h], b[j][h], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < SPREAD; ++c)
+          if (i * SPREAD + c < NA + NB) load(i * SPREAD + c, base + (STAGE - at));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      at = STAGE - at;
+      if (stage + 1 == blocks) break;
+      if (stage + 2 < blocks) {
+        a_from += QB;
+        b_from += QB;
+        a_bytes -= QB;
+        b_bytes -= QB;
+      } else {
+        aim(next, blocks - 1);
+        load_scales(next, turn ^ 1);
+      }
+      meet();
+    }
+    // C through the buffer that is used up.  The next tile's loads are waited for before
+    // the first store, so that the first stage need not wait for stores.
+    if (now.m0 >= 0) {        // always so, but for the groups that locate leaves out
+      auto store = [&](auto element) {
+        store_tile<decltype(element), TM, TN, WM, WN, STAGE>(
+            g, acc, lds + (blocks > 0 ? STAGE - at : 0), now.m0, now.n0, now.n, tid, false,
+            [&](int i, float(&v)[8]) { __builtin_memcpy(v, __builtin_assume_aligned(scales[turn] + i, 16), sizeof v); },
+            [&](int j) { return scales[turn][TM + j]; }, [] { __builtin_amdgcn_s_waitcnt(0); });
+      };
+      if (g.dt == TLR_F32) store(float{});
+      else if (g.dt == TLR_F16) store((_Float16)0.0f);
+      else store((__bf16)0.0f);
+    } else {
+      __builtin_amdgcn_s_waitcnt(0);
+    }
+    meet_lds();
+    now = next;
+  }
+  if constexpr (GROUPED) {
+    if (!g.clear) return;
+    const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int up = (g.m + 7) / 8;
+    for (int j = begin[g.groups] + blockIdx.x; j < g.n; j += gridDim.x)
+      for (int i = tid; i < up; i += T) store8(g, 8 * i, j, zeros);
+  }
 }
 
 // C from PARTS m x n matrices of sums: a thread takes 8 consecutive rows of a column.
@@ -671,7 +879,7 @@ template <int PARTS> __global__ __launch_bounds__(256) void parts_kernel(RowGemm
 
 // ---- which kernel ------------------------------------------------------------------------------------
 
-enum Kind { STRIP, STRIP_2, TILE_64, TILE_128, TILE_128W, TILE_256 };
+enum Kind { STRIP, STRIP_2, TILE_64, TILE_128, TILE_128W, STREAM };
 struct Shape {
   int rows, cols, threads;  // of C and of the workgroup that computes them
 };
@@ -690,11 +898,14 @@ int64_t most_pieces(Kind kind, int64_t n, int32_t groups) {
   return groups ? std::min(n, (n + (groups + 1) * (tn - 1)) / tn) : cdiv(n, tn);
 }
 
-// A launch has less than 2^32 threads along x.  128 x 128 tiles of four waves fit
-// whatever the others do, where a result has less than 2^24 of them.
-constexpr int64_t THREAD_LIM = (int64_t)1 << 32, TILE_LIM = (int64_t)1 << 24;
+// A launch has less than 2^32 threads along x; a workgroup for each tile, but one a CU
+// of those that go through several.  128 x 128 tiles of four waves fit whatever the others
+// do, where a result has less than 2^24 of them.
+constexpr int64_t CUS = 256, THREAD_LIM = (int64_t)1 << 32, TILE_LIM = (int64_t)1 << 24;
 int64_t workgroups(Kind kind, int64_t m, int64_t n, int32_t groups) {
-  return kind <= STRIP_2 ? cdiv(m, 16) : cdiv(m, SHAPE[kind].rows) * most_pieces(kind, n, groups);      // along x
+  if (kind <= STRIP_2) return cdiv(m, 16);
+  const int64_t tiles = cdiv(m, SHAPE[kind].rows) * most_pieces(kind, n, groups);
+  return kind == STREAM ? std::min(tiles, CUS) : tiles;
 }
 bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
   return workgroups(kind, m, n, groups) * SHAPE[kind].threads < THREAD_LIM && (kind > STRIP_2 || most_pieces(kind, n, groups) <= 65535) &&
@@ -702,8 +913,8 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 }
 
 // The kernel with the least estimated time (us).  The estimates are fits to measured
-// times (graph replays, 16-bit C) of every kernel at 36 products and 14 of groups; the
-// choice costs 0.4% against the best of them, 9% at most.  Some of them, the kernel
+// times (graph replays, 16-bit C) of every kernel at 44 products and 22 of groups; the
+// choice costs 0.2% against the best of them, 5% at most.  Some of them, the kernel
 // chosen first:
 //   4608 x 37 x 2568     strip 8.5, of 32 columns 8.9, 128 x 64 tiles in four parts 9.1
 //   8192 x 24 x 2048     strip of 32 columns 7.5, of 16 9.5
@@ -711,8 +922,9 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 //   2501 x 1111 x 1747   128 x 128 on eight waves 12.0, on four 12.8, 128 x 64 16
 //   2000 x 1000 x 8000   128 x 64 27, 128 x 128 on eight waves 34
 //   2048 x 4096 x 2048   128 x 128 on four waves 19, on eight 24
-//   4096 x 4096 x 4096   256 x 256 57, 128 x 128 on four waves 64
-//   64 groups, 28672 rows, 2816 x 2048   256 x 256 239, 128 x 128 248
+//   4096 x 4096 x 4096   256 x 256 56, 128 x 128 on four waves 64
+//   64 groups, 28672 rows, 2816 x 2048   256 x 256 216, 128 x 128 245
+//   64 groups, 8192 rows, 2048 x 1408    128 x 128 on four waves 48, 256 x 256 61
 //   32 groups, 96 rows, 2048 x 2048      128 x 128 on four waves 22, 128 x 64 24, strip 28
 //   64 groups, 40 rows, 1024 x 4096      128 x 64 20, 128 x 128 on four waves 26
 Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
@@ -749,13 +961,13 @@ Choice least_estimate(int64_t m, int64_t n, int64_t k, int32_t groups) {
       double us = first + (rounds - 1) * next + std::ceil(nb / parts) * ((rounds - 1) * two + (rest <= 256 ? one : two));
       if (parts > 1) us += 2.8 + parts * (0.1 + (double)m * (double)n * 2.1e-6);
       offer(kind, parts, kind == TILE_128 && t < 384 ? 4.4 : rate, us);
-      if (kind == TILE_256 || (kind == TILE_128 && parts == 2)) break;
+      if (kind == STREAM || (kind == TILE_128 && parts == 2)) break;
     }
   };
   tiles(TILE_64, 2, 5.0, 0.312, 0.865, 3.6, 4.4);
   tiles(TILE_128W, 1, 4.8, 0.505, 0.65, 3.85, 4.0);
   tiles(TILE_128, 2, 5.6, 0.62, 0.94, 3.8, 8.0);
-  tiles(TILE_256, 1, 4.6, 1.455, 1.455, 7.3, 11.6);
+  tiles(STREAM, 1, 4.6, 1.455, 1.455, 7.3, 11.6);
   return best;
 }
 
@@ -778,7 +990,6 @@ size_t parts_bytes(const Choice &c, int64_t m, int64_t n) { return c.parts > 1 ?
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int64_t SIZE_LIM = 0x7fffffff, PRODUCT_LIM = SIZE_LIM - 511, LD_LIM = (int64_t)1 << 22, K_LIM = 131071;
-constexpr int MOST_GROUPS = 1024;
 
 tlr_status launched(const char *what) {
   const hipError_t e = hipGetLastError();
@@ -856,19 +1067,27 @@ LinearParts linear_parts(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-template <Kind KIND, int WM, int WN, int NS, int SPREAD> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
+template <Kind KIND, int WM, int WN, int NS> void tile_launch(const RowGemmArgs &g, int parts, int *ws, hipStream_t st) {
   constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, T = 64 * WM * WN;
   static_assert(SHAPE[KIND].threads == T, "");
   const dim3 grid((unsigned)workgroups(KIND, g.m, g.n, g.groups), (unsigned)parts);
-  if (g.groups) return tile_kernel<true, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(g);
-  if (parts == 1) return tile_kernel<false, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(g);
+  if (g.groups) return tile_kernel<true, TM, TN, WM, WN, NS><<<grid, T, 0, st>>>(g);
+  if (parts == 1) return tile_kernel<false, TM, TN, WM, WN, NS><<<grid, T, 0, st>>>(g);
   RowGemmArgs h = g;
   h.c = ws;
-  tile_kernel<false, TM, TN, WM, WN, NS, SPREAD><<<grid, T, 0, st>>>(h);
+  tile_kernel<false, TM, TN, WM, WN, NS><<<grid, T, 0, st>>>(h);
   const unsigned sum = (unsigned)cdiv(cdiv(g.m, 8) * g.n, 256);
   if (parts == 2) parts_kernel<2><<<sum, 256, 0, st>>>(g, ws);
   else if (parts == 4) parts_kernel<4><<<sum, 256, 0, st>>>(g, ws);
   else parts_kernel<8><<<sum, 256, 0, st>>>(g, ws);
+}
+
+template <Kind KIND, int WM, int WN, int SPREAD> void stream_launch(const RowGemmArgs &g, hipStream_t st) {
+  constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, T = 64 * WM * WN;
+  static_assert(SHAPE[KIND].threads == T, "");
+  const unsigned grid = (unsigned)workgroups(KIND, g.m, g.n, g.groups);
+  if (g.groups) stream_kernel<true, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
+  else stream_kernel<false, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
 }
 
 template <Kind KIND> void strip_launch(const RowGemmArgs &g, hipStream_t st) {
@@ -882,10 +1101,10 @@ void gemm_launch(const RowGemmArgs &g, const Choice &c, int *ws, hipStream_t st)
   switch (c.kind) {
     case STRIP: return strip_launch<STRIP>(g, st);
     case STRIP_2: return strip_launch<STRIP_2>(g, st);
-    case TILE_64: return tile_launch<TILE_64, 4, 2, 3, 0>(g, c.parts, ws, st);
-    case TILE_128: return tile_launch<TILE_128, 2, 2, 2, 0>(g, c.parts, ws, st);
-    case TILE_128W: return tile_launch<TILE_128W, 2, 4, 3, 0>(g, c.parts, ws, st);
-    case TILE_256: return tile_launch<TILE_256, 2, 4, 2, 2>(g, c.parts, ws, st);
+    case TILE_64: return tile_launch<TILE_64, 4, 2, 3>(g, c.parts, ws, st);
+    case TILE_128: return tile_launch<TILE_128, 2, 2, 2>(g, c.parts, ws, st);
+    case TILE_128W: return tile_launch<TILE_128W, 2, 4, 3>(g, c.parts, ws, st);
+    default: return stream_launch<STREAM, 2, 4, 2>(g, st);
   }
 }
 

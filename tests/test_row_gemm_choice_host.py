@@ -10,12 +10,10 @@ from hpc_linear_algebra_amd import tlrgemm as T
 def grid(m, n, k, groups=0):
     c = T.tlr_row_gemm_plan(m, n, k, groups)
     assert c.grid_x * c.threads < 1 << 32 and c.grid_y * c.parts < 1 << 16, (m, n, k, groups, c.rows, c.cols, c.grid_x, c.grid_y)
-    across = -(-m // c.rows)
-    if groups == 0:
-        assert c.grid_x * c.grid_y == across * -(-n // c.cols)      # every entry of C has its workgroup
-    else:
-        # whatever the groups' sizes: all but one piece of each, and of the rows behind the last, are whole
-        assert c.parts == 1 and c.grid_x * c.grid_y == across * min(n, (n + (groups + 1) * (c.cols - 1)) // c.cols)
+    # every entry of C has its workgroup; whatever groups' sizes: all but one piece of each, and of the rows behind the
+    # last, are whole.  One workgroup a CU goes through tiles of 256 x 256.
+    tiles = -(-m // c.rows) * (min(n, (n + (groups + 1) * (c.cols - 1)) // c.cols) if groups else -(-n // c.cols))
+    assert c.grid_x * c.grid_y == (tiles if c.rows < 256 else min(tiles, 256)) and (c.parts == 1 or groups == 0)
     return c
 
 
@@ -86,6 +84,9 @@ def test_the_shapes_that_stand_for_each_kernel_take_it_and_leave_none_out():
     for shapes in (row_gemm_shapes.ONE, row_gemm_shapes.GROUPS):
         for want, shape in shapes.items():
             assert kind(*shape) == want, shape
+    for shape in row_gemm_shapes.SEVERAL + row_gemm_shapes.SEVERAL_GROUPS:
+        c = T.tlr_row_gemm_plan(*shape)
+        assert c.rows == c.cols == 256 and -(-shape[0] // 256) * -(-shape[1] // 256) > c.grid_x == 256, shape
     rng = random.Random(2)
     one, groups = set(), set()
     for _ in range(60000):

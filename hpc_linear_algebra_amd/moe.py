@@ -9,7 +9,9 @@ MoELayer is a whole layer for a few tokens: router, softmax, top-k, gated expert
     ...                                         # each expert on its rows
     out = moe.combine(y, weights, order)        # rows back to tokens; differentiable
 
-and Int8Experts, which runs the experts between the two on 8-bit integers.
+and Int8Experts, which runs the experts between the two on 8-bit integers.  A backward
+pass in a captured graph takes torch.autograd.grad, or leaves that no live eager graph
+holds: their accumulation belongs to its stream.
 """
 from __future__ import annotations
 

@@ -144,7 +144,7 @@ struct RowGemmArgs {
   // groups of B's rows (offsets null: one of all rows, with A)
   const int32_t *offsets;
   int64_t code_step, scale_step;        // from one group's A to the next
-  int32_t groups, clear;                // clear: rows behind the last group become zeros
+  int32_t groups, clear;                // clear: rows of no group become zeros
 };
 
 // The rows of B that a workgroup takes, and what belongs to them.
@@ -163,13 +163,13 @@ __device__ __forceinline__ int scan64(int x, int lane) {
 }
 
 // Pieces of TN rows, counted through the groups, those of the rows behind the last group
-// (to be zeroed) at the end.  A lane has one of 64 groups; with more of them they are
+// and before the first (to be zeroed) at the end.  A lane has one of 64 groups; with more of them they are
 // gone through again to find a piece.  Offsets out of order or range give empty or
 // shorter groups.
 template <int TN> struct Pieces {
   const RowGemmArgs &g;
   int lane, lo, hi, mine, upto;         // of the lane's group in the 64 looked at last
-  int in_groups, behind, total;
+  int in_groups, behind, front, in_behind, total;        // in_groups, in_behind: pieces
   __device__ __forceinline__ void look(int e0, int before) {
     const int e = e0 + lane;
     lo = e < g.groups ? min(max(g.offsets[e], 0), g.n) : 0;
@@ -179,17 +179,20 @@ template <int TN> struct Pieces {
   }
   __device__ __forceinline__ Pieces(const RowGemmArgs &args) : g(args), lane(threadIdx.x & 63) {
     behind = g.clear ? min(max(g.offsets[g.groups], 0), g.n) : g.n;
+    front = g.clear ? min(max(g.offsets[0], 0), g.n) : 0;
     in_groups = 0;
     for (int e0 = 0; e0 < g.groups; e0 += 64) {
       look(e0, in_groups);
       in_groups = __builtin_amdgcn_readlane(upto, 63);
     }
-    total = in_groups + (g.n - behind + TN - 1) / TN;
+    in_behind = (g.n - behind + TN - 1) / TN;
+    total = in_groups + in_behind + (front + TN - 1) / TN;
   }
   __device__ __forceinline__ Rows find(int at) {
     if (at >= in_groups) {
-      const int first = behind + (at - in_groups) * TN;
-      return first >= behind && first < g.n ? Rows{first, g.n, g.groups} : Rows{0, 0, -1};
+      const bool last = at - in_groups < in_behind;
+      const int from = last ? behind : 0, end = last ? g.n : front, first = from + (at - in_groups - (last ? 0 : in_behind)) * TN;
+      return first >= from && first < end ? Rows{first, end, g.groups} : Rows{0, 0, -1};
     }
     int e0 = 0, before = 0;
     if (g.groups > 64) look(0, 0);
@@ -843,8 +846,9 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     if (!g.clear) return;
     const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int up = (g.m + 7) / 8;
-    for (int j = begin[g.groups] + blockIdx.x; j < g.n; j += gridDim.x)
-      for (int i = tid; i < up; i += T) store8(g, 8 * i, j, zeros);
+    const int front = begin[0], behind = begin[g.groups], all = front + g.n - behind;
+    for (int x = blockIdx.x; x < all; x += gridDim.x)
+      for (int i = tid; i < up; i += T) store8(g, 8 * i, x < front ? x : behind + x - front, zeros);
   }
 }
 
@@ -892,10 +896,10 @@ struct Choice {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Pieces of B's rows at most: each group ends with a piece that may be short, and so
-// do the rows behind the last.
+// do the rows before the first and behind the last.
 int64_t most_pieces(Kind kind, int64_t n, int32_t groups) {
   const int64_t tn = SHAPE[kind].cols;
-  return groups ? std::min(n, (n + (groups + 1) * (tn - 1)) / tn) : cdiv(n, tn);
+  return groups ? std::min(n, (n + (groups + 2) * (tn - 1)) / tn) : cdiv(n, tn);
 }
 
 // A launch has less than 2^32 threads along x; a workgroup for each tile, but one a CU

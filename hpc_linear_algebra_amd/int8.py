@@ -83,10 +83,10 @@ def gemm(A: RowScaled, B: RowScaled, offsets: Optional[torch.Tensor] = None, out
     a new tensor of type ``dtype``.  Sums are exact (32-bit integers), scaled in
     float and rounded once; k is 131071 at most.
 
-    ``offsets`` (groups + 1, int32, on the GPU, ascending from 0): A has a matrix for
-    each group (3 dimensions), and rows offsets[g] .. offsets[g+1] - 1 of B take the
-    g-th.  Rows behind the last group are zeros in a new result, and left as they are
-    in a given one.
+    ``offsets`` (groups + 1, int32, on the GPU, ascending): A has a matrix for each
+    group (3 dimensions), and rows offsets[g] .. offsets[g+1] - 1 of B take the g-th.
+    Rows of no group, before the first or behind the last, are zeros in a new result,
+    and left as they are in a given one.
 
     It has no gradient: where gradients are on, scales or an out that require one are
     refused."""

@@ -630,13 +630,13 @@ tlr_status tlr_row_quantize(tlr_dtype dt, int64_t rows, int64_t k, const void *X
 /* Rows of B in consecutive groups, each with an A of its own: rows
  * offsets[g] .. offsets[g + 1] - 1 take the codes at A->codes + g*code_step (bytes,
  * a multiple of 16) with the scales at A->scales + g*scale_step (floats).  offsets is
- * device memory, count + 1 int32 in ascending order from 0 to at most n (others are
+ * device memory, count + 1 int32 in ascending order within 0 .. n (others are
  * cut to 0 .. n; groups that end before they begin are empty). */
 typedef struct {
   const int32_t *offsets;
   int64_t code_step, scale_step;
   int32_t count;           /* 1 .. 1024 */
-  int32_t clear;           /* columns of C behind the last group: 0 left as they are, 1 set to zero */
+  int32_t clear;           /* columns of C of no group: 0 left as they are, 1 set to zero */
 } tlr_row_groups;
 
 /*

@@ -78,6 +78,29 @@ def test_every_kernel_of_groups(kind, shape):
     assert (whole[ends[-1]:] == 3.0).all()
 
 
+@pytest.mark.parametrize("shape", [*row_gemm_shapes.GROUPS.values(), *row_gemm_shapes.SEVERAL_GROUPS])
+def test_groups_that_begin_later(shape):
+    """Offsets of some of the experts: rows before the first and behind the last are of no group."""
+    m, n, k, groups = shape
+    g = torch.Generator(device="cuda").manual_seed(n)
+    a, sa = operand(g, groups, m, k=k)
+    b, sb = operand(g, n, k=k)
+    for first, last in ((n // 3, n - n // 4), (n // 2, n // 2), (n, n), (1, n)):
+        ends = [first + (last - first) * i // groups for i in range(groups + 1)]
+        offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        want = torch.zeros(n, m, dtype=torch.float64, device="cuda")
+        for e in range(groups):
+            lo, hi = ends[e], ends[e + 1]
+            if hi > lo:
+                want[lo:hi] = exact(a[e], sa[e], b[lo:hi], sb[lo:hi], k)
+        A, B = int8.RowScaled(a, sa, k), int8.RowScaled(b, sb, k)
+        check(int8.gemm(A, B, offsets=offsets, dtype="f32"), want, "f32")
+        whole = torch.full((n, m), 3.0, device="cuda")
+        int8.gemm(A, B, offsets=offsets, out=whole)
+        check(whole[first:last], want[first:last], "f32")
+        assert (whole[:first] == 3.0).all() and (whole[last:] == 3.0).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("n,k", [(1, 1), (1, 127), (1, 2570), (1, 4096), (1, 4097), (1, 16384), (1, 16385), (2, 100), (2, 8192), (3, 4090),
                                  (4, 2049), (5, 2048), (6, 7), (7, 130), (8, 2048), (8, 2049), (9, 512)])

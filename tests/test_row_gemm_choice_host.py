@@ -10,9 +10,9 @@ from hpc_linear_algebra_amd import tlrgemm as T
 def grid(m, n, k, groups=0):
     c = T.tlr_row_gemm_plan(m, n, k, groups)
     assert c.grid_x * c.threads < 1 << 32 and c.grid_y * c.parts < 1 << 16, (m, n, k, groups, c.rows, c.cols, c.grid_x, c.grid_y)
-    # every entry of C has its workgroup; whatever groups' sizes: all but one piece of each, and of the rows behind the
-    # last, are whole.  One workgroup a CU goes through tiles of 256 x 256.
-    tiles = -(-m // c.rows) * (min(n, (n + (groups + 1) * (c.cols - 1)) // c.cols) if groups else -(-n // c.cols))
+    # every entry of C has its workgroup; whatever groups' sizes: all but one piece of each, of the rows before the first
+    # and of those behind the last are whole.  One workgroup a CU goes through tiles of 256 x 256.
+    tiles = -(-m // c.rows) * (min(n, (n + (groups + 2) * (c.cols - 1)) // c.cols) if groups else -(-n // c.cols))
     assert c.grid_x * c.grid_y == (tiles if c.rows < 256 else min(tiles, 256)) and (c.parts == 1 or groups == 0)
     return c
 
@@ -25,7 +25,7 @@ def test_every_launch_of_an_accepted_size_fits(m, n, k, groups):
     try:
         grid(m, n, k, groups)
     except T.TLRError as e:
-        pieces = min(n, (n + (groups + 1) * 127) // 128) if groups else -(-n // 128)
+        pieces = min(n, (n + (groups + 2) * 127) // 128) if groups else -(-n // 128)
         assert e.status == T.TLR_ERR_INVALID_ARG and -(-m // 128) * pieces >= 1 << 24
 
 
@@ -37,7 +37,7 @@ def test_every_launch_of_a_sampled_size_fits():
         try:
             T.tlr_row_gemm_plan(m, n, k, groups)
         except T.TLRError as e:
-            pieces = min(n, (n + (groups + 1) * 127) // 128) if groups else -(-n // 128)
+            pieces = min(n, (n + (groups + 2) * 127) // 128) if groups else -(-n // 128)
             assert e.status == T.TLR_ERR_INVALID_ARG
             assert max(m, n) > (1 << 31) - 512 or -(-m // 128) * pieces >= 1 << 24
             continue

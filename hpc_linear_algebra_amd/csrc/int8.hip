@@ -163,9 +163,9 @@ __device__ __forceinline__ int scan64(int x, int lane) {
 }
 
 // Pieces of TN rows, counted through the groups, those of the rows behind the last group
-// and before the first (to be zeroed) at the end.  A lane has one of 64 groups; with more of them they are
-// gone through again to find a piece.  Offsets out of order or range give empty or
-// shorter groups.
+// and before the first (to be zeroed) at the end.  A lane has one of 64 groups; with more
+// of them they are gone through again to find a piece.  Offsets out of order or range give
+// empty or shorter groups.
 template <int TN> struct Pieces {
   const RowGemmArgs &g;
   int lane, lo, hi, mine, upto;         // of the lane's group in the 64 looked at last
@@ -425,63 +425,64 @@ __device__ __forceinline__ void meet_lds() {
   asm volatile("" ::: "memory");
 }
 
-// A tile's sums, scaled, to C, up to column `end`.  They go through LDS (ROOM bytes, in
-// passes if they need more), a column's TM entries in a row, 16-byte pieces XOR-placed, so
-// that whole stretches of C's columns are stored, past the caches: 2501 x 1111 x 1747 in
-// 128 x 128 on four waves 12.8 us, through the caches 13.2, straight from the registers,
-// 64 bytes of a column at a time, 15.7.  `rows(i, v)` gives the scales of the tile's rows i ..
-// i + 7, `column(j)` that of its column j; `before` runs before the first store.
-template <typename E, int TM, int TN, int WM, int WN, int ROOM, int RI, int CJ, typename ROWS, typename COLUMN, typename BEFORE>
-__device__ __forceinline__ void store_tile(const RowGemmArgs &g, const i4 (&acc)[RI][CJ], uint8_t *lds, int m0, int n0, int end, int tid, bool zero,
-                                           ROWS rows, COLUMN column, BEFORE before) {
-  constexpr int T = 64 * WM * WN, WIDE = sizeof(E) / 2, PIECES = WIDE * TM / 8;      // pieces of 8 entries; of a column
-  constexpr int SIZE = (int)sizeof(E) * TM * TN, PASSES = (SIZE + ROOM - 1) / ROOM, JS = CJ / PASSES, COLS = T / PIECES;
-  static_assert(CJ % PASSES == 0 && SIZE / PASSES <= ROOM, "");
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+// A wave's sums, scaled, to C from row m0 and column n0 on, up to column `end`.  They go
+// through 2 KB of LDS that only this wave uses, 16 columns of 128 bytes at a time, so that
+// no wave waits for another: a wave's accesses to LDS stay in their order.  STORES of
+// them, where all of the entries exist.
+template <typename E, int RI, int CJ, bool PAST> struct WaveStore {
+  static constexpr int HS = 4 / sizeof(E), STORES = RI * CJ * (int)sizeof(E) / 4;      // pairs of row tiles at a time
+  static __device__ __forceinline__ void run(const RowGemmArgs &g, const i4 (&acc)[RI][CJ], uint8_t *slice, const float *row_scales,
+                                             const float *column_scales, int m0, int n0, int end, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    static_assert(RI % (2 * HS) == 0, "");
 #pragma unroll
-  for (int pass = 0; pass < PASSES; ++pass) {
-    meet_lds();
+    for (int h0 = 0; h0 < RI / 2; h0 += HS) {
+      float sa[HS][8];
 #pragma unroll
-    for (int h = 0; h < RI / 2; ++h) {
-      const int row = wm * (TM / WM) + 32 * h + 8 * q;
-      float sa[8];
-      rows(row, sa);
+      for (int h = 0; h < HS; ++h) __builtin_memcpy(sa[h], __builtin_assume_aligned(row_scales + 32 * (h0 + h) + 8 * q, 16), sizeof sa[h]);
 #pragma unroll
-      for (int jj = 0; jj < JS; ++jj) {
-        const int at = 16 * (wn * JS + jj) + r, j = pass * JS + jj;      // column in LDS
-        const float sb = column(wn * (TN / WN) + 16 * j + r);
-        E v[8];
+      for (int j = 0; j < CJ; ++j) {
+        const float sb = column_scales[16 * j + r];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (E)(zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e]);
-        u4 w[WIDE];
-        __builtin_memcpy(w, v, sizeof v);
+        for (int h = 0; h < HS; ++h) {
+          E v[8];
 #pragma unroll
-        for (int p = 0; p < WIDE; ++p) *reinterpret_cast<u4 *>(lds + at * 16 * PIECES + 16 * ((WIDE * (row >> 3) + p) ^ (at & 15))) = w[p];
-      }
-    }
-    if (pass == 0) before();
-    meet_lds();
-    constexpr int N = 8 / WIDE;                   // entries of a piece
-    const int piece = tid % PIECES, row = m0 + N * piece;
-#pragma unroll 4
-    for (int at = tid / PIECES; at < TN / PASSES; at += COLS) {
-      const int col = n0 + at / (16 * JS) * (TN / WN) + 16 * JS * pass + at % (16 * JS);
-      if (col < end && row < g.m) {
-        const u4 w = *reinterpret_cast<const u4 *>(lds + at * 16 * PIECES + 16 * (piece ^ (at & 15)));
-        E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
-        if (row + N <= g.m) {
-          put16<true>(to, w);
-        } else {
-          E v[N];
-          __builtin_memcpy(v, &w, 16);
+          for (int e = 0; e < 8; ++e) v[e] = (E)((float)acc[2 * (h0 + h) + (e >> 2)][j][e & 3] * sb * sa[h][e]);
+          u4 w[sizeof v / 16];
+          __builtin_memcpy(w, v, sizeof v);
 #pragma unroll
-          for (int e = 0; e < N - 1; ++e)
-            if (row + e < g.m) to[e] = v[e];
+          for (int p = 0; p < (int)(sizeof v / 16); ++p)
+            *reinterpret_cast<u4 *>(slice + r * 128 + 16 * (((4 * h + q) * (int)(sizeof v / 16) + p) ^ (r & 7))) = w[p];
+        }
+        asm volatile("" ::: "memory");
+        u4 w[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int at = 8 * t + (lane >> 3);
+          w[t] = *reinterpret_cast<const u4 *>(slice + at * 128 + 16 * ((lane & 7) ^ (at & 7)));
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          constexpr int N = 16 / sizeof(E);
+          const int col = n0 + 16 * j + 8 * t + (lane >> 3), row = m0 + 32 * h0 + N * (lane & 7);
+          if (col < end && row < g.m) {
+            E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
+            if (row + N <= g.m) {
+              put16<PAST>(to, w[t]);
+            } else {
+              E v[N];
+              __builtin_memcpy(v, &w[t], 16);
+#pragma unroll
+              for (int e = 0; e < N - 1; ++e)
+                if (row + e < g.m) to[e] = v[e];
+            }
+          }
         }
       }
     }
   }
-}
+};
 
 // C tiles of TM x TN, WM x WN waves, each RI x CJ tiles of 16 x 16; blocks of 128
 // columns pass through a ring of NS stages in LDS.  A wave goes through a stage row tile
@@ -641,10 +642,57 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
       }
     return;
   }
+  // C goes through LDS, a column's TM entries in a row, 16-byte pieces XOR-placed, so
+  // that whole stretches of its columns are stored, past the caches: 2501 x 1111 x 1747
+  // in 128 x 128 on four waves 12.8 us, through the caches 13.2, straight from the
+  // registers, 64 bytes of a column at a time, 15.7.
   auto store = [&](auto element) {
-    store_tile<decltype(element), TM, TN, WM, WN, NS * STAGE>(
-        g, acc, lds, m0, n0, g.n, tid, zero, [&](int i, float(&v)[8]) { get8(g.a.scales + m0 + i, g.m - m0 - i, v); },
-        [&](int j) { return g.b.scales[min(n0 + j, g.n - 1)]; }, [] {});
+    typedef decltype(element) E;
+    constexpr int WIDE = sizeof(E) / 2, PIECES = WIDE * TM / 8;       // pieces of 8 entries; of a column
+    constexpr int PASSES = (int)sizeof(E) * TM * TN > NS * STAGE ? 2 : 1, JS = CJ / PASSES, COLS = T / PIECES;
+    static_assert((int)sizeof(E) * TM * TN <= PASSES * NS * STAGE && CJ % PASSES == 0, "");
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < RI / 2; ++h) {
+        const int row = wm * (TM / WM) + 32 * h + 8 * q;
+        float sa[8];
+        get8(g.a.scales + m0 + row, g.m - m0 - row, sa);
+#pragma unroll
+        for (int jj = 0; jj < JS; ++jj) {
+          const int at = 16 * (wn * JS + jj) + r, j = pass * JS + jj;      // column in LDS
+          const float sb = g.b.scales[min(col0 + 16 * j + r, g.n - 1)];
+          E v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (E)(zero ? 0.0f : (float)acc[2 * h + (e >> 2)][j][e & 3] * sb * sa[e]);
+          u4 w[WIDE];
+          __builtin_memcpy(w, v, sizeof v);
+#pragma unroll
+          for (int p = 0; p < WIDE; ++p) *reinterpret_cast<u4 *>(lds + at * 16 * PIECES + 16 * ((WIDE * (row >> 3) + p) ^ (at & 15))) = w[p];
+        }
+      }
+      __syncthreads();
+      constexpr int N = 8 / WIDE;                   // entries of a piece
+      const int piece = tid % PIECES, row = m0 + N * piece;
+#pragma unroll 4
+      for (int at = tid / PIECES; at < TN / PASSES; at += COLS) {
+        const int col = n0 + at / (16 * JS) * (TN / WN) + 16 * JS * pass + at % (16 * JS);
+        if (col < g.n && row < g.m) {
+          const u4 w = *reinterpret_cast<const u4 *>(lds + at * 16 * PIECES + 16 * (piece ^ (at & 15)));
+          E *to = static_cast<E *>(g.c) + (int64_t)col * g.ldc + row;
+          if (row + N <= g.m) {
+            put16<true>(to, w);
+          } else {
+            E v[N];
+            __builtin_memcpy(v, &w, 16);
+#pragma unroll
+            for (int e = 0; e < N - 1; ++e)
+              if (row + e < g.m) to[e] = v[e];
+          }
+        }
+      }
+    }
   };
   if (g.dt == TLR_F32) store(float{});
   else if (g.dt == TLR_F16) store((_Float16)0.0f);
@@ -654,18 +702,22 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 // Large products: one workgroup a CU goes through C tiles of TM x TN, its share of those
 // of its XCD.  As in tile_kernel, a ring of two stages in LDS and one barrier a stage; but
 // the stages of all its tiles are one sequence.  A tile's first stage and its scales are
-// loaded under the last stage of the tile before, and wait in LDS while that is stored
-// through the other buffer: 64 groups, 28672 rows, 2816 x 2048 in 256 x 256 tiles 231 us,
-// with a workgroup for each tile 265; 8192 x 16384 x 1024 137 and 152.  SPREAD loads of
-// the next stage follow each row tile's matrix instructions, which so long a stage likes
-// better than all of them at its start.  Groups' pieces are counted once, into LDS.
-template <bool GROUPED, int TM, int TN, int WM, int WN, int SPREAD>
+// loaded under the last stage of the tile before, its second one before that is stored
+// (64 groups, 28672 rows, 2048 x 1408 in 256 x 256 tiles 106 us, stored through a buffer of
+// the ring 117, which a workgroup for each tile takes 13% longer than; 8192 x 16384 x 1024
+// 138, 150).  SPREAD loads of the next stage follow each row tile's matrix instructions,
+// which so long a stage likes better than all of them at its start.  Groups' pieces are
+// counted once, into LDS.  PAST: stores go past the caches, which wants columns of C that
+// begin with a cache line (8 groups, 16384 rows, 4096 x 4096 241 us, through the caches 273);
+// the pieces of others meet in the caches (6001 x 9000 x 500 47 us, past them 100).
+template <bool GROUPED, bool PAST, int TM, int TN, int WM, int WN, int SPREAD>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void stream_kernel(RowGemmArgs g) {
   constexpr int T = 64 * WM * WN, RI = TM / WM / 16, CJ = TN / WN / 16, NA = TM * 8 / T, NB = TN * 8 / T;
   static_assert(RI % 2 == 0 && SPREAD * RI >= NA + NB, "");
   constexpr int AT_B = TM * QB, STAGE = (TM + TN) * QB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   __shared__ __attribute__((aligned(16))) float scales[2][TM + TN];       // of this tile's rows and columns, and the next one's
+  __shared__ __attribute__((aligned(16))) uint8_t slices[WM * WN][2048];  // results on their way
   __shared__ int upto[GROUPED ? MOST_GROUPS : 1], begin[GROUPED ? MOST_GROUPS + 1 : 1];      // pieces up to and with a group; its rows
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
@@ -768,16 +820,26 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   };
 
   // A tile's first stage is its last block, the one cut at column k; stage i > 0 is block
-  // i - 1.
+  // i - 1.  The second one is loaded before the stores of the tile before, so that the
+  // wait for it, in order, leaves them under way.
+  constexpr int LOADS = NA + NB;
+  auto load_all = [&](uint32_t to) {
+#pragma unroll
+    for (int p = 0; p < LOADS; ++p) load(p, to);
+  };
   Tile now = locate(t);
   int at = 0, turn = 0;       // LDS stage that is computed; scales of this tile
+  int stores = 0;             // of the tile before, behind the second stage's loads; 0: not known
   load_scales(now, 0);
   if (blocks > 0) {
     aim(now, blocks - 1);
-#pragma unroll
-    for (int p = 0; p < NA + NB; ++p) load(p, base);
+    load_all(base);
   }
   meet();
+  if (blocks > 1) {
+    aim(now, 0);
+    load_all(base + STAGE);
+  }
   for (; t < end; t += peers, turn ^= 1) {
     const Tile next = locate(t + peers);
     i4 acc[RI][CJ];
@@ -789,13 +851,8 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
       Panel<TN, T, false>::cut(g.k & (QB - 1), lds + at + AT_B, tid);
       meet_lds();
     }
-    if (blocks < 2) {
-      aim(next, blocks - 1);
-      load_scales(next, turn ^ 1);
-    } else {
-      aim(now, 0);
-    }
-    for (int stage = 0; stage < blocks; ++stage) {
+    // All products of a stage, with the loads of the next one.
+    auto products = [&](auto live) {
       const uint8_t *l = lds + at;
       read_b(l);
       read_a(l, 0);
@@ -806,42 +863,68 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < CJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i & 1][h], b[j][h], acc[i][j], 0, 0, 0);
+        if constexpr (decltype(live)::value)
 #pragma unroll
-        for (int c = 0; c < SPREAD; ++c)
-          if (i * SPREAD + c < NA + NB) load(i * SPREAD + c, base + (STAGE - at));
+          for (int c = 0; c < SPREAD; ++c)
+            if (i * SPREAD + c < LOADS) load(i * SPREAD + c, base + (STAGE - at));
         __builtin_amdgcn_sched_barrier(0);
       }
       at = STAGE - at;
-      if (stage + 1 == blocks) break;
-      if (stage + 2 < blocks) {
-        a_from += QB;
-        b_from += QB;
-        a_bytes -= QB;
-        b_bytes -= QB;
-      } else {
-        aim(next, blocks - 1);
-        load_scales(next, turn ^ 1);
+    };
+    if (blocks > 1) {
+      products(std::false_type{});
+      asm volatile("" ::: "memory");
+      if (stores == 16) __builtin_amdgcn_s_waitcnt(0 | 1 << 14 | 7 << 4);
+      else if (stores == 32) __builtin_amdgcn_s_waitcnt(0 | 2 << 14 | 7 << 4);
+      else __builtin_amdgcn_s_waitcnt(0);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      for (int stage = 1; stage < blocks; ++stage) {
+        if (stage + 1 < blocks) {
+          a_from += QB;
+          b_from += QB;
+          a_bytes -= QB;
+          b_bytes -= QB;
+        } else {
+          load_scales(next, turn ^ 1);
+          aim(next, blocks - 1);
+        }
+        products(std::true_type{});
+        if (stage + 1 < blocks) meet();
       }
-      meet();
+      meet_lds();
+      aim(next, 0);
+      load_all(base + (STAGE - at));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(LOADS | 7 << 4 | 0xf << 8);      // those before them
+      asm volatile("" ::: "memory");
+    } else {
+      load_scales(next, turn ^ 1);
+      if (blocks > 0) {
+        aim(next, blocks - 1);
+        products(std::true_type{});
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0);
+      asm volatile("" ::: "memory");
     }
-    // C through the buffer that is used up.  The next tile's loads are waited for before
-    // the first store, so that the first stage need not wait for stores.
+    stores = 0;
     if (now.m0 >= 0) {        // always so, but for the groups that locate leaves out
       auto store = [&](auto element) {
-        store_tile<decltype(element), TM, TN, WM, WN, STAGE>(
-            g, acc, lds + (blocks > 0 ? STAGE - at : 0), now.m0, now.n0, now.n, tid, false,
-            [&](int i, float(&v)[8]) { __builtin_memcpy(v, __builtin_assume_aligned(scales[turn] + i, 16), sizeof v); },
-            [&](int j) { return scales[turn][TM + j]; }, [] { __builtin_amdgcn_s_waitcnt(0); });
+        typedef WaveStore<decltype(element), RI, CJ, PAST> Store;
+        const int row = wm * (TM / WM), col = wn * (TN / WN);
+        Store::run(g, acc, slices[wave], scales[turn] + row, scales[turn] + TM + col, now.m0 + row, now.n0 + col, now.n, lane);
+        static_assert(Store::STORES == 16 || Store::STORES == 32, "");
+        if (now.m0 + TM <= g.m && now.n0 + TN <= now.n) stores = Store::STORES;
       };
       if (g.dt == TLR_F32) store(float{});
       else if (g.dt == TLR_F16) store((_Float16)0.0f);
       else store((__bf16)0.0f);
-    } else {
-      __builtin_amdgcn_s_waitcnt(0);
     }
     meet_lds();
     now = next;
   }
+  __builtin_amdgcn_s_waitcnt(0);        // no load is left that writes LDS
   if constexpr (GROUPED) {
     if (!g.clear) return;
     const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -1090,8 +1173,11 @@ template <Kind KIND, int WM, int WN, int SPREAD> void stream_launch(const RowGem
   constexpr int TM = SHAPE[KIND].rows, TN = SHAPE[KIND].cols, T = 64 * WM * WN;
   static_assert(SHAPE[KIND].threads == T, "");
   const unsigned grid = (unsigned)workgroups(KIND, g.m, g.n, g.groups);
-  if (g.groups) stream_kernel<true, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
-  else stream_kernel<false, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
+  const bool past = ((reinterpret_cast<uintptr_t>(g.c) | (uintptr_t)(g.ldc * (g.dt == TLR_F32 ? 4 : 2))) & 127) == 0;
+  if (g.groups && past) stream_kernel<true, true, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
+  else if (g.groups) stream_kernel<true, false, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
+  else if (past) stream_kernel<false, true, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
+  else stream_kernel<false, false, TM, TN, WM, WN, SPREAD><<<grid, T, 0, st>>>(g);
 }
 
 template <Kind KIND> void strip_launch(const RowGemmArgs &g, hipStream_t st) {

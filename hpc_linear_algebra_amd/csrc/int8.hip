@@ -1001,7 +1001,7 @@ bool fits(Kind kind, int parts, int64_t m, int64_t n, int32_t groups) {
 
 // The kernel with the least estimated time (us).  The estimates are fits to measured
 // times (graph replays, 16-bit C) of every kernel at 44 products and 22 of groups; the
-// choice costs 0.2% against the best of them, 5% at most.  Some of them, the kernel
+// choice costs 0.2% against the best of them, 4% at most.  Some of them, the kernel
 // chosen first:
 //   4608 x 37 x 2568     strip 8.5, of 32 columns 8.9, 128 x 64 tiles in four parts 9.1
 //   8192 x 24 x 2048     strip of 32 columns 7.5, of 16 9.5

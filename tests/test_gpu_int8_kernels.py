@@ -78,6 +78,28 @@ def test_every_kernel_of_groups(kind, shape):
     assert (whole[ends[-1]:] == 3.0).all()
 
 
+@pytest.mark.parametrize("shape", [(6000, 4500, 130), (4096, 8192, 1024), (5001, 5000, 2000), (2816, 12000, 700, 30), (2050, 15000, 640, 9)])
+def test_large_products_are_the_same_every_time(shape):
+    """On two streams at once: stores of one tile and loads of the next are under way together."""
+    m, n, k, groups = (*shape, 0)[:4]
+    assert T.tlr_row_gemm_plan(m, n, k, groups).rows == 256
+    g = torch.Generator(device="cuda").manual_seed(k)
+    a, sa = operand(g, *([groups] if groups else []), m, k=k)
+    b, sb = operand(g, n, k=k)
+    offsets = torch.arange(groups + 1, dtype=torch.int32, device="cuda") * (n // groups) if groups else None
+    A, B = int8.RowScaled(a, sa, k), int8.RowScaled(b, sb, k)
+    first = {dtype: int8.gemm(A, B, offsets=offsets, dtype=dtype) for dtype in DT}
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for dtype, want in first.items():
+        got = []
+        for i in range(8):
+            with torch.cuda.stream(streams[i % 2]):
+                got.append(int8.gemm(A, B, offsets=offsets, dtype=dtype))
+        torch.cuda.synchronize()
+        assert all(torch.equal(c, want) for c in got)
+
+
 @pytest.mark.parametrize("shape", [*row_gemm_shapes.GROUPS.values(), *row_gemm_shapes.SEVERAL_GROUPS])
 def test_groups_that_begin_later(shape):
     """Offsets of some of the experts: rows before the first and behind the last are of no group."""

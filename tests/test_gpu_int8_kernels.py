@@ -169,3 +169,21 @@ def test_far_operands():
     got = int8.gemm(W, x8, dtype="f32")
     for c in (0, 6000, m - 1):
         assert torch.equal(got[:, c], 32.0 * torch.arange(1, n + 1, device="cuda", dtype=torch.float32))
+
+
+@pytest.mark.parametrize("m,n,groups", [(70000, 1500, 0), (4096, 20000, 20)])
+def test_far_operands_of_large_tiles(m, n, groups):
+    """Rows and groups of weights whose offsets pass 2^32 bytes.  Sums stay below 2^24, scales are 1: exact."""
+    k, all_rows = 65536, m * max(groups, 1)
+    assert T.tlr_row_gemm_plan(m, n, k, groups).rows == 256
+    a = (torch.arange(all_rows, device="cuda") % 101).to(torch.int8)
+    b = (torch.arange(n, device="cuda") % 5 - 2).to(torch.int8)
+    shape = (groups, m) if groups else (m,)
+    A = int8.RowScaled(a.unsqueeze(1).repeat(1, k).view(*shape, k), torch.ones(shape, device="cuda"), k)
+    B = int8.RowScaled(b.unsqueeze(1).repeat(1, k), torch.ones(n, device="cuda"), k)
+    offsets = torch.arange(groups + 1, dtype=torch.int32, device="cuda") * (n // groups) if groups else None
+    got = int8.gemm(A, B, offsets=offsets, dtype="f32")
+    for e in range(max(groups, 1)):
+        rows = slice(e * (n // groups), (e + 1) * (n // groups)) if groups else slice(0, n)
+        want = b[rows].float().unsqueeze(1) * a[e * m:(e + 1) * m].float() * k
+        assert torch.equal(got[rows], want)

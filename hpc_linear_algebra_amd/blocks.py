@@ -223,7 +223,9 @@ def gated_forward(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Te
     """(y, codes, scales) of a 2-d x: y = silu(gate) * up, and x as int8 codes
     (rows, 2, inter rounded up to 16) with a float32 scale for every 128 of them
     (rows, 2, ceil(inter/128)), gate first.  The scale is the largest magnitude over
-    127.  Codes and scales are views of one allocation."""
+    127.  Codes and scales are views of one allocation.  None of them carries a gradient,
+    whatever x does, and a tangent of forward mode is refused: gated is the function
+    for autograd."""
     got = binding().gated_forward(x)
     if type(got) is int:
         T._check(got, "tlr_gated")
@@ -247,8 +249,9 @@ def gated(x: torch.Tensor) -> torch.Tensor:
     one scale for every 128 entries, a byte an entry in place of x; the gradient is
     that at the values the codes stand for (off by at most the block's largest
     magnitude / 254).  A block that holds an infinity or a NaN has NaN gradients.
-    No double backward.  In a captured graph take torch.autograd.grad, or leaves that
-    no live eager graph holds: their accumulation belongs to its stream."""
+    No double backward, no forward mode: a tangent is refused.  In a captured graph take
+    torch.autograd.grad, or leaves that no live eager graph holds: their accumulation
+    belongs to its stream."""
     got = binding().gated(x)
     if type(got) is int:
         T._check(got, "tlr_gated")

@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <stdexcept>
 #include <string>
 #include <vector>
@@ -51,6 +52,17 @@ void *stream_of(const at::Device &d) { return c10::hip::getCurrentHIPStream(d.in
 PyObject *value_error(const char *text) {
   PyErr_SetString(PyExc_ValueError, text);
   return nullptr;
+}
+
+// Whether none of the tensors carries a tangent of forward mode, which no operator here computes: its result would come
+// back without one.  Otherwise the error is set.  Tangents travel where gradients are off as well.
+bool no_tangent(const char *name, std::initializer_list<const at::Tensor *> tensors) {
+  for (const at::Tensor *t : tensors)
+    if (t->defined() && t->_fw_grad(0).defined()) {
+      PyErr_Format(PyExc_RuntimeError, "%s has no forward-mode derivative: call it on tensors without a tangent", name);
+      return false;
+    }
+  return true;
 }
 
 template <typename F> void take(F &entry, PyObject *address) { entry = reinterpret_cast<F>(PyLong_AsVoidPtr(address)); }
@@ -211,7 +223,7 @@ PyObject *moe(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const long most = PyLong_AsLong(args[2]);
   void *ws = PyLong_AsVoidPtr(args[3]);
   const size_t bytes = PyLong_AsSize_t(args[4]);
-  if (PyErr_Occurred()) return nullptr;
+  if (PyErr_Occurred() || !no_tangent("MoELayer", {&x})) return nullptr;
   if (x.dim() != 2 || x.size(1) != layer->hidden || code_of(x) != layer->dt || !x.is_cuda())
     return value_error("MoELayer: x is (tokens, hidden), of the layer's type and on its GPU");
   const int64_t tokens = x.size(0);
@@ -348,6 +360,9 @@ PyObject *row_gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   const long type = PyLong_AsLong(args[7]);
   if (PyErr_Occurred()) return nullptr;
   const at::Tensor &a_codes = THPVariable_Unpack(args[0]), &b_codes = THPVariable_Unpack(args[2]);
+  if (!no_tangent("int8.gemm", {&THPVariable_Unpack(args[1]), &THPVariable_Unpack(args[3])}) ||
+      (args[6] != Py_None && !no_tangent("int8.gemm", {&THPVariable_Unpack(args[6])})))
+    return nullptr;
   tlr_row_matrix A{}, B{};
   if (const char *wrong = row_operand(a_codes, THPVariable_Unpack(args[1]), k, &A)) return value_error(wrong);
   if (const char *wrong = row_operand(b_codes, THPVariable_Unpack(args[3]), k, &B)) return value_error(wrong);
@@ -412,7 +427,7 @@ PyObject *row_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
   at::Tensor x = THPVariable_Unpack(args[0]), ws;
   const at::Tensor &codes = THPVariable_Unpack(args[1]);
   const int64_t k = PyLong_AsLongLong(args[3]);
-  if (PyErr_Occurred()) return nullptr;
+  if (PyErr_Occurred() || !no_tangent("int8.linear", {&x, &THPVariable_Unpack(args[2])})) return nullptr;
   const bool grad = c10::GradMode::is_enabled();
   if (grad && x.requires_grad()) {
     PyErr_SetString(PyExc_RuntimeError, "int8.linear has no backward pass: call it under torch.no_grad() or on detached tensors");
@@ -575,6 +590,7 @@ PyObject *gather(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 3 || !THPVariable_Check(args[0])) return value_error("gather: 3 tensors");
   const at::Tensor &x = THPVariable_Unpack(args[0]);
+  if (!no_tangent("gather", {&x})) return nullptr;
   if (const char *wrong = not_an_order(args[1], args[2], x.device())) return value_error(wrong);
   const Order o(THPVariable_Unpack(args[1]), THPVariable_Unpack(args[2]));
   if (const char *wrong = rows_of(x, o.tokens())) return value_error(wrong);
@@ -593,14 +609,13 @@ PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n != 4 || !THPVariable_Check(args[0]) || !(args[1] == Py_None || THPVariable_Check(args[1]))) return value_error("combine: 4 tensors");
   const at::Tensor &y = THPVariable_Unpack(args[0]);
   at::Tensor w;
+  if (args[1] != Py_None) w = THPVariable_Unpack(args[1]);
+  if (!no_tangent("combine", {&y, &w})) return nullptr;
   if (const char *wrong = not_an_order(args[2], args[3], y.device())) return value_error(wrong);
   const Order o(THPVariable_Unpack(args[2]), THPVariable_Unpack(args[3]));
   if (const char *wrong = rows_of(y, o.tokens() * o.topk())) return value_error(wrong);
-  if (args[1] != Py_None) {
-    w = THPVariable_Unpack(args[1]);
-    if (w.scalar_type() != at::kFloat || w.dim() != 2 || w.size(0) != o.tokens() || w.size(1) != o.topk() || w.device() != y.device())
-      return value_error("weights: a float32 (tokens, topk) tensor on the operands' device is needed");
-  }
+  if (w.defined() && (w.scalar_type() != at::kFloat || w.dim() != 2 || w.size(0) != o.tokens() || w.size(1) != o.topk() || w.device() != y.device()))
+    return value_error("weights: a float32 (tokens, topk) tensor on the operands' device is needed");
   try {
     if (c10::GradMode::is_enabled() && (y.requires_grad() || (w.defined() && w.requires_grad()))) {
       if (!w.defined()) {
@@ -666,6 +681,7 @@ const char *const NOT_GATEABLE = "gated: a float32, float16 or bfloat16 tensor (
 // gated(x) -> y or a status; with its gradient where x has one
 PyObject *gated(PyObject *, PyObject *x_) {
   HANDLE_TH_ERRORS
+  if (THPVariable_Check(x_) && !no_tangent("gated", {&THPVariable_Unpack(x_)})) return nullptr;
   if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_))) return value_error(NOT_GATEABLE);
   const at::Tensor &x = THPVariable_Unpack(x_);
   const c10::DeviceGuard guard(x.device());
@@ -682,6 +698,7 @@ PyObject *gated(PyObject *, PyObject *x_) {
 // gated_forward(x of 2 dimensions) -> (y, codes, scales) or a status
 PyObject *gated_forward(PyObject *, PyObject *x_) {
   HANDLE_TH_ERRORS
+  if (THPVariable_Check(x_) && !no_tangent("gated_forward", {&THPVariable_Unpack(x_)})) return nullptr;
   if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_)) || THPVariable_Unpack(x_).dim() != 2) return value_error(NOT_GATEABLE);
   const at::Tensor &x = THPVariable_Unpack(x_);
   const c10::DeviceGuard guard(x.device());
@@ -701,6 +718,7 @@ PyObject *gated_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   for (const int i : {0, 1, 2})
     if (!THPVariable_Check(args[i])) return value_error("gated_backward: 3 tensors");
   const at::Tensor &dy = THPVariable_Unpack(args[0]), &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]);
+  if (!no_tangent("gated_backward", {&dy, &scales})) return nullptr;
   if (code_of(dy) < 0 || dy.dim() != 2 || !dy.is_cuda()) return value_error("gated_backward: dy is a 2-d float32, float16 or bfloat16 tensor on a GPU");
   const int64_t rows = dy.size(0), inter = dy.size(1), ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
   if (codes.scalar_type() != at::kChar || codes.sizes() != at::IntArrayRef({rows, 2, ld}) || !codes.is_contiguous() || codes.device() != dy.device() ||
@@ -715,10 +733,20 @@ PyObject *gated_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+// no_tangent(name, x): None, or the error
+PyObject *no_tangent(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *name = n == 2 && PyUnicode_Check(args[0]) ? PyUnicode_AsUTF8(args[0]) : nullptr;
+  if (!name || !THPVariable_Check(args[1])) return value_error("no_tangent: a name and a tensor");
+  if (!no_tangent(name, {&THPVariable_Unpack(args[1])})) return nullptr;
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(static_cast<PyObject *(*)(PyObject *, PyObject *const *, Py_ssize_t)>(f))), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(connect), METHOD(quantize), METHOD(gemm), METHOD(moe), METHOD(row_quantize), METHOD(row_gemm),
                          METHOD(row_linear), METHOD(sort), METHOD(gather), METHOD(combine), {"gated", gated, METH_O, nullptr},
-                         {"gated_forward", gated_forward, METH_O, nullptr}, METHOD(gated_backward), {nullptr, nullptr, 0, nullptr}};
+                         {"gated_forward", gated_forward, METH_O, nullptr}, METHOD(gated_backward), METHOD(no_tangent), {nullptr, nullptr, 0, nullptr}};
 #undef METHOD
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -9,8 +9,9 @@ plumbing around tlr_row_quantize and tlr_row_gemm, include/tlrgemm.h).
     order = moe.sort(ids, len(experts))
     y = int8.gemm(E8, int8.quantize(x, rows=order.rows), offsets=order.offsets)
 
-For inference: nothing here has a gradient.  Every call runs on torch's current
-stream of the operands' device.
+For inference: nothing here has a gradient, and codes, being integers, pass none on.
+A tangent of forward mode is refused by the products.  Every call runs on torch's
+current stream of the operands' device.
 """
 from __future__ import annotations
 
@@ -89,7 +90,7 @@ def gemm(A: RowScaled, B: RowScaled, offsets: Optional[torch.Tensor] = None, out
     and left as they are in a given one.
 
     It has no gradient: where gradients are on, scales or an out that require one are
-    refused."""
+    refused (codes made of an x that requires one are not: quantize has cut it)."""
     if A.k != B.k:
         raise ValueError(f"gemm: contraction lengths differ ({A.k} and {B.k})")
     new = _NEW.get(dtype)
@@ -104,7 +105,7 @@ def gemm(A: RowScaled, B: RowScaled, offsets: Optional[torch.Tensor] = None, out
 def linear(x: torch.Tensor, w: RowScaled) -> torch.Tensor:
     """x W^T for x (..., k) in float32, float16 or bfloat16, quantized with a scale
     for each token, and a weight of 2 dimensions; in x's type.  There is no backward
-    pass: where gradients are on, an x that requires one is refused."""
+    pass: where gradients are on, an x or scales that require one are refused."""
     got = binding().row_linear(x, w.codes, w.scales, w.k)
     if type(got) is int:
         T._check(got, "tlr_row_linear")

@@ -59,7 +59,7 @@ class MoELayer:
     the layer has to live until the call's work has ended.
 
     There is no backward pass: where gradients are on, an x or weights that
-    require one are refused.
+    require one are refused, and an x with a tangent of forward mode always.
     """
 
     def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, topk: int,
@@ -155,7 +155,7 @@ def gather(x: torch.Tensor, order: Order) -> torch.Tensor:
     """Each token x (tokens, hidden) at the rows of its assignments, (tokens * topk,
     hidden); rows of no expert are zeros.  The gradient of a token is the sum of its
     rows', in float, rounded once, in the order of its assignments; rows of no expert
-    add nothing.  No double backward."""
+    add nothing.  No double backward, no forward mode: a tangent is refused."""
     got = binding().gather(x, order.place, order.offsets)
     if type(got) is int:
         T._check(got, "tlr_expert_gather")
@@ -166,7 +166,8 @@ def combine(y: torch.Tensor, weights: Optional[torch.Tensor], order: Order) -> t
     """The rows y (tokens * topk, hidden) of each token's assignments added with its
     weights (tokens, topk), float32 (None: 1): (tokens, hidden) in y's type, sums in
     float in the order of the assignments.  Rows of no expert are not read.  Gradients
-    of y (zeros for rows of no expert) and of the weights.  No double backward."""
+    of y (zeros for rows of no expert) and of the weights.  No double backward, no
+    forward mode: a tangent is refused."""
     got = binding().combine(y, weights, order.place, order.offsets)
     if type(got) is int:
         T._check(got, "tlr_expert_combine")
@@ -182,7 +183,9 @@ class Int8Experts:
 
     A call sorts the tokens by expert, quantizes them on the way to their rows,
     multiplies each expert's rows with its weights, and the same for the gated
-    results; every product rounds to x's type.  No backward pass.
+    results; every product rounds to x's type.  No backward pass, no forward mode:
+    where gradients are on, x or weights that require one are refused, and a tangent
+    always.
     """
 
     def __init__(self, gate_up: int8.RowScaled, down: int8.RowScaled):
@@ -198,6 +201,8 @@ class Int8Experts:
         weights (tokens, topk), float32, for its choices ids; in x's type."""
         if torch.is_grad_enabled() and (x.requires_grad or weights.requires_grad):
             raise RuntimeError("Int8Experts has no backward pass: call it under torch.no_grad() or on detached tensors")
+        for t in (x, weights):
+            binding().no_tangent("Int8Experts", t)
         if x.dim() != 2 or x.shape[1] != self.hidden or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
             raise ValueError(f"Int8Experts: x is (tokens, {self.hidden}) and ids (tokens, topk)")
         dtype = _NAME.get(x.dtype)

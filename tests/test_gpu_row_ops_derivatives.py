@@ -1,0 +1,37 @@
+"""What torch is told of the operators on sorted rows, of the gated activation and of the linear layers: tangents, traces,
+results changed in place, memory that waits for the backward pass."""
+import pytest
+import torch
+import torch.autograd.forward_ad as forward
+
+from hpc_linear_algebra_amd import blocks, int8, moe
+
+pytestmark = pytest.mark.gpu
+
+
+def order_of(tokens, topk, experts):
+    return moe.sort(torch.randint(0, experts, (tokens, topk), device="cuda"), experts)
+
+
+def test_tangents_are_refused():
+    """A result without its tangent would be a derivative of zero."""
+    order = order_of(5, 2, 3)
+    x, y, w, z = (torch.randn(*s, device="cuda") for s in ((5, 16), (10, 16), (5, 2), (2, 3, 64)))
+    W, x8 = int8.quantize(torch.randn(8, 16, device="cuda")), int8.quantize(x)
+    G, D = int8.quantize(torch.randn(3, 32, 16, device="cuda")), int8.quantize(torch.randn(3, 16, 16, device="cuda"))
+    _, codes, scales = blocks.gated_forward(z[0])
+    layer = moe.MoELayer(torch.randn(4, 16, device="cuda").half(), torch.randn(4, 32, 16, device="cuda").half(),
+                         torch.randn(4, 16, 16, device="cuda").half(), 2)
+    ids = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    calls = [(lambda v: moe.gather(v, order), x), (lambda v: moe.combine(v, w, order), y), (lambda v: moe.combine(y, v, order), w),
+             (lambda v: moe.combine(v, None, order), y), (blocks.gated, z), (blocks.gated, z[0]), (blocks.gated_forward, z[0]),
+             (lambda v: blocks.gated_backward(v, codes, scales), torch.randn(3, 32, device="cuda")), (lambda v: int8.linear(v, W), x),
+             (lambda v: int8.gemm(int8.RowScaled(W.codes, v, 16), x8), W.scales), (lambda v: int8.gemm(W, x8, out=v), torch.zeros(5, 8, device="cuda")),
+             (lambda v: moe.Int8Experts(G, D)(v, ids, w), x), (lambda v: moe.Int8Experts(G, D)(x, ids, v), w), (layer, x.half())]
+    for call, v in calls:
+        with forward.dual_level():
+            for leaf in (v, v.detach().requires_grad_()):
+                with torch.no_grad(), pytest.raises(RuntimeError, match="forward-mode derivative"):
+                    call(forward.make_dual(leaf, torch.ones_like(leaf)))
+            with torch.no_grad():
+                call(v)

@@ -249,9 +249,9 @@ def gated(x: torch.Tensor) -> torch.Tensor:
     one scale for every 128 entries, a byte an entry in place of x; the gradient is
     that at the values the codes stand for (off by at most the block's largest
     magnitude / 254).  A block that holds an infinity or a NaN has NaN gradients.
-    No double backward, no forward mode: a tangent is refused.  In a captured graph take
-    torch.autograd.grad, or leaves that no live eager graph holds: their accumulation
-    belongs to its stream."""
+    No double backward, no forward mode: a tangent is refused, and a call within
+    torch.jit.trace.  In a captured graph take torch.autograd.grad, or leaves that no
+    live eager graph holds: their accumulation belongs to its stream."""
     got = binding().gated(x)
     if type(got) is int:
         T._check(got, "tlr_gated")

@@ -4,6 +4,7 @@
 // Python 8.9 and 7.1).  The C entries are handed over by address at start-up; a status other than
 // TLR_OK is returned as an int for the caller to raise.
 #include <ATen/ATen.h>
+#include <ATen/TracerMode.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
@@ -63,6 +64,14 @@ bool no_tangent(const char *name, std::initializer_list<const at::Tensor *> tens
       return false;
     }
   return true;
+}
+
+// Whether torch.jit.trace is not at work, which would record a call as the allocation of its result alone.  Otherwise the
+// error is set.
+bool no_trace(const char *name) {
+  if (!at::tracer::impl::is_dispatch_enabled()) return true;
+  PyErr_Format(PyExc_RuntimeError, "%s cannot be traced: torch.jit.trace would record an empty result", name);
+  return false;
 }
 
 template <typename F> void take(F &entry, PyObject *address) { entry = reinterpret_cast<F>(PyLong_AsVoidPtr(address)); }
@@ -297,6 +306,7 @@ tlr_status quantize_rows(const at::Tensor &x, const int32_t *index, int64_t rows
 PyObject *row_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 2 || !THPVariable_Check(args[0])) return value_error("quantize: a tensor and rows");
+  if (!no_trace("int8.quantize")) return nullptr;
   at::Tensor x = THPVariable_Unpack(args[0]), index;
   if (const char *wrong = quantizable(x)) return value_error(wrong);
   if (args[1] != Py_None) {
@@ -360,7 +370,7 @@ PyObject *row_gemm(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
   const long type = PyLong_AsLong(args[7]);
   if (PyErr_Occurred()) return nullptr;
   const at::Tensor &a_codes = THPVariable_Unpack(args[0]), &b_codes = THPVariable_Unpack(args[2]);
-  if (!no_tangent("int8.gemm", {&THPVariable_Unpack(args[1]), &THPVariable_Unpack(args[3])}) ||
+  if (!no_trace("int8.gemm") || !no_tangent("int8.gemm", {&THPVariable_Unpack(args[1]), &THPVariable_Unpack(args[3])}) ||
       (args[6] != Py_None && !no_tangent("int8.gemm", {&THPVariable_Unpack(args[6])})))
     return nullptr;
   tlr_row_matrix A{}, B{};
@@ -427,7 +437,7 @@ PyObject *row_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
   at::Tensor x = THPVariable_Unpack(args[0]), ws;
   const at::Tensor &codes = THPVariable_Unpack(args[1]);
   const int64_t k = PyLong_AsLongLong(args[3]);
-  if (PyErr_Occurred() || !no_tangent("int8.linear", {&x, &THPVariable_Unpack(args[2])})) return nullptr;
+  if (PyErr_Occurred() || !no_trace("int8.linear") || !no_tangent("int8.linear", {&x, &THPVariable_Unpack(args[2])})) return nullptr;
   const bool grad = c10::GradMode::is_enabled();
   if (grad && x.requires_grad()) {
     PyErr_SetString(PyExc_RuntimeError, "int8.linear has no backward pass: call it under torch.no_grad() or on detached tensors");
@@ -462,7 +472,7 @@ PyObject *sort(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n != 2 || !THPVariable_Check(args[0])) return value_error("sort: a tensor and a number");
   at::Tensor ids = THPVariable_Unpack(args[0]);
   const long experts = PyLong_AsLong(args[1]);
-  if (PyErr_Occurred()) return nullptr;
+  if (PyErr_Occurred() || !no_trace("sort")) return nullptr;
   if (ids.dim() != 2 || !ids.is_cuda() || (ids.scalar_type() != at::kInt && ids.scalar_type() != at::kLong))
     return value_error("sort: ids is a (tokens, topk) int32 or int64 tensor on a GPU");
   if (experts < 1 || experts > 1024 || ids.size(1) < 1 || ids.size(1) > 64) return value_error("sort: experts are 1 .. 1024, topk 1 .. 64");
@@ -590,7 +600,7 @@ PyObject *gather(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 3 || !THPVariable_Check(args[0])) return value_error("gather: 3 tensors");
   const at::Tensor &x = THPVariable_Unpack(args[0]);
-  if (!no_tangent("gather", {&x})) return nullptr;
+  if (!no_trace("gather") || !no_tangent("gather", {&x})) return nullptr;
   if (const char *wrong = not_an_order(args[1], args[2], x.device())) return value_error(wrong);
   const Order o(THPVariable_Unpack(args[1]), THPVariable_Unpack(args[2]));
   if (const char *wrong = rows_of(x, o.tokens())) return value_error(wrong);
@@ -610,7 +620,7 @@ PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const at::Tensor &y = THPVariable_Unpack(args[0]);
   at::Tensor w;
   if (args[1] != Py_None) w = THPVariable_Unpack(args[1]);
-  if (!no_tangent("combine", {&y, &w})) return nullptr;
+  if (!no_trace("combine") || !no_tangent("combine", {&y, &w})) return nullptr;
   if (const char *wrong = not_an_order(args[2], args[3], y.device())) return value_error(wrong);
   const Order o(THPVariable_Unpack(args[2]), THPVariable_Unpack(args[3]));
   if (const char *wrong = rows_of(y, o.tokens() * o.topk())) return value_error(wrong);
@@ -681,7 +691,7 @@ const char *const NOT_GATEABLE = "gated: a float32, float16 or bfloat16 tensor (
 // gated(x) -> y or a status; with its gradient where x has one
 PyObject *gated(PyObject *, PyObject *x_) {
   HANDLE_TH_ERRORS
-  if (THPVariable_Check(x_) && !no_tangent("gated", {&THPVariable_Unpack(x_)})) return nullptr;
+  if (!no_trace("gated") || (THPVariable_Check(x_) && !no_tangent("gated", {&THPVariable_Unpack(x_)}))) return nullptr;
   if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_))) return value_error(NOT_GATEABLE);
   const at::Tensor &x = THPVariable_Unpack(x_);
   const c10::DeviceGuard guard(x.device());
@@ -698,7 +708,7 @@ PyObject *gated(PyObject *, PyObject *x_) {
 // gated_forward(x of 2 dimensions) -> (y, codes, scales) or a status
 PyObject *gated_forward(PyObject *, PyObject *x_) {
   HANDLE_TH_ERRORS
-  if (THPVariable_Check(x_) && !no_tangent("gated_forward", {&THPVariable_Unpack(x_)})) return nullptr;
+  if (!no_trace("gated_forward") || (THPVariable_Check(x_) && !no_tangent("gated_forward", {&THPVariable_Unpack(x_)}))) return nullptr;
   if (!THPVariable_Check(x_) || !gateable(THPVariable_Unpack(x_)) || THPVariable_Unpack(x_).dim() != 2) return value_error(NOT_GATEABLE);
   const at::Tensor &x = THPVariable_Unpack(x_);
   const c10::DeviceGuard guard(x.device());
@@ -718,7 +728,7 @@ PyObject *gated_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   for (const int i : {0, 1, 2})
     if (!THPVariable_Check(args[i])) return value_error("gated_backward: 3 tensors");
   const at::Tensor &dy = THPVariable_Unpack(args[0]), &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]);
-  if (!no_tangent("gated_backward", {&dy, &scales})) return nullptr;
+  if (!no_trace("gated_backward") || !no_tangent("gated_backward", {&dy, &scales})) return nullptr;
   if (code_of(dy) < 0 || dy.dim() != 2 || !dy.is_cuda()) return value_error("gated_backward: dy is a 2-d float32, float16 or bfloat16 tensor on a GPU");
   const int64_t rows = dy.size(0), inter = dy.size(1), ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
   if (codes.scalar_type() != at::kChar || codes.sizes() != at::IntArrayRef({rows, 2, ld}) || !codes.is_contiguous() || codes.device() != dy.device() ||

@@ -10,8 +10,9 @@ plumbing around tlr_row_quantize and tlr_row_gemm, include/tlrgemm.h).
     y = int8.gemm(E8, int8.quantize(x, rows=order.rows), offsets=order.offsets)
 
 For inference: nothing here has a gradient, and codes, being integers, pass none on.
-A tangent of forward mode is refused by the products.  Every call runs on torch's
-current stream of the operands' device.
+A tangent of forward mode is refused by the products, and every call within
+torch.jit.trace, which records torch's own operations alone.  Every call runs on
+torch's current stream of the operands' device.
 """
 from __future__ import annotations
 

@@ -9,7 +9,8 @@ MoELayer is a whole layer for a few tokens: router, softmax, top-k, gated expert
     ...                                         # each expert on its rows
     out = moe.combine(y, weights, order)        # rows back to tokens; differentiable
 
-and Int8Experts, which runs the experts between the two on 8-bit integers.  A backward
+and Int8Experts, which runs the experts between the two on 8-bit integers.  Within
+torch.jit.trace, which records torch's own operations alone, these are refused.  A backward
 pass in a captured graph takes torch.autograd.grad, or leaves that no live eager graph
 holds: their accumulation belongs to its stream.
 """

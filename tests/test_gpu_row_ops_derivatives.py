@@ -35,3 +35,15 @@ def test_tangents_are_refused():
                     call(forward.make_dual(leaf, torch.ones_like(leaf)))
             with torch.no_grad():
                 call(v)
+
+
+def test_traces_are_refused():
+    order = order_of(5, 2, 3)
+    W = int8.quantize(torch.randn(8, 16, device="cuda"))
+    x, y = torch.randn(5, 16, device="cuda"), torch.randn(10, 16, device="cuda")
+    for call, v in ((lambda v: moe.gather(v, order), x), (lambda v: moe.combine(v, None, order), y), (blocks.gated, x), (lambda v: int8.linear(v, W), x),
+                    (lambda v: int8.quantize(v).scales, x), (lambda v: moe.sort(v, 3).place, order.place)):
+        for leaf in (v, v.clone().requires_grad_()) if v.is_floating_point() else (v,):
+            with torch.no_grad(), pytest.raises(RuntimeError, match="cannot be traced"):
+                torch.jit.trace(call, (leaf,), check_trace=False)
+        call(v)

@@ -43,3 +43,19 @@ def test_tangents_are_refused(name, grad):
             call(x)
         with forward._set_fwd_grad_enabled(False), pytest.raises(ValueError):
             call(forward.make_dual(x, torch.ones_like(x)))
+
+
+@pytest.mark.parametrize("name", [*CALLS, "sort", "quantize", "quantize of rows"])
+def test_traces_are_refused(name):
+    """torch.jit.trace records torch's own operations alone: of these calls that would be an empty result."""
+    call, x = CALLS.get(name) or {"sort": (lambda ids: moe.sort(ids, 4), PLACE), "quantize": (int8.quantize, ROW),
+                                  "quantize of rows": (lambda r: int8.quantize(ROW, rows=r), PLACE[0])}[name]
+
+    def traced(v):
+        got = call(v)
+        return got if torch.is_tensor(got) else got[0]
+
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        torch.jit.trace(traced, (x,), check_trace=False)
+    with pytest.raises(ValueError):                            # and later calls are what they were
+        call(x)

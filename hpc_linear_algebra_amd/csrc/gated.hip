@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "int8.h"
 #include "tlr_ops.h"
@@ -19,19 +20,35 @@ namespace tlr {
 
 namespace {
 
-// 1 / (1 + exp(-g)) and 1 minus it, both to float precision: the exponential of a
-// negative number never overflows, and neither result comes from a difference.
+// 1 / (1 + exp(-g)) and 1 minus it, both to float precision where they are normal
+// floats: the exponential of a negative number never overflows, and neither result
+// comes from a difference.  The hardware's exponential has no results below 2^-126
+// but 0, so the smaller of the two is 0 from |g| = 87.34 on.  Beside the larger one
+// that is nothing; the sigmoid of a far negative gate is replaced (below).
 struct Sigmoid {
   float s, rest;
 };
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
   // exp(-|g|) = 2^t; t's rounding is carried along, which keeps full precision
-  // where t is large.  Past -150 it is 0 (and an infinity gives no difference of two)
+  // where t is large.  Past -150 it is 0 anyway (and an infinity gives no difference of two)
   const float a = fmaxf(-__builtin_fabsf(g), -150.0f), log2e = 0x1.715476p0f, low = 0x1.4ae0cp-26f;
   const float t = a * log2e, c = __builtin_fmaf(a, low, __builtin_fmaf(a, log2e, -t));
   const float p = __builtin_amdgcn_exp2f(t), e = __builtin_fmaf(p * 0x1.62e43p-1f, c, p);
   const float r = __builtin_amdgcn_rcpf(1.0f + e), n = e * r;
   return g < 0.0f ? Sigmoid{n, r} : Sigmoid{r, n};
+}
+
+// Gates whose sigmoid is exp(g) to more than a double's precision and near or below the
+// smallest normal float.  Times large factors it may be an ordinary number (-88 and
+// 1e38: -53), so that products with it are in doubles.  An infinite one stays: -inf times 0.
+// Halves are 65504 at most: three of them times exp(-86) are nothing.
+constexpr float FAR = 86.0f;
+template <typename T> constexpr bool WIDE_RANGE = !std::is_same<T, _Float16>::value;
+__device__ __forceinline__ bool is_far(float g) { return g < -FAR && g >= -0x1.fffffep127f; }
+__device__ __forceinline__ double far_sigmoid(float g) {
+  const float a = fmaxf(g, -700.0f), log2e = 0x1.715476p0f, low = 0x1.4ae0cp-26f;       // 2^-1010: nothing times any floats
+  const float n = __builtin_rintf(a * log2e);
+  return ldexp((double)__builtin_amdgcn_exp2f(__builtin_fmaf(a, low, __builtin_fmaf(a, log2e, -n))), (int)n);
 }
 
 struct GatedArgs {
@@ -64,16 +81,22 @@ template <typename T, bool KEEP> __global__ __launch_bounds__(256) void gated_ke
     xu.get(u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = g[e] * sigmoid(g[e]).s * u[e];
+    uint32_t top[2] = {0, 0};           // largest magnitudes of the lane's g and u
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top[0] = max(top[0], mag(g[e]));
+    if (WIDE_RANGE<T> && top[0] > mag(FAR))
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (is_far(g[e])) y[e] = (float)(g[e] * far_sigmoid(g[e]) * u[e]);
     put8(static_cast<T *>(a.y) + row * a.ldy + col, left, y);
     if constexpr (KEEP) {
       const int64_t at = 2 * row;
 #pragma unroll
+      for (int e = 0; e < 8; ++e) top[1] = max(top[1], mag(u[e]));
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float(&v)[8] = h ? u : g;
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, mag(v[e]));
-        const float s = int8_scale(max16(m));
+        const float s = int8_scale(max16(top[h]));
         if (c == 0) a.scales[(at + h) * a.lds + q] = s;
         if (left > 0) *reinterpret_cast<u2 *>(a.codes + (at + h) * a.ldq + col) = int8_codes8(v, s, 1.0f / s);
       }
@@ -94,6 +117,7 @@ template <typename T> __global__ __launch_bounds__(256) void gated_grad_kernel(G
     const float sg = a.scales[at * a.lds + q], su = a.scales[(at + 1) * a.lds + q];
     float dy[8], dg[8], du[8];
     get8(static_cast<const T *>(a.dy) + row * a.lddy + col, left, dy);
+    uint32_t least = 0xffffffffu;       // of the dy, without their signs; zeros are above all others
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float g = sg * code(cg, e), u = su * code(cu, e);
@@ -101,7 +125,22 @@ template <typename T> __global__ __launch_bounds__(256) void gated_grad_kernel(G
       const float d = dy[e] * s.s;
       dg[e] = d * u * __builtin_fmaf(g, s.rest, 1.0f);
       du[e] = d * g;
+      least = min(least, 2 * __builtin_bit_cast(uint32_t, dy[e]) - 1);
     }
+    // Where dy s falls below the normal floats, u or g may bring the product back: such ones again, in doubles.  There are none
+    // in a block whose gates are 32 at most (the sigmoid 2^-47 at least) where dy is 0 or 2^-79 at least.
+    if (WIDE_RANGE<T> && (sg > 32.0f / 128 || least < 2 * __builtin_bit_cast(uint32_t, 0x1p-79f) - 1))
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = sg * code(cg, e), u = su * code(cu, e);
+        const Sigmoid s = sigmoid(g);
+        const bool far = is_far(g);
+        if (dy[e] != 0.0f && (far || __builtin_fabsf(dy[e] * s.s) < 0x1p-126f)) {
+          const double d = dy[e] * (far ? far_sigmoid(g) : s.s);
+          dg[e] = (float)(d * u * (far ? 1.0f + g : __builtin_fmaf(g, s.rest, 1.0f)));
+          du[e] = (float)(d * g);
+        }
+      }
     T *dx = static_cast<T *>(a.dx) + row * a.lddx + col;
     put8(dx, left, dg);
     put8(dx + a.inter, left, du);

@@ -728,7 +728,9 @@ tlr_status tlr_expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, i
 
 /*
  * tlr_gated: Y = silu(g) u for rows of X that hold `inter` entries of g, then as many
- * of u; silu(g) = g / (1 + exp(-g)), in float, Y rounded once.
+ * of u; silu(g) = g / (1 + exp(-g)), in float, Y rounded once.  A far negative gate
+ * counts for what it is where the other factors are large, though exp(g) is no normal
+ * float: the products with it are in doubles, here and in the gradient.
  *   codes, ldq, scales, lds   NULL, or where the row is kept for the backward pass:
  *           int8 codes of g at codes + 2*i*ldq and of u at codes + (2*i + 1)*ldq,
  *           one scale for every 128 of them (the last ones fewer) at scales + 2*i*lds

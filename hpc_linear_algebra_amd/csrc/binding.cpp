@@ -569,24 +569,36 @@ struct Gather : torch::autograd::Function<Gather> {
   }
 };
 
+// y's count of changes without its memory: saved in its place, a change of y is noticed all the same.
+at::Tensor changes_of(const at::Tensor &y) {
+  at::Tensor t = at::empty({0}, y.options());
+  t.unsafeGetTensorImpl()->set_version_counter(y.unsafeGetTensorImpl()->version_counter());
+  return t;
+}
+
+// The rows are kept for the gradient of the weights alone (8192 x 8 x 4096 in bf16: 512 MB).
 struct Combine : torch::autograd::Function<Combine> {
   static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &y, const at::Tensor &w, const at::Tensor &place,
                             const at::Tensor &offsets) {
-    ctx->save_for_backward({y, w, place, offsets});
+    ctx->save_for_backward({w.requires_grad() ? y : changes_of(y), w, place, offsets});
     return combine_rows(y, w, Order(place, offsets));
   }
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, const torch::autograd::variable_list &grads) {
     const auto saved = ctx->get_saved_variables();
     const Order o(saved[2], saved[3]);
     const c10::DeviceGuard guard(grads[0].device());
-    const at::Tensor dout = with_rows(grads[0]), y = with_rows(saved[0]), w = saved[1].contiguous();
-    at::Tensor dy, dw;
-    if (ctx->needs_input_grad(0)) dy = like(y, y.size(0), y.size(1));
-    if (ctx->needs_input_grad(1)) dw = like(w, o.tokens(), o.topk());
-    must(combine_grad_entry((tlr_dtype)code_of(y), o.tokens(), (int32_t)o.topk(), y.size(1), dout.data_ptr(), row_stride(dout), y.data_ptr(),
-                            row_stride(y), o.at(), o.end(), static_cast<const float *>(w.data_ptr()), dy.defined() ? dy.data_ptr() : nullptr,
-                            dy.defined() ? row_stride(dy) : y.size(1), dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr,
-                            stream_of(dout.device())));
+    const at::Tensor dout = with_rows(grads[0]), w = saved[1].contiguous();
+    const int64_t hidden = dout.size(1);
+    at::Tensor y, dy, dw;
+    if (ctx->needs_input_grad(0)) dy = like(dout, o.tokens() * o.topk(), hidden);
+    if (ctx->needs_input_grad(1)) {
+      y = with_rows(saved[0]);
+      dw = like(w, o.tokens(), o.topk());
+    }
+    must(combine_grad_entry((tlr_dtype)code_of(dout), o.tokens(), (int32_t)o.topk(), hidden, dout.data_ptr(), row_stride(dout),
+                            y.defined() ? y.data_ptr() : nullptr, y.defined() ? row_stride(y) : hidden, o.at(), o.end(),
+                            static_cast<const float *>(w.data_ptr()), dy.defined() ? dy.data_ptr() : nullptr, dy.defined() ? row_stride(dy) : hidden,
+                            dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr, stream_of(dout.device())));
     return once("combine", {dy, dw, at::Tensor(), at::Tensor()});
   }
 };

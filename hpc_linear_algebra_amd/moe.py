@@ -167,7 +167,8 @@ def combine(y: torch.Tensor, weights: Optional[torch.Tensor], order: Order) -> t
     """The rows y (tokens * topk, hidden) of each token's assignments added with its
     weights (tokens, topk), float32 (None: 1): (tokens, hidden) in y's type, sums in
     float in the order of the assignments.  Rows of no expert are not read.  Gradients
-    of y (zeros for rows of no expert) and of the weights.  No double backward, no
+    of y (zeros for rows of no expert) and of the weights; y's memory is kept for the
+    latter alone, though a change of y in place is always noticed.  No double backward, no
     forward mode: a tangent is refused."""
     got = binding().combine(y, weights, order.place, order.offsets)
     if type(got) is int:

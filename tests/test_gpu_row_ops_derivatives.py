@@ -47,3 +47,41 @@ def test_traces_are_refused():
             with torch.no_grad(), pytest.raises(RuntimeError, match="cannot be traced"):
                 torch.jit.trace(call, (leaf,), check_trace=False)
         call(v)
+
+
+@pytest.mark.parametrize("weights", ["none", "given", "trained"])
+def test_rows_are_kept_for_gradients_of_the_weights_alone(weights):
+    """The gradient of the rows needs the weights, not the rows."""
+    tokens, topk, hidden = 512, 4, 256
+    order = order_of(tokens, topk, 8)
+    base = torch.randn(tokens * topk, hidden, device="cuda", requires_grad=True)
+    w = None if weights == "none" else torch.rand(tokens, topk, device="cuda", requires_grad=weights == "trained")
+    dout = torch.randn(tokens, hidden, device="cuda")
+    want, = torch.autograd.grad(moe.combine(base, w, order), [base], dout)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    out = moe.combine(base * 1.0, w, order)
+    kept = torch.cuda.memory_allocated() - before - 4 * tokens * hidden - (4 * tokens * topk if w is None else 0)
+    assert kept == (4 * tokens * topk * hidden if weights == "trained" else 0)
+    got, = torch.autograd.grad(out, [base], dout)
+    assert torch.equal(got, want)
+    y = torch.zeros(hidden, tokens * topk, device="cuda").t().copy_(base.detach()).requires_grad_()          # columns, not rows
+    got, = torch.autograd.grad(moe.combine(y, w, order), [y], dout)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("trained", [True, False])
+def test_changes_in_place_are_noticed_whether_rows_are_kept_or_not(trained):
+    order = order_of(5, 2, 3)
+    base, w = torch.randn(10, 16, device="cuda", requires_grad=True), torch.rand(5, 2, device="cuda", requires_grad=trained)
+    y = base * 1.0
+    out = moe.combine(y, w, order)
+    y.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    y = base * 1.0
+    out = moe.combine(y, w, order)
+    with torch.no_grad():
+        w.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()

@@ -655,13 +655,15 @@ PyObject *combine(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // ---- gated activation -----------------------------------------------------------------------------------
 
-// y (rows, inter) of x (rows, 2 inter); with codes (rows, 2, ld) and scales (rows, 2, blocks), in one allocation, if kept.
+// y (..., inter) of x (..., 2 inter), no view of another tensor: a result of autograd that is one cannot be changed in place.
+// With codes (rows, 2, ld) and scales (rows, 2, blocks), in one allocation, if kept.
 struct GatedResult {
   at::Tensor y, codes, scales;
-  GatedResult(const at::Tensor &x, bool keep) {
-    const c10::DeviceGuard guard(x.device());
+  GatedResult(const at::Tensor &given, bool keep) {
+    const c10::DeviceGuard guard(given.device());
+    const at::Tensor x = as_matrix(given);
     const int64_t rows = x.size(0), inter = x.size(1) / 2, ld = (inter + 15) / 16 * 16, nq = (inter + 127) / 128;
-    y = like(x, rows, inter);
+    y = at::empty(sizes_with(given, inter), at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
     if (keep) {
       const int64_t scales_at = (2 * rows * ld + 255) / 256 * 256;
       codes = at::empty({scales_at + 8 * rows * nq}, at::TensorOptions().dtype(at::kChar).device(x.device()));
@@ -669,7 +671,7 @@ struct GatedResult {
       scales.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, nq});
       codes.unsafeGetTensorImpl()->set_sizes_contiguous({rows, 2, ld});
     }
-    must(gated_entry((tlr_dtype)code_of(x), rows, inter, x.data_ptr(), row_stride(x), y.data_ptr(), row_stride(y),
+    must(gated_entry((tlr_dtype)code_of(x), rows, inter, x.data_ptr(), row_stride(x), y.data_ptr(), std::max<int64_t>(inter, 1),
                      keep ? codes.data_ptr() : nullptr, ld, keep ? static_cast<float *>(scales.data_ptr()) : nullptr, nq, stream_of(x.device())));
   }
 };
@@ -685,9 +687,9 @@ at::Tensor gated_rows_grad(const at::Tensor &dy, const at::Tensor &codes, const 
 
 struct Gated : torch::autograd::Function<Gated> {
   static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &x) {
-    const GatedResult r(as_matrix(x), true);
+    const GatedResult r(x, true);
     ctx->save_for_backward({r.codes, r.scales});
-    return x.dim() == 2 ? r.y : r.y.view(sizes_with(x, r.y.size(1)));
+    return r.y;
   }
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, const torch::autograd::variable_list &grads) {
     const auto saved = ctx->get_saved_variables();
@@ -709,8 +711,7 @@ PyObject *gated(PyObject *, PyObject *x_) {
   const c10::DeviceGuard guard(x.device());
   try {
     if (c10::GradMode::is_enabled() && x.requires_grad()) return wrap(Gated::apply(x));
-    const GatedResult r(as_matrix(x), false);
-    return wrap(x.dim() == 2 ? r.y : r.y.view(sizes_with(x, r.y.size(1))));
+    return wrap(GatedResult(x, false).y);
   } catch (const Failed &f) {
     return PyLong_FromLong(f.status);
   }
@@ -725,7 +726,7 @@ PyObject *gated_forward(PyObject *, PyObject *x_) {
   const at::Tensor &x = THPVariable_Unpack(x_);
   const c10::DeviceGuard guard(x.device());
   try {
-    const GatedResult r(with_rows(x), true);
+    const GatedResult r(x, true);
     return tuple_of({r.y, r.codes, r.scales});
   } catch (const Failed &f) {
     return PyLong_FromLong(f.status);

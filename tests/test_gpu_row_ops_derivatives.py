@@ -85,3 +85,20 @@ def test_changes_in_place_are_noticed_whether_rows_are_kept_or_not(trained):
         w.add_(1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(64,), (3, 64), (2, 3, 64), (2, 1, 3, 64)])
+def test_gated_results_can_be_changed_in_place(shape):
+    """A result that were a view of another tensor could not be, of any number of dimensions but two."""
+    x = torch.randn(*shape, device="cuda", requires_grad=True)
+    dy = torch.randn(*shape[:-1], 32, device="cuda")
+    y = blocks.gated(x)
+    want, = torch.autograd.grad(y, [x], 2.0 * dy)
+    kept = y.detach().clone()
+    y = blocks.gated(x)
+    y.mul_(2.0).add_(1.0)
+    got, = torch.autograd.grad(y, [x], dy)
+    assert torch.equal(got, want) and torch.equal(y.detach(), 2.0 * kept + 1.0)
+    with torch.no_grad():
+        z = blocks.gated(x)
+    assert torch.equal(z.add_(1.0), kept + 1.0)

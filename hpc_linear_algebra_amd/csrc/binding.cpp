@@ -449,18 +449,19 @@ PyObject *row_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (codes.dim() != 2 || codes.device() != x.device() || x.size(-1) != k) return value_error("linear: x is (..., k) on the device of a weight of 2 dimensions");
   if (grad && THPVariable_Unpack(args[2]).requires_grad()) return value_error("linear: scales that require a gradient would get none");
   const c10::DeviceGuard guard(x.device());
-  const at::Tensor given = x;
+  const int64_t m = codes.size(0);
+  // no view of another tensor: one made without gradients cannot be changed in place with them
+  const at::Tensor c = at::empty(sizes_with(x, m), at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
   x = as_matrix(x);
-  const int64_t m = codes.size(0), tokens = x.size(0);
-  const at::Tensor c = at::empty({tokens, m}, at::TensorOptions().device(x.device()).dtype(x.scalar_type()));
+  const int64_t tokens = x.size(0);
   size_t bytes = 0;
   tlr_status st = row_linear_bytes_entry(m, tokens, k, &bytes);
   if (st != TLR_OK) return PyLong_FromLong(st);
   if (bytes > 0) ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(x.device()));
-  st = row_linear_entry((tlr_dtype)code_of(x), m, tokens, k, &A, x.data_ptr(), row_stride(x), c.data_ptr(), row_stride(c),
+  st = row_linear_entry((tlr_dtype)code_of(x), m, tokens, k, &A, x.data_ptr(), row_stride(x), c.data_ptr(), std::max<int64_t>(m, 1),
                         bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream_of(x.device()));
   if (st != TLR_OK) return PyLong_FromLong(st);
-  return wrap(given.dim() == 2 ? c : c.view(sizes_with(given, m)));
+  return wrap(c);
   END_HANDLE_TH_ERRORS
 }
 

@@ -102,3 +102,17 @@ def test_gated_results_can_be_changed_in_place(shape):
     with torch.no_grad():
         z = blocks.gated(x)
     assert torch.equal(z.add_(1.0), kept + 1.0)
+
+
+@pytest.mark.parametrize("shape", [(48,), (3, 48), (2, 3, 48), (2, 1, 30, 48)])
+def test_results_without_gradients_take_some_in_place(shape):
+    """A frozen layer's result, made without gradients, and what is trained beside it."""
+    x, W = torch.randn(*shape, device="cuda"), int8.quantize(torch.randn(16, 48, device="cuda"))
+    for frozen in (lambda: int8.linear(x, W), lambda: blocks.gated(x[..., :32])):
+        with torch.no_grad():
+            y = frozen()
+        beside = torch.randn_like(y).requires_grad_()
+        kept = y.clone()
+        y += 2.0 * beside
+        got, = torch.autograd.grad(y.sum(), [beside])
+        assert torch.equal(got, torch.full_like(got, 2.0)) and torch.equal(y.detach(), kept + 2.0 * beside.detach())

@@ -178,8 +178,10 @@ class _Linear(torch.autograd.Function):
         ctx.save_for_backward(*_parts(x8t), *_parts(w8t))
         ctx.grad_fmt, ctx.fast = grad_fmt, fast
         ctx.shape, ctx.types = x.shape, (x.dtype, w.dtype)
-        out = torch.empty((x2.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-        return gemm(w8, x8, out=out, fast=fast and x.dtype != torch.float32).reshape(*x.shape[:-1], w.shape[0])
+        # no view of another tensor is returned: autograd refuses changes of one in place
+        out = torch.empty((*x.shape[:-1], w.shape[0]), dtype=x.dtype, device=x.device)
+        gemm(w8, x8, out=out.view(x2.shape[0], w.shape[0]), fast=fast and x.dtype != torch.float32)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable

@@ -116,3 +116,15 @@ def test_results_without_gradients_take_some_in_place(shape):
         y += 2.0 * beside
         got, = torch.autograd.grad(y.sum(), [beside])
         assert torch.equal(got, torch.full_like(got, 2.0)) and torch.equal(y.detach(), kept + 2.0 * beside.detach())
+
+
+@pytest.mark.parametrize("shape", [(3, 48), (2, 3, 48), (2, 1, 3, 48), (0, 3, 48)])
+def test_linear_results_can_be_changed_in_place(shape):
+    x, w = torch.randn(*shape, device="cuda", requires_grad=True), torch.randn(16, 48, device="cuda", requires_grad=True)
+    dy = torch.randn(*shape[:-1], 16, device="cuda")
+    y = blocks.linear(x, w)
+    want = torch.autograd.grad(y, [x, w], dy)
+    kept = y.detach().clone()
+    y = blocks.linear(x, w)
+    y += 1.0
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, [x, w], dy), want)) and torch.equal(y.detach(), kept + 1.0)

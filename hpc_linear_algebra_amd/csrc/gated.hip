@@ -98,7 +98,7 @@ template <typename T, bool KEEP> __global__ __launch_bounds__(256) void gated_ke
         const float(&v)[8] = h ? u : g;
         const float s = int8_scale(max16(top[h]));
         if (c == 0) a.scales[(at + h) * a.lds + q] = s;
-        if (left > 0) *reinterpret_cast<u2 *>(a.codes + (at + h) * a.ldq + col) = int8_codes8(v, s, 1.0f / s);
+        if (col < ((a.inter + 15) & ~15)) *reinterpret_cast<u2 *>(a.codes + (at + h) * a.ldq + col) = int8_codes8(v, s, 1.0f / s);
       }
     }
   }

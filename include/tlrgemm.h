@@ -735,8 +735,9 @@ tlr_status tlr_expert_combine_grad(tlr_dtype dt, int64_t tokens, int32_t topk, i
  *           int8 codes of g at codes + 2*i*ldq and of u at codes + (2*i + 1)*ldq,
  *           one scale for every 128 of them (the last ones fewer) at scales + 2*i*lds
  *           and scales + (2*i + 1)*lds.  Scale and codes as tlr_row_quantize's, a
- *           block of 128 in place of a row.  ldq >= inter, a multiple of 16, codes
- *           16-byte aligned; lds >= ceil(inter / 128).
+ *           block of 128 in place of a row; bytes inter .. inter rounded up to 16 of
+ *           each are written as zero.  ldq >= inter, a multiple of 16, codes 16-byte
+ *           aligned; lds >= ceil(inter / 128).
  * tlr_gated_grad: the gradient at the values g', u' that the codes stand for:
  *   dX = (dY u' s (1 + g' (1 - s)), dY g' s), s = 1 / (1 + exp(-g')), rounded once.
  * dt is TLR_F32, TLR_F16 or TLR_BF16 for X, Y and their gradients, any alignment of

@@ -1,8 +1,9 @@
-"""The gated activation over the whole range of its operands."""
+"""The gated activation over the whole range of its operands, and what stands behind the last code of a row."""
 import pytest
 import torch
 
 from hpc_linear_algebra_amd import blocks
+from hpc_linear_algebra_amd import tlrgemm as T
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +82,19 @@ def test_small_gradients_of_large_factors():
     factor = d * u * torch.sigmoid(g)
     check(dx[:, 127], factor * (1.0 + g * torch.sigmoid(-g)), g, "f32", factor.abs() * (1.0 + g.abs()))
     check(dx[:, 255], d * g * torch.sigmoid(g), g, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("inter", [1, 8, 9, 16, 120, 130, 200, 264])
+def test_codes_behind_the_last_entry_are_zeros(inter, dtype):
+    """As the row quantizer's, up to a multiple of 16; what a longer row holds behind that stays."""
+    rows, up = 5, -(-inter // 16) * 16
+    x = torch.randn(rows, 2 * inter, device="cuda").to(DT[dtype])
+    x[1, 0] = float("nan")
+    y = torch.empty(rows, inter, dtype=DT[dtype], device="cuda")
+    ldq, lds = up + 32, -(-inter // 128) + 1
+    codes, scales = torch.full((rows, 2, ldq), 85, dtype=torch.int8, device="cuda"), torch.zeros(rows, 2, lds, device="cuda")
+    T.tlr_gated(dtype, rows, inter, x.data_ptr(), 2 * inter, y.data_ptr(), inter, codes.data_ptr(), ldq, scales.data_ptr(), lds,
+                torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert not codes[:, :, inter:up].any() and bool((codes[:, :, up:] == 85).all())

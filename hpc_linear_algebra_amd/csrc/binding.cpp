@@ -232,7 +232,7 @@ PyObject *moe(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const long most = PyLong_AsLong(args[2]);
   void *ws = PyLong_AsVoidPtr(args[3]);
   const size_t bytes = PyLong_AsSize_t(args[4]);
-  if (PyErr_Occurred() || !no_tangent("MoELayer", {&x})) return nullptr;
+  if (PyErr_Occurred() || !no_trace("MoELayer") || !no_tangent("MoELayer", {&x})) return nullptr;
   if (x.dim() != 2 || x.size(1) != layer->hidden || code_of(x) != layer->dt || !x.is_cuda())
     return value_error("MoELayer: x is (tokens, hidden), of the layer's type and on its GPU");
   const int64_t tokens = x.size(0);

@@ -60,7 +60,8 @@ class MoELayer:
     the layer has to live until the call's work has ended.
 
     There is no backward pass: where gradients are on, an x or weights that
-    require one are refused, and an x with a tangent of forward mode always.
+    require one are refused, and an x with a tangent of forward mode always, as is
+    a call within torch.jit.trace.
     """
 
     def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, topk: int,

@@ -128,3 +128,20 @@ def test_linear_results_can_be_changed_in_place(shape):
     y = blocks.linear(x, w)
     y += 1.0
     assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, [x, w], dy), want)) and torch.equal(y.detach(), kept + 1.0)
+
+
+def test_traces_of_layers_are_refused():
+    layer = moe.MoELayer(torch.randn(4, 16, device="cuda").half(), torch.randn(4, 32, 16, device="cuda").half(),
+                         torch.randn(4, 16, 16, device="cuda").half(), 2)
+    G, D = int8.quantize(torch.randn(3, 32, 16, device="cuda")), int8.quantize(torch.randn(3, 16, 16, device="cuda"))
+    x, ids, w = torch.randn(5, 16, device="cuda").half(), torch.zeros(5, 2, dtype=torch.int32, device="cuda"), torch.rand(5, 2, device="cuda")
+    for call in (lambda v: layer(v)[0], lambda v: moe.Int8Experts(G, D)(v, ids, w)):
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            torch.jit.trace(call, (x,), check_trace=False)
+        assert torch.equal(call(x), call(x))
+    # a product within a function of autograd is recorded as that function
+    v = torch.randn(8, 16, device="cuda")
+    with torch.no_grad():
+        traced = torch.jit.trace(lambda z: blocks.linear(z, v) + 1.0, (torch.zeros(5, 16, device="cuda"),), check_trace=False)
+        z = torch.randn(5, 16, device="cuda")
+        assert torch.equal(traced(z), blocks.linear(z, v) + 1.0)

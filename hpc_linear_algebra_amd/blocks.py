@@ -225,9 +225,9 @@ def gated_forward(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Te
     """(y, codes, scales) of a 2-d x: y = silu(gate) * up, and x as int8 codes
     (rows, 2, inter rounded up to 16) with a float32 scale for every 128 of them
     (rows, 2, ceil(inter/128)), gate first.  The scale is the largest magnitude over
-    127.  Codes and scales are views of one allocation.  None of them carries a gradient,
-    whatever x does, and a tangent of forward mode is refused: gated is the function
-    for autograd."""
+    127, codes behind the last entry are zeros.  Codes and scales are views of one
+    allocation.  None of them carries a gradient, whatever x does, and a tangent of
+    forward mode is refused: gated is the function for autograd."""
     got = binding().gated_forward(x)
     if type(got) is int:
         T._check(got, "tlr_gated")
